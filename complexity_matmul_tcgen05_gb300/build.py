@@ -31,6 +31,10 @@ SOURCES = [
     "fgemm_kern_skinny.cu",
     "fgemm_kern_mx.cu",
     "fgemm_kern_lcma.cu",
+    "fgemm_ops_api.cu",
+    "fgemm_kern_norm.cu",
+    "fgemm_kern_w4.cu",
+    "fgemm_kern_sample.cu",
 ]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE,

@@ -689,6 +689,18 @@ fgemm_status_t load_calibration(fgemm_handle_t h, const char* path) {
 
 // ====================================================================== ABI
 
+namespace fgemm {
+cudaStream_t handle_stream(const fgemm_handle_s* h) { return h->stream; }
+int handle_sms(const fgemm_handle_s* h) { return h->num_sms; }
+int handle_fail(fgemm_handle_s* h, int status, const char* text) noexcept {
+  try {
+    return set_msg(h, static_cast<fgemm_status_t>(status), text);
+  } catch (...) {  // no memory for the text: the status stands without it
+    return status;
+  }
+}
+}  // namespace fgemm
+
 extern "C" {
 
 const char* fgemm_status_string(fgemm_status_t s) {

@@ -7,6 +7,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+struct fgemm_handle_s;
+
 namespace fgemm {
 
 constexpr int kBM = 128;          // output tile rows (tcgen05 M = 128, one CTA)
@@ -152,6 +154,12 @@ FGEMM_HD inline long long stream_k_slot(int tiles, int k_blocks, int ctas, int u
   const long long lo = static_cast<long long>(c) * total / ctas;
   return static_cast<long long>(c) * 2 + (lo >= tile_lo ? 0 : 1);
 }
+
+// What the entry points outside fgemm_api.cu need of a handle.
+cudaStream_t handle_stream(const fgemm_handle_s* h);
+int handle_sms(const fgemm_handle_s* h);
+// Records the text fgemm_last_message returns and gives back the status.
+int handle_fail(fgemm_handle_s* h, int status, const char* text) noexcept;
 
 struct KernelParams {
   CUtensorMap tmap_a;  // A: inner dim K, outer M, box {64, 128}, 128B swizzle
@@ -349,6 +357,76 @@ struct MxJob {
 
 // Converts one or two such matrices (njobs 1 or 2) in a single launch.
 cudaError_t launch_mx_dequant(const MxJob* jobs, int njobs, int num_sms, cudaStream_t stream);
+
+// Root-mean-square norm with the residual's addition (fgemm_kern_norm.cu).
+// q != null: block-scaled 8-bit output in q and scales, else 16-bit in y.
+struct NormParams {
+  const uint16_t* x;
+  const uint16_t* res;   // or null
+  const uint16_t* gain;  // n entries
+  uint16_t* total;       // or null: not stored
+  uint16_t* y;
+  uint8_t* q;
+  uint8_t* scales;
+  float* inv_rms;        // m entries, or null
+  long long m, ldx, ldr, ldt, ldy, ldq, lds;
+  int n, mx_format, is_bf16;
+  float eps;
+  int tpr, out_vec;      // set by the launch: threads a row, y or q takes whole-chunk stores
+};
+cudaError_t launch_norm(const NormParams& p, cudaStream_t stream);
+
+struct NormBackParams {
+  const uint16_t* dy;
+  const uint16_t* total;
+  const uint16_t* gain;
+  const uint16_t* dtotal;  // or null
+  const float* inv_rms;    // m entries
+  uint16_t* dx;
+  float* dgain;            // n entries, or null
+  float* partials;         // ctas x n, or null with dgain
+  float* dots;             // m entries
+  long long m, lddy, ldt, lddt, lddx;
+  int n, is_bf16, ctas;    // ctas = norm_back_ctas(m, SMs)
+};
+int norm_back_ctas(long long m, int num_sms);
+size_t norm_back_workspace(long long m, int n, int num_sms);
+cudaError_t launch_norm_back(const NormBackParams& p, cudaStream_t stream);
+
+// Products with 4-bit weights (fgemm_kern_w4.cu): c (m x n_out) =
+// epi(alpha a W^T + bias), W[j][k] = (code - zero) * scale of the group of
+// `group` (32, 64 or 128) values of k, two codes to a byte, the even one low.
+struct W4Params {
+  const uint16_t* a;
+  const uint8_t* w;
+  const uint16_t* scales;
+  const uint8_t* zeros;  // or null: 8
+  const uint16_t* bias;  // or null
+  uint16_t* c;
+  long long lda, ldw, lds, ldz, ldc;
+  int m, n, k, n_out, group, epi, is_bf16;
+  float alpha;
+  int tiles, k_blocks, m_tile;  // set by the launch
+};
+cudaError_t launch_w4(const W4Params& p, int num_sms, cudaStream_t stream);
+
+// Sampling (fgemm_kern_sample.cu).
+struct SampleParams {
+  const void* logits;
+  long long ld;
+  const float* u;
+  const float* temperature;  // rows entries each, or null: the value beside it
+  const int* top_k;
+  const float* top_p;
+  const float* min_p;
+  float temperature0, top_p0, min_p0;
+  int top_k0;
+  int* token;
+  float* prob;               // or null
+  int rows, vocab, type;     // type: 0 f16, 1 bf16, 2 f32
+  int slice;                 // set by the launch: logits of one CTA
+};
+cudaError_t launch_sample(const SampleParams& p, int num_sms, cudaStream_t stream);
 
 // One-level Winograd variant on the single-CTA kernel (bn = 128 or 256): the
 // Strassen kernel with up to four source blocks per formed operand; `tab`

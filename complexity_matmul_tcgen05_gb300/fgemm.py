@@ -34,6 +34,12 @@ class Rms(ctypes.Structure):
                 ("eps", ctypes.c_float)]
 
 
+class Sampling(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_float), ("top_k", ctypes.c_int32), ("top_p", ctypes.c_float),
+                ("min_p", ctypes.c_float), ("temperatures", ctypes.c_void_p), ("top_ks", ctypes.c_void_p),
+                ("top_ps", ctypes.c_void_p), ("min_ps", ctypes.c_void_p)]
+
+
 class FgemmError(RuntimeError):
     def __init__(self, status: int, message: str):
         self.status = status
@@ -94,6 +100,16 @@ def lib() -> ctypes.CDLL:
         L.fgemm_matmul_mx.argtypes = [vp, i64, i64, i64, vp, i64, vp, i64, i32, vp, i64, vp, i64,
                                       i32, vp, i64, epi_p, st, i32, i32]
         L.fgemm_mx_to_bf16.argtypes = [vp, i64, i64, vp, i64, vp, i64, i32, i32, vp, i64]
+        f32, size = ctypes.c_float, ctypes.c_size_t
+        norm = [vp, i64, i64, vp, i64, vp, i64, vp, f32, st, vp, i64]
+        L.fgemm_rms_norm.argtypes = norm + [vp, i64, vp]
+        L.fgemm_rms_norm_mx.argtypes = norm + [i32, vp, i64, vp, i64, vp]
+        L.fgemm_rms_norm_backward.argtypes = [vp, i64, i64, vp, i64, vp, i64, vp, vp, vp, i64, st, vp, i64, vp, vp,
+                                              size]
+        L.fgemm_rms_norm_backward_workspace.argtypes = [vp, i64, i64]
+        L.fgemm_rms_norm_backward_workspace.restype = size
+        L.fgemm_matmul_w4.argtypes = [vp, i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32, vp, i64, st, epi_p]
+        L.fgemm_sample.argtypes = [vp, i64, i64, vp, i64, i32, vp, ctypes.POINTER(Sampling), vp, vp]
         L.fgemm_plan.argtypes = [vp, i64, i64, i64, st, epi_p, ctypes.POINTER(st),
                                  ctypes.POINTER(i32), ctypes.POINTER(i32),
                                  ctypes.POINTER(ctypes.c_double)]
@@ -157,7 +173,8 @@ def lib() -> ctypes.CDLL:
                      "fgemm_strassen_matmul_static", "fgemm_selftest_wait_timeout",
                      "fgemm_set_split_mode", "fgemm_set_lcma_formation", "fgemm_call_launches", "fgemm_matmul_host", "fgemm_matmul_host_ex", "fgemm_matmul_rms", "fgemm_matmul_mx",
                      "fgemm_mx_to_bf16", "fgemm_strassen_static_get_error",
-                     "fgemm_strassen_static_selftest_timeout"):
+                     "fgemm_strassen_static_selftest_timeout", "fgemm_rms_norm", "fgemm_rms_norm_mx",
+                     "fgemm_rms_norm_backward", "fgemm_matmul_w4", "fgemm_sample"):
             getattr(L, name).restype = st
         _lib = L
         return L
@@ -541,3 +558,206 @@ def plan(M: int, N: int, K: int, dtype: torch.dtype = torch.bfloat16, epilogue: 
     """(algorithm, tile_m, tile_n, predicted microseconds) the decision model picks."""
     h = default_handle()
     return h.plan(M, N, K, _dtype_code(dtype), make_epilogue(epilogue))
+
+
+# ------------------------------------------- operators of a token step
+
+
+def _rows(t: torch.Tensor | None, name: str, shape, dtype, device) -> tuple[int | None, int]:
+    """(address, leading dimension) of a 2-D operand, checked; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        raise FgemmError(ERR_INVALID_ARG, f"{name} must be a {tuple(shape)} {dtype} tensor on {device}")
+    rows, cols = shape
+    if cols > 1 and t.stride(1) != 1:
+        raise FgemmError(ERR_INVALID_ARG, f"{name} must be row-major with unit column stride")
+    return t.data_ptr(), t.stride(0) if rows > 1 else max(cols, 1)
+
+
+def _vector(t: torch.Tensor | None, name: str, n: int, dtype, device) -> int | None:
+    """Address of a contiguous vector of n entries, checked; None for None."""
+    if t is None:
+        return None
+    if t.dim() != 1 or t.shape[0] != n or t.dtype != dtype or t.device != device or (n > 1 and t.stride(0) != 1):
+        raise FgemmError(ERR_INVALID_ARG, f"{name} must be a contiguous vector of {n} {dtype} entries on {device}")
+    return t.data_ptr()
+
+
+def _on(t: torch.Tensor, name: str, handle: Handle | None) -> Handle:
+    """The handle of a call whose main operand is t, set to the current stream of t's device."""
+    if not t.is_cuda:
+        raise FgemmError(ERR_INVALID_ARG, f"{name} must be a CUDA tensor")
+    if t.dim() != 2:
+        raise FgemmError(ERR_INVALID_ARG, f"{name} must be 2-D")
+    h = handle if handle is not None else default_handle()
+    if t.device.index != h.device:
+        raise FgemmError(ERR_INVALID_ARG, f"{name} is on {t.device}, the handle on cuda:{h.device}")
+    lib().fgemm_set_stream(h.ptr, torch.cuda.current_stream(t.device).cuda_stream)
+    return h
+
+
+def _norm_args(x, gain, residual, total, inv_rms, handle):
+    h = _on(x, "x", handle)
+    dt = _dtype_code(x.dtype)
+    m, n = shape = x.shape
+    if total is None:
+        total = x if residual is None else torch.empty(shape, dtype=x.dtype, device=x.device)
+    if inv_rms is None:
+        inv_rms = torch.empty(m, dtype=torch.float32, device=x.device)
+    return h, m, n, dt, total, inv_rms
+
+
+def rms_norm(x: torch.Tensor, gain: torch.Tensor, *, residual: torch.Tensor | None = None, eps: float = 1e-6,
+             out: torch.Tensor | None = None, total: torch.Tensor | None = None,
+             inv_rms: torch.Tensor | None = None, handle: Handle | None = None):
+    """(y, total, inv_rms) of fgemm_rms_norm: total = x + residual rounded to
+    x's type (x itself, not copied, without a residual), y = total * inv_rms *
+    gain with inv_rms = 1 / sqrt(mean(total^2) + eps) per row (fp32).
+
+    x and residual are M x N fp16 or bf16, gain has N entries.  out, total and
+    inv_rms, if given, are written (out and total may be x, total may be the
+    residual)."""
+    given = total
+    h, m, n, dt, total, inv_rms = _norm_args(x, gain, residual, total, inv_rms, handle)
+    dev, t, shape = x.device, x.dtype, x.shape
+    if out is None:
+        out = torch.empty(shape, dtype=t, device=dev)
+    xp, ldx = _rows(x, "x", shape, t, dev)
+    rp, ldr = _rows(residual, "residual", shape, t, dev)
+    tp, ldt = _rows(total, "total", shape, t, dev) if residual is not None or given is not None else (None, 0)
+    yp, ldy = _rows(out, "out", shape, t, dev)
+    s = lib().fgemm_rms_norm(h.ptr, m, n, xp, ldx, rp, ldr, _vector(gain, "gain", n, t, dev), eps, dt, tp, ldt, yp, ldy,
+                             _vector(inv_rms, "inv_rms", m, torch.float32, dev))
+    if s != OK:
+        _check(s, h.ptr)
+    return out, total, inv_rms
+
+
+def rms_norm_mx(x: torch.Tensor, gain: torch.Tensor, *, residual: torch.Tensor | None = None, eps: float = 1e-6,
+                fmt: str = "e4m3", total: torch.Tensor | None = None, inv_rms: torch.Tensor | None = None,
+                handle: Handle | None = None):
+    """(q, scales, total, inv_rms) of fgemm_rms_norm_mx: rms_norm with its
+    output in block-scaled 8 bits, q (M x N uint8) and E8M0 scales (M x
+    ceil(N / 32) uint8) as matmul_mx takes its A and scale_a."""
+    given = total
+    h, m, n, dt, total, inv_rms = _norm_args(x, gain, residual, total, inv_rms, handle)
+    if fmt not in FP8_FORMATS:
+        raise FgemmError(ERR_INVALID_ARG, f"fmt must be one of {sorted(FP8_FORMATS)}")
+    dev, t, shape = x.device, x.dtype, x.shape
+    blocks = (n + 31) // 32
+    q = torch.empty(shape, dtype=torch.uint8, device=dev)
+    scales = torch.empty((m, blocks), dtype=torch.uint8, device=dev)
+    xp, ldx = _rows(x, "x", shape, t, dev)
+    rp, ldr = _rows(residual, "residual", shape, t, dev)
+    tp, ldt = _rows(total, "total", shape, t, dev) if residual is not None or given is not None else (None, 0)
+    s = lib().fgemm_rms_norm_mx(h.ptr, m, n, xp, ldx, rp, ldr, _vector(gain, "gain", n, t, dev), eps, dt, tp, ldt,
+                                FP8_FORMATS[fmt], q.data_ptr(), max(n, 1), scales.data_ptr(), max(blocks, 1),
+                                _vector(inv_rms, "inv_rms", m, torch.float32, dev))
+    if s != OK:
+        _check(s, h.ptr)
+    return q, scales, total, inv_rms
+
+
+def rms_norm_backward(dy: torch.Tensor, total: torch.Tensor, gain: torch.Tensor, inv_rms: torch.Tensor, *,
+                      dtotal: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                      dgain: torch.Tensor | None = None, handle: Handle | None = None):
+    """(dx, dgain) of fgemm_rms_norm_backward, from dy and what rms_norm
+    returned.  dx (dy's type) is the gradient of x and of the residual alike
+    and includes dtotal, the gradient that reaches total by other ways; dgain
+    (N fp32 entries) is summed over the rows.  out and dgain, if given, are
+    written (out may be dy or dtotal)."""
+    h = _on(dy, "dy", handle)
+    dt = _dtype_code(dy.dtype)
+    m, n = shape = dy.shape
+    dev, t = dy.device, dy.dtype
+    if out is None:
+        out = torch.empty(shape, dtype=t, device=dev)
+    if dgain is None:
+        dgain = torch.empty(n, dtype=torch.float32, device=dev)
+    dyp, lddy = _rows(dy, "dy", shape, t, dev)
+    tp, ldt = _rows(total, "total", shape, t, dev)
+    dtp, lddt = _rows(dtotal, "dtotal", shape, t, dev)
+    op, ldo = _rows(out, "out", shape, t, dev)
+    size = lib().fgemm_rms_norm_backward_workspace(h.ptr, m, n)
+    work = torch.empty(size, dtype=torch.uint8, device=dev)
+    s = lib().fgemm_rms_norm_backward(h.ptr, m, n, dyp, lddy, tp, ldt, _vector(gain, "gain", n, t, dev),
+                                      _vector(inv_rms, "inv_rms", m, torch.float32, dev), dtp, lddt, dt, op, ldo,
+                                      _vector(dgain, "dgain", n, torch.float32, dev), work.data_ptr(), size)
+    if s != OK:
+        _check(s, h.ptr)
+    return out, dgain
+
+
+def matmul_w4(A: torch.Tensor, W: torch.Tensor, scales: torch.Tensor, *, zeros: torch.Tensor | None = None,
+              group: int = 128, out: torch.Tensor | None = None, epilogue: str = "none", alpha: float = 1.0,
+              bias: torch.Tensor | None = None, handle: Handle | None = None) -> torch.Tensor:
+    """C = epi(alpha * A @ Wv.T + bias) through fgemm_matmul_w4, with 4-bit
+    weights Wv[j, k] = (code[j, k] - zero[j, k // group]) * scale[j, k // group].
+
+    A is M x K (fp16 or bf16), W is N x ceil(K / 2) uint8 (two codes to a byte
+    along K, the even k in the low half), scales N x ceil(K / group) of A's
+    type, zeros the same shape in uint8 (None: 8 everywhere), group 32, 64 or
+    128.  Epilogues and bias as in matmul (swiglu: rows [0, N / 2) of W are
+    the gate, the output is M x N / 2)."""
+    h = _on(A, "A", handle)
+    dt = _dtype_code(A.dtype)
+    m, k = A.shape
+    n = W.shape[0]
+    if epilogue not in EPILOGUES:
+        raise FgemmError(ERR_INVALID_ARG, f"epilogue must be one of {sorted(EPILOGUES)}")
+    if group not in (32, 64, 128):
+        raise FgemmError(ERR_INVALID_ARG, "group must be 32, 64 or 128")
+    dev, t = A.device, A.dtype
+    n_out = n // 2 if epilogue == "swiglu" else n
+    groups = (n, (k + group - 1) // group)
+    if out is None:
+        out = torch.empty((m, n_out), dtype=t, device=dev)
+    ap, lda = _rows(A, "A", (m, k), t, dev)
+    wp, ldw = _rows(W, "W", (n, (k + 1) // 2), torch.uint8, dev)
+    sp, lds = _rows(scales, "scales", groups, t, dev)
+    zp, ldz = _rows(zeros, "zeros", groups, torch.uint8, dev)
+    cp, ldc = _rows(out, "out", (m, n_out), t, dev)
+    epi = Epilogue(EPILOGUES[epilogue], alpha, _vector(bias, "bias", n, t, dev))
+    s = lib().fgemm_matmul_w4(h.ptr, m, n, k, ap, lda, wp, ldw, sp, lds, zp, ldz, group, cp, ldc, dt,
+                              ctypes.byref(epi))
+    if s != OK:
+        _check(s, h.ptr)
+    return out
+
+
+LOGIT_TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, *, temperature: float | torch.Tensor = 1.0,
+           top_k: int | torch.Tensor = 0, top_p: float | torch.Tensor = 1.0, min_p: float | torch.Tensor = 0.0,
+           handle: Handle | None = None):
+    """(token, prob) of fgemm_sample: one token (int32) from each row of
+    logits (rows x vocab, fp16, bf16 or fp32) by the uniform numbers u (fp32,
+    one a row), and its probability among the tokens that were kept (fp32).
+
+    temperature (0: the largest logit), top_k (0: off), top_p (1: off) and
+    min_p (0: off) are one number for all rows, or vectors with an entry for
+    each (fp32; top_k int32).  A row with nothing above -inf gives token -1
+    and prob 0."""
+    h = _on(logits, "logits", handle)
+    rows, vocab = logits.shape
+    code = LOGIT_TYPES.get(logits.dtype)
+    if code is None:
+        raise FgemmError(ERR_INVALID_ARG, f"logits must be float16, bfloat16 or float32, not {logits.dtype}")
+    dev = logits.device
+    how = Sampling(1.0, 0, 1.0, 0.0, None, None, None, None)
+    for name, value, dtype in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
+                               ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
+        if isinstance(value, torch.Tensor):
+            setattr(how, name + "s", _vector(value, name, rows, dtype, dev))
+        else:
+            setattr(how, name, value)
+    lp, ld = _rows(logits, "logits", (rows, vocab), logits.dtype, dev)
+    token = torch.empty(rows, dtype=torch.int32, device=dev)
+    prob = torch.empty(rows, dtype=torch.float32, device=dev)
+    s = lib().fgemm_sample(h.ptr, rows, vocab, lp, ld, code, _vector(u, "u", rows, torch.float32, dev),
+                           ctypes.byref(how), token.data_ptr(), prob.data_ptr())
+    if s != OK:
+        _check(s, h.ptr)
+    return token, prob

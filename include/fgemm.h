@@ -34,6 +34,7 @@
 #ifndef FGEMM_H
 #define FGEMM_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -320,6 +321,127 @@ fgemm_status_t fgemm_plan_ex(fgemm_handle_t h, int64_t M, int64_t N, int64_t K,
                              fgemm_dtype_t dtype, const fgemm_epilogue_t* epi, fgemm_algo_t algo,
                              int32_t tile_m_in, int32_t tile_n_in, fgemm_algo_t* algo_out,
                              int32_t* tile_m, int32_t* tile_n, double* predicted_us);
+
+/* ------------------------------------------------------------------------
+ * Operators of a token step, next to the products: the root-mean-square norm
+ * in front of a projection, projections with 4-bit weights, and the choice
+ * of the next token. They allocate nothing, keep nothing in the handle and
+ * do not synchronise, so they may be captured into a graph and their
+ * arguments may live on any stream's memory. Sizes of 0 .. 2^31 - 1024; any
+ * address aligned to its element type and any leading dimension is accepted
+ * unless stated (16-byte aligned rows are faster).
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Root-mean-square norm with the residual's addition. For each of M rows of
+ * N values (x and the rest of type dtype):
+ *   total = x + residual (rounded to dtype; residual NULL: total = x)
+ *   inv   = 1 / sqrt(mean_j total_j^2 + eps)
+ *   y_j   = total_j * inv * gain_j           (fp32, rounded once)
+ *   residual  NULL or M x N, ldr.  gain  N entries.  eps finite, >= 0.
+ *   total     NULL or M x N, ldt: written (the next residual; may be x or
+ *             residual itself).
+ *   y         M x N, ldy (may be x itself).
+ *   inv_rms   NULL or M entries: written, for the backward pass.
+ * A row whose inv is infinite (all zeros with eps 0) gives NaN.
+ */
+fgemm_status_t fgemm_rms_norm(fgemm_handle_t h, int64_t M, int64_t N, const void* x, int64_t ldx,
+                              const void* residual, int64_t ldr, const void* gain, float eps,
+                              fgemm_dtype_t dtype, void* total, int64_t ldt, void* y, int64_t ldy,
+                              float* inv_rms);
+
+/*
+ * fgemm_rms_norm with y in block-scaled 8 bits, as fgemm_matmul_mx takes its
+ * A: q (M x N bytes, ldq) and E8M0 scales (M x ceil(N / 32), lds). The scale
+ * of a block of 32 is 2^(floor(log2 max|y|) - 8) for E4M3, - 15 for E5M2,
+ * held to 2^-127 and above; elements are y / scale rounded to nearest even
+ * from fp32, those beyond the largest finite value set to it. A block with an
+ * infinity or a NaN gets the NaN scale.
+ */
+fgemm_status_t fgemm_rms_norm_mx(fgemm_handle_t h, int64_t M, int64_t N, const void* x, int64_t ldx,
+                                 const void* residual, int64_t ldr, const void* gain, float eps,
+                                 fgemm_dtype_t dtype, void* total, int64_t ldt, int32_t format, void* q,
+                                 int64_t ldq, void* scales, int64_t lds, float* inv_rms);
+
+/*
+ * Backward pass of fgemm_rms_norm (and of fgemm_rms_norm_mx with the rounding
+ * to 8 bits taken as the identity). With u = total * inv_rms, a = dy * gain:
+ *   dx_j    = inv_rms (a_j - u_j mean_k(a_k u_k)) + dtotal_j
+ *   dgain_j = sum over rows of dy_j u_j
+ * dx is the gradient of x and of the residual alike.
+ *   dtotal     NULL or M x N, lddt: the gradient that reaches total by other
+ *              ways (the residual stream).
+ *   dx         M x N, lddx (may be dy or dtotal itself).
+ *   dgain      NULL or N fp32 entries (written; zeros for M == 0).
+ *   workspace  at least fgemm_rms_norm_backward_workspace(h, M, N) bytes of
+ *              device memory, 4-byte aligned, left with nothing of use.
+ * Sums are fp32 in an order that depends on the sizes and the SM count only.
+ */
+size_t fgemm_rms_norm_backward_workspace(fgemm_handle_t h, int64_t M, int64_t N);
+fgemm_status_t fgemm_rms_norm_backward(fgemm_handle_t h, int64_t M, int64_t N, const void* dy, int64_t lddy,
+                                       const void* total, int64_t ldt, const void* gain, const float* inv_rms,
+                                       const void* dtotal, int64_t lddt, fgemm_dtype_t dtype, void* dx,
+                                       int64_t lddx, float* dgain, void* workspace, size_t workspace_bytes);
+
+/*
+ * C = epi(alpha * A * W^T + bias) with 4-bit weights and group scales:
+ *   W[j][k] = (code[j][k] - zero[j][k / group]) * scale[j][k / group]
+ *   A, lda       M x K of dtype.
+ *   W, ldw       N x ceil(K / 2) bytes, ldw in bytes: two codes (0 .. 15) to
+ *                a byte along K, the even k in the low half. (N x K, unlike
+ *                B of fgemm_matmul: codes are read along K.)
+ *   scales, lds  N x ceil(K / group) of dtype.
+ *   zeros, ldz   N x ceil(K / group) bytes, or NULL: every zero point is 8.
+ *   group        32, 64 or 128.
+ *   C, ldc, epi  as fgemm_matmul (columns of C: N, or N / 2 with SWIGLU;
+ *                the gate is rows [0, N / 2) of W).
+ * The codes are multiplied as they are and the scale is applied to fp32 sums
+ * of a group: no weight is rounded.
+ * A and W 16-byte aligned, lda a multiple of 8, ldw of 16, else
+ * FGEMM_ERR_ALIGNMENT. K == 0: C = epi(bias).
+ */
+fgemm_status_t fgemm_matmul_w4(fgemm_handle_t h, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
+                               const void* W, int64_t ldw, const void* scales, int64_t lds, const void* zeros,
+                               int64_t ldz, int32_t group, void* C, int64_t ldc, fgemm_dtype_t dtype,
+                               const fgemm_epilogue_t* epi);
+
+/*
+ * One token from each row of logits, by one given uniform number u in [0, 1).
+ * For a row x with largest value m (a NaN counts as -infinity):
+ *   w_i = exp((x_i - m) / temperature); order: larger x, then lower index
+ *   top_k > 0: the first top_k of the order
+ *   top_p < 1: of those, the shortest prefix whose w sum to at least top_p of
+ *              theirs (at least one)
+ *   min_p > 0: of those, the ones with w_i >= min_p (at least the first)
+ *   token = the first i, in index order, at which the running sum of the kept
+ *           w exceeds u times their sum; prob = w_i / their sum.
+ * temperature not above 0: the first largest logit, prob 1. A row with
+ * nothing above -infinity (vocab 0 among them): token -1, prob 0. w holds
+ * about 36 bits and sums are exact, so results do not depend on order and
+ * follow the formula wherever no border is nearer than about 1e-11.
+ *   logits, ld   rows x vocab of logits_type.  u  rows entries; one outside
+ *                [0, 1) counts as the nearest number inside, a NaN as 0.
+ *   how          for each setting an array of one entry per row, or NULL and
+ *                the one value beside it for all rows. Device pointers; the
+ *                struct itself is host memory and read during the call.
+ *   token        rows entries.  prob  rows entries or NULL.
+ * vocab above FGEMM_SAMPLE_MAX_VOCAB -> FGEMM_ERR_UNSUPPORTED.
+ */
+#define FGEMM_LOGITS_F32 2 /* a logits_type beside FGEMM_F16 and FGEMM_BF16 */
+#define FGEMM_SAMPLE_MAX_VOCAB ((int64_t)1 << 19)
+typedef struct {
+  float temperature;
+  int32_t top_k;
+  float top_p;
+  float min_p;
+  const float* temperatures;
+  const int32_t* top_ks;
+  const float* top_ps;
+  const float* min_ps;
+} fgemm_sampling_t;
+fgemm_status_t fgemm_sample(fgemm_handle_t h, int64_t rows, int64_t vocab, const void* logits, int64_t ld,
+                            int32_t logits_type, const float* u, const fgemm_sampling_t* how, int32_t* token,
+                            float* prob);
 
 /* Synchronises the handle's stream, then returns and clears the latched
  * device error (FGEMM_OK, FGEMM_ERR_TIMEOUT or FGEMM_ERR_CUDA). */
