@@ -34,6 +34,7 @@ SOURCES = [
     "fgemm_ops_api.cu",
     "fgemm_kern_norm.cu",
     "fgemm_kern_w4.cu",
+    "fgemm_kern_w4mm.cu",
     "fgemm_kern_sample.cu",
 ]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -692,6 +692,19 @@ fgemm_status_t load_calibration(fgemm_handle_t h, const char* path) {
 namespace fgemm {
 cudaStream_t handle_stream(const fgemm_handle_s* h) { return h->stream; }
 int handle_sms(const fgemm_handle_s* h) { return h->num_sms; }
+unsigned int* handle_err(const fgemm_handle_s* h) { return h->d_err; }
+unsigned long long handle_spin_ns(const fgemm_handle_s* h) { return h->spin_ns; }
+bool encode_map_2d(CUtensorMap* out, const void* ptr, int bytes, uint64_t inner, uint64_t outer, uint64_t pitch,
+                   uint32_t box_inner, uint32_t box_outer) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = get_encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {inner, outer}, strides[1] = {pitch};
+  const cuuint32_t box[2] = {box_inner, box_outer}, step[2] = {1, 1};
+  return enc(out, bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+             const_cast<void*>(ptr), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             box_inner * bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 int handle_fail(fgemm_handle_s* h, int status, const char* text) noexcept {
   try {
     return set_msg(h, static_cast<fgemm_status_t>(status), text);

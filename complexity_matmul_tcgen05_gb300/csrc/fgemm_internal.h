@@ -158,6 +158,8 @@ FGEMM_HD inline long long stream_k_slot(int tiles, int k_blocks, int ctas, int u
 // What the entry points outside fgemm_api.cu need of a handle.
 cudaStream_t handle_stream(const fgemm_handle_s* h);
 int handle_sms(const fgemm_handle_s* h);
+unsigned int* handle_err(const fgemm_handle_s* h);       // its device error word
+unsigned long long handle_spin_ns(const fgemm_handle_s* h);
 // Records the text fgemm_last_message returns and gives back the status.
 int handle_fail(fgemm_handle_s* h, int status, const char* text) noexcept;
 
@@ -396,7 +398,11 @@ cudaError_t launch_norm_back(const NormBackParams& p, cudaStream_t stream);
 // Products with 4-bit weights (fgemm_kern_w4.cu): c (m x n_out) =
 // epi(alpha a W^T + bias), W[j][k] = (code - zero) * scale of the group of
 // `group` (32, 64 or 128) values of k, two codes to a byte, the even one low.
+// The few-rows kernel takes up to kW4FewRows rows of A; more go through tcgen05
+// (fgemm_kern_w4mm.cu), which needs w4_workspace bytes.
+constexpr int kW4FewRows = 8;
 struct W4Params {
+  CUtensorMap tmap_w, tmap_x;  // the codes, and A as the pre-pass packs it (set by launch_w4mm)
   const uint16_t* a;
   const uint8_t* w;
   const uint16_t* scales;
@@ -404,11 +410,28 @@ struct W4Params {
   const uint16_t* bias;  // or null
   uint16_t* c;
   long long lda, ldw, lds, ldz, ldc;
+  unsigned int* err;           // device error word
+  unsigned long long spin_ns;  // bound of every wait
   int m, n, k, n_out, group, epi, is_bf16;
   float alpha;
-  int tiles, k_blocks, m_tile;  // set by the launch
+  // set by the launches: tiles, CTAs along K and k (few rows) or steps of 128 k
+  // (tcgen05) of each, k of A kept in shared memory
+  int tiles, slices, slice, chunk;
+  uint16_t* x;   // m x k_pad packed A
+  float* sx;     // groups x m_pad sums
+  float* unit;   // m units
+  int k_pad;
+  long long m_pad;
 };
-cudaError_t launch_w4(const W4Params& p, int num_sms, cudaStream_t stream);
+size_t w4_workspace(long long m, long long k, int group);
+cudaError_t launch_w4(const W4Params& p, void* workspace, int num_sms, cudaStream_t stream);
+cudaError_t launch_w4mm(const W4Params& p, void* workspace, int num_sms, cudaStream_t stream);
+
+// A 2D map of `bytes`-wide elements (1: integers, 2: fp16), inner x outer with
+// rows `pitch` bytes apart, in boxes of box_inner x box_outer whose rows of 64
+// or 128 bytes are swizzled.  False if the driver refuses it.
+bool encode_map_2d(CUtensorMap* out, const void* ptr, int bytes, uint64_t inner, uint64_t outer, uint64_t pitch,
+                   uint32_t box_inner, uint32_t box_outer);
 
 // Sampling (fgemm_kern_sample.cu).
 struct SampleParams {

@@ -7,27 +7,29 @@
 // A few rows of A (a decode step's tokens) against all of W: bound by
 // reading the codes, 0.5 byte a weight.
 //
-// The codes are never turned into weights.  q goes into the top mantissa
-// bits of a 16-bit 1.0, which makes 1 + q/16 (exact in fp16 and bf16) in one
-// shift and one logical operation for two codes, and the tensor cores sum
-//   acc = sum_k (1 + q/16) x,   sx = sum_k x      (fp32, over one group)
-// from which the group's part of the product is
-//   sum_k (q - z) s x = 16 s (acc - (1 + z/16) sx),
-// added to the running fp32 sum.  No weight is rounded, and scales and zero
-// points cost a few operations a group instead of one a weight.  sx comes
-// from one more tensor-core product with a matrix of ones, in the register
-// layout of acc.  An infinite or NaN x makes acc - sx meaningless: an output
-// that is not finite is computed again term by term (w4_exact).
+// The codes are never turned into weights: the scale of a group is applied to
+// the fp32 sums of its codes,
+//   sum_k (q - z) s x = s (acc - z sx),   acc = sum_k q x,   sx = sum_k x,
+// so no weight is rounded, and scales and zero points cost a few operations a
+// group instead of one a weight.
+//
+// A code is a 16-bit operand of the tensor cores as it stands: four bits at
+// the bottom of an fp16 number are the subnormal q 2^-24, four bits above them
+// q 2^-20, both exact, so one logical operation makes two operands and one
+// shift serves four.  The factor 2^4 between the two kinds goes into A.  For
+// that, A too is held as fp16, scaled by a power of two for each row and group
+// (the largest value below 2^15; 2^11 for the k whose codes are the upper
+// kind), bf16 as well: its 8 significant bits fit, and what falls below fp16's
+// range is under 2^-35 of the group's largest value, less than the fp32 sums
+// resolve.
+// An infinite or NaN x makes acc - z sx meaningless: an output that is not
+// finite is computed again term by term (w4_exact).
 //
 // mma.sync with the codes as the 16-row operand and 8 rows of A as the other:
 // the operand goes from the ring in shared memory through registers, where
 // it is expanded, into the tensor core, with no second trip through shared
 // memory as tcgen05 operands would take; at 8 rows of A its rate is not the
 // bound.
-//
-// Each warp takes every eighth block of 256 k of the CTA's 16 R columns of C
-// with a ring of its own (cp.async, three blocks), so warps never wait for
-// each other until their sums meet in shared memory, once a tile.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -36,13 +38,21 @@
 
 #include "fgemm_internal.h"
 #include "fgemm_ptx.cuh"
+#include "fgemm_w4.cuh"
 
 namespace fgemm {
 
 namespace {
 
-constexpr int kW4Warps = 8;
-constexpr int kW4Block = 256;  // k of one ring slot: 128 bytes of codes a row
+constexpr int kW4Warps = 8;     // of a team, which works on one tile
+constexpr int kW4Teams = 2;     // of a CTA; they share A
+constexpr int kW4Threads = kW4Teams * kW4Warps * 32;
+constexpr int kW4Rows = 32;    // rows of W (columns of C) of a tile
+constexpr int kW4Block = 128;  // k of one ring slot: 64 bytes of codes a row
+constexpr int kW4Stages = 3;
+// Of A in shared memory; finer groups have more scales beside it, more rows more sums.
+template <int NT, int GC>
+constexpr int kW4ABytes = ((GC > 1 ? 64 : 48) - (NT > 1 ? 16 : 0)) * 1024;
 
 // 16 bytes global -> shared; bytes past `valid` (0..16) are zero and not read.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int valid) {
@@ -54,154 +64,241 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a)
-               : "memory");
-  return v;
-}
-
-template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if (BF16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <bool BF16>
-__device__ __forceinline__ float w4_f32(uint16_t v) {
-  if (BF16) return __uint_as_float(static_cast<uint32_t>(v) << 16);
-  return __half2float(__ushort_as_half(v));
-}
-
-// The eight codes of a word as 1 + q/16, in pairs: p[i] holds code i in its
-// low half and code i + 4 in its high half.
-template <bool BF16>
-__device__ __forceinline__ void expand(uint32_t w, uint32_t (&p)[4]) {
-  constexpr uint32_t one = BF16 ? 0x3F803F80u : 0x3C003C00u;
-  constexpr uint32_t mask = BF16 ? 0x00780078u : 0x03C003C0u;
-  constexpr int top = BF16 ? 3 : 6;  // where a code's low bit goes
-  p[0] = ((w << top) & mask) | one;
-  p[1] = (top >= 4 ? (w << (top >= 4 ? top - 4 : 0)) & mask : (w >> (top >= 4 ? 0 : 4 - top)) & mask) | one;
-  p[2] = ((w >> (8 - top)) & mask) | one;
-  p[3] = ((w >> (12 - top)) & mask) | one;
-}
-
-__device__ __forceinline__ float w4_silu(float v) { return v / (1.0f + __expf(-v)); }
-
-// Column j of W against row i of A, term by term.
-template <bool BF16>
-__device__ __noinline__ float w4_exact(const W4Params& p, long long i, long long j) {
-  float sum = 0.0f;
-  for (int k = 0; k < p.k; ++k) {
-    const int q = (p.w[j * p.ldw + (k >> 1)] >> (4 * (k & 1))) & 15;
-    const int g = k / p.group;
-    const float z = p.zeros ? static_cast<float>(p.zeros[j * p.ldz + g]) : 8.0f;
-    sum += w4_f32<BF16>(p.a[i * p.lda + k]) * ((static_cast<float>(q) - z) * w4_f32<BF16>(p.scales[j * p.lds + g]));
-  }
-  return sum;
-}
-
-// The column of W that virtual row r (0 .. 16 R - 1) of a tile stands for.
-// SwiGLU: rows 0-7 of each 16 are gate columns and rows 8-15 the up columns
-// they pair with, so that a tile yields 8 R outputs.
-__device__ __forceinline__ int w4_column(const W4Params& p, int tile, int r, int rows) {
-  if (p.epi != kEpiSwiglu) return tile * rows + r;
-  const int j = tile * (rows / 2) + (r >> 4) * 8 + (r & 7);
-  return j >= p.n_out ? p.n : (r & 8) ? p.n_out + j : j;
-}
-
-template <bool BF16, int R, int NT, int STAGES, int GC>  // GC: group / 32
-__global__ void __launch_bounds__(kW4Warps * 32) w4_kernel(const __grid_constant__ W4Params p) {
+// The few-rows kernel: tiles of 32 rows of W against all (at most 16) rows
+// of A.
+//
+// A sits in shared memory for as long as the CTA lives (when it fits; else a
+// chunk of K at a time), its values already in the order in which expand()
+// pairs codes, with the sums sx of each group beside it.  The codes stream
+// through a ring of the warp's own: warp w of a team takes the blocks w,
+// w + 8, ... of 128 k of a tile, so warps wait for each other once a tile,
+// when their sums meet, while the blocks of the next tile are already on
+// their way.  With few tiles, the CTAs of a cluster take a slice of K each and
+// add their sums through distributed shared memory, in rank order.
+template <bool BF16, int NT, int GC>  // GC: group / 32
+__global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant__ W4Params p) {
   extern __shared__ __align__(128) unsigned char smem[];
-  constexpr int ROWS = 16 * R;
-  constexpr int GROUPS = 8 / GC;                       // groups of a block
-  constexpr int PER = GROUPS > 4 ? GROUPS / 4 : 1;     // of them, a lane's
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int R = kW4Rows / 16;
+  constexpr int GROUPS = 4 / GC;  // groups of a block
+  constexpr int G = GC * 32;
+  const int team = threadIdx.x / (kW4Warps * 32), tid = threadIdx.x % (kW4Warps * 32);
+  const int warp = tid >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int m0 = blockIdx.y * (8 * NT);
-  const int mt = min(p.m - m0, 8 * NT);
-  const uint32_t a_bytes = static_cast<uint32_t>(p.m_tile) * 512;
-  const uint32_t slot_bytes = ROWS * 128 + a_bytes;
-  float* red = reinterpret_cast<float*>(smem);  // [warp][row][8 NT + 1]
-  constexpr int kPitch = 8 * NT + 1;
-  const uint32_t ring = ptx::smem_u32(smem) + ((kW4Warps * ROWS * kPitch * 4 + 127) / 128 * 128) +
-                        static_cast<uint32_t>(warp) * STAGES * slot_bytes;
-  const int w_bytes = (p.k + 1) / 2;
-  const int groups = (p.k + p.group - 1) / p.group;
+  const int slices = p.slices;
+  const int rank = slices > 1 ? static_cast<int>(ptx::cluster_ctarank()) : 0;
+  const int mt = p.m;
+  // k of this CTA
+  const int k_lo = rank * p.slice, k_hi = min(p.k, k_lo + p.slice);
+  const int blocks = k_hi > k_lo ? (k_hi - k_lo + kW4Block - 1) / kW4Block : 0;
+  const int chunk_blocks = p.chunk / kW4Block;
 
-  // this warp's blocks: (tile, kb), kb = warp, warp + 8, ... of each tile
-  int load_tile = blockIdx.x, load_kb = warp, load_slot = 0;
-  if (load_kb >= p.k_blocks) load_tile = p.tiles;
-  auto issue = [&]() {
-    if (load_tile < p.tiles) {
-      const uint32_t slot = ring + static_cast<uint32_t>(load_slot) * slot_bytes;
-      // codes: 16-byte chunk c of row r at chunk c ^ (r & 7)
+  // shared memory: the warps' rings of codes and of scales, A, sx, the warps'
+  // sums, the teams' sums
+  constexpr int kSlot = kW4Rows * 64, kScales = kW4Rows * GROUPS;
+  unsigned char* const ring = smem + (threadIdx.x >> 5) * (kW4Stages * kSlot);
+  float2* const scale_ring = reinterpret_cast<float2*>(smem + kW4Teams * kW4Warps * kW4Stages * kSlot) +
+                             (threadIdx.x >> 5) * (kW4Stages * kScales);  // [group][row]: scale, zero point
+  unsigned char* const a_at = smem + kW4Teams * kW4Warps * kW4Stages * (kSlot + kScales * 8);
+  const int a_pitch = p.chunk * 2;
+  float2* const sx_at = reinterpret_cast<float2*>(a_at + static_cast<size_t>(a_pitch) * mt);  // [group of the chunk][8 NT]
+  float* const red = reinterpret_cast<float*>(sx_at + p.chunk / G * (8 * NT)) + team * ((kW4Warps + 2) * kW4Rows * mt);  // [warp][row of A][row]
+  float* const part = red + kW4Warps * kW4Rows * mt;  // [2][row of A][row], read by the cluster
+  const int w_bytes = (p.k + 1) / 2 - k_lo / 2;  // of a row, from this CTA's first
+  const int groups = (p.k + G - 1) / G;
+  const int tile_step = gridDim.x / slices * kW4Teams;
+  const int first_tile = blockIdx.x / slices + team * (gridDim.x / slices);
+
+  // this warp's blocks in the order it works on them: tile by tile, chunk by
+  // chunk, block warp, warp + 8, ... of the chunk.  A lane copies 16 bytes of
+  // four rows of a block and fetches the scales and zero points of row `lane`;
+  // rows past the last repeat it, and their sums go nowhere.
+  int load_tile = first_tile, load_chunk = 0, load_b = warp, load_slot = 0;
+  const uint8_t* w_row[4];
+  const uint16_t* s_row;
+  const uint8_t* z_row;
+  const int tile_rows = p.epi == kEpiSwiglu ? kW4Rows / 2 : kW4Rows;  // rows of W from one tile to the next
+  auto aim = [&]() {  // the rows of load_tile
 #pragma unroll
-      for (int i = 0; i < ROWS / 4; ++i) {
-        const int r = i * 4 + (lane >> 3), c = lane & 7;
-        const int col = w4_column(p, load_tile, r, ROWS);
-        const int byte = load_kb * 128 + c * 16;
-        const int valid = col < p.n ? max(0, min(16, w_bytes - byte)) : 0;
-        const uint8_t* src = valid > 0 ? p.w + col * p.ldw + byte : p.w;
-        cp_async16(slot + r * 128 + ((c ^ (r & 7)) << 4), src, valid);
-      }
-      // rows of A: chunk c of row r at chunk c ^ 4 (r & 1)
-      for (int r = 0; r < mt; ++r) {
-        const int k0 = load_kb * kW4Block + lane * 8;
-        const int valid = max(0, min(16, (p.k - k0) * 2));
-        const uint16_t* src = valid > 0 ? p.a + (m0 + r) * p.lda + k0 : p.a;
-        cp_async16(slot + ROWS * 128 + r * 512 + ((lane ^ ((r & 1) << 2)) << 4), src, valid);
-      }
-      load_slot = load_slot + 1 == STAGES ? 0 : load_slot + 1;
-      load_kb += kW4Warps;
-      if (load_kb >= p.k_blocks) {
-        load_kb = warp;
-        load_tile += gridDim.x;
+    for (int i = 0; i < 4; ++i)
+      w_row[i] = p.w + min(w4_column(p, load_tile, i * 8 + (lane >> 2), kW4Rows), p.n - 1) * p.ldw + (lane & 3) * 16 +
+                 k_lo / 2;
+    const long long row = min(w4_column(p, load_tile, lane, kW4Rows), p.n - 1);
+    s_row = p.scales + row * p.lds;
+    z_row = p.zeros + row * p.ldz;
+  };
+  const long long w_step = static_cast<long long>(tile_step) * tile_rows * p.ldw;
+  const long long s_step = static_cast<long long>(tile_step) * tile_rows * p.lds;
+  const long long z_step = static_cast<long long>(tile_step) * tile_rows * p.ldz;
+  auto next_tile = [&]() {
+    load_tile += tile_step;
+    if (load_tile + 1 >= p.tiles) {  // perhaps a ragged one
+      if (load_tile < p.tiles) aim();
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w_row[i] += w_step;
+    s_row += s_step;
+    z_row += z_step;
+    // the first of these is read a block later
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(s_row + k_lo / G));
+    if (p.zeros) asm volatile("prefetch.global.L2 [%0];" ::"l"(z_row + k_lo / G));
+  };
+  auto settle = [&]() {  // past what this warp has no block of
+    while (load_chunk + load_b >= min(blocks, load_chunk + chunk_blocks)) {
+      load_b = warp;
+      load_chunk += chunk_blocks;
+      if (load_chunk >= blocks) {
+        load_chunk = 0;
+        if (min(blocks, chunk_blocks) <= warp) load_tile = p.tiles;  // none in any tile
+        next_tile();
+        if (load_tile >= p.tiles) return;
       }
     }
+  };
+  // Scales are fetched with their block's codes, but through registers: they
+  // are stored to the ring when the next block's are fetched, one block later,
+  // so that no instruction waits for them.
+  uint16_t s_next[GROUPS];
+  uint32_t z_next[GROUPS];
+#pragma unroll
+  for (int i = 0; i < GROUPS; ++i) s_next[i] = 0, z_next[i] = 8;
+  auto issue = [&]() {
+    const int before = load_slot == 0 ? kW4Stages - 1 : load_slot - 1;  // the slot of the block issued last
+#pragma unroll
+    for (int i = 0; i < GROUPS; ++i)
+      scale_ring[before * kScales + i * kW4Rows + lane] =
+          make_float2(w4_f32<BF16>(s_next[i]), __uint_as_float(0x4B000000u | z_next[i]) - 8388608.0f);
+    if (load_tile < p.tiles) {
+      const int block = load_chunk + load_b, byte = block * (kW4Block / 2);
+      // 16-byte chunk c of row r at chunk c ^ (r >> 1 & 3)
+      const uint32_t dst = ptx::smem_u32(ring) + load_slot * kSlot + (lane >> 2) * 64 +
+                           (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+      if (byte + kW4Block / 2 <= w_bytes) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cp_async16(dst + i * 512, w_row[i] + byte, 16);
+      } else {
+        const int valid = max(0, min(16, w_bytes - byte - (lane & 3) * 16));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cp_async16(dst + i * 512, valid > 0 ? w_row[i] + byte : p.w, valid);
+      }
+      const int gi = k_lo / G + block * GROUPS;
+#pragma unroll
+      for (int i = 0; i < GROUPS; ++i) {
+        const int at = min(gi + i, groups - 1);  // past the last group A is zero
+        s_next[i] = s_row[at];
+        if (p.zeros) z_next[i] = z_row[at];
+      }
+      load_b += kW4Warps;
+      settle();
+    }
+    load_slot = load_slot + 1 == kW4Stages ? 0 : load_slot + 1;
     cp_async_commit();  // possibly empty: the count of groups stays in step
   };
-  // scales and zero points of a block: lane t of a quad holds groups t PER ..
-  // of its row's GROUPS (lanes past GROUPS / PER repeat)
-  struct Scales {
-    float s[2 * R][PER], z[2 * R][PER];
+  // Run `run` (8 values) of row m of A from k0 on; values from k_hi on are zero.
+  auto fetch_run = [&](int m, int k0) {
+    uint4 x = make_uint4(0, 0, 0, 0);
+    const uint16_t* src = p.a + m * p.lda + k0;
+    if (k0 + 8 <= k_hi) {
+      x = *reinterpret_cast<const uint4*>(src);
+    } else if (k0 < k_hi) {
+      uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (k0 + j < k_hi) w[j >> 1] |= static_cast<uint32_t>(src[j]) << (16 * (j & 1));
+      x = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return x;
   };
-  auto fetch = [&](Scales& v, int tile, int kb) {
+  // A's rows of one chunk into shared memory as scaled fp16, each run of 8
+  // values in the order 0 4 1 5 2 6 3 7, and for each group its scale and sum.
+  // The G / 8 lanes that hold a group agree on its largest value.
+  // begin(), once, runs between the first loads and their use.
+  const int runs = p.chunk / 8;  // of a row of the chunk, a multiple of 32: a warp is in one row
+  auto load_a = [&](int chunk0, auto begin) {
+    constexpr int kBatch = 4;
+    for (int run0 = 0; run0 < runs; run0 += kW4Threads) {
+      const int run = run0 + threadIdx.x;
+      for (int m0 = 0; m0 < mt; m0 += kBatch) {
+        uint4 x[kBatch];
 #pragma unroll
-    for (int r = 0; r < 2 * R; ++r) {
-      const long long col = w4_column(p, tile, (r >> 1) * 16 + (r & 1) * 8 + g, ROWS);
+        for (int i = 0; i < kBatch; ++i)
+          if (run < runs && m0 + i < mt) x[i] = fetch_run(m0 + i, k_lo + chunk0 * kW4Block + run * 8);
+        if (run0 == 0 && m0 == 0) begin();
+        if (run >= runs) break;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int gi = kb * GROUPS + (t * PER + i) % GROUPS;
-        const bool ok = col < p.n && gi < groups;
-        v.s[r][i] = ok ? 16.0f * w4_f32<BF16>(p.scales[col * p.lds + gi]) : 0.0f;
-        v.z[r][i] = ok && p.zeros ? 1.0f + 0.0625f * static_cast<float>(p.zeros[col * p.ldz + gi]) : 1.5f;
+        for (int i = 0; i < kBatch; ++i) {
+          const int m = m0 + i;
+          if (m >= mt) break;
+          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          const uint32_t pair = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                                         __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+          uint32_t most = max(pair & 0xFFFFu, pair >> 16);
+          float v[8], s = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            v[j] = w4_f32<BF16>(static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1))));
+            s += v[j];
+          }
+#pragma unroll
+          for (int o = 1; o < G / 8; o <<= 1) {
+            most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+            s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+          }
+          const int e = w4_shift<BF16>(most);
+          if (run % (G / 8) == 0) sx_at[run / (G / 8) * (8 * NT) + m] = make_float2(s, w4_pow2(24 - e));
+          const float even = w4_pow2(e), odd = even * 0.0625f;
+          uint32_t o[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float f = j & 1 ? odd : even;
+            const __half2 h = __floats2half2_rn(v[j] * f, v[j + 4] * f);
+            o[j] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          *reinterpret_cast<uint4*>(a_at + m * a_pitch + ((run ^ ((m & 1) << 2)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
       }
     }
+    __syncthreads();
   };
 
+  if (blocks > 0 && load_tile < p.tiles) {
+    aim();
+    settle();
+  } else {
+    load_tile = p.tiles;
+  }
+  auto start = [&]() {
 #pragma unroll
-  for (int i = 0; i < STAGES - 1; ++i) issue();
-  int slot_i = 0;
-  const uint32_t ones[4] = {BF16 ? 0x3F803F80u : 0x3C003C00u, BF16 ? 0x3F803F80u : 0x3C003C00u,
-                            BF16 ? 0x3F803F80u : 0x3C003C00u, BF16 ? 0x3F803F80u : 0x3C003C00u};
+    for (int i = 0; i < kW4Stages - 1; ++i) issue();
+  };
+  const bool resident = chunk_blocks >= blocks;
+  if (resident)
+    load_a(0, start);
+  else
+    start();
+  int slot_i = 0, side = 0;
+  // A's rows as the tensor core's columns; those past mt repeat the last one
+  // and their sums go nowhere.  Run 4 c + t of a block is at 4 (c ^ row % 2) + t.
+  const unsigned char* a_row[NT][2];  // by c % 2
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int m = min(8 * n + g, mt - 1);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) a_row[n][c] = a_at + m * a_pitch + ((4 * (c ^ (m & 1)) + t) << 4);
+  }
 
-  for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
+  // A team without a last tile goes along where the CTA or the cluster meets.
+  const bool meets = !resident || slices > 1;
+  for (int tile = first_tile; meets ? tile - team * (gridDim.x / slices) < p.tiles : tile < p.tiles;
+       tile += tile_step, side ^= 1) {
+    const bool live = tile < p.tiles;
     float sum[R][NT][4];
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -210,155 +307,194 @@ __global__ void __launch_bounds__(kW4Warps * 32) w4_kernel(const __grid_constant
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum[r][n][i] = 0.0f;
 
-    Scales next;
-    if (warp < p.k_blocks) fetch(next, tile, warp);
-    for (int kb = warp; kb < p.k_blocks; kb += kW4Warps) {
-      const Scales sc = next;
-      if (kb + kW4Warps < p.k_blocks) fetch(next, tile, kb + kW4Warps);
-      cp_async_wait<STAGES - 2>();
-      __syncwarp();  // every lane's copies are in, and every lane is done with the slot that is filled next
-      issue();
-      const uint32_t slot = ring + static_cast<uint32_t>(slot_i) * slot_bytes;
-      slot_i = slot_i + 1 == STAGES ? 0 : slot_i + 1;
+    for (int chunk0 = 0; chunk0 < blocks; chunk0 += chunk_blocks) {
+      if (!resident) {
+        __syncthreads();  // every warp is done with the chunk before
+        load_a(chunk0, [] {});
+      }
+      const int end = min(blocks - chunk0, chunk_blocks);
+      for (int b = warp; live && b < end; b += kW4Warps) {
+        cp_async_wait<kW4Stages - 2>();
+        __syncwarp();  // every lane's copies are in, and every lane is done with the slot that is filled next
+        issue();
+        const unsigned char* slot = ring + slot_i * kSlot + g * 64 + t * 4;
+        const float2* scales = scale_ring + slot_i * kScales + g;
+        slot_i = slot_i + 1 == kW4Stages ? 0 : slot_i + 1;
 #pragma unroll
-      for (int grp = 0; grp < GROUPS; ++grp) {
-        float acc[R][NT][4], sx[NT][4];
+        for (int grp = 0; grp < GROUPS; ++grp) {
+          float acc[R][NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+          for (int r = 0; r < R; ++r)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            sx[n][i] = 0.0f;
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int r = 0; r < R; ++r) acc[r][n][i] = 0.0f;
-          }
+              for (int i = 0; i < 4; ++i) acc[r][n][i] = 0.0f;
 #pragma unroll
-        for (int cc = 0; cc < GC; ++cc) {
-          const int c = grp * GC + cc;
-          uint32_t b[NT][4];
+          for (int cc = 0; cc < GC; ++cc) {
+            const int c = grp * GC + cc;
+            uint4 x[NT];
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (8 * n + g < mt)
-              x = lds128(slot + ROWS * 128 + (8 * n + g) * 512 + (((4 * c + t) ^ ((g & 1) << 2)) << 4));
-            b[n][0] = __byte_perm(x.x, x.z, 0x5410);
-            b[n][1] = __byte_perm(x.x, x.z, 0x7632);
-            b[n][2] = __byte_perm(x.y, x.w, 0x5410);
-            b[n][3] = __byte_perm(x.y, x.w, 0x7632);
-            mma16816<BF16>(sx[n], ones, b[n][0], b[n][1]);
-            mma16816<BF16>(sx[n], ones, b[n][2], b[n][3]);
-          }
+            for (int n = 0; n < NT; ++n)
+              x[n] = *reinterpret_cast<const uint4*>(a_row[n][c & 1] + b * 256 + (c >> 1) * 128);
+            const unsigned char* at = slot + ((c ^ ((g >> 1) & 3)) << 4);
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const uint32_t at = slot + (r * 16 + g) * 128 + ((c ^ g) << 4) + t * 4;
-            uint32_t lo[4], hi[4];
-            expand<BF16>(lds32(at), lo);
-            expand<BF16>(lds32(at + 1024), hi);
-            const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
+            for (int r = 0; r < R; ++r) {
+              uint32_t lo[4], hi[4];
+              w4_expand(*reinterpret_cast<const uint32_t*>(at + r * 1024), lo);
+              w4_expand(*reinterpret_cast<const uint32_t*>(at + r * 1024 + 512), hi);
+              // the lower kind of codes in one product, the upper in the other
+              const uint32_t a0[4] = {lo[0], hi[0], lo[2], hi[2]}, a1[4] = {lo[1], hi[1], lo[3], hi[3]};
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma16816<BF16>(acc[r][n], a0, b[n][0], b[n][1]);
-              mma16816<BF16>(acc[r][n], a1, b[n][2], b[n][3]);
+              for (int n = 0; n < NT; ++n) {
+                mma16816(acc[r][n], a0, x[n].x, x[n].z);
+                mma16816(acc[r][n], a1, x[n].y, x[n].w);
+              }
             }
           }
-        }
-        const int from = (lane & ~3) | (grp / PER);
+          float4 sx[NT];  // sum and unit of acc, of two rows of A
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float s0 = __shfl_sync(0xFFFFFFFFu, sc.s[2 * r][grp % PER], from);
-          const float s1 = __shfl_sync(0xFFFFFFFFu, sc.s[2 * r + 1][grp % PER], from);
-          const float z0 = __shfl_sync(0xFFFFFFFFu, sc.z[2 * r][grp % PER], from);
-          const float z1 = __shfl_sync(0xFFFFFFFFu, sc.z[2 * r + 1][grp % PER], from);
+          for (int n = 0; n < NT; ++n)
+            sx[n] = *reinterpret_cast<const float4*>(sx_at + (b * GROUPS + grp) * (8 * NT) + 8 * n + 2 * t);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            sum[r][n][0] = fmaf(s0, fmaf(-z0, sx[n][0], acc[r][n][0]), sum[r][n][0]);
-            sum[r][n][1] = fmaf(s0, fmaf(-z0, sx[n][1], acc[r][n][1]), sum[r][n][1]);
-            sum[r][n][2] = fmaf(s1, fmaf(-z1, sx[n][2], acc[r][n][2]), sum[r][n][2]);
-            sum[r][n][3] = fmaf(s1, fmaf(-z1, sx[n][3], acc[r][n][3]), sum[r][n][3]);
-          }
+          for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float2 sz = scales[grp * kW4Rows + r * 16 + h * 8];
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                float* to = sum[r][n] + 2 * h;
+                to[0] = fmaf(sz.x, fmaf(-sz.y, sx[n].x, acc[r][n][2 * h] * sx[n].y), to[0]);
+                to[1] = fmaf(sz.x, fmaf(-sz.y, sx[n].z, acc[r][n][2 * h + 1] * sx[n].w), to[1]);
+              }
+            }
         }
       }
     }
 
-    // the warps' sums meet in shared memory and are added in warp order
+    // the warps' sums are added in warp order, then the CTAs' in rank order
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int i = 0; i < 2; ++i)
+        if (8 * n + 2 * t + i < mt) {
+          float* const to = red + (warp * mt + 8 * n + 2 * t + i) * kW4Rows + g;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          red[(warp * ROWS + r * 16 + g + (i >> 1) * 8) * kPitch + 8 * n + 2 * t + (i & 1)] = sum[r][n][i];
-    __syncthreads();
+          for (int r = 0; r < R; ++r) {
+            to[r * 16] = sum[r][n][i];
+            to[r * 16 + 8] = sum[r][n][i + 2];
+          }
+        }
+    ptx::named_bar_sync(1 + team, kW4Warps * 32);
     const bool glu = p.epi == kEpiSwiglu;
-    const int outs = glu ? ROWS / 2 : ROWS;
-    for (int e = threadIdx.x; e < outs * mt; e += kW4Warps * 32) {
-      const int i = e / outs, o = e % outs;
+    const int outs_log2 = glu ? 4 : 5;  // columns of C of a tile
+    if (slices > 1) {
+      float* const mine = part + side * (kW4Rows * mt);
+      for (int e = tid; e < kW4Rows * mt; e += kW4Warps * 32) {
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kW4Warps; ++w) s += red[w * mt * kW4Rows + e];
+        mine[e] = s;
+      }
+      __syncwarp();
+      // two buffers: a rank that reads this tile's sums keeps its cluster
+      // from the next meeting, so nobody writes them before the one after
+      ptx::cluster_sync();
+    }
+    for (int e = tid + rank * (kW4Warps * 32); live && e < (mt << outs_log2); e += kW4Warps * 32 * slices) {
+      const int i = e >> outs_log2, o = e & ((1 << outs_log2) - 1);
       const int row = glu ? (o >> 3) * 16 + (o & 7) : o;
-      const int j = tile * outs + o;
+      const int j = (tile << outs_log2) + o;
       if (j >= p.n_out) continue;
       float v[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (h == 1 && !glu) break;
+        const int at = i * kW4Rows + row + 8 * h;
         float s = 0.0f;
+        if (slices > 1) {
+          const uint32_t here = ptx::smem_u32(part + side * (kW4Rows * mt) + at);
+          for (int q = 0; q < slices; ++q) s += ld_cluster_f32(ptx::mapa(here, q));
+        } else {
 #pragma unroll
-        for (int w = 0; w < kW4Warps; ++w) s += red[(w * ROWS + row + 8 * h) * kPitch + i];
+          for (int w = 0; w < kW4Warps; ++w) s += red[w * mt * kW4Rows + at];
+        }
         const long long col = j + static_cast<long long>(h) * p.n_out;
-        if (!isfinite(s)) s = w4_exact<BF16>(p, m0 + i, col);
+        if (!isfinite(s)) s = w4_exact<BF16>(p, i, col);
         v[h] = p.alpha * s + (p.bias ? w4_f32<BF16>(p.bias[col]) : 0.0f);
       }
       const float out = glu ? w4_silu(v[0]) * v[1] : p.epi == kEpiSilu ? w4_silu(v[0]) : v[0];
-      p.c[(m0 + i) * p.ldc + j] = BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(out))
-                                       : __half_as_ushort(__float2half_rn(out));
+      p.c[i * p.ldc + j] = BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(out))
+                                : __half_as_ushort(__float2half_rn(out));
     }
-    __syncthreads();
+    if (slices == 1) ptx::named_bar_sync(1 + team, kW4Warps * 32);  // red is read
   }
   cp_async_wait<0>();
+  __syncwarp();
+  if (slices > 1) ptx::cluster_sync();  // no CTA leaves while its sums may be read
 }
 
-template <bool BF16, int R, int NT, int STAGES, int GC>
-cudaError_t launch_w4_of(W4Params p, int num_sms, cudaStream_t stream) {
-  constexpr int rows = 16 * R;
-  const int per_tile = p.epi == kEpiSwiglu ? rows / 2 : rows;
+template <bool BF16, int NT, int GC>
+cudaError_t launch_w4_few(W4Params p, int num_sms, cudaStream_t stream) {
+  const int per_tile = p.epi == kEpiSwiglu ? kW4Rows / 2 : kW4Rows;
   p.tiles = (p.n_out + per_tile - 1) / per_tile;
-  p.k_blocks = (p.k + kW4Block - 1) / kW4Block;
-  p.m_tile = p.m < 8 * NT ? p.m : 8 * NT;
-  const size_t smem = (kW4Warps * rows * (8 * NT + 1) * 4 + 127) / 128 * 128 +
-                      static_cast<size_t>(kW4Warps) * STAGES * (rows * 128 + static_cast<size_t>(p.m_tile) * 512);
-  auto kernel = w4_kernel<BF16, R, NT, STAGES, GC>;
+  const int blocks = (p.k + kW4Block - 1) / kW4Block;
+  // K is cut into slices, a CTA of a cluster each: while there are SMs without
+  // a tile and every warp keeps a block, and until A's slice fits
+  int slices = 1;
+  const int most_chunk = kW4ABytes<NT, GC> / (2 * p.m) / 256 * 256;
+  while (slices < 8 && blocks >= 2 * slices * kW4Warps && static_cast<long long>(p.tiles) * slices * 2 <= num_sms * kW4Teams)
+    slices *= 2;
+  while (slices < 8 && (blocks + slices - 1) / slices * kW4Block > most_chunk) slices *= 2;
+  p.slices = slices;
+  p.slice = ((blocks + slices - 1) / slices * kW4Block + 255) / 256 * 256;
+  p.chunk = p.slice < most_chunk ? (p.slice > 0 ? p.slice : 256) : most_chunk;
+  const size_t smem = static_cast<size_t>(kW4Teams * kW4Warps) * kW4Stages * kW4Rows * (64 + 4 / GC * 8) +
+                      static_cast<size_t>(p.chunk) * 2 * p.m + static_cast<size_t>(p.chunk / (GC * 32)) * 8 * NT * 8 +
+                      static_cast<size_t>(kW4Teams * (kW4Warps + 2)) * kW4Rows * p.m * 4;
+  auto kernel = w4_kernel<BF16, NT, GC>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  const int resident = static_cast<int>(227 * 1024 / (smem + 1024));
-  const long long slots = static_cast<long long>(num_sms) * (resident < 1 ? 1 : resident > 4 ? 4 : resident);
-  const dim3 grid(static_cast<unsigned>(p.tiles < slots ? p.tiles : slots),
-                  static_cast<unsigned>((p.m + 8 * NT - 1) / (8 * NT)));
-  kernel<<<grid, kW4Warps * 32, smem, stream>>>(p);
-  return cudaGetLastError();
+  const int clusters = num_sms / slices;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((p.tiles < clusters ? p.tiles : clusters) * slices));
+  cfg.blockDim = dim3(kW4Threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = static_cast<unsigned>(slices);
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = slices > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 template <bool BF16>
 cudaError_t launch_w4_type(const W4Params& p, int num_sms, cudaStream_t stream) {
-#define FGEMM_W4_GROUP(R, NT, ST)                                        \
-  (p.group == 32    ? launch_w4_of<BF16, R, NT, ST, 1>(p, num_sms, stream) \
-   : p.group == 64  ? launch_w4_of<BF16, R, NT, ST, 2>(p, num_sms, stream) \
-                    : launch_w4_of<BF16, R, NT, ST, 4>(p, num_sms, stream))
-  if (p.m > 8) return FGEMM_W4_GROUP(2, 2, 2);
-  return FGEMM_W4_GROUP(2, 1, 3);
-#undef FGEMM_W4_GROUP
+  return p.group == 32   ? launch_w4_few<BF16, 1, 1>(p, num_sms, stream)
+         : p.group == 64 ? launch_w4_few<BF16, 1, 2>(p, num_sms, stream)
+                         : launch_w4_few<BF16, 1, 4>(p, num_sms, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_w4(const W4Params& all, int num_sms, cudaStream_t stream) {
-  constexpr int kSlab = 65535 * 8;  // rows of one launch: tiles of at least 8 along a grid dimension of at most 65535
-  for (long long m0 = 0; m0 < all.m; m0 += kSlab) {
-    W4Params p = all;
-    p.a += m0 * p.lda;
-    p.c += m0 * p.ldc;
-    p.m = all.m - m0 < kSlab ? static_cast<int>(all.m - m0) : kSlab;
-    const cudaError_t e = p.is_bf16 ? launch_w4_type<true>(p, num_sms, stream) : launch_w4_type<false>(p, num_sms, stream);
-    if (e != cudaSuccess) return e;
+cudaError_t launch_w4(const W4Params& p, void* workspace, int num_sms, cudaStream_t stream) {
+  if (p.k == 0) {
+    KernelParams q{};
+    q.C = p.c;
+    q.ldc = p.ldc;
+    q.bias = p.bias;
+    q.M = p.m;
+    q.N = p.n;
+    q.n_out = p.n_out;
+    q.epi = p.epi;
+    q.is_bf16 = p.is_bf16;
+    q.alpha = p.alpha;
+    return launch_k0_fill(q, stream);
   }
-  return cudaSuccess;
+  if (p.m > kW4FewRows) return launch_w4mm(p, workspace, num_sms, stream);
+  return p.is_bf16 ? launch_w4_type<true>(p, num_sms, stream) : launch_w4_type<false>(p, num_sms, stream);
 }
 
 }  // namespace fgemm

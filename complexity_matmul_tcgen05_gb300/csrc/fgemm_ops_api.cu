@@ -149,13 +149,18 @@ fgemm_status_t fgemm_rms_norm_backward(fgemm_handle_t h, int64_t M, int64_t N, c
   return launched(h, fgemm::launch_norm_back(p, fgemm::handle_stream(h)));
 }
 
+size_t fgemm_matmul_w4_workspace(int64_t M, int64_t K, int32_t group) {
+  if (M <= 0 || K <= 0 || M > (int64_t{1} << 22) || K > (int64_t{1} << 30) || (group != 32 && group != 64 && group != 128)) return 0;
+  return fgemm::w4_workspace(M, K, group);
+}
+
 fgemm_status_t fgemm_matmul_w4(fgemm_handle_t h, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
                                const void* W, int64_t ldw, const void* scales, int64_t lds, const void* zeros,
                                int64_t ldz, int32_t group, void* C, int64_t ldc, fgemm_dtype_t dtype,
-                               const fgemm_epilogue_t* epi) {
+                               const fgemm_epilogue_t* epi, void* workspace, size_t workspace_bytes) {
   if (!is_16bit(dtype)) return bad_arg(h, "dtype must be FGEMM_F16 or FGEMM_BF16");
-  if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim)
-    return bad_arg(h, "sizes must be in 0 .. 2^31 - 1024");
+  if (M < 0 || N < 0 || K < 0 || M > (int64_t{1} << 22) || N > kMaxDim || K > (int64_t{1} << 30))
+    return bad_arg(h, "sizes must be in 0 .. 2^31 - 1024, M in 0 .. 2^22, K in 0 .. 2^30");
   if (group != 32 && group != 64 && group != 128) return bad_arg(h, "group must be 32, 64 or 128");
   const int32_t kind = epi ? epi->kind : FGEMM_EPI_NONE;
   if (kind < FGEMM_EPI_NONE || kind > FGEMM_EPI_SWIGLU) return bad_arg(h, "unknown epilogue kind");
@@ -176,6 +181,10 @@ fgemm_status_t fgemm_matmul_w4(fgemm_handle_t h, int64_t M, int64_t N, int64_t K
     if (off(A, 16) || off(W, 16) || (M > 1 && lda % 8 != 0) || (N > 1 && ldw % 16 != 0))
       return bad(h, FGEMM_ERR_ALIGNMENT, "A and W must be 16-byte aligned, lda a multiple of 8 and ldw of 16");
     if (off(scales, 2)) return bad(h, FGEMM_ERR_ALIGNMENT, "scales must be 2-byte aligned");
+    const size_t need = fgemm::w4_workspace(M, K, group);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+      return bad_arg(h, "the workspace is smaller than fgemm_matmul_w4_workspace says");
+    if (need > 0 && off(workspace, 256)) return bad(h, FGEMM_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
   }
   if (!h) return no_handle();
   fgemm::W4Params p{};
@@ -198,7 +207,9 @@ fgemm_status_t fgemm_matmul_w4(fgemm_handle_t h, int64_t M, int64_t N, int64_t K
   p.epi = kind;
   p.is_bf16 = dtype == FGEMM_BF16;
   p.alpha = epi ? epi->alpha : 1.0f;
-  return launched(h, fgemm::launch_w4(p, fgemm::handle_sms(h), fgemm::handle_stream(h)));
+  p.err = fgemm::handle_err(h);
+  p.spin_ns = fgemm::handle_spin_ns(h);
+  return launched(h, fgemm::launch_w4(p, workspace, fgemm::handle_sms(h), fgemm::handle_stream(h)));
 }
 
 fgemm_status_t fgemm_sample(fgemm_handle_t h, int64_t rows, int64_t vocab, const void* logits, int64_t ld,

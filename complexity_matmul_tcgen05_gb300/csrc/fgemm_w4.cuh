@@ -1,0 +1,79 @@
+// fgemm_w4.cuh -- what the two kernels of products with 4-bit weights share.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "fgemm_internal.h"
+
+namespace fgemm {
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a)
+               : "memory");
+  return v;
+}
+
+template <bool BF16>
+__device__ __forceinline__ float w4_f32(uint16_t v) {
+  if (BF16) return __uint_as_float(static_cast<uint32_t>(v) << 16);
+  return __half2float(__ushort_as_half(v));
+}
+
+// The eight codes of a word as fp16 pairs: p[i] holds code i in its low half
+// and code i + 4 in its high half, times 2^-24 for even i and 2^-20 for odd.
+__device__ __forceinline__ void w4_expand(uint32_t w, uint32_t (&p)[4]) {
+  const uint32_t v = w >> 8;
+  p[0] = w & 0x000F000Fu;
+  p[1] = w & 0x00F000F0u;
+  p[2] = v & 0x000F000Fu;
+  p[3] = v & 0x00F000F0u;
+}
+
+__device__ __forceinline__ float w4_silu(float v) { return v / (1.0f + __expf(-v)); }
+
+
+// Column j of W against row i of A, term by term.
+template <bool BF16>
+static __device__ __noinline__ float w4_exact(const W4Params& p, long long i, long long j) {
+  float sum = 0.0f;
+  for (int k = 0; k < p.k; ++k) {
+    const int q = (p.w[j * p.ldw + (k >> 1)] >> (4 * (k & 1))) & 15;
+    const int g = k / p.group;
+    const float z = p.zeros ? static_cast<float>(p.zeros[j * p.ldz + g]) : 8.0f;
+    sum += w4_f32<BF16>(p.a[i * p.lda + k]) * ((static_cast<float>(q) - z) * w4_f32<BF16>(p.scales[j * p.lds + g]));
+  }
+  return sum;
+}
+
+// The column of W that virtual row r (0 .. 16 R - 1) of a tile stands for.
+// SwiGLU: rows 0-7 of each 16 are gate columns and rows 8-15 the up columns
+// they pair with, so that a tile yields 8 R outputs.
+__device__ __forceinline__ int w4_column(const W4Params& p, int tile, int r, int rows) {
+  if (p.epi != kEpiSwiglu) return tile * rows + r;
+  const int j = tile * (rows / 2) + (r >> 4) * 8 + (r & 7);
+  return j >= p.n_out ? p.n : (r & 8) ? p.n_out + j : j;
+}
+
+// 2^e, infinite or zero where fp32 has none.
+__device__ __forceinline__ float w4_pow2(int e) {
+  return __uint_as_float(static_cast<uint32_t>(min(max(e + 127, 0), 255)) << 23);
+}
+
+// The power of two that brings values whose largest magnitude has these bits
+// below 2^15 (0 for zeros; at most 2^120, which fp32 holds).
+template <bool BF16>
+__device__ __forceinline__ int w4_shift(uint32_t most) {
+  const int field = static_cast<int>(most) >> (BF16 ? 7 : 10);
+  return most == 0 ? 0 : min(120, 14 - (field - (BF16 ? 127 : 15)));
+}
+
+}  // namespace fgemm

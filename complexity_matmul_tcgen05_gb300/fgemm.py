@@ -108,7 +108,10 @@ def lib() -> ctypes.CDLL:
                                               size]
         L.fgemm_rms_norm_backward_workspace.argtypes = [vp, i64, i64]
         L.fgemm_rms_norm_backward_workspace.restype = size
-        L.fgemm_matmul_w4.argtypes = [vp, i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32, vp, i64, st, epi_p]
+        L.fgemm_matmul_w4.argtypes = [vp, i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32, vp, i64, st, epi_p,
+                                      vp, size]
+        L.fgemm_matmul_w4_workspace.argtypes = [i64, i64, i32]
+        L.fgemm_matmul_w4_workspace.restype = size
         L.fgemm_sample.argtypes = [vp, i64, i64, vp, i64, i32, vp, ctypes.POINTER(Sampling), vp, vp]
         L.fgemm_plan.argtypes = [vp, i64, i64, i64, st, epi_p, ctypes.POINTER(st),
                                  ctypes.POINTER(i32), ctypes.POINTER(i32),
@@ -563,49 +566,71 @@ def plan(M: int, N: int, K: int, dtype: torch.dtype = torch.bfloat16, epilogue: 
 # ------------------------------------------- operators of a token step
 
 
-def _rows(t: torch.Tensor | None, name: str, shape, dtype, device) -> tuple[int | None, int]:
-    """(address, leading dimension) of a 2-D operand, checked; (None, 0) for None."""
+# The raw handle of a device's current stream: torch.cuda.current_stream builds
+# an object around it, which costs as much as one of these kernels.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _rows(t: torch.Tensor | None, name: str, shape, dtype, dev: int) -> tuple[int | None, int]:
+    """(address, leading dimension) of a 2-D operand on device dev, checked;
+    (None, 0) for None."""
     if t is None:
         return None, 0
-    if t.shape != shape or t.dtype != dtype or t.device != device:
-        raise FgemmError(ERR_INVALID_ARG, f"{name} must be a {tuple(shape)} {dtype} tensor on {device}")
-    rows, cols = shape
-    if cols > 1 and t.stride(1) != 1:
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev:
+        raise FgemmError(ERR_INVALID_ARG, f"{name} must be a {tuple(shape)} {dtype} tensor on cuda:{dev}")
+    ld, unit = t.stride()
+    if unit != 1 and shape[1] > 1:
         raise FgemmError(ERR_INVALID_ARG, f"{name} must be row-major with unit column stride")
-    return t.data_ptr(), t.stride(0) if rows > 1 else max(cols, 1)
+    return t.data_ptr(), ld if shape[0] > 1 else max(shape[1], 1)
 
 
-def _vector(t: torch.Tensor | None, name: str, n: int, dtype, device) -> int | None:
-    """Address of a contiguous vector of n entries, checked; None for None."""
+def _vector(t: torch.Tensor | None, name: str, n: int, dtype, dev: int) -> int | None:
+    """Address of a contiguous vector of n entries on device dev, checked; None for None."""
     if t is None:
         return None
-    if t.dim() != 1 or t.shape[0] != n or t.dtype != dtype or t.device != device or (n > 1 and t.stride(0) != 1):
-        raise FgemmError(ERR_INVALID_ARG, f"{name} must be a contiguous vector of {n} {dtype} entries on {device}")
+    if t.shape != (n,) or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+        raise FgemmError(ERR_INVALID_ARG, f"{name} must be a contiguous vector of {n} {dtype} entries on cuda:{dev}")
     return t.data_ptr()
 
 
-def _on(t: torch.Tensor, name: str, handle: Handle | None) -> Handle:
-    """The handle of a call whose main operand is t, set to the current stream of t's device."""
-    if not t.is_cuda:
+def _on(t: torch.Tensor, name: str, handle: Handle | None):
+    """(library, handle pointer, device index) of a call whose main operand is
+    t; the handle is set to the current stream of t's device."""
+    dev = t.get_device()
+    if dev < 0:
         raise FgemmError(ERR_INVALID_ARG, f"{name} must be a CUDA tensor")
     if t.dim() != 2:
         raise FgemmError(ERR_INVALID_ARG, f"{name} must be 2-D")
     h = handle if handle is not None else default_handle()
-    if t.device.index != h.device:
-        raise FgemmError(ERR_INVALID_ARG, f"{name} is on {t.device}, the handle on cuda:{h.device}")
-    lib().fgemm_set_stream(h.ptr, torch.cuda.current_stream(t.device).cuda_stream)
-    return h
+    if dev != h.device:
+        raise FgemmError(ERR_INVALID_ARG, f"{name} is on cuda:{dev}, the handle on cuda:{h.device}")
+    L = _lib or lib()
+    L.fgemm_set_stream(h._h, _raw_stream(dev))
+    return L, h._h, dev
 
 
-def _norm_args(x, gain, residual, total, inv_rms, handle):
-    h = _on(x, "x", handle)
-    dt = _dtype_code(x.dtype)
-    m, n = shape = x.shape
-    if total is None:
-        total = x if residual is None else torch.empty(shape, dtype=x.dtype, device=x.device)
+def _norm_operands(x, gain, residual, total, inv_rms, eps, handle):
+    """The arguments both forms of the norm share, in the order of the C calls
+    (through total's leading dimension), with the outputs they return."""
+    L, h, dev = _on(x, "x", handle)
+    t, shape = x.dtype, x.shape
+    m, n = shape
+    dt = _dtype_code(t)
+    xp, ldx = _rows(x, "x", shape, t, dev)
+    gp = _vector(gain, "gain", n, t, dev)
+    if residual is None and total is None:
+        total, rp, ldr, tp, ldt = x, None, 0, None, 0
+    else:
+        rp, ldr = _rows(residual, "residual", shape, t, dev)
+        if total is None:
+            total = torch.empty_like(x)
+        tp, ldt = _rows(total, "total", shape, t, dev)
     if inv_rms is None:
         inv_rms = torch.empty(m, dtype=torch.float32, device=x.device)
-    return h, m, n, dt, total, inv_rms
+        ip = inv_rms.data_ptr()
+    else:
+        ip = _vector(inv_rms, "inv_rms", m, torch.float32, dev)
+    return L, h, dev, (h, m, n, xp, ldx, rp, ldr, gp, eps, dt, tp, ldt), total, inv_rms, ip
 
 
 def rms_norm(x: torch.Tensor, gain: torch.Tensor, *, residual: torch.Tensor | None = None, eps: float = 1e-6,
@@ -618,19 +643,13 @@ def rms_norm(x: torch.Tensor, gain: torch.Tensor, *, residual: torch.Tensor | No
     x and residual are M x N fp16 or bf16, gain has N entries.  out, total and
     inv_rms, if given, are written (out and total may be x, total may be the
     residual)."""
-    given = total
-    h, m, n, dt, total, inv_rms = _norm_args(x, gain, residual, total, inv_rms, handle)
-    dev, t, shape = x.device, x.dtype, x.shape
+    L, h, dev, args, total, inv_rms, ip = _norm_operands(x, gain, residual, total, inv_rms, eps, handle)
     if out is None:
-        out = torch.empty(shape, dtype=t, device=dev)
-    xp, ldx = _rows(x, "x", shape, t, dev)
-    rp, ldr = _rows(residual, "residual", shape, t, dev)
-    tp, ldt = _rows(total, "total", shape, t, dev) if residual is not None or given is not None else (None, 0)
-    yp, ldy = _rows(out, "out", shape, t, dev)
-    s = lib().fgemm_rms_norm(h.ptr, m, n, xp, ldx, rp, ldr, _vector(gain, "gain", n, t, dev), eps, dt, tp, ldt, yp, ldy,
-                             _vector(inv_rms, "inv_rms", m, torch.float32, dev))
+        out = torch.empty_like(x)
+    yp, ldy = _rows(out, "out", x.shape, x.dtype, dev)
+    s = L.fgemm_rms_norm(*args, yp, ldy, ip)
     if s != OK:
-        _check(s, h.ptr)
+        _check(s, h)
     return out, total, inv_rms
 
 
@@ -640,22 +659,16 @@ def rms_norm_mx(x: torch.Tensor, gain: torch.Tensor, *, residual: torch.Tensor |
     """(q, scales, total, inv_rms) of fgemm_rms_norm_mx: rms_norm with its
     output in block-scaled 8 bits, q (M x N uint8) and E8M0 scales (M x
     ceil(N / 32) uint8) as matmul_mx takes its A and scale_a."""
-    given = total
-    h, m, n, dt, total, inv_rms = _norm_args(x, gain, residual, total, inv_rms, handle)
+    L, h, dev, args, total, inv_rms, ip = _norm_operands(x, gain, residual, total, inv_rms, eps, handle)
     if fmt not in FP8_FORMATS:
         raise FgemmError(ERR_INVALID_ARG, f"fmt must be one of {sorted(FP8_FORMATS)}")
-    dev, t, shape = x.device, x.dtype, x.shape
+    m, n = x.shape
     blocks = (n + 31) // 32
-    q = torch.empty(shape, dtype=torch.uint8, device=dev)
-    scales = torch.empty((m, blocks), dtype=torch.uint8, device=dev)
-    xp, ldx = _rows(x, "x", shape, t, dev)
-    rp, ldr = _rows(residual, "residual", shape, t, dev)
-    tp, ldt = _rows(total, "total", shape, t, dev) if residual is not None or given is not None else (None, 0)
-    s = lib().fgemm_rms_norm_mx(h.ptr, m, n, xp, ldx, rp, ldr, _vector(gain, "gain", n, t, dev), eps, dt, tp, ldt,
-                                FP8_FORMATS[fmt], q.data_ptr(), max(n, 1), scales.data_ptr(), max(blocks, 1),
-                                _vector(inv_rms, "inv_rms", m, torch.float32, dev))
+    q = torch.empty((m, n), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((m, blocks), dtype=torch.uint8, device=x.device)
+    s = L.fgemm_rms_norm_mx(*args, FP8_FORMATS[fmt], q.data_ptr(), max(n, 1), scales.data_ptr(), max(blocks, 1), ip)
     if s != OK:
-        _check(s, h.ptr)
+        _check(s, h)
     return q, scales, total, inv_rms
 
 
@@ -667,25 +680,27 @@ def rms_norm_backward(dy: torch.Tensor, total: torch.Tensor, gain: torch.Tensor,
     and includes dtotal, the gradient that reaches total by other ways; dgain
     (N fp32 entries) is summed over the rows.  out and dgain, if given, are
     written (out may be dy or dtotal)."""
-    h = _on(dy, "dy", handle)
-    dt = _dtype_code(dy.dtype)
-    m, n = shape = dy.shape
-    dev, t = dy.device, dy.dtype
-    if out is None:
-        out = torch.empty(shape, dtype=t, device=dev)
-    if dgain is None:
-        dgain = torch.empty(n, dtype=torch.float32, device=dev)
+    L, h, dev = _on(dy, "dy", handle)
+    t, shape = dy.dtype, dy.shape
+    m, n = shape
+    dt = _dtype_code(t)
     dyp, lddy = _rows(dy, "dy", shape, t, dev)
     tp, ldt = _rows(total, "total", shape, t, dev)
+    gp = _vector(gain, "gain", n, t, dev)
+    ip = _vector(inv_rms, "inv_rms", m, torch.float32, dev)
     dtp, lddt = _rows(dtotal, "dtotal", shape, t, dev)
+    if out is None:
+        out = torch.empty_like(dy)
     op, ldo = _rows(out, "out", shape, t, dev)
-    size = lib().fgemm_rms_norm_backward_workspace(h.ptr, m, n)
-    work = torch.empty(size, dtype=torch.uint8, device=dev)
-    s = lib().fgemm_rms_norm_backward(h.ptr, m, n, dyp, lddy, tp, ldt, _vector(gain, "gain", n, t, dev),
-                                      _vector(inv_rms, "inv_rms", m, torch.float32, dev), dtp, lddt, dt, op, ldo,
-                                      _vector(dgain, "dgain", n, torch.float32, dev), work.data_ptr(), size)
+    if dgain is None:
+        dgain = torch.empty(n, dtype=torch.float32, device=dy.device)
+    dgp = _vector(dgain, "dgain", n, torch.float32, dev)
+    size = L.fgemm_rms_norm_backward_workspace(h, m, n)
+    work = torch.empty(size, dtype=torch.uint8, device=dy.device)
+    s = L.fgemm_rms_norm_backward(h, m, n, dyp, lddy, tp, ldt, gp, ip, dtp, lddt, dt, op, ldo, dgp, work.data_ptr(),
+                                  size)
     if s != OK:
-        _check(s, h.ptr)
+        _check(s, h)
     return out, dgain
 
 
@@ -700,29 +715,32 @@ def matmul_w4(A: torch.Tensor, W: torch.Tensor, scales: torch.Tensor, *, zeros: 
     type, zeros the same shape in uint8 (None: 8 everywhere), group 32, 64 or
     128.  Epilogues and bias as in matmul (swiglu: rows [0, N / 2) of W are
     the gate, the output is M x N / 2)."""
-    h = _on(A, "A", handle)
-    dt = _dtype_code(A.dtype)
+    L, h, dev = _on(A, "A", handle)
+    t = A.dtype
+    dt = _dtype_code(t)
     m, k = A.shape
     n = W.shape[0]
     if epilogue not in EPILOGUES:
         raise FgemmError(ERR_INVALID_ARG, f"epilogue must be one of {sorted(EPILOGUES)}")
     if group not in (32, 64, 128):
         raise FgemmError(ERR_INVALID_ARG, "group must be 32, 64 or 128")
-    dev, t = A.device, A.dtype
     n_out = n // 2 if epilogue == "swiglu" else n
     groups = (n, (k + group - 1) // group)
-    if out is None:
-        out = torch.empty((m, n_out), dtype=t, device=dev)
     ap, lda = _rows(A, "A", (m, k), t, dev)
     wp, ldw = _rows(W, "W", (n, (k + 1) // 2), torch.uint8, dev)
     sp, lds = _rows(scales, "scales", groups, t, dev)
     zp, ldz = _rows(zeros, "zeros", groups, torch.uint8, dev)
+    bp = _vector(bias, "bias", n, t, dev)
+    if out is None:
+        out = torch.empty((m, n_out), dtype=t, device=A.device)
     cp, ldc = _rows(out, "out", (m, n_out), t, dev)
-    epi = Epilogue(EPILOGUES[epilogue], alpha, _vector(bias, "bias", n, t, dev))
-    s = lib().fgemm_matmul_w4(h.ptr, m, n, k, ap, lda, wp, ldw, sp, lds, zp, ldz, group, cp, ldc, dt,
-                              ctypes.byref(epi))
+    size = L.fgemm_matmul_w4_workspace(m, k, group)
+    work = torch.empty(size, dtype=torch.uint8, device=A.device) if size else None
+    s = L.fgemm_matmul_w4(h, m, n, k, ap, lda, wp, ldw, sp, lds, zp, ldz, group, cp, ldc, dt,
+                          ctypes.byref(Epilogue(EPILOGUES[epilogue], alpha, bp)),
+                          None if work is None else work.data_ptr(), size)
     if s != OK:
-        _check(s, h.ptr)
+        _check(s, h)
     return out
 
 
@@ -740,24 +758,26 @@ def sample(logits: torch.Tensor, u: torch.Tensor, *, temperature: float | torch.
     min_p (0: off) are one number for all rows, or vectors with an entry for
     each (fp32; top_k int32).  A row with nothing above -inf gives token -1
     and prob 0."""
-    h = _on(logits, "logits", handle)
+    L, h, dev = _on(logits, "logits", handle)
     rows, vocab = logits.shape
     code = LOGIT_TYPES.get(logits.dtype)
     if code is None:
         raise FgemmError(ERR_INVALID_ARG, f"logits must be float16, bfloat16 or float32, not {logits.dtype}")
-    dev = logits.device
-    how = Sampling(1.0, 0, 1.0, 0.0, None, None, None, None)
-    for name, value, dtype in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
-                               ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
+    one, each = [], []
+    for name, value, off, dtype in (("temperature", temperature, 1.0, torch.float32), ("top_k", top_k, 0, torch.int32),
+                                    ("top_p", top_p, 1.0, torch.float32), ("min_p", min_p, 0.0, torch.float32)):
         if isinstance(value, torch.Tensor):
-            setattr(how, name + "s", _vector(value, name, rows, dtype, dev))
+            one.append(off)
+            each.append(_vector(value, name, rows, dtype, dev))
         else:
-            setattr(how, name, value)
+            one.append(value)
+            each.append(None)
     lp, ld = _rows(logits, "logits", (rows, vocab), logits.dtype, dev)
-    token = torch.empty(rows, dtype=torch.int32, device=dev)
-    prob = torch.empty(rows, dtype=torch.float32, device=dev)
-    s = lib().fgemm_sample(h.ptr, rows, vocab, lp, ld, code, _vector(u, "u", rows, torch.float32, dev),
-                           ctypes.byref(how), token.data_ptr(), prob.data_ptr())
+    up = _vector(u, "u", rows, torch.float32, dev)
+    token = torch.empty(rows, dtype=torch.int32, device=logits.device)
+    prob = torch.empty(rows, dtype=torch.float32, device=logits.device)
+    s = L.fgemm_sample(h, rows, vocab, lp, ld, code, up, ctypes.byref(Sampling(*one, *each)), token.data_ptr(),
+                       prob.data_ptr())
     if s != OK:
-        _check(s, h.ptr)
+        _check(s, h)
     return token, prob

@@ -386,7 +386,7 @@ fgemm_status_t fgemm_rms_norm_backward(fgemm_handle_t h, int64_t M, int64_t N, c
 /*
  * C = epi(alpha * A * W^T + bias) with 4-bit weights and group scales:
  *   W[j][k] = (code[j][k] - zero[j][k / group]) * scale[j][k / group]
- *   A, lda       M x K of dtype.
+ *   A, lda       M x K of dtype, M at most 2^22, K at most 2^30.
  *   W, ldw       N x ceil(K / 2) bytes, ldw in bytes: two codes (0 .. 15) to
  *                a byte along K, the even k in the low half. (N x K, unlike
  *                B of fgemm_matmul: codes are read along K.)
@@ -395,15 +395,19 @@ fgemm_status_t fgemm_rms_norm_backward(fgemm_handle_t h, int64_t M, int64_t N, c
  *   group        32, 64 or 128.
  *   C, ldc, epi  as fgemm_matmul (columns of C: N, or N / 2 with SWIGLU;
  *                the gate is rows [0, N / 2) of W).
+ *   workspace    at least fgemm_matmul_w4_workspace(M, K, group) bytes of
+ *                device memory, 256-byte aligned (0 bytes for a few rows: may
+ *                be NULL), left with nothing of use.
  * The codes are multiplied as they are and the scale is applied to fp32 sums
  * of a group: no weight is rounded.
  * A and W 16-byte aligned, lda a multiple of 8, ldw of 16, else
  * FGEMM_ERR_ALIGNMENT. K == 0: C = epi(bias).
  */
+size_t fgemm_matmul_w4_workspace(int64_t M, int64_t K, int32_t group);
 fgemm_status_t fgemm_matmul_w4(fgemm_handle_t h, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
                                const void* W, int64_t ldw, const void* scales, int64_t lds, const void* zeros,
                                int64_t ldz, int32_t group, void* C, int64_t ldc, fgemm_dtype_t dtype,
-                               const fgemm_epilogue_t* epi);
+                               const fgemm_epilogue_t* epi, void* workspace, size_t workspace_bytes);
 
 /*
  * One token from each row of logits, by one given uniform number u in [0, 1).

@@ -107,6 +107,7 @@ def test_norm_backward_workspace_without_handle(L):
     (dict(M=0), BAD, "handle is NULL"),
     (dict(dtype=3), BAD, "dtype"),
     (dict(K=-1), BAD, "sizes"),
+    (dict(K=(1 << 30) + 1), BAD, "sizes"),
     (dict(group=16), BAD, "group"),
     (dict(kind=9), BAD, "epilogue"),
     (dict(kind=3, N=63), BAD, "even N"),
@@ -127,12 +128,16 @@ def test_norm_backward_workspace_without_handle(L):
     (dict(lda=257), ALIGN, "16-byte"),
     (dict(ldw=136), ALIGN, "16-byte"),
     (dict(scales=17), ALIGN, "scales"),
+    (dict(M=100), BAD, "workspace"),
+    (dict(M=100, work=256, size=1000), BAD, "workspace"),
+    (dict(M=100, work=272, size=1 << 20), ALIGN, "workspace"),
+    (dict(M=100, work=256, size=1 << 20), BAD, "handle is NULL"),
 ])
 def test_w4_refusals(L, kw, status, text):
     a = {**dict(M=4, N=64, K=256, A=16, lda=256, W=16, ldw=128, scales=16, lds=2, zeros=None, ldz=0, group=128, C=16,
-                ldc=64, dtype=fgemm.BF16, kind=0, bias=None), **kw}
-    epi = fgemm.Epilogue(a.pop("kind"), 1.0, a.pop("bias"))
-    refused(L, status, L.fgemm_matmul_w4(None, *a.values(), ctypes.byref(epi)), text)
+                ldc=64, dtype=fgemm.BF16, kind=0, bias=None, work=None, size=0), **kw}
+    epi, work = fgemm.Epilogue(a.pop("kind"), 1.0, a.pop("bias")), (a.pop("work"), a.pop("size"))
+    refused(L, status, L.fgemm_matmul_w4(None, *a.values(), ctypes.byref(epi), *work), text)
 
 
 @pytest.mark.parametrize("kw,status,text", [
