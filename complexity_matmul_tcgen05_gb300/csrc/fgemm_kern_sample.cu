@@ -15,15 +15,19 @@
 // units of 2^-44.  Integer sums do not depend on their order, which also
 // makes the shared-memory atomics below deterministic.
 //
-// No sort: top-k and top-p are each a threshold on x, found by histograms.
-// The first one bins x linearly between m and m - 32 T (the masses below are
-// under 2^-46); the bin the threshold falls in is searched again with bins
-// over its key range (keys: x's bits, ordered as integers) until one key is
-// left.  Ties at that key are cut by index.
+// The vocabulary is not sorted: top-k and top-p are each a threshold on x,
+// found by histograms.  The first one bins x linearly between m and m - 32 T
+// (masses below are under 2^-46).  When top-k's threshold falls in a bin and
+// that bin and those above hold at most 2048 logits, these are gathered in one
+// CTA, sorted there, and the rest of the work is on a short list.  Otherwise
+// the bin is searched again with bins over its key range (keys: x's bits,
+// ordered as integers) until one key is left, and ties at that key are cut by
+// index.
 //
 // A cluster of CTAs works on a row, each on a slice kept in shared memory,
 // so the logits are read from memory once; the CTAs read each other's
-// histograms and sums through distributed shared memory.
+// histograms and sums through distributed shared memory.  What bounds it:
+// with many rows the arithmetic of the masses, with few the cluster's meetings.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -47,23 +51,32 @@ constexpr int kUnit = 44;  // masses are multiples of 2^-44
 constexpr u64 kOne = 1ull << kUnit;
 constexpr int kMaxCluster = 8;
 
-// 2^(j/32) for j = -16 .. 16 in units of 2^-44.
-__constant__ u64 kPow[33] = {
-    12439554047902ull, 12711944812080ull, 12990300157313ull, 13274750690919ull, 13565429880144ull,
-    13862474114787ull, 14166022771192ull, 14476218277651ull, 14793206181226ull, 15117135216047ull,
-    15448157373097ull, 15786427971528ull, 16132105731538ull, 16485352848846ull, 16846335070792ull,
-    17215221774115ull, 17592186044416ull, 17977404757381ull, 18371058661769ull, 18773332464219ull,
-    19184414915921ull, 19604498901178ull, 20033781527906ull, 20472464220127ull, 20920752812471ull,
-    21378857646762ull, 21846993670708ull, 22325380538761ull, 22814242715178ull, 23313809579344ull,
-    23824315533396ull, 24346000112214ull, 24879108095804ull,
+// 2^(j/32) in units of 2^-44.
+__constant__ u64 kPow[32] = {
+    17592186044416ull, 17977404757381ull, 18371058661769ull, 18773332464219ull,
+    19184414915921ull, 19604498901178ull, 20033781527906ull, 20472464220127ull,
+    20920752812471ull, 21378857646762ull, 21846993670708ull, 22325380538761ull,
+    22814242715178ull, 23313809579344ull, 23824315533396ull, 24346000112214ull,
+    24879108095804ull, 25423889624159ull, 25980600314626ull, 26549501381838ull,
+    27130859760289ull, 27724948229574ull, 28332045542385ull, 28952436555301ull,
+    29586412362452ull, 30234270432094ull, 30896314746195ull, 31572855943056ull,
+    32264211463077ull, 32970705697691ull, 33692670141585ull, 34430443548229ull,
 };
 
+constexpr int kList = 2048;
+constexpr int kLimb = 15;  // bits: a CTA's slice of 2^17 logits cannot overflow a 32-bit sum of limbs
+
 struct SampleShared {
-  u64 hist[kBins];
-  u64 pow[33];
+  unsigned int hist[3][kBins];  // sums of the masses' limbs (counts: the first)
+  u64 list[kList];              // the short list (rank 0): key, then the index from above
+  u64 mass[kList];              // its masses; before, this CTA's part of the list
+  u64 pow[32];
   u64 warp64[kWarps];
+  u64 warp64b[kWarps];
   u64 total;         // this CTA's sum, read by the others
   u64 sel_before;    // what lies above the selected bin
+  u64 sel_upto;      // and with it
+  unsigned int gathered, place;
   int sel_bin;
   unsigned int warp32[kWarps];
   unsigned int best; // this CTA's largest key
@@ -71,6 +84,7 @@ struct SampleShared {
   int found;         // index located by locate(), in the CTA that finds it
   u64 found_mass;
   unsigned int range[2];
+  float ch, cl;      // log2(e) / temperature in two floats
 };
 
 // Keys: order of floats as unsigned integers (x is never NaN, -0 never).
@@ -87,33 +101,58 @@ __device__ __forceinline__ float value_of(unsigned int k) {
 // rounding error by a two-sum, the product's error by an fma); then
 // 2^y = 2^n 2^(j/32) 2^r with a table for 2^(j/32) and the exponential series
 // for 2^r, |r| <= 1/64, whose first-order term is again kept in two floats.
+// Numbers become integers by adding 1.5 2^23, whose unit in the last place is
+// 1: the conversion instruction runs at a fraction of the rate.
 struct Masses {
   float m, ch, cl;  // ch + cl = log2(e) / T
   const u64* pow;
   __device__ __forceinline__ u64 operator()(float x) const {
+    constexpr float magic = 12582912.0f;
+    constexpr int magic_bits = 0x4B400000;
     if (x == m) return kOne;
     const float s = x - m;
-    const float yh = __fmul_rn(s, ch);  // rounded here: not to be fused into the subtraction below
+    const float yh = __fmul_rn(s, ch);  // rounded here: not to be fused into a sum below
     if (!(yh > -46.0f)) return 0;
     const float bb = s - x;
     const float e = (x - (s - bb)) + (-m - bb);
     const float yl = fmaf(s, ch, -yh) + fmaf(s, cl, e * ch);
-    const float n = rintf(yh);
-    const float f = yh - n;
-    const float j = rintf(f * 32.0f);
-    const float r = fmaf(j, -0.03125f, f);
+    const float t = fmaf(yh, 32.0f, magic);  // 32 y, rounded
+    const int j = __float_as_int(t) - magic_bits;
+    const float r = fmaf(t - magic, -0.03125f, yh);
     constexpr float l1 = 0.693147182464599609375f, l2 = -1.90465429995776804525e-09f;  // ln 2
     const float zh = __fmul_rn(r, l1);
     const float zl = fmaf(r, l1, -zh) + fmaf(r, l2, yl * l1);
     const float q = zh * zh * fmaf(zh, fmaf(zh, fmaf(zh, 1.0f / 120, 1.0f / 24), 1.0f / 6), 0.5f);
-    const int series = __float2int_rn(zh * 137438953472.0f) + __float2int_rn((zl + q) * 137438953472.0f);  // 2^37
-    const u64 t = pow[static_cast<int>(j) + 16];
-    const long long v =
-        static_cast<long long>(t) + ((static_cast<long long>(t >> 13) * static_cast<long long>(series)) >> 24);
-    const int shift = -static_cast<int>(n);
-    return (static_cast<u64>(v) + ((1ull << shift) >> 1)) >> shift;
+    // zh + q + zl in units of 2^-37: the upper part in units of 2^-22, the rest
+    const float t2 = fmaf(zh + q, 4194304.0f, magic);
+    const float rest = (fmaf(t2 - magic, -2.384185791015625e-07f, zh) + q) + zl;
+    const float t3 = fmaf(rest, 137438953472.0f, magic);
+    const int series = ((__float_as_int(t2) - magic_bits) << 15) + (__float_as_int(t3) - magic_bits);
+    const u64 p = pow[j & 31];
+    const u64 v = p + static_cast<u64>((static_cast<long long>(static_cast<int>(p >> 15)) * series) >> 22);
+    const int shift = -(j >> 5);
+    return (v + ((1ull << shift) >> 1)) >> shift;
   }
 };
+
+// a f for 0 < f < 1 exactly, rounded down or up.
+__device__ __forceinline__ u64 times(u64 a, float f, bool up) {
+  if (!(f < 1.0f)) return a;
+  const int b = __float_as_int(f), field = b >> 23;
+  const u64 m = field ? (b & 0x7FFFFF) | 0x800000 : b;
+  const int e = 150 - (field ? field : 1);  // f = m 2^-e, e >= 24
+  const u64 lo = a * m, hi = __umul64hi(a, m);
+  u64 v, rest;
+  if (e < 64) {
+    v = (hi << (64 - e)) | (lo >> e);
+    rest = lo & ((1ull << e) - 1);
+  } else {
+    const int h = e - 64;
+    v = h < 64 ? hi >> h : 0;
+    rest = lo | (h < 64 ? hi & ((1ull << h) - 1) : hi);
+  }
+  return v + (up && rest ? 1 : 0);
+}
 
 template <typename T>
 __device__ __forceinline__ float raw_value(T v);
@@ -176,17 +215,31 @@ __device__ __forceinline__ u64 warp_scan(u64 v) {  // inclusive
 
 struct Threshold {
   unsigned int key;  // larger keys are in
-  u64 above;         // their count or mass
+  int bin;           // of the first histogram, when the search stopped there (key 0)
+  u64 above;         // the count or mass of larger keys
+  u64 upto;          // the sum of the first histogram's bins down to the one found
+  u64 target;
 };
 
 // The key at which the sum of weight(x) over the candidates, from the
-// largest down, reaches target (1 <= target <= the whole sum).  weight 0:
-// not a candidate.  Every thread of the cluster gets the result.
-template <typename S, typename W>
+// largest down, reaches target_of(the whole sum) (for counts: of the bins).
+// weight 0: not a candidate.  COUNT: the weights are 0 or 1, and the search
+// stops after the first histogram (key 0) when the bins down to the one found
+// hold at most kList.  Masses: it stops there (key 0) when the target lies
+// above their sum.  Every thread of the cluster gets the result.
+//
+// Masses are summed in three 32-bit limbs of 15 bits: shared-memory atomics
+// of 32 bits are native, those of 64 a loop.
+template <bool COUNT, typename S, typename W, typename G>
 __device__ Threshold find_threshold(const S& slice, SampleShared& sh, cg::cluster_group& cluster, float m, float scale,
-                                    u64 target, W weight) {
+                                    W weight, G target_of) {
   const int ranks = cluster.num_blocks();
-  Threshold res{0, 0};
+  Threshold res;
+  res.key = 0;
+  res.bin = 0;
+  res.above = 0;
+  res.upto = 0;
+  res.target = 0;
   unsigned int lo = 0, hi = 0xFFFFFFFFu;  // keys still in question, once `linear` is done
   bool linear = true;
   int shift = 0;
@@ -196,7 +249,13 @@ __device__ Threshold find_threshold(const S& slice, SampleShared& sh, cg::cluste
     return k < lo || k > hi ? -1 : static_cast<int>((hi - k) >> shift);
   };
   while (true) {
-    for (int b = threadIdx.x; b < kBins; b += kThreads) sh.hist[b] = 0;
+    for (int b = threadIdx.x; b < kBins; b += kThreads) {
+      sh.hist[0][b] = 0;
+      if (!COUNT) {
+        sh.hist[1][b] = 0;
+        sh.hist[2][b] = 0;
+      }
+    }
     if (threadIdx.x == 0) sh.sel_bin = kBins - 1;
     __syncthreads();
     slice.each([&](float x, int) {
@@ -204,15 +263,30 @@ __device__ Threshold find_threshold(const S& slice, SampleShared& sh, cg::cluste
       // the last linear bin holds all that lies far below: it is what is left
       if (b < 0 || (linear && b == kBins - 1)) return;
       const u64 w = weight(x);
-      if (w) atomicAdd(&sh.hist[b], w);
+      if (COUNT) {
+        if (w) atomicAdd(&sh.hist[0][b], 1u);
+      } else if (w) {
+        constexpr unsigned int mask = (1u << kLimb) - 1;
+        const unsigned int low = static_cast<unsigned int>(w) & mask;
+        const unsigned int mid = static_cast<unsigned int>(w >> kLimb) & mask;
+        const unsigned int top = static_cast<unsigned int>(w >> (2 * kLimb));
+        atomicAdd(&sh.hist[0][b], low);
+        if (mid) atomicAdd(&sh.hist[1][b], mid);
+        if (top) atomicAdd(&sh.hist[2][b], top);
+      }
     });
     cluster.sync();
     // thread t: bins 2t and 2t + 1 over all CTAs
     u64 v[2] = {0, 0};
     for (int r = 0; r < ranks; ++r) {
-      const u64* h = cluster.map_shared_rank(sh.hist, r);
-      v[0] += h[2 * threadIdx.x];
-      v[1] += h[2 * threadIdx.x + 1];
+      const unsigned int* h = cluster.map_shared_rank(&sh.hist[0][0], r);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const unsigned int* at = h + 2 * threadIdx.x + i;
+        v[i] += at[0];
+        if (!COUNT)
+          v[i] += (static_cast<u64>(at[kBins]) << kLimb) + (static_cast<u64>(at[2 * kBins]) << (2 * kLimb));
+      }
     }
     const u64 mine = warp_scan(v[0] + v[1]);
     if ((threadIdx.x & 31) == 31) sh.warp64[threadIdx.x >> 5] = mine;
@@ -224,33 +298,77 @@ __device__ Threshold find_threshold(const S& slice, SampleShared& sh, cg::cluste
       if (w < (threadIdx.x >> 5)) before += sh.warp64[w];
       all += sh.warp64[w];
     }
-    if (threadIdx.x == 0) sh.sel_before = all;  // the last linear bin, unless another bin reaches the target
+    if (linear) res.target = target_of(all);
+    const u64 target = res.target;
+    if (threadIdx.x == 0) {  // the last linear bin, unless another bin reaches the target
+      sh.sel_before = all;
+      sh.sel_upto = ~0ull;
+    }
     __syncthreads();
-    if (before < target && target <= before + v[0]) {
-      sh.sel_bin = 2 * threadIdx.x;
-      sh.sel_before = before;
-    } else if (before + v[0] < target && target <= before + v[0] + v[1]) {
-      sh.sel_bin = 2 * threadIdx.x + 1;
-      sh.sel_before = before + v[0];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (before < target && target <= before + v[i]) {
+        sh.sel_bin = 2 * threadIdx.x + i;
+        sh.sel_before = before;
+        sh.sel_upto = before + v[i];
+      }
+      before += v[i];
     }
     cluster.sync();  // the others are done with this CTA's histogram
     const int bin = sh.sel_bin;
     res.above = sh.sel_before;
     if (linear) {
-      // the bin's key range: keys at which bin_of, which falls as keys grow, is `bin`
+      res.bin = bin;
+      res.upto = sh.sel_upto;
+      if (COUNT ? res.upto <= kList : res.upto == ~0ull) return res;
+      // The bin's key range: keys at which bin_of, which falls as keys grow, is
+      // `bin`.  Thread 0: the smallest key with bin_of <= bin; thread 1: the
+      // largest with bin_of >= bin.  Each begins where the bin's edge lies
+      // before rounding and widens its step until the key is enclosed.
       if (threadIdx.x < 2) {
-        // thread 0: the smallest key with bin_of <= bin; thread 1: the largest with bin_of >= bin
-        unsigned int a = key_of(-INFINITY), b = key_of(m);
-        while (a < b) {
-          const unsigned int mid = threadIdx.x == 0 ? a + (b - a) / 2 : a + (b - a) / 2 + 1;
-          const int at = bin_of(value_of(mid));
-          if (threadIdx.x == 0) {
-            if (at <= bin) b = mid; else a = mid + 1;
-          } else {
-            if (at >= bin) a = mid; else b = mid - 1;
+        const bool low = threadIdx.x == 0;
+        const unsigned int first = key_of(-INFINITY), last = key_of(m);
+        const float edge = m - (static_cast<float>(bin) + (low ? 1.0f : 0.0f)) / scale;
+        unsigned int at = edge == edge ? key_of(edge + 0.0f) : last;
+        at = at < first ? first : at > last ? last : at;
+        auto ok = [&](unsigned int k) { return low ? bin_of(value_of(k)) <= bin : bin_of(value_of(k)) >= bin; };
+        unsigned int good, bad, step = 4;  // the key sought lies from good towards bad, bad excluded
+        const unsigned int end_good = low ? last : first, end_bad = low ? first : last;
+        if (ok(at)) {
+          good = at;
+          while (true) {  // towards bad
+            const unsigned int room = low ? good - end_bad : end_bad - good;
+            if (room == 0) break;
+            const unsigned int d = step < room ? step : room;
+            const unsigned int k = low ? good - d : good + d;
+            if (!ok(k)) {
+              bad = k;
+              break;
+            }
+            good = k;
+            step = step < 0x40000000u ? step * 4 : step;
+          }
+          if (good == end_bad) bad = good;
+        } else {
+          bad = at;
+          good = end_good;
+          while (true) {  // towards good
+            const unsigned int room = low ? end_good - bad : bad - end_good;
+            const unsigned int d = step < room ? step : room;
+            const unsigned int k = low ? bad + d : bad - d;
+            if (d == 0 || ok(k)) {
+              good = k;
+              break;
+            }
+            bad = k;
+            step = step < 0x40000000u ? step * 4 : step;
           }
         }
-        sh.range[threadIdx.x] = a;
+        while (low ? good > bad + 1 && good != bad : bad > good + 1) {
+          const unsigned int mid = low ? bad + (good - bad) / 2 : good + (bad - good) / 2;
+          if (ok(mid)) good = mid; else bad = mid;
+        }
+        sh.range[threadIdx.x] = good;
       }
       __syncthreads();
       lo = sh.range[0];
@@ -262,7 +380,7 @@ __device__ Threshold find_threshold(const S& slice, SampleShared& sh, cg::cluste
       lo = top - lo > width ? top - width : lo;
       hi = top;
     }
-    if (lo == hi) break;
+    if (lo >= hi) break;
     const int bits = 32 - __clz(hi - lo);
     shift = bits > 10 ? bits - 10 : 0;
     __syncthreads();
@@ -358,6 +476,107 @@ __device__ int locate(const S& slice, SampleShared& sh, u64* segs, cg::cluster_g
   return found;
 }
 
+// Descending bitonic sort of n (a power of two, at most kList) numbers.
+__device__ void sort_down(u64* a, int n) {
+  for (int k = 2; k <= n; k <<= 1)
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      for (int i = threadIdx.x; i < n / 2; i += kThreads) {
+        const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
+        const u64 x = a[lo], y = a[hi];
+        if ((x < y) == ((lo & k) == 0)) {
+          a[lo] = y;
+          a[hi] = x;
+        }
+      }
+      __syncthreads();
+    }
+}
+
+// Inclusive sums of v[0 .. n) in place; n <= kList.  Returns the whole.
+__device__ u64 scan_list(SampleShared& sh, u64* v, int n) {
+  constexpr int kEach = kList / kThreads;
+  u64 x[kEach], s = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int at = threadIdx.x * kEach + i;
+    x[i] = at < n ? v[at] : 0;
+    s += x[i];
+  }
+  const u64 upto = warp_scan(s);
+  if ((threadIdx.x & 31) == 31) sh.warp64b[threadIdx.x >> 5] = upto;
+  __syncthreads();
+  u64 before = upto - s, all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < (threadIdx.x >> 5)) before += sh.warp64b[w];
+    all += sh.warp64b[w];
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    before += x[i];
+    const int at = threadIdx.x * kEach + i;
+    if (at < n) v[at] = before;
+  }
+  __syncthreads();
+  return all;
+}
+
+// How many of the ascending v[0 .. n) are below t (by every thread).
+__device__ __forceinline__ int below(const u64* v, int n, u64 t) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (v[mid] < t) lo = mid + 1; else hi = mid;
+  }
+  return lo;
+}
+
+// One CTA finishes on the short list: all logits of the row that can be kept
+// are among its n entries.
+__device__ void finish_list(SampleShared& sh, const Masses& mass, int n, int top_k, float top_p, u64 least, float u,
+                            int* token, float* prob) {
+  int size = 2;
+  while (size < n) size <<= 1;
+  for (int i = n + threadIdx.x; i < size; i += kThreads) sh.list[i] = 0;
+  __syncthreads();
+  sort_down(sh.list, size);
+  n = min(n, top_k);
+  for (int i = threadIdx.x; i < n; i += kThreads) sh.mass[i] = mass(value_of(static_cast<unsigned int>(sh.list[i] >> 32)));
+  __syncthreads();
+  const u64 whole = scan_list(sh, sh.mass, n);
+  int keep = n;
+  if (top_p < 1.0f) {
+    const u64 target = times(whole, top_p, true);
+    keep = min(n, below(sh.mass, n, target < 1 ? 1 : target) + 1);
+  }
+  if (least > 0) {  // masses fall along the list
+    int lo = 1, hi = keep;
+    while (lo < hi) {  // the first entry from 1 on that is too small
+      const int mid = (lo + hi) >> 1;
+      if (mass(value_of(static_cast<unsigned int>(sh.list[mid] >> 32))) >= least) lo = mid + 1; else hi = mid;
+    }
+    keep = lo;
+  }
+  __syncthreads();
+  // by index: the entries' lower half is the index from above, so its order
+  // is that of falling entries
+  size = 2;
+  while (size < keep) size <<= 1;
+  for (int i = threadIdx.x; i < size; i += kThreads)
+    sh.list[i] = i < keep ? (sh.list[i] << 32) | (sh.list[i] >> 32) : 0;
+  __syncthreads();
+  sort_down(sh.list, size);
+  for (int i = threadIdx.x; i < keep; i += kThreads) sh.mass[i] = mass(value_of(static_cast<unsigned int>(sh.list[i])));
+  __syncthreads();
+  const u64 kept = scan_list(sh, sh.mass, keep);
+  if (threadIdx.x == 0) {
+    const int at = below(sh.mass, keep, times(kept, u, false) + 1);  // the first sum above u times the whole
+    const u64 w = sh.mass[at] - (at ? sh.mass[at - 1] : 0);
+    *token = static_cast<int>(0xFFFFFFFFu - static_cast<unsigned int>(sh.list[at] >> 32));
+    if (prob) *prob = static_cast<float>(static_cast<double>(w) / static_cast<double>(kept));
+  }
+}
+
 template <typename T, bool CACHED>
 __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant__ SampleParams p) {
   extern __shared__ __align__(16) unsigned char dyn[];
@@ -375,7 +594,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   slice.global = static_cast<const T*>(p.logits) + row * p.ld + first;
   u64* segs = reinterpret_cast<u64*>(dyn);
   slice.cache = reinterpret_cast<T*>(dyn + static_cast<size_t>(slice.rounds) * kWarps * 8);
-  if (threadIdx.x < 33) sh.pow[threadIdx.x] = kPow[threadIdx.x];
+  if (threadIdx.x < 32) sh.pow[threadIdx.x] = kPow[threadIdx.x];
 
   // the slice into shared memory, its largest key and its candidates
   float top = -INFINITY;
@@ -393,6 +612,20 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
       top = fmaxf(top, x);
       count += x > -INFINITY;
     });
+  }
+  const float temperature = p.temperature ? p.temperature[row] : p.temperature0;
+  const float top_p = p.top_p ? p.top_p[row] : p.top_p0;
+  const float min_p = p.min_p ? p.min_p[row] : p.min_p0;
+  const int top_k = p.top_k ? p.top_k[row] : p.top_k0;
+  // the largest float below 1 stands for anything above it, 0 for anything below and for NaN
+  const float u = fminf(fmaxf(p.u[row], 0.0f), 0.999999940395355224609375f);
+  const bool greedy = !(temperature > 0.0f) || top_k == 1 || top_p <= 0.0f || min_p > 1.0f;
+  if (threadIdx.x == 0) {
+    sh.gathered = 0;
+    sh.place = 0;
+    const double c = 1.4426950408889634074 / static_cast<double>(greedy ? 1.0f : temperature);
+    sh.ch = static_cast<float>(c);
+    sh.cl = isinf(sh.ch) ? 0.0f : static_cast<float>(c - static_cast<double>(sh.ch));
   }
   unsigned int best = key_of(top);
   best = __reduce_max_sync(0xFFFFFFFFu, best);
@@ -419,21 +652,18 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     count += *cluster.map_shared_rank(&sh.count, r);
   }
   const float m = value_of(best);
-  const float temperature = p.temperature ? p.temperature[row] : p.temperature0;
-  const float top_p = p.top_p ? p.top_p[row] : p.top_p0;
-  const float min_p = p.min_p ? p.min_p[row] : p.min_p0;
-  const int top_k = p.top_k ? p.top_k[row] : p.top_k0;
-  const bool greedy = !(temperature > 0.0f) || top_k == 1 || top_p <= 0.0f || min_p > 1.0f;
-
   int token = -1;
   float prob = 0.0f;
   if (count) {
     Masses mass;
     mass.m = m;
     mass.pow = sh.pow;
-    const double c = 1.4426950408889634074 / static_cast<double>(greedy ? 1.0f : temperature);
-    mass.ch = static_cast<float>(c);
-    mass.cl = isinf(mass.ch) ? 0.0f : static_cast<float>(c - static_cast<double>(mass.ch));
+    mass.ch = sh.ch;
+    mass.cl = sh.cl;
+    // logits below this have no mass, or less than min_p
+    float floor_x = m - 32.5f * temperature;
+    if (min_p > 0.0f) floor_x = fmaxf(floor_x, m + temperature * (__logf(min_p) - 0.01f) - fabsf(m) * 1e-6f);
+    if (!(floor_x == floor_x)) floor_x = -INFINITY;
     const float scale = kBins / (32.0f * (greedy ? 1.0f : temperature));
 
     // kept: keys above `cut`, and those at `cut` up to index `last`
@@ -446,31 +676,48 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
       ties = 1;
     } else {
       if (top_k > 0 && static_cast<unsigned int>(top_k) < count) {
-        const Threshold t = find_threshold(slice, sh, cluster, m, scale, static_cast<u64>(top_k),
-                                           [](float x) -> u64 { return x > -INFINITY ? 1 : 0; });
+        const Threshold t = find_threshold<true>(
+            slice, sh, cluster, m, scale, [](float x) -> u64 { return x > -INFINITY ? 1 : 0; },
+            [&](u64) { return static_cast<u64>(top_k); });
+        if (t.key == 0) {  // a short list: everything in the bins down to t.bin
+          slice.each([&](float x, int i) {
+            if (x > -INFINITY && (x == m || fminf((m - x) * scale, kBins - 1.0f) < t.bin + 1.0f))
+              sh.mass[atomicAdd(&sh.gathered, 1u)] =
+                  static_cast<u64>(key_of(x)) << 32 | (0xFFFFFFFFu - static_cast<unsigned int>(first + i));
+          });
+          __syncthreads();
+          const unsigned int mine = sh.gathered;
+          if (threadIdx.x == 0) sh.found = static_cast<int>(atomicAdd(cluster.map_shared_rank(&sh.place, 0), mine));
+          __syncthreads();
+          u64* const to = cluster.map_shared_rank(&sh.list[0], 0) + sh.found;
+          for (unsigned int i = threadIdx.x; i < mine; i += kThreads) to[i] = sh.mass[i];
+          cluster.sync();
+          if (rank == 0)
+            finish_list(sh, mass, static_cast<int>(t.upto), top_k, top_p, min_p > 0.0f ? times(kOne, min_p, true) : 0, u,
+                        p.token + row, p.prob ? p.prob + row : nullptr);
+          return;  // nobody reads another CTA's memory any more
+        }
         cut = t.key;
         ties = static_cast<u64>(top_k) - t.above;
       }
       if (top_p < 1.0f) {
-        // the mass of what top-k keeps
-        u64 whole = 0, unused = 0;
+        // of what top-k keeps: the mass above its threshold, and the ties'
         const u64 at_cut = ties ? mass(value_of(cut)) : 0;
-        locate(slice, sh, segs, cluster, first,
-               [&](float x, int) -> u64 { return x > -INFINITY && key_of(x) > cut ? mass(x) : 0; },
-               [](u64) -> u64 { return 0; }, &unused, &above);
-        whole = above + ties * at_cut;
-        u64 target = static_cast<u64>(ceil(static_cast<double>(top_p) * static_cast<double>(whole)));
-        target = target < 1 ? 1 : target > whole ? whole : target;
-        if (target > above) {  // the prefix ends among the ties at top-k's threshold
-          const u64 need = (target - above + at_cut - 1) / at_cut;
+        const Threshold t = find_threshold<false>(
+            slice, sh, cluster, m, scale,
+            [&](float x) -> u64 { return x > -INFINITY && key_of(x) > cut ? mass(x) : 0; },
+            [&](u64 all) {
+              above = all;
+              const u64 target = times(all + ties * at_cut, top_p, true);
+              return target < 1 ? static_cast<u64>(1) : target;
+            });
+        if (t.target > above) {  // the prefix ends among the ties at top-k's threshold
+          const u64 need = (t.target - above + at_cut - 1) / at_cut;
           ties = need < ties ? need : ties;
         } else {
-          const Threshold t = find_threshold(
-              slice, sh, cluster, m, scale, target,
-              [&](float x) -> u64 { return x > -INFINITY && key_of(x) > cut ? mass(x) : 0; });
           cut = t.key;
           const u64 each = mass(value_of(cut));
-          ties = (target - t.above + each - 1) / each;
+          ties = (t.target - t.above + each - 1) / each;
         }
       }
     }
@@ -482,23 +729,18 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
       token = last;
       prob = 1.0f;
     } else {
-      const u64 least = min_p > 0.0f ? static_cast<u64>(ceil(static_cast<double>(min_p) * kOne)) : 0;
-      // the largest float below 1 stands for anything above it, 0 for anything below and for NaN
-      const double u = static_cast<double>(fminf(fmaxf(p.u[row], 0.0f), 0.999999940395355224609375f));
+      const u64 least = min_p > 0.0f ? times(kOne, min_p, true) : 0;
       token = locate(
           slice, sh, segs, cluster, first,
           [&](float x, int i) -> u64 {
             const unsigned int k = key_of(x);
-            if (!(x > -INFINITY) || k < cut || (k == cut && first + i > last)) return 0;
+            if (!(x > -INFINITY) || x < floor_x || k < cut || (k == cut && first + i > last)) return 0;
             const u64 w = mass(x);
             return w >= least ? w : 0;
           },
-          [&](u64 all) -> u64 {
-            const u64 at = static_cast<u64>(u * static_cast<double>(all));
-            return at < all ? at : all - 1;
-          },
+          [&](u64 all) -> u64 { return times(all, u, false); },
           &chosen, &whole);
-      prob = static_cast<float>(static_cast<double>(chosen) / static_cast<double>(whole));
+      if (threadIdx.x == 0) prob = static_cast<float>(static_cast<double>(chosen) / static_cast<double>(whole));
     }
   }
   if (rank == 0 && threadIdx.x == 0) {
@@ -513,12 +755,12 @@ cudaError_t launch_sample_of(SampleParams p, int num_sms, cudaStream_t stream) {
   constexpr int E = 16 / sizeof(T);
   constexpr int step = kThreads * E;
   int ranks = 1;
-  while (ranks < kMaxCluster && static_cast<long long>(p.rows) * ranks * 2 <= 2ll * num_sms &&
+  while (ranks < kMaxCluster && static_cast<long long>(p.rows) * ranks * 2 <= 4ll * num_sms &&
          p.vocab > ranks * step)
     ranks *= 2;
   auto slice_of = [&](int r) { return ((p.vocab + r - 1) / r + step - 1) / step * step; };
   // enough CTAs that the slice fits in shared memory
-  constexpr size_t most = 200 * 1024;
+  constexpr size_t most = 176 * 1024;
   while (ranks < kMaxCluster && static_cast<size_t>(slice_of(ranks)) * sizeof(T) > most) ranks *= 2;
   p.slice = slice_of(ranks);
   const size_t segs = static_cast<size_t>(p.slice / step) * kWarps * 8;
