@@ -219,7 +219,117 @@ struct Threshold {
   u64 above;         // the count or mass of larger keys
   u64 upto;          // the sum of the first histogram's bins down to the one found
   u64 target;
+  int last;          // of the logits at `key`: the index of the last one in, -1 when not known
 };
+
+// Descending bitonic sort of n (a power of two, at most kList) numbers.
+__device__ void sort_down(u64* a, int n) {
+  for (int k = 2; k <= n; k <<= 1)
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      for (int i = threadIdx.x; i < n / 2; i += kThreads) {
+        const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
+        const u64 x = a[lo], y = a[hi];
+        if ((x < y) == ((lo & k) == 0)) {
+          a[lo] = y;
+          a[hi] = x;
+        }
+      }
+      __syncthreads();
+    }
+}
+
+// Inclusive sums of v[0 .. n) in place; n <= kList.  Returns the whole.
+__device__ u64 scan_list(SampleShared& sh, u64* v, int n) {
+  constexpr int kEach = kList / kThreads;
+  u64 x[kEach], s = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int at = threadIdx.x * kEach + i;
+    x[i] = at < n ? v[at] : 0;
+    s += x[i];
+  }
+  const u64 upto = warp_scan(s);
+  if ((threadIdx.x & 31) == 31) sh.warp64b[threadIdx.x >> 5] = upto;
+  __syncthreads();
+  u64 before = upto - s, all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < (threadIdx.x >> 5)) before += sh.warp64b[w];
+    all += sh.warp64b[w];
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    before += x[i];
+    const int at = threadIdx.x * kEach + i;
+    if (at < n) v[at] = before;
+  }
+  __syncthreads();
+  return all;
+}
+
+// How many of the ascending v[0 .. n) are below t (by every thread).
+__device__ __forceinline__ int below(const u64* v, int n, u64 t) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (v[mid] < t) lo = mid + 1; else hi = mid;
+  }
+  return lo;
+}
+
+// The logits with in(x), of all CTAs, gathered in rank 0's list.  Returns how
+// many there are (to every CTA); above kList the list is not complete.
+template <typename S, typename P>
+__device__ int gather(const S& slice, SampleShared& sh, cg::cluster_group& cluster, int first, P in) {
+  slice.each([&](float x, int i) {
+    if (!in(x)) return;
+    const unsigned int at = atomicAdd(&sh.gathered, 1u);
+    if (at < kList)
+      sh.mass[at] = static_cast<u64>(key_of(x)) << 32 | (0xFFFFFFFFu - static_cast<unsigned int>(first + i));
+  });
+  __syncthreads();
+  const unsigned int mine = sh.gathered;
+  if (threadIdx.x == 0) sh.found = static_cast<int>(atomicAdd(cluster.map_shared_rank(&sh.place, 0), mine));
+  __syncthreads();
+  const unsigned int base = static_cast<unsigned int>(sh.found);
+  if (base + mine <= kList) {
+    u64* const to = cluster.map_shared_rank(&sh.list[0], 0) + base;
+    for (unsigned int i = threadIdx.x; i < mine; i += kThreads) to[i] = sh.mass[i];
+  }
+  cluster.sync();
+  return static_cast<int>(*cluster.map_shared_rank(&sh.place, 0));
+}
+
+// The threshold's bin, when few logits are in it: sorted and summed in rank 0.
+template <typename S, typename P>
+__device__ bool short_border(const S& slice, SampleShared& sh, cg::cluster_group& cluster, int first,
+                             const Masses& mass, Threshold& res, P in) {
+  const int n = gather(slice, sh, cluster, first, in);
+  if (n > kList) {
+    cluster.sync();  // sh.place has been read
+    return false;
+  }
+  if (cluster.block_rank() == 0) {
+    int size = 2;
+    while (size < n) size <<= 1;
+    for (int i = n + threadIdx.x; i < size; i += kThreads) sh.list[i] = 0;
+    __syncthreads();
+    sort_down(sh.list, size);
+    for (int i = threadIdx.x; i < n; i += kThreads) sh.mass[i] = mass(value_of(static_cast<unsigned int>(sh.list[i] >> 32)));
+    __syncthreads();
+    scan_list(sh, sh.mass, n);
+    if (threadIdx.x == 0) {
+      const int at = min(below(sh.mass, n, res.target - res.above), n - 1);
+      sh.range[0] = static_cast<unsigned int>(sh.list[at] >> 32);
+      sh.found = static_cast<int>(0xFFFFFFFFu - static_cast<unsigned int>(sh.list[at]));
+    }
+  }
+  cluster.sync();
+  res.key = cluster.map_shared_rank(&sh.range[0], 0)[0];
+  res.last = *cluster.map_shared_rank(&sh.found, 0);
+  cluster.sync();  // both have been read
+  return true;
+}
 
 // The key at which the sum of weight(x) over the candidates, from the
 // largest down, reaches target_of(the whole sum) (for counts: of the bins).
@@ -231,8 +341,9 @@ struct Threshold {
 // Masses are summed in three 32-bit limbs of 15 bits: shared-memory atomics
 // of 32 bits are native, those of 64 a loop.
 template <bool COUNT, typename S, typename W, typename G>
-__device__ Threshold find_threshold(const S& slice, SampleShared& sh, cg::cluster_group& cluster, float m, float scale,
-                                    W weight, G target_of) {
+__device__ Threshold find_threshold(const S& slice, SampleShared& sh, cg::cluster_group& cluster, const Masses& mass,
+                                    float scale, int first_index, W weight, G target_of) {
+  const float m = mass.m;
   const int ranks = cluster.num_blocks();
   Threshold res;
   res.key = 0;
@@ -240,6 +351,7 @@ __device__ Threshold find_threshold(const S& slice, SampleShared& sh, cg::cluste
   res.above = 0;
   res.upto = 0;
   res.target = 0;
+  res.last = -1;
   unsigned int lo = 0, hi = 0xFFFFFFFFu;  // keys still in question, once `linear` is done
   bool linear = true;
   int shift = 0;
@@ -278,16 +390,17 @@ __device__ Threshold find_threshold(const S& slice, SampleShared& sh, cg::cluste
     cluster.sync();
     // thread t: bins 2t and 2t + 1 over all CTAs
     u64 v[2] = {0, 0};
-    for (int r = 0; r < ranks; ++r) {
-      const unsigned int* h = cluster.map_shared_rank(&sh.hist[0][0], r);
+    constexpr int kLimbs = COUNT ? 1 : 3;
+    unsigned int h[kMaxCluster][2 * kLimbs];  // all on their way together
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const unsigned int* at = h + 2 * threadIdx.x + i;
-        v[i] += at[0];
-        if (!COUNT)
-          v[i] += (static_cast<u64>(at[kBins]) << kLimb) + (static_cast<u64>(at[2 * kBins]) << (2 * kLimb));
-      }
-    }
+    for (int r = 0; r < kMaxCluster; ++r)
+#pragma unroll
+      for (int i = 0; i < 2 * kLimbs; ++i)
+        h[r][i] = r < ranks ? cluster.map_shared_rank(&sh.hist[0][0], r)[(i >> 1) * kBins + 2 * threadIdx.x + (i & 1)] : 0;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+#pragma unroll
+      for (int i = 0; i < 2 * kLimbs; ++i) v[i & 1] += static_cast<u64>(h[r][i]) << ((i >> 1) * kLimb);
     const u64 mine = warp_scan(v[0] + v[1]);
     if ((threadIdx.x & 31) == 31) sh.warp64[threadIdx.x >> 5] = mine;
     __syncthreads();
@@ -321,6 +434,9 @@ __device__ Threshold find_threshold(const S& slice, SampleShared& sh, cg::cluste
       res.bin = bin;
       res.upto = sh.sel_upto;
       if (COUNT ? res.upto <= kList : res.upto == ~0ull) return res;
+      if (!COUNT && short_border(slice, sh, cluster, first_index, mass, res,
+                                 [&](float x) { return bin_of(x) == bin && weight(x) > 0; }))
+        return res;
       // The bin's key range: keys at which bin_of, which falls as keys grow, is
       // `bin`.  Thread 0: the smallest key with bin_of <= bin; thread 1: the
       // largest with bin_of >= bin.  Each begins where the bin's edge lies
@@ -392,9 +508,14 @@ __device__ Threshold find_threshold(const S& slice, SampleShared& sh, cg::cluste
 // The first index of the row at which the running sum of weight(x, index)
 // exceeds target(whole sum); -1 if the whole sum is 0.  Every thread of the
 // cluster gets it; *mass is that element's weight and *whole the sum.
-template <typename S, typename W, typename G>
-__device__ int locate(const S& slice, SampleShared& sh, u64* segs, cg::cluster_group& cluster, int first, W weight,
-                      G target_of, u64* mass, u64* whole) {
+//
+// A warp sums the weights of its vectors of a round; with DENSE, in_sum(x,
+// index) says which of them have one, and those are first moved together, so
+// that weight_of (costly) is evaluated on full warps.
+template <bool DENSE, typename S, typename I, typename V, typename G>
+__device__ int locate(const S& slice, SampleShared& sh, u64* segs, cg::cluster_group& cluster, int first, I in_sum,
+                      V weight_of, G target_of, u64* mass, u64* whole) {
+  auto weight = [&](float x, int i) -> u64 { return in_sum(x, i) ? weight_of(x) : 0; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
   constexpr int E = S::E;
@@ -404,9 +525,25 @@ __device__ int locate(const S& slice, SampleShared& sh, u64* segs, cg::cluster_g
     float x[E];
     slice.get(vec, x);
     u64 s = 0;
+    if (DENSE) {
+      float* const room = reinterpret_cast<float*>(sh.mass) + warp * (32 * E);
+      int n = 0;
 #pragma unroll
-    for (int e = 0; e < E; ++e) s += weight(x[e], vec * E + e);
-    s = warp_sum(s);
+      for (int e = 0; e < E; ++e) {
+        const bool in = in_sum(x[e], vec * E + e);
+        const unsigned int who = __ballot_sync(0xFFFFFFFFu, in);
+        if (in) room[n + __popc(who & ((1u << lane) - 1))] = x[e];
+        n += __popc(who);
+      }
+      __syncwarp();
+      for (int i = lane; i < n; i += 32) s += weight_of(room[i]);
+      __syncwarp();
+      if (n) s = warp_sum(s);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) s += weight(x[e], vec * E + e);
+      s = warp_sum(s);
+    }
     if (lane == 0) segs[r * kWarps + warp] = s;
     sum += s;
   }
@@ -474,61 +611,6 @@ __device__ int locate(const S& slice, SampleShared& sh, u64* segs, cg::cluster_g
   }
   cluster.sync();  // sh.total and sh.found may be written again
   return found;
-}
-
-// Descending bitonic sort of n (a power of two, at most kList) numbers.
-__device__ void sort_down(u64* a, int n) {
-  for (int k = 2; k <= n; k <<= 1)
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      for (int i = threadIdx.x; i < n / 2; i += kThreads) {
-        const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
-        const u64 x = a[lo], y = a[hi];
-        if ((x < y) == ((lo & k) == 0)) {
-          a[lo] = y;
-          a[hi] = x;
-        }
-      }
-      __syncthreads();
-    }
-}
-
-// Inclusive sums of v[0 .. n) in place; n <= kList.  Returns the whole.
-__device__ u64 scan_list(SampleShared& sh, u64* v, int n) {
-  constexpr int kEach = kList / kThreads;
-  u64 x[kEach], s = 0;
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int at = threadIdx.x * kEach + i;
-    x[i] = at < n ? v[at] : 0;
-    s += x[i];
-  }
-  const u64 upto = warp_scan(s);
-  if ((threadIdx.x & 31) == 31) sh.warp64b[threadIdx.x >> 5] = upto;
-  __syncthreads();
-  u64 before = upto - s, all = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < (threadIdx.x >> 5)) before += sh.warp64b[w];
-    all += sh.warp64b[w];
-  }
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    before += x[i];
-    const int at = threadIdx.x * kEach + i;
-    if (at < n) v[at] = before;
-  }
-  __syncthreads();
-  return all;
-}
-
-// How many of the ascending v[0 .. n) are below t (by every thread).
-__device__ __forceinline__ int below(const u64* v, int n, u64 t) {
-  int lo = 0, hi = n;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (v[mid] < t) lo = mid + 1; else hi = mid;
-  }
-  return lo;
 }
 
 // One CTA finishes on the short list: all logits of the row that can be kept
@@ -677,21 +759,13 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     } else {
       if (top_k > 0 && static_cast<unsigned int>(top_k) < count) {
         const Threshold t = find_threshold<true>(
-            slice, sh, cluster, m, scale, [](float x) -> u64 { return x > -INFINITY ? 1 : 0; },
+            slice, sh, cluster, mass, scale, first, [](float x) -> u64 { return x > -INFINITY ? 1 : 0; },
             [&](u64) { return static_cast<u64>(top_k); });
         if (t.key == 0) {  // a short list: everything in the bins down to t.bin
-          slice.each([&](float x, int i) {
-            if (x > -INFINITY && (x == m || fminf((m - x) * scale, kBins - 1.0f) < t.bin + 1.0f))
-              sh.mass[atomicAdd(&sh.gathered, 1u)] =
-                  static_cast<u64>(key_of(x)) << 32 | (0xFFFFFFFFu - static_cast<unsigned int>(first + i));
+          gather(slice, sh, cluster, first, [&](float x) {
+            return x > -INFINITY && (x == m || fminf((m - x) * scale, kBins - 1.0f) < t.bin + 1.0f);
           });
-          __syncthreads();
-          const unsigned int mine = sh.gathered;
-          if (threadIdx.x == 0) sh.found = static_cast<int>(atomicAdd(cluster.map_shared_rank(&sh.place, 0), mine));
-          __syncthreads();
-          u64* const to = cluster.map_shared_rank(&sh.list[0], 0) + sh.found;
-          for (unsigned int i = threadIdx.x; i < mine; i += kThreads) to[i] = sh.mass[i];
-          cluster.sync();
+          cluster.sync();  // sh.place has been read
           if (rank == 0)
             finish_list(sh, mass, static_cast<int>(t.upto), top_k, top_p, min_p > 0.0f ? times(kOne, min_p, true) : 0, u,
                         p.token + row, p.prob ? p.prob + row : nullptr);
@@ -704,7 +778,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         // of what top-k keeps: the mass above its threshold, and the ties'
         const u64 at_cut = ties ? mass(value_of(cut)) : 0;
         const Threshold t = find_threshold<false>(
-            slice, sh, cluster, m, scale,
+            slice, sh, cluster, mass, scale, first,
             [&](float x) -> u64 { return x > -INFINITY && key_of(x) > cut ? mass(x) : 0; },
             [&](u64 all) {
               above = all;
@@ -716,25 +790,34 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
           ties = need < ties ? need : ties;
         } else {
           cut = t.key;
-          const u64 each = mass(value_of(cut));
-          ties = (t.target - t.above + each - 1) / each;
+          if (t.last >= 0) {
+            last = t.last;
+            ties = 0;
+          } else {
+            const u64 each = mass(value_of(cut));
+            ties = (t.target - t.above + each - 1) / each;
+          }
         }
       }
     }
     u64 chosen = 0, whole = 0;
     if (ties)  // the index of the last tie that is kept
-      last = locate(slice, sh, segs, cluster, first, [&](float x, int) -> u64 { return key_of(x) == cut ? 1 : 0; },
-                    [&](u64 all) -> u64 { return (ties < all ? ties : all) - 1; }, &chosen, &whole);
+      last = locate<false>(
+          slice, sh, segs, cluster, first, [&](float x, int) { return key_of(x) == cut; }, [](float) -> u64 { return 1; },
+          [&](u64 all) -> u64 { return (ties < all ? ties : all) - 1; }, &chosen, &whole);
     if (greedy) {
       token = last;
       prob = 1.0f;
     } else {
       const u64 least = min_p > 0.0f ? times(kOne, min_p, true) : 0;
-      token = locate(
+      token = locate<true>(
           slice, sh, segs, cluster, first,
-          [&](float x, int i) -> u64 {
+          [&](float x, int i) {
+            if (!(x > -INFINITY) || x < floor_x) return false;
             const unsigned int k = key_of(x);
-            if (!(x > -INFINITY) || x < floor_x || k < cut || (k == cut && first + i > last)) return 0;
+            return k > cut || (k == cut && first + i <= last);
+          },
+          [&](float x) -> u64 {
             const u64 w = mass(x);
             return w >= least ? w : 0;
           },
