@@ -447,7 +447,7 @@ struct SampleParams {
   int* token;
   float* prob;               // or null
   int rows, vocab, type;     // type: 0 f16, 1 bf16, 2 f32
-  int slice;                 // set by the launch: logits of one CTA
+  int slice, pad;            // set by the launch: logits of one CTA, of them kept free for alignment
 };
 cudaError_t launch_sample(const SampleParams& p, int num_sms, cudaStream_t stream);
 

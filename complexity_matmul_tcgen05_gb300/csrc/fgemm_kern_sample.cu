@@ -34,6 +34,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <cstring>
 
 #include "fgemm_internal.h"
 
@@ -63,6 +64,8 @@ __constant__ u64 kPow[32] = {
     32264211463077ull, 32970705697691ull, 33692670141585ull, 34430443548229ull,
 };
 
+// Bins that masses above 2^-14 fall into: (m - x) / T < 14 ln 2 = 9.71, 32 bins to 1.
+constexpr int kFewBins = 311;
 constexpr int kList = 2048;
 constexpr int kLimb = 15;  // bits: a CTA's slice of 2^17 logits cannot overflow a 32-bit sum of limbs
 
@@ -96,8 +99,8 @@ __device__ __forceinline__ float value_of(unsigned int k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 
-// exp((x - m) / T) in units of 2^-44, to about 2^-36 of its value.
-// y = (x - m) log2(e) / T is held as a sum of two floats (x - m and its
+// exp((x - m) / T) in units of 2^-44, to about 2^-36 (of its value, or of 1 for
+// masses below 2^-14).  y = (x - m) log2(e) / T is held as a sum of two floats (x - m and its
 // rounding error by a two-sum, the product's error by an fma); then
 // 2^y = 2^n 2^(j/32) 2^r with a table for 2^(j/32) and the exponential series
 // for 2^r, |r| <= 1/64, whose first-order term is again kept in two floats.
@@ -106,13 +109,32 @@ __device__ __forceinline__ float value_of(unsigned int k) {
 struct Masses {
   float m, ch, cl;  // ch + cl = log2(e) / T
   const u64* pow;
+  // How small a mass is: y rounded, from which low() or high() goes on.
+  __device__ __forceinline__ float size(float x) const { return x == m ? 0.0f : fmaf(x - m, ch, (x - m) * cl); }
+  // A mass below 2^-14: fp32 is enough for its 30 bits (the error is below
+  // 2^-36 of m's mass, and not of one sign).
+  static constexpr float kSmall = -14.0f;
+  __device__ __forceinline__ unsigned int low(float y) const {
+    constexpr float magic = 12582912.0f;
+    constexpr int magic_bits = 0x4B400000;
+    if (!(y > -46.0f)) return 0;
+    const float t = fmaf(y, 32.0f, magic);  // 32 y, rounded
+    const int j = __float_as_int(t) - magic_bits;
+    const float z = fmaf(t - magic, -0.03125f, y) * 0.693147182464599609375f;
+    const float p = z * fmaf(z, fmaf(z, 1.0f / 6, 0.5f), 1.0f);
+    const float f = static_cast<float>(static_cast<unsigned int>(pow[j & 31] >> 14));  // 2^(j/32) in units of 2^-30
+    return __float2uint_rn(fmaf(f, p, f) * __int_as_float((14 + (j >> 5) + 127) << 23));
+  }
   __device__ __forceinline__ u64 operator()(float x) const {
+    const float y = size(x);
+    return y > kSmall ? high(x) : low(y);
+  }
+  __device__ __forceinline__ u64 high(float x) const {
     constexpr float magic = 12582912.0f;
     constexpr int magic_bits = 0x4B400000;
     if (x == m) return kOne;
     const float s = x - m;
     const float yh = __fmul_rn(s, ch);  // rounded here: not to be fused into a sum below
-    if (!(yh > -46.0f)) return 0;
     const float bb = s - x;
     const float e = (x - (s - bb)) + (-m - bb);
     const float yl = fmaf(s, ch, -yh) + fmaf(s, cl, e * ch);
@@ -310,15 +332,31 @@ __device__ bool short_border(const S& slice, SampleShared& sh, cg::cluster_group
     return false;
   }
   if (cluster.block_rank() == 0) {
-    int size = 2;
-    while (size < n) size <<= 1;
-    for (int i = n + threadIdx.x; i < size; i += kThreads) sh.list[i] = 0;
-    __syncthreads();
-    sort_down(sh.list, size);
-    for (int i = threadIdx.x; i < n; i += kThreads) sh.mass[i] = mass(value_of(static_cast<unsigned int>(sh.list[i] >> 32)));
-    __syncthreads();
-    scan_list(sh, sh.mass, n);
-    if (threadIdx.x == 0) {
+    if (n <= kThreads) {  // each entry finds what is before it by itself
+      const u64 mine = threadIdx.x < n ? sh.list[threadIdx.x] : 0;
+      const u64 w = threadIdx.x < n ? mass(value_of(static_cast<unsigned int>(mine >> 32))) : 0;
+      if (threadIdx.x < n) sh.mass[threadIdx.x] = w;
+      if (threadIdx.x == 0) sh.range[0] = 0;
+      __syncthreads();
+      u64 before = res.above;
+      if (threadIdx.x < n)
+        for (int i = 0; i < n; ++i) before += sh.list[i] > mine ? sh.mass[i] : 0;
+      if (threadIdx.x < n && before < res.target && res.target <= before + w) {
+        sh.range[0] = static_cast<unsigned int>(mine >> 32);
+        sh.found = static_cast<int>(0xFFFFFFFFu - static_cast<unsigned int>(mine));
+      }
+    } else {
+      int size = 2;
+      while (size < n) size <<= 1;
+      for (int i = n + threadIdx.x; i < size; i += kThreads) sh.list[i] = 0;
+      __syncthreads();
+      sort_down(sh.list, size);
+      for (int i = threadIdx.x; i < n; i += kThreads)
+        sh.mass[i] = mass(value_of(static_cast<unsigned int>(sh.list[i] >> 32)));
+      __syncthreads();
+      scan_list(sh, sh.mass, n);
+    }
+    if (n > kThreads && threadIdx.x == 0) {
       const int at = min(below(sh.mass, n, res.target - res.above), n - 1);
       sh.range[0] = static_cast<unsigned int>(sh.list[at] >> 32);
       sh.found = static_cast<int>(0xFFFFFFFFu - static_cast<unsigned int>(sh.list[at]));
@@ -331,18 +369,17 @@ __device__ bool short_border(const S& slice, SampleShared& sh, cg::cluster_group
   return true;
 }
 
-// The key at which the sum of weight(x) over the candidates, from the
-// largest down, reaches target_of(the whole sum) (for counts: of the bins).
-// weight 0: not a candidate.  COUNT: the weights are 0 or 1, and the search
-// stops after the first histogram (key 0) when the bins down to the one found
+// The key at which the sum of 1 (COUNT) or of the masses over the logits with
+// is_in(x), from the largest down, reaches target_of(the whole sum; for counts:
+// of the bins).  Counts: the search stops after the first histogram (key 0) when the bins down to the one found
 // hold at most kList.  Masses: it stops there (key 0) when the target lies
 // above their sum.  Every thread of the cluster gets the result.
 //
 // Masses are summed in three 32-bit limbs of 15 bits: shared-memory atomics
 // of 32 bits are native, those of 64 a loop.
-template <bool COUNT, typename S, typename W, typename G>
+template <bool COUNT, typename S, typename I, typename G>
 __device__ Threshold find_threshold(const S& slice, SampleShared& sh, cg::cluster_group& cluster, const Masses& mass,
-                                    float scale, int first_index, W weight, G target_of) {
+                                    float scale, int first_index, I is_in, G target_of) {
   const float m = mass.m;
   const int ranks = cluster.num_blocks();
   Threshold res;
@@ -354,6 +391,7 @@ __device__ Threshold find_threshold(const S& slice, SampleShared& sh, cg::cluste
   res.last = -1;
   unsigned int lo = 0, hi = 0xFFFFFFFFu;  // keys still in question, once `linear` is done
   bool linear = true;
+  bool few = !COUNT;  // the first histogram has bins for large masses only
   int shift = 0;
   auto bin_of = [&](float x) -> int {
     if (linear) return x == m ? 0 : static_cast<int>(fminf((m - x) * scale, kBins - 1.0f));
@@ -370,37 +408,96 @@ __device__ Threshold find_threshold(const S& slice, SampleShared& sh, cg::cluste
     }
     if (threadIdx.x == 0) sh.sel_bin = kBins - 1;
     __syncthreads();
-    slice.each([&](float x, int) {
-      const int b = bin_of(x);
+    u64 rest = 0;  // in units of 2^-44, of this thread's small masses (first histogram)
+    if (COUNT) {
       // the last linear bin holds all that lies far below: it is what is left
-      if (b < 0 || (linear && b == kBins - 1)) return;
-      const u64 w = weight(x);
-      if (COUNT) {
-        if (w) atomicAdd(&sh.hist[0][b], 1u);
-      } else if (w) {
-        constexpr unsigned int mask = (1u << kLimb) - 1;
-        const unsigned int low = static_cast<unsigned int>(w) & mask;
-        const unsigned int mid = static_cast<unsigned int>(w >> kLimb) & mask;
-        const unsigned int top = static_cast<unsigned int>(w >> (2 * kLimb));
-        atomicAdd(&sh.hist[0][b], low);
-        if (mid) atomicAdd(&sh.hist[1][b], mid);
-        if (top) atomicAdd(&sh.hist[2][b], top);
+      slice.each([&](float x, int) {
+        const int b = bin_of(x);
+        if (b < 0 || (linear && b == kBins - 1)) return;
+        if (is_in(x)) atomicAdd(&sh.hist[0][b], 1u);
+      });
+    } else {
+      constexpr unsigned int mask = (1u << kLimb) - 1;
+      constexpr int E = S::E;
+      const int lane = threadIdx.x & 31;
+      float* const room = reinterpret_cast<float*>(sh.mass) + (threadIdx.x >> 5) * (32 * E);
+      for (int r = 0; r < slice.rounds; ++r) {
+        float x[E];
+        slice.get(r * kThreads + threadIdx.x, x);
+        int n = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float y = mass.size(x[e]);
+          const bool in = is_in(x[e]);
+          bool dense;
+          if (few) {  // large masses into bins; small ones only into their sum
+            dense = in && y > Masses::kSmall;
+            if (in && !dense) rest += mass.low(y);
+          } else {
+            dense = in && y > -46.0f && bin_of(x[e]) >= 0;
+          }
+          const unsigned int who = __ballot_sync(0xFFFFFFFFu, dense);
+          if (dense) room[n + __popc(who & ((1u << lane) - 1))] = x[e];
+          n += __popc(who);
+        }
+        __syncwarp();
+        for (int i = lane; i < n; i += 32) {  // on full warps: a mass takes long
+          const float v = room[i];
+          const int b = bin_of(v);
+          const u64 w = mass(v);
+          atomicAdd(&sh.hist[0][b], static_cast<unsigned int>(w) & mask);
+          if (w >> kLimb) atomicAdd(&sh.hist[1][b], static_cast<unsigned int>(w >> kLimb) & mask);
+          if (w >> (2 * kLimb)) atomicAdd(&sh.hist[2][b], static_cast<unsigned int>(w >> (2 * kLimb)));
+        }
+        __syncwarp();
       }
-    });
+      if (few) {
+        rest = warp_sum(rest);
+        if (lane == 0) sh.warp64b[threadIdx.x >> 5] = rest;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+          rest = 0;
+          for (int w = 0; w < kWarps; ++w) rest += sh.warp64b[w];
+          sh.total = rest;
+        }
+      }
+    }
     cluster.sync();
     // thread t: bins 2t and 2t + 1 over all CTAs
     u64 v[2] = {0, 0};
-    constexpr int kLimbs = COUNT ? 1 : 3;
-    unsigned int h[kMaxCluster][2 * kLimbs];  // all on their way together
+    u64 rests = 0;
+    if (COUNT) {
+      unsigned int h[kMaxCluster][2];  // all on their way together
 #pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r)
+      for (int r = 0; r < kMaxCluster; ++r) {
+        const unsigned int* const at = cluster.map_shared_rank(&sh.hist[0][0], r < ranks ? r : 0) + 2 * threadIdx.x;
+        h[r][0] = at[0];
+        h[r][1] = at[1];
+      }
 #pragma unroll
-      for (int i = 0; i < 2 * kLimbs; ++i)
-        h[r][i] = r < ranks ? cluster.map_shared_rank(&sh.hist[0][0], r)[(i >> 1) * kBins + 2 * threadIdx.x + (i & 1)] : 0;
+      for (int r = 0; r < kMaxCluster; ++r)
+        if (r < ranks) v[0] += h[r][0], v[1] += h[r][1];
+    } else {
 #pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r)
+      for (int i = 0; i < 2; ++i) {
+        if (few && 2 * threadIdx.x + i >= kFewBins) break;
+        unsigned int h[kMaxCluster][3];
 #pragma unroll
-      for (int i = 0; i < 2 * kLimbs; ++i) v[i & 1] += static_cast<u64>(h[r][i]) << ((i >> 1) * kLimb);
+        for (int r = 0; r < kMaxCluster; ++r) {
+          const unsigned int* const at =
+              cluster.map_shared_rank(&sh.hist[0][0], r < ranks ? r : 0) + 2 * threadIdx.x + i;
+          h[r][0] = at[0];
+          h[r][1] = at[kBins];
+          h[r][2] = at[2 * kBins];
+        }
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+          if (r < ranks)
+            v[i] += h[r][0] + (static_cast<u64>(h[r][1]) << kLimb) + (static_cast<u64>(h[r][2]) << (2 * kLimb));
+      }
+      if (few)
+        for (int r = 0; r < ranks; ++r) rests += *cluster.map_shared_rank(&sh.total, r);
+    }
     const u64 mine = warp_scan(v[0] + v[1]);
     if ((threadIdx.x & 31) == 31) sh.warp64[threadIdx.x >> 5] = mine;
     __syncthreads();
@@ -411,7 +508,7 @@ __device__ Threshold find_threshold(const S& slice, SampleShared& sh, cg::cluste
       if (w < (threadIdx.x >> 5)) before += sh.warp64[w];
       all += sh.warp64[w];
     }
-    if (linear) res.target = target_of(all);
+    if (linear) res.target = target_of(all + rests);
     const u64 target = res.target;
     if (threadIdx.x == 0) {  // the last linear bin, unless another bin reaches the target
       sh.sel_before = all;
@@ -433,9 +530,21 @@ __device__ Threshold find_threshold(const S& slice, SampleShared& sh, cg::cluste
     if (linear) {
       res.bin = bin;
       res.upto = sh.sel_upto;
-      if (COUNT ? res.upto <= kList : res.upto == ~0ull) return res;
+      if (COUNT && res.upto <= kList) return res;
+      if (!COUNT && few) {
+        if (res.target > res.above && res.upto == ~0ull && res.target > res.above + rests) return res;
+        // (above is what the bins hold when none of them reaches the target;
+        // the last of them also has small masses that are not in it)
+        if (res.upto == ~0ull || bin >= kFewBins - 1) {  // among the small masses: all over again with bins for them
+          few = false;
+          res.above = 0;
+          __syncthreads();
+          continue;
+        }
+      }
+      if (!COUNT && res.upto == ~0ull) return res;
       if (!COUNT && short_border(slice, sh, cluster, first_index, mass, res,
-                                 [&](float x) { return bin_of(x) == bin && weight(x) > 0; }))
+                                 [&](float x) { return bin_of(x) == bin && is_in(x); }))
         return res;
       // The bin's key range: keys at which bin_of, which falls as keys grow, is
       // `bin`.  Thread 0: the smallest key with bin_of <= bin; thread 1: the
@@ -490,6 +599,7 @@ __device__ Threshold find_threshold(const S& slice, SampleShared& sh, cg::cluste
       lo = sh.range[0];
       hi = sh.range[1];
       linear = false;
+      few = false;
     } else {
       const unsigned int top = hi - (static_cast<unsigned int>(bin) << shift);
       const unsigned int width = (1u << shift) - 1;
@@ -507,14 +617,14 @@ __device__ Threshold find_threshold(const S& slice, SampleShared& sh, cg::cluste
 
 // The first index of the row at which the running sum of weight(x, index)
 // exceeds target(whole sum); -1 if the whole sum is 0.  Every thread of the
-// cluster gets it; *mass is that element's weight and *whole the sum.
+// cluster gets it; *mass is full_of that element and *whole the sum.
 //
 // A warp sums the weights of its vectors of a round; with DENSE, in_sum(x,
-// index) says which of them have one, and those are first moved together, so
-// that weight_of (costly) is evaluated on full warps.
-template <bool DENSE, typename S, typename I, typename V, typename G>
-__device__ int locate(const S& slice, SampleShared& sh, u64* segs, cg::cluster_group& cluster, int first, I in_sum,
-                      V weight_of, G target_of, u64* mass, u64* whole) {
+// index) says which of them have one (none below floor_x), and those are first
+// moved together, so that weight_of (costly) is evaluated on full warps.
+template <bool DENSE, typename S, typename I, typename V, typename F, typename G>
+__device__ int locate(const S& slice, SampleShared& sh, u64* segs, cg::cluster_group& cluster, int first, float floor_x, I in_sum,
+                      V weight_of, F full_of, G target_of, u64* mass, u64* whole) {
   auto weight = [&](float x, int i) -> u64 { return in_sum(x, i) ? weight_of(x) : 0; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
@@ -528,6 +638,10 @@ __device__ int locate(const S& slice, SampleShared& sh, u64* segs, cg::cluster_g
     if (DENSE) {
       float* const room = reinterpret_cast<float*>(sh.mass) + warp * (32 * E);
       int n = 0;
+      float most = x[0];
+#pragma unroll
+      for (int e = 1; e < E; ++e) most = fmaxf(most, x[e]);
+      if (__any_sync(0xFFFFFFFFu, most >= floor_x))
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const bool in = in_sum(x[e], vec * E + e);
@@ -556,59 +670,74 @@ __device__ int locate(const S& slice, SampleShared& sh, u64* segs, cg::cluster_g
     sh.found = -1;
   }
   cluster.sync();
-  u64 all = 0, before = 0, own = 0;
-  for (int r = 0; r < ranks; ++r) {
-    const u64 t = *cluster.map_shared_rank(&sh.total, r);
+  u64 all = 0, before = 0, own = 0, totals[kMaxCluster];
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r) totals[r] = *cluster.map_shared_rank(&sh.total, r < ranks ? r : 0);
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r) {
+    const u64 t = r < ranks ? totals[r] : 0;
     if (r < rank) before += t;
     if (r == rank) own = t;
     all += t;
   }
   const u64 target = all ? target_of(all) : 0;
   *whole = all;
-  if (all && before <= target && target < before + own && warp == 0) {
-    // the segment, 32 at a time, then the element in it
+  if (all && before <= target && target < before + own) {
+    // the segment, as many at a time as there are threads, then the element in it
     const int n = slice.rounds * kWarps;
     u64 base = before;
-    for (int s0 = 0; s0 < n; s0 += 32) {
-      const u64 v = s0 + lane < n ? segs[s0 + lane] : 0;
-      const u64 upto = base + warp_scan(v);
-      const unsigned int hit = __ballot_sync(0xFFFFFFFFu, upto > target);
-      if (hit) {
-        const int at = __ffs(hit) - 1;
-        const u64 seg_before = __shfl_sync(0xFFFFFFFFu, upto - v, at);
-        const int seg = s0 + at;
-        const int vec = (seg / kWarps) * kThreads + (seg % kWarps) * 32 + lane;
-        float x[E];
-        slice.get(vec, x);
-        u64 w[E], s = 0;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          w[e] = weight(x[e], vec * E + e);
-          s += w[e];
-        }
-        u64 run = seg_before + warp_scan(s) - s;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          if (run <= target && target < run + w[e]) {
-            sh.found = first + vec * E + e;
-            sh.found_mass = w[e];
-          }
-          run += w[e];
-        }
-        break;
+    if (threadIdx.x == 0) sh.sel_bin = -1;
+    for (int s0 = 0; s0 < n; s0 += kThreads) {
+      const int seg = s0 + threadIdx.x;
+      const u64 v = seg < n ? segs[seg] : 0;
+      const u64 upto = warp_scan(v);
+      if (lane == 31) sh.warp64b[warp] = upto;
+      __syncthreads();
+      u64 from = base + upto - v;
+      for (int w = 0; w < kWarps; ++w) {
+        const u64 t = sh.warp64b[w];
+        if (w < warp) from += t;
+        base += t;
       }
-      base = __shfl_sync(0xFFFFFFFFu, upto, 31);
+      if (from <= target && target < from + v) {
+        sh.sel_bin = seg;
+        sh.sel_before = from;
+      }
+      __syncthreads();
+      if (sh.sel_bin >= 0) break;
+    }
+    if (warp == 0) {
+      const int seg = sh.sel_bin;
+      const int vec = (seg / kWarps) * kThreads + (seg % kWarps) * 32 + lane;
+      float x[E];
+      slice.get(vec, x);
+      u64 w[E], s = 0;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        w[e] = weight(x[e], vec * E + e);
+        s += w[e];
+      }
+      u64 run = sh.sel_before + warp_scan(s) - s;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        if (run <= target && target < run + w[e]) {
+          sh.found = first + vec * E + e;
+          sh.found_mass = full_of(x[e]);
+        }
+        run += w[e];
+      }
     }
   }
   cluster.sync();
-  int found = -1;
-  for (int r = 0; r < ranks; ++r) {
-    const int f = *cluster.map_shared_rank(&sh.found, r);
-    if (f >= 0) {
-      found = f;
+  int found = -1, at[kMaxCluster];
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r) at[r] = *cluster.map_shared_rank(&sh.found, r < ranks ? r : 0);
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r)
+    if (r < ranks && at[r] >= 0) {
+      found = at[r];
       *mass = *cluster.map_shared_rank(&sh.found_mass, r);
     }
-  }
   cluster.sync();  // sh.total and sh.found may be written again
   return found;
 }
@@ -617,6 +746,47 @@ __device__ int locate(const S& slice, SampleShared& sh, u64* segs, cg::cluster_g
 // are among its n entries.
 __device__ void finish_list(SampleShared& sh, const Masses& mass, int n, int top_k, float top_p, u64 least, float u,
                             int* token, float* prob) {
+  if (n <= kThreads) {
+    // Without a sort: each entry adds up what comes before it, by rank, then
+    // by index.
+    const bool here = threadIdx.x < n;
+    const u64 mine = here ? sh.list[threadIdx.x] : 0;
+    int rank = 0;
+    if (here)
+      for (int i = 0; i < n; ++i) rank += sh.list[i] > mine;
+    u64 w = here && rank < top_k ? mass(value_of(static_cast<unsigned int>(mine >> 32))) : 0;
+    if (here) sh.mass[threadIdx.x] = w;
+    __syncthreads();
+    if (top_p < 1.0f) {
+      u64 before = 0, whole = 0;
+      if (here)
+        for (int i = 0; i < n; ++i) {
+          const u64 v = sh.mass[i];
+          whole += v;
+          before += sh.list[i] > mine ? v : 0;
+        }
+      const u64 target = times(whole, top_p, true);
+      if (before >= (target < 1 ? 1 : target)) w = 0;
+    }
+    if (rank > 0 && w < least) w = 0;
+    __syncthreads();
+    if (here) sh.mass[threadIdx.x] = w;
+    __syncthreads();
+    u64 before = 0, kept = 0;
+    if (here && w)
+      for (int i = 0; i < n; ++i) {
+        const u64 v = sh.mass[i];
+        kept += v;  // a lower index is a larger lower half
+        before += static_cast<unsigned int>(sh.list[i]) > static_cast<unsigned int>(mine) ? v : 0;
+      }
+    const u64 at = times(kept, u, false);
+    if (here && w && before <= at && at < before + w) {
+      *token = static_cast<int>(0xFFFFFFFFu - static_cast<unsigned int>(mine));
+      w = mass.high(value_of(static_cast<unsigned int>(mine >> 32)));  // (its probability is told to fp32 precision)
+      if (prob) *prob = static_cast<float>(static_cast<double>(w) / static_cast<double>(kept));
+    }
+    return;
+  }
   int size = 2;
   while (size < n) size <<= 1;
   for (int i = n + threadIdx.x; i < size; i += kThreads) sh.list[i] = 0;
@@ -653,14 +823,14 @@ __device__ void finish_list(SampleShared& sh, const Masses& mass, int n, int top
   const u64 kept = scan_list(sh, sh.mass, keep);
   if (threadIdx.x == 0) {
     const int at = below(sh.mass, keep, times(kept, u, false) + 1);  // the first sum above u times the whole
-    const u64 w = sh.mass[at] - (at ? sh.mass[at - 1] : 0);
+    const u64 w = mass.high(value_of(static_cast<unsigned int>(sh.list[at])));
     *token = static_cast<int>(0xFFFFFFFFu - static_cast<unsigned int>(sh.list[at] >> 32));
     if (prob) *prob = static_cast<float>(static_cast<double>(w) / static_cast<double>(kept));
   }
 }
 
 template <typename T, bool CACHED>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant__ SampleParams p) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleParams p) {
   extern __shared__ __align__(16) unsigned char dyn[];
   __shared__ SampleShared sh;
   cg::cluster_group cluster = cg::this_cluster();
@@ -670,10 +840,15 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
 
   Slice<T, CACHED> slice;
   const int per = p.slice;
-  const int first = min(rank * per, p.vocab);
-  slice.len = min(p.vocab - first, per);
+  // The slice takes per - pad logits: as many as fit behind a start that is
+  // not on 16 bytes.  `first` is the index of the vectors' first element.
+  const int begin = min(rank * (per - p.pad), p.vocab), len = min(p.vocab - begin, per - p.pad);
+  const T* const from = static_cast<const T*>(p.logits) + row * p.ld + begin;
+  const int shift = CACHED ? static_cast<int>(reinterpret_cast<uintptr_t>(from) % 16 / sizeof(T)) : 0;
+  const int first = begin - shift;
+  slice.len = len;
   slice.rounds = per / (kThreads * E);
-  slice.global = static_cast<const T*>(p.logits) + row * p.ld + first;
+  slice.global = from - shift;
   u64* segs = reinterpret_cast<u64*>(dyn);
   slice.cache = reinterpret_cast<T*>(dyn + static_cast<size_t>(slice.rounds) * kWarps * 8);
   if (threadIdx.x < 32) sh.pow[threadIdx.x] = kPow[threadIdx.x];
@@ -682,12 +857,30 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   float top = -INFINITY;
   unsigned int count = 0;
   if (CACHED) {
-    for (int i = threadIdx.x; i < per; i += kThreads) {
-      const T v = i < slice.len ? slice.global[i] : static_cast<T>(-INFINITY);
-      slice.cache[i] = v;
-      const float x = clean(raw_value<T>(v));
-      top = fmaxf(top, x);
-      count += x > -INFINITY;
+    // Vectors from the 16-byte boundary at or before the slice; what lies
+    // outside it counts as -inf.
+#pragma unroll 4
+    for (int v = threadIdx.x; v < per / E; v += kThreads) {
+      uint4 raw;
+      const int i0 = v * E - shift;  // of the slice
+      if (i0 >= 0 && i0 + E <= len) {
+        raw = *reinterpret_cast<const uint4*>(slice.global + v * E);
+      } else {
+        T part[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          part[e] = i0 + e >= 0 && i0 + e < len ? slice.global[v * E + e] : static_cast<T>(-INFINITY);
+        memcpy(&raw, part, 16);
+      }
+      reinterpret_cast<uint4*>(slice.cache)[v] = raw;
+      T part[E];
+      memcpy(part, &raw, 16);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float x = clean(raw_value<T>(part[e]));
+        top = fmaxf(top, x);
+        count += x > -INFINITY;
+      }
     }
   } else {
     slice.each([&](float x, int) {
@@ -759,7 +952,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     } else {
       if (top_k > 0 && static_cast<unsigned int>(top_k) < count) {
         const Threshold t = find_threshold<true>(
-            slice, sh, cluster, mass, scale, first, [](float x) -> u64 { return x > -INFINITY ? 1 : 0; },
+            slice, sh, cluster, mass, scale, first, [](float x) { return x > -INFINITY; },
             [&](u64) { return static_cast<u64>(top_k); });
         if (t.key == 0) {  // a short list: everything in the bins down to t.bin
           gather(slice, sh, cluster, first, [&](float x) {
@@ -779,7 +972,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         const u64 at_cut = ties ? mass(value_of(cut)) : 0;
         const Threshold t = find_threshold<false>(
             slice, sh, cluster, mass, scale, first,
-            [&](float x) -> u64 { return x > -INFINITY && key_of(x) > cut ? mass(x) : 0; },
+            [&](float x) { return x > -INFINITY && key_of(x) > cut; },
             [&](u64 all) {
               above = all;
               const u64 target = times(all + ties * at_cut, top_p, true);
@@ -803,24 +996,23 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     u64 chosen = 0, whole = 0;
     if (ties)  // the index of the last tie that is kept
       last = locate<false>(
-          slice, sh, segs, cluster, first, [&](float x, int) { return key_of(x) == cut; }, [](float) -> u64 { return 1; },
+          slice, sh, segs, cluster, first, -INFINITY, [&](float x, int) { return key_of(x) == cut; },
+          [](float) -> u64 { return 1; }, [](float) -> u64 { return 1; },
           [&](u64 all) -> u64 { return (ties < all ? ties : all) - 1; }, &chosen, &whole);
     if (greedy) {
       token = last;
       prob = 1.0f;
     } else {
       const u64 least = min_p > 0.0f ? times(kOne, min_p, true) : 0;
+      const float limit = cut ? value_of(cut) : -INFINITY, lowest = fmaxf(floor_x, limit);
       token = locate<true>(
-          slice, sh, segs, cluster, first,
-          [&](float x, int i) {
-            if (!(x > -INFINITY) || x < floor_x) return false;
-            const unsigned int k = key_of(x);
-            return k > cut || (k == cut && first + i <= last);
-          },
+          slice, sh, segs, cluster, first, lowest,
+          [&](float x, int i) { return x > lowest || (x == lowest && x > -INFINITY && (x > limit || first + i <= last)); },
           [&](float x) -> u64 {
             const u64 w = mass(x);
             return w >= least ? w : 0;
           },
+          [&](float x) -> u64 { return mass.high(x); },  // (its probability is told to fp32 precision)
           [&](u64 all) -> u64 { return times(all, u, false); },
           &chosen, &whole);
       if (threadIdx.x == 0) prob = static_cast<float>(static_cast<double>(chosen) / static_cast<double>(whole));
@@ -841,7 +1033,9 @@ cudaError_t launch_sample_of(SampleParams p, int num_sms, cudaStream_t stream) {
   while (ranks < kMaxCluster && static_cast<long long>(p.rows) * ranks * 2 <= 4ll * num_sms &&
          p.vocab > ranks * step)
     ranks *= 2;
-  auto slice_of = [&](int r) { return ((p.vocab + r - 1) / r + step - 1) / step * step; };
+  // rows on 16 bytes need no room in front
+  p.pad = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 && p.ld * sizeof(T) % 16 == 0 ? 0 : E;
+  auto slice_of = [&](int r) { return ((p.vocab + r - 1) / r + p.pad + step - 1) / step * step; };
   // enough CTAs that the slice fits in shared memory
   constexpr size_t most = 176 * 1024;
   while (ranks < kMaxCluster && static_cast<size_t>(slice_of(ranks)) * sizeof(T) > most) ranks *= 2;
