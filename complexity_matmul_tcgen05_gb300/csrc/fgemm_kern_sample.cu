@@ -74,6 +74,7 @@ struct SampleShared {
   u64 list[kList];              // the short list (rank 0): key, then the index from above
   u64 mass[kList];              // its masses; before, this CTA's part of the list
   u64 pow[32];
+  float powf[32];
   u64 warp64[kWarps];
   u64 warp64b[kWarps];
   u64 total;         // this CTA's sum, read by the others
@@ -109,6 +110,7 @@ __device__ __forceinline__ float value_of(unsigned int k) {
 struct Masses {
   float m, ch, cl;  // ch + cl = log2(e) / T
   const u64* pow;
+  const float* powf;  // 2^(j/32)
   // How small a mass is: y rounded, from which low() or high() goes on.
   __device__ __forceinline__ float size(float x) const { return x == m ? 0.0f : fmaf(x - m, ch, (x - m) * cl); }
   // A mass below 2^-14: fp32 is enough for its 30 bits (the error is below
@@ -117,13 +119,15 @@ struct Masses {
   __device__ __forceinline__ unsigned int low(float y) const {
     constexpr float magic = 12582912.0f;
     constexpr int magic_bits = 0x4B400000;
-    if (!(y > -46.0f)) return 0;
-    const float t = fmaf(y, 32.0f, magic);  // 32 y, rounded
+    // without branches, so that a thread's logits go through side by side
+    const float c = fminf(fmaxf(y, -46.0f), kSmall);
+    const float t = fmaf(c, 32.0f, magic);  // 32 y, rounded
     const int j = __float_as_int(t) - magic_bits;
-    const float z = fmaf(t - magic, -0.03125f, y) * 0.693147182464599609375f;
+    const float z = fmaf(t - magic, -0.03125f, c) * 0.693147182464599609375f;
     const float p = z * fmaf(z, fmaf(z, 1.0f / 6, 0.5f), 1.0f);
-    const float f = static_cast<float>(static_cast<unsigned int>(pow[j & 31] >> 14));  // 2^(j/32) in units of 2^-30
-    return __float2uint_rn(fmaf(f, p, f) * __int_as_float((14 + (j >> 5) + 127) << 23));
+    const float f = powf[j & 31];
+    const unsigned int w = __float2uint_rn(fmaf(f, p, f) * __int_as_float((44 + (j >> 5) + 127) << 23));
+    return y > -46.0f ? w : 0;
   }
   __device__ __forceinline__ u64 operator()(float x) const {
     const float y = size(x);
@@ -424,24 +428,28 @@ __device__ Threshold find_threshold(const S& slice, SampleShared& sh, cg::cluste
       for (int r = 0; r < slice.rounds; ++r) {
         float x[E];
         slice.get(r * kThreads + threadIdx.x, x);
-        int n = 0;
+        bool dense[E];  // its mass takes long: on full warps
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           const float y = mass.size(x[e]);
           const bool in = is_in(x[e]);
-          bool dense;
           if (few) {  // large masses into bins; small ones only into their sum
-            dense = in && y > Masses::kSmall;
-            if (in && !dense) rest += mass.low(y);
+            dense[e] = in && y > Masses::kSmall;
+            const unsigned int w = mass.low(y);
+            rest += in && !dense[e] ? w : 0;
           } else {
-            dense = in && y > -46.0f && bin_of(x[e]) >= 0;
+            dense[e] = in && y > -46.0f && bin_of(x[e]) >= 0;
           }
-          const unsigned int who = __ballot_sync(0xFFFFFFFFu, dense);
-          if (dense) room[n + __popc(who & ((1u << lane) - 1))] = x[e];
+        }
+        int n = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const unsigned int who = __ballot_sync(0xFFFFFFFFu, dense[e]);
+          if (dense[e]) room[n + __popc(who & ((1u << lane) - 1))] = x[e];
           n += __popc(who);
         }
         __syncwarp();
-        for (int i = lane; i < n; i += 32) {  // on full warps: a mass takes long
+        for (int i = lane; i < n; i += 32) {
           const float v = room[i];
           const int b = bin_of(v);
           const u64 w = mass(v);
@@ -455,10 +463,9 @@ __device__ Threshold find_threshold(const S& slice, SampleShared& sh, cg::cluste
         rest = warp_sum(rest);
         if (lane == 0) sh.warp64b[threadIdx.x >> 5] = rest;
         __syncthreads();
-        if (threadIdx.x == 0) {
-          rest = 0;
-          for (int w = 0; w < kWarps; ++w) rest += sh.warp64b[w];
-          sh.total = rest;
+        if (threadIdx.x < 32) {
+          rest = warp_sum(lane < kWarps ? sh.warp64b[lane] : 0);
+          if (lane == 0) sh.total = rest;
         }
       }
     }
@@ -663,11 +670,12 @@ __device__ int locate(const S& slice, SampleShared& sh, u64* segs, cg::cluster_g
   }
   if (lane == 0) sh.warp64[warp] = sum;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    u64 t = 0;
-    for (int w = 0; w < kWarps; ++w) t += sh.warp64[w];
-    sh.total = t;
-    sh.found = -1;
+  if (warp == 0) {
+    const u64 t = warp_sum(lane < kWarps ? sh.warp64[lane] : 0);
+    if (lane == 0) {
+      sh.total = t;
+      sh.found = -1;
+    }
   }
   cluster.sync();
   u64 all = 0, before = 0, own = 0, totals[kMaxCluster];
@@ -851,7 +859,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   slice.global = from - shift;
   u64* segs = reinterpret_cast<u64*>(dyn);
   slice.cache = reinterpret_cast<T*>(dyn + static_cast<size_t>(slice.rounds) * kWarps * 8);
-  if (threadIdx.x < 32) sh.pow[threadIdx.x] = kPow[threadIdx.x];
+  if (threadIdx.x < 32) {
+    sh.pow[threadIdx.x] = kPow[threadIdx.x];
+    sh.powf[threadIdx.x] = static_cast<float>(kPow[threadIdx.x]) * 0x1p-44f;
+  }
 
   // the slice into shared memory, its largest key and its candidates
   float top = -INFINITY;
@@ -933,6 +944,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     Masses mass;
     mass.m = m;
     mass.pow = sh.pow;
+    mass.powf = sh.powf;
     mass.ch = sh.ch;
     mass.cl = sh.cl;
     // logits below this have no mass, or less than min_p
