@@ -374,9 +374,11 @@ struct NormParams {
   long long m, ldx, ldr, ldt, ldy, ldq, lds;
   int n, mx_format, is_bf16;
   float eps;
-  int tpr, out_vec;      // set by the launch: threads a row, y or q takes whole-chunk stores
+  // set by the launch: threads a row, whether y or q takes whole-chunk stores,
+  // whether rows start behind a 16-byte boundary
+  int tpr, out_vec, shifted;
 };
-cudaError_t launch_norm(const NormParams& p, cudaStream_t stream);
+cudaError_t launch_norm(const NormParams& p, int num_sms, cudaStream_t stream);
 
 struct NormBackParams {
   const uint16_t* dy;
@@ -386,7 +388,7 @@ struct NormBackParams {
   const float* inv_rms;    // m entries
   uint16_t* dx;
   float* dgain;            // n entries, or null
-  float* partials;         // ctas x n, or null with dgain
+  float* partials;         // at most ctas x n, or null with dgain
   float* dots;             // m entries
   long long m, lddy, ldt, lddt, lddx;
   int n, is_bf16, ctas;    // ctas = norm_back_ctas(m, SMs)

@@ -66,14 +66,15 @@ __device__ __forceinline__ float elem(const Chunk<VEC>& c, int i) {
   return to_f32<BF16>((i & 1) ? c.w[i >> 1] >> 16 : c.w[i >> 1] & 0xFFFFu);
 }
 
-// The chunk at columns [c0, c0 + VEC) of a row; columns past n read as zero.
+// The chunk at columns [c0, c0 + VEC) of a row; columns outside [0, n) read as
+// zero.  row + c0 is on 16 bytes.
 template <int VEC>
 __device__ __forceinline__ void load_chunk(Chunk<VEC>& c, const uint16_t* row, int c0, int n) {
   if (VEC == 1) {
     c.w[0] = c0 < n ? row[c0] : 0u;
     return;
   }
-  if (c0 + VEC <= n) {
+  if (c0 >= 0 && c0 + VEC <= n) {
     const uint4 v = *reinterpret_cast<const uint4*>(row + c0);
     c.w[0] = v.x;
     c.w[1 % ((VEC + 1) / 2)] = v.y;
@@ -83,10 +84,34 @@ __device__ __forceinline__ void load_chunk(Chunk<VEC>& c, const uint16_t* row, i
   }
 #pragma unroll
   for (int i = 0; i < (VEC + 1) / 2; ++i) {
-    const uint32_t lo = c0 + 2 * i < n ? row[c0 + 2 * i] : 0u;
-    const uint32_t hi = c0 + 2 * i + 1 < n ? row[c0 + 2 * i + 1] : 0u;
+    const uint32_t lo = c0 + 2 * i >= 0 && c0 + 2 * i < n ? row[c0 + 2 * i] : 0u;
+    const uint32_t hi = c0 + 2 * i + 1 >= 0 && c0 + 2 * i + 1 < n ? row[c0 + 2 * i + 1] : 0u;
     c.w[i] = lo | (hi << 16);
   }
+}
+
+// The same of a vector that is on 16 bytes itself, at any c0.
+template <int VEC>
+__device__ __forceinline__ void load_chunk_any(Chunk<VEC>& c, const uint16_t* v, int c0, int n) {
+  if (VEC == 1 || (c0 & 7) == 0) {
+    load_chunk<VEC>(c, v, c0, n);
+    return;
+  }
+  if (c0 < 0 || c0 + 10 > n) {
+#pragma unroll
+    for (int i = 0; i < (VEC + 1) / 2; ++i) {
+      const uint32_t lo = c0 + 2 * i >= 0 && c0 + 2 * i < n ? v[c0 + 2 * i] : 0u;
+      const uint32_t hi = c0 + 2 * i + 1 >= 0 && c0 + 2 * i + 1 < n ? v[c0 + 2 * i + 1] : 0u;
+      c.w[i] = lo | (hi << 16);
+    }
+    return;
+  }
+  const uint32_t* const w = reinterpret_cast<const uint32_t*>(v) + (c0 >> 1);
+  uint32_t x[5];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) x[i] = w[i];
+#pragma unroll
+  for (int i = 0; i < (VEC + 1) / 2; ++i) c.w[i] = __funnelshift_r(x[i], x[i + 1], (c0 & 1) * 16);
 }
 
 template <int VEC>
@@ -95,14 +120,14 @@ __device__ __forceinline__ void store_chunk(const Chunk<VEC>& c, uint16_t* row, 
     if (c0 < n) row[c0] = static_cast<uint16_t>(c.w[0]);
     return;
   }
-  if (vec && c0 + VEC <= n) {
+  if (vec && c0 >= 0 && c0 + VEC <= n) {
     *reinterpret_cast<uint4*>(row + c0) =
         make_uint4(c.w[0], c.w[1 % ((VEC + 1) / 2)], c.w[2 % ((VEC + 1) / 2)], c.w[3 % ((VEC + 1) / 2)]);
     return;
   }
 #pragma unroll
   for (int i = 0; i < VEC; ++i)
-    if (c0 + i < n) row[c0 + i] = static_cast<uint16_t>(c.w[i >> 1] >> (16 * (i & 1)));
+    if (c0 + i >= 0 && c0 + i < n) row[c0 + i] = static_cast<uint16_t>(c.w[i >> 1] >> (16 * (i & 1)));
 }
 
 // Sum over the tpr threads of a row; every one of them gets it.  tpr is 32
@@ -161,7 +186,7 @@ template <bool BF16, int VEC, bool MX>
 __device__ __forceinline__ void finish_chunk(const NormParams& p, const Chunk<VEC>& t, float r, long long row,
                                              int c0) {
   Chunk<VEC> g;
-  load_chunk<VEC>(g, p.gain, c0, p.n);
+  load_chunk_any<VEC>(g, p.gain, c0, p.n);
   float y[VEC];
 #pragma unroll
   for (int i = 0; i < VEC; ++i) y[i] = elem<BF16, VEC>(t, i) * r * elem<BF16, VEC>(g, i);
@@ -196,20 +221,22 @@ __device__ __forceinline__ void total_chunk(const NormParams& p, Chunk<VEC>& t, 
 
 // One row on tpr = blockDim.x / rows_per_cta threads, VPT chunks a thread in
 // registers.
-template <bool BF16, int VEC, int VPT, bool MX>
-__global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ NormParams p) {
+template <bool BF16, int VEC, int VPT, bool MX, int MAXT>
+__global__ void __launch_bounds__(MAXT) norm_kernel(const __grid_constant__ NormParams p) {
   __shared__ float red[32];
   const int tpr = p.tpr;
   const long long row = static_cast<long long>(blockIdx.x) * (blockDim.x / tpr) + threadIdx.x / tpr;
   if (row >= p.m) return;  // whole warps (tpr 32) or the whole CTA
   const int lane = threadIdx.x % tpr;
+  // rows that do not start on 16 bytes: chunks from the boundary before them
+  const int shift = VEC == 1 ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(p.x + row * p.ldx) % 16 / 2);
   Chunk<VEC> t[VPT];
   float sum = 0.0f;
 #pragma unroll
-  for (int v = 0; v < VPT; ++v) total_chunk<BF16, VEC>(p, t[v], row, (v * tpr + lane) * VEC);
+  for (int v = 0; v < VPT; ++v) total_chunk<BF16, VEC>(p, t[v], row, (v * tpr + lane) * VEC - shift);
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
-    const int c0 = (v * tpr + lane) * VEC;
+    const int c0 = (v * tpr + lane) * VEC - shift;
     if (p.total) store_chunk<VEC>(t[v], p.total + row * p.ldt, c0, p.n);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
@@ -220,10 +247,23 @@ __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ Norm
   sum = row_sum(sum, tpr, red);
   const float r = 1.0f / sqrtf(sum / static_cast<float>(p.n) + p.eps);
   if (lane == 0 && p.inv_rms) p.inv_rms[row] = r;
+  if (MX && p.shifted) {  // chunks would straddle blocks of 32: element by element
+    __syncwarp();  // the row's total, stored above by other threads (a CTA's row: the sum's barrier)
+    for (int c0 = lane & ~31; c0 < p.n; c0 += tpr) {
+      const int c = c0 + (lane & 31) < p.n ? c0 + (lane & 31) : p.n;
+      Chunk<1> one;
+      if (p.total)
+        load_chunk<1>(one, p.total + row * p.ldt, c, p.n);
+      else
+        total_chunk<BF16, 1>(p, one, row, c);
+      finish_chunk<BF16, 1, MX>(p, one, r, row, c);
+    }
+    return;
+  }
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
-    const int c0 = (v * tpr + lane) * VEC;
-    if ((v * tpr + (lane & ~31)) * VEC < p.n)  // whole warps: a block's lanes stay together
+    const int c0 = (v * tpr + lane) * VEC - shift;
+    if ((v * tpr + (lane & ~31)) * VEC - shift < p.n)  // whole warps: a block's lanes stay together
       finish_chunk<BF16, VEC, MX>(p, t[v], r, row, c0);
   }
 }
@@ -261,52 +301,64 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const __grid_constant__
   }
 }
 
-// Backward.  CTA b takes rows b, b + gridDim.x, ...; a thread keeps the
-// gain's gradient of its columns over them in registers and stores it to row
-// b of the partials, which norm_dgain_kernel adds up in row order, so that
-// results do not depend on which CTA ends first.
+// Backward.  CTA b takes rows b, b + gridDim.x, ..., the next row's loads on
+// their way while a row is reduced and written; a thread keeps the gain's
+// gradient of its columns over them in registers and stores it to row b of the
+// partials, which norm_dgain_kernel adds up in row order, so that results do
+// not depend on which CTA ends first.  (Clusters that add theirs up first were
+// slower: 304 CTAs in clusters of 8 do not fit the GPCs at once, 90 us for
+// 8192 x 4096.)
 template <bool BF16, int VEC, int VPT, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_back_kernel(const __grid_constant__ NormBackParams p) {
   __shared__ float red[2][32];
   const int tpr = blockDim.x;
   float dg[VPT][VEC];
-  Chunk<VEC> g[VPT];
+  Chunk<VEC> g[VPT], t[VPT], dy[VPT];
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     load_chunk<VEC>(g[v], p.gain, (v * tpr + threadIdx.x) * VEC, p.n);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) dg[v][i] = 0.0f;
   }
-  int side = 0;
-  for (long long row = blockIdx.x; row < p.m; row += gridDim.x, side ^= 1) {
-    Chunk<VEC> t[VPT], dy[VPT], dt[VPT];
+  float r = 0.0f;
+  auto fetch = [&](long long row) {
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int c0 = (v * tpr + threadIdx.x) * VEC;
       load_chunk<VEC>(t[v], p.total + row * p.ldt, c0, p.n);
       load_chunk<VEC>(dy[v], p.dy + row * p.lddy, c0, p.n);
-      if (p.dtotal) load_chunk<VEC>(dt[v], p.dtotal + row * p.lddt, c0, p.n);
     }
-    const float r = p.inv_rms[row];
-    float dot = 0.0f;
+    r = p.inv_rms[row];
+  };
+  int side = 0;
+  if (blockIdx.x < p.m) fetch(blockIdx.x);
+  for (long long row = blockIdx.x; row < p.m; row += gridDim.x, side ^= 1) {
+    Chunk<VEC> dt[VPT];
+    if (p.dtotal)
+#pragma unroll
+      for (int v = 0; v < VPT; ++v)
+        load_chunk<VEC>(dt[v], p.dtotal + row * p.lddt, (v * tpr + threadIdx.x) * VEC, p.n);
+    float u[VPT][VEC], a[VPT][VEC], dot = 0.0f;
+    const float rr = r;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        const float u = elem<BF16, VEC>(t[v], i) * r, d = elem<BF16, VEC>(dy[v], i);
-        dot = fmaf(d * elem<BF16, VEC>(g[v], i), u, dot);
-        dg[v][i] = fmaf(d, u, dg[v][i]);
+        const float d = elem<BF16, VEC>(dy[v], i);
+        u[v][i] = elem<BF16, VEC>(t[v], i) * rr;
+        a[v][i] = d * elem<BF16, VEC>(g[v], i);
+        dot = fmaf(a[v][i], u[v][i], dot);
+        dg[v][i] = fmaf(d, u[v][i], dg[v][i]);
       }
     }
+    if (row + gridDim.x < p.m) fetch(row + gridDim.x);
     dot = row_sum(dot, tpr, red[side]) / static_cast<float>(p.n);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       float o[VEC];
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        const float u = elem<BF16, VEC>(t[v], i) * r;
-        const float a = elem<BF16, VEC>(dy[v], i) * elem<BF16, VEC>(g[v], i);
-        o[i] = r * fmaf(-u, dot, a);
+        o[i] = rr * fmaf(-u[v][i], dot, a[v][i]);
         if (p.dtotal) o[i] += elem<BF16, VEC>(dt[v], i);
       }
       Chunk<VEC> c;
@@ -386,24 +438,30 @@ bool aligned16(const void* p, long long ld) {
 }
 
 template <bool BF16, int VEC, bool MX>
-cudaError_t launch_fwd(NormParams p, cudaStream_t stream) {
-  const int chunks = (p.n + VEC - 1) / VEC;
-  if (chunks <= 128) {  // a warp a row, four rows a CTA
+cudaError_t launch_fwd(NormParams p, int num_sms, cudaStream_t stream) {
+  const int chunks = (p.n + VEC - 1) / VEC + (p.shifted ? 1 : 0);
+  const bool many = p.m >= 16ll * num_sms;  // rows enough that each need not be quick
+  if (chunks <= 128 || (many && chunks <= 256)) {  // a warp a row, four rows a CTA
     p.tpr = 32;
     const unsigned grid = static_cast<unsigned>((p.m + 3) / 4);
     if (chunks <= 32)
-      norm_kernel<BF16, VEC, 1, MX><<<grid, 128, 0, stream>>>(p);
+      norm_kernel<BF16, VEC, 1, MX, 128><<<grid, 128, 0, stream>>>(p);
+    else if (chunks <= 128)
+      norm_kernel<BF16, VEC, 4, MX, 128><<<grid, 128, 0, stream>>>(p);
     else
-      norm_kernel<BF16, VEC, 4, MX><<<grid, 128, 0, stream>>>(p);
+      norm_kernel<BF16, VEC, 8, MX, 128><<<grid, 128, 0, stream>>>(p);
     return cudaGetLastError();
   }
   const unsigned grid = static_cast<unsigned>(p.m);
-  if (chunks <= 2048) {
+  if (many && chunks <= 1024) {
+    p.tpr = (chunks + 127) / 128 * 32;
+    norm_kernel<BF16, VEC, 4, MX, 256><<<grid, p.tpr, 0, stream>>>(p);
+  } else if (chunks <= 2048) {
     p.tpr = (chunks + 63) / 64 * 32;
-    norm_kernel<BF16, VEC, 2, MX><<<grid, p.tpr, 0, stream>>>(p);
+    norm_kernel<BF16, VEC, 2, MX, 1024><<<grid, p.tpr, 0, stream>>>(p);
   } else if (chunks <= 8192) {
     p.tpr = (chunks + 255) / 256 * 32;
-    norm_kernel<BF16, VEC, 8, MX><<<grid, p.tpr, 0, stream>>>(p);
+    norm_kernel<BF16, VEC, 8, MX, 1024><<<grid, p.tpr, 0, stream>>>(p);
   } else {
     norm_long_kernel<BF16, VEC, MX><<<grid, 1024, 0, stream>>>(p);
   }
@@ -411,14 +469,23 @@ cudaError_t launch_fwd(NormParams p, cudaStream_t stream) {
 }
 
 template <bool BF16>
-cudaError_t launch_fwd_of(NormParams p, cudaStream_t stream) {
-  // The output's alignment only decides how it is stored, so that both forms
-  // of it come from the same sums.
+cudaError_t launch_fwd_of(NormParams p, int num_sms, cudaStream_t stream) {
+  // The output's form and alignment only decide how it is stored: every form
+  // comes from the same sums.
   const bool vec = aligned16(p.x, p.ldx) && aligned16(p.gain, 0) && (!p.res || aligned16(p.res, p.ldr)) &&
                    (!p.total || aligned16(p.total, p.ldt));
-  p.out_vec = p.q ? reinterpret_cast<uintptr_t>(p.q) % 8 == 0 && p.ldq % 8 == 0 : aligned16(p.y, p.ldy);
-  if (p.q) return vec ? launch_fwd<BF16, 8, true>(p, stream) : launch_fwd<BF16, 1, true>(p, stream);
-  return vec ? launch_fwd<BF16, 8, false>(p, stream) : launch_fwd<BF16, 1, false>(p, stream);
+  // Rows that all start equally far behind a 16-byte boundary: chunks from
+  // there (f16, 1537 x 5127: 19.4 us element by element).
+  auto like_x = [&](const void* a, long long ld) {
+    return reinterpret_cast<uintptr_t>(a) % 16 == reinterpret_cast<uintptr_t>(p.x) % 16 && (ld - p.ldx) % 8 == 0;
+  };
+  p.shifted = !vec && p.n <= 65528 && aligned16(p.gain, 0) && (!p.res || like_x(p.res, p.ldr)) &&
+              (!p.total || like_x(p.total, p.ldt));
+  p.out_vec = p.q ? reinterpret_cast<uintptr_t>(p.q) % 8 == 0 && p.ldq % 8 == 0
+                  : p.shifted ? like_x(p.y, p.ldy) : aligned16(p.y, p.ldy);
+  if (p.q)
+    return vec || p.shifted ? launch_fwd<BF16, 8, true>(p, num_sms, stream) : launch_fwd<BF16, 1, true>(p, num_sms, stream);
+  return vec || p.shifted ? launch_fwd<BF16, 8, false>(p, num_sms, stream) : launch_fwd<BF16, 1, false>(p, num_sms, stream);
 }
 
 // Columns a row of the register kernel may have.
@@ -429,30 +496,32 @@ bool back_vec(const NormBackParams& p) {
          (!p.dtotal || aligned16(p.dtotal, p.lddt));
 }
 
+template <bool BF16, int VEC, int VPT, int MAXT>
+cudaError_t launch_back_regs(const NormBackParams& p, cudaStream_t stream) {
+  const int chunks = (p.n + VEC - 1) / VEC;
+  norm_back_kernel<BF16, VEC, VPT, MAXT>
+      <<<static_cast<unsigned>(p.ctas), static_cast<unsigned>((chunks + 32 * VPT - 1) / (32 * VPT) * 32), 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
 template <bool BF16>
 cudaError_t launch_back(const NormBackParams& p, cudaStream_t stream) {
   const bool vec = back_vec(p);
-  const unsigned grid = static_cast<unsigned>(p.ctas);
+  cudaError_t e;
   if (vec && p.n <= kBackRegs16) {
-    const int chunks = (p.n + 7) / 8;
-    if (chunks <= 512)
-      norm_back_kernel<BF16, 8, 1, 512><<<grid, (chunks + 31) / 32 * 32, 0, stream>>>(p);
-    else if (chunks <= 1024)
-      norm_back_kernel<BF16, 8, 2, 512><<<grid, (chunks + 63) / 64 * 32, 0, stream>>>(p);
-    else
-      norm_back_kernel<BF16, 8, 4, 512><<<grid, (chunks + 127) / 128 * 32, 0, stream>>>(p);
+    e = p.n <= 4096   ? launch_back_regs<BF16, 8, 1, 512>(p, stream)
+        : p.n <= 8192 ? launch_back_regs<BF16, 8, 2, 512>(p, stream)
+                      : launch_back_regs<BF16, 8, 4, 512>(p, stream);
   } else if (!vec && p.n <= kBackRegs2) {
-    if (p.n <= 1024)
-      norm_back_kernel<BF16, 1, 1, 1024><<<grid, (p.n + 31) / 32 * 32, 0, stream>>>(p);
-    else
-      norm_back_kernel<BF16, 1, 8, 1024><<<grid, (p.n + 255) / 256 * 32, 0, stream>>>(p);
+    e = p.n <= 1024 ? launch_back_regs<BF16, 1, 1, 1024>(p, stream) : launch_back_regs<BF16, 1, 8, 1024>(p, stream);
   } else {
     norm_back_dot_kernel<BF16><<<static_cast<unsigned>(p.m), 1024, 0, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    norm_back_cols_kernel<BF16><<<dim3(static_cast<unsigned>((p.n + 255) / 256), grid), 256, 0, stream>>>(p);
+    norm_back_cols_kernel<BF16><<<dim3(static_cast<unsigned>((p.n + 255) / 256), static_cast<unsigned>(p.ctas)), 256, 0,
+                                  stream>>>(p);
+    e = cudaGetLastError();
   }
-  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !p.partials) return e;
   norm_dgain_kernel<<<static_cast<unsigned>((p.n + 31) / 32), 1024, 0, stream>>>(p.partials, p.ctas, p.n, p.dgain);
   return cudaGetLastError();
@@ -460,12 +529,13 @@ cudaError_t launch_back(const NormBackParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_norm(const NormParams& p, cudaStream_t stream) {
-  return p.is_bf16 ? launch_fwd_of<true>(p, stream) : launch_fwd_of<false>(p, stream);
+cudaError_t launch_norm(const NormParams& p, int num_sms, cudaStream_t stream) {
+  return p.is_bf16 ? launch_fwd_of<true>(p, num_sms, stream) : launch_fwd_of<false>(p, num_sms, stream);
 }
 
 int norm_back_ctas(long long m, int num_sms) {
-  const long long most = 2ll * num_sms;
+  // two CTAs an SM; of few rows one, or the partials outweigh the rows
+  const long long most = m >= 8ll * num_sms ? 2ll * num_sms : num_sms;
   return static_cast<int>(m < most ? m : most);
 }
 
