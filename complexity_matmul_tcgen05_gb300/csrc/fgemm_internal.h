@@ -378,7 +378,7 @@ struct NormParams {
   // whether rows start behind a 16-byte boundary
   int tpr, out_vec, shifted;
 };
-cudaError_t launch_norm(const NormParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_norm(const NormParams& p, cudaStream_t stream);
 
 struct NormBackParams {
   const uint16_t* dy;
@@ -391,9 +391,9 @@ struct NormBackParams {
   float* partials;         // at most ctas x n, or null with dgain
   float* dots;             // m entries
   long long m, lddy, ldt, lddt, lddx;
-  int n, is_bf16, ctas;    // ctas = norm_back_ctas(m, SMs)
+  int n, is_bf16, ctas;    // ctas = norm_back_ctas(m, n, SMs)
 };
-int norm_back_ctas(long long m, int num_sms);
+int norm_back_ctas(long long m, int n, int num_sms);
 size_t norm_back_workspace(long long m, int n, int num_sms);
 cudaError_t launch_norm_back(const NormBackParams& p, cudaStream_t stream);
 

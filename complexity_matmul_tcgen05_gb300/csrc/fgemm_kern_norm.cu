@@ -308,9 +308,10 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const __grid_constant__
 // not depend on which CTA ends first.  (Clusters that add theirs up first were
 // slower: 304 CTAs in clusters of 8 do not fit the GPCs at once, 90 us for
 // 8192 x 4096.)
-template <bool BF16, int VEC, int VPT, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_back_kernel(const __grid_constant__ NormBackParams p) {
+template <bool BF16, int VEC, int VPT, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) norm_back_kernel(const __grid_constant__ NormBackParams p) {
   __shared__ float red[2][32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tpr = blockDim.x;
   float dg[VPT][VEC];
   Chunk<VEC> g[VPT], t[VPT], dy[VPT];
@@ -330,35 +331,35 @@ __global__ void __launch_bounds__(MAXT) norm_back_kernel(const __grid_constant__
     }
     r = p.inv_rms[row];
   };
+  const float inv_n = 1.0f / static_cast<float>(p.n);
   int side = 0;
   if (blockIdx.x < p.m) fetch(blockIdx.x);
   for (long long row = blockIdx.x; row < p.m; row += gridDim.x, side ^= 1) {
-    Chunk<VEC> dt[VPT];
-    if (p.dtotal)
-#pragma unroll
-      for (int v = 0; v < VPT; ++v)
-        load_chunk<VEC>(dt[v], p.dtotal + row * p.lddt, (v * tpr + threadIdx.x) * VEC, p.n);
-    float u[VPT][VEC], a[VPT][VEC], dot = 0.0f;
+    Chunk<VEC> dt[VPT], tc[VPT], dc[VPT];  // this row's
+    float dot = 0.0f;
     const float rr = r;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
+      if (p.dtotal) load_chunk<VEC>(dt[v], p.dtotal + row * p.lddt, (v * tpr + threadIdx.x) * VEC, p.n);
+      tc[v] = t[v];
+      dc[v] = dy[v];
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        const float d = elem<BF16, VEC>(dy[v], i);
-        u[v][i] = elem<BF16, VEC>(t[v], i) * rr;
-        a[v][i] = d * elem<BF16, VEC>(g[v], i);
-        dot = fmaf(a[v][i], u[v][i], dot);
-        dg[v][i] = fmaf(d, u[v][i], dg[v][i]);
+        const float u = elem<BF16, VEC>(tc[v], i) * rr, d = elem<BF16, VEC>(dc[v], i);
+        dot = fmaf(d * elem<BF16, VEC>(g[v], i), u, dot);
+        dg[v][i] = fmaf(d, u, dg[v][i]);
       }
     }
     if (row + gridDim.x < p.m) fetch(row + gridDim.x);
-    dot = row_sum(dot, tpr, red[side]) / static_cast<float>(p.n);
+    dot = row_sum(dot, tpr, red[side]) * inv_n;
+    const float rd = rr * rr * dot;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       float o[VEC];
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        o[i] = rr * fmaf(-u[v][i], dot, a[v][i]);
+        // r (a - u mean(a u)) with u = t r
+        o[i] = fmaf(-elem<BF16, VEC>(tc[v], i), rd, rr * (elem<BF16, VEC>(dc[v], i) * elem<BF16, VEC>(g[v], i)));
         if (p.dtotal) o[i] += elem<BF16, VEC>(dt[v], i);
       }
       Chunk<VEC> c;
@@ -384,10 +385,12 @@ __global__ void __launch_bounds__(MAXT) norm_back_kernel(const __grid_constant__
 // the slices in order.
 __global__ void __launch_bounds__(1024) norm_dgain_kernel(const float* partials, int rows, int n, float* dgain) {
   __shared__ float part[32][33];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // for the partials
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.0f;
   if (c < n)
+#pragma unroll 8
     for (int r = warp; r < rows; r += 32) s += partials[static_cast<long long>(r) * n + c];
   part[warp][lane] = s;
   __syncthreads();
@@ -438,25 +441,20 @@ bool aligned16(const void* p, long long ld) {
 }
 
 template <bool BF16, int VEC, bool MX>
-cudaError_t launch_fwd(NormParams p, int num_sms, cudaStream_t stream) {
+cudaError_t launch_fwd(NormParams p, cudaStream_t stream) {
   const int chunks = (p.n + VEC - 1) / VEC + (p.shifted ? 1 : 0);
-  const bool many = p.m >= 16ll * num_sms;  // rows enough that each need not be quick
-  if (chunks <= 128 || (many && chunks <= 256)) {  // a warp a row, four rows a CTA
+  if (chunks <= 128) {  // a warp a row, four rows a CTA
     p.tpr = 32;
     const unsigned grid = static_cast<unsigned>((p.m + 3) / 4);
     if (chunks <= 32)
       norm_kernel<BF16, VEC, 1, MX, 128><<<grid, 128, 0, stream>>>(p);
-    else if (chunks <= 128)
-      norm_kernel<BF16, VEC, 4, MX, 128><<<grid, 128, 0, stream>>>(p);
     else
-      norm_kernel<BF16, VEC, 8, MX, 128><<<grid, 128, 0, stream>>>(p);
+      norm_kernel<BF16, VEC, 4, MX, 128><<<grid, 128, 0, stream>>>(p);
     return cudaGetLastError();
   }
   const unsigned grid = static_cast<unsigned>(p.m);
-  if (many && chunks <= 1024) {
-    p.tpr = (chunks + 127) / 128 * 32;
-    norm_kernel<BF16, VEC, 4, MX, 256><<<grid, p.tpr, 0, stream>>>(p);
-  } else if (chunks <= 2048) {
+  // 8192 x 4096 to 8 bits: two chunks a thread 43.3 us, four 44.4, eight 56.5
+  if (chunks <= 2048) {
     p.tpr = (chunks + 63) / 64 * 32;
     norm_kernel<BF16, VEC, 2, MX, 1024><<<grid, p.tpr, 0, stream>>>(p);
   } else if (chunks <= 8192) {
@@ -469,7 +467,7 @@ cudaError_t launch_fwd(NormParams p, int num_sms, cudaStream_t stream) {
 }
 
 template <bool BF16>
-cudaError_t launch_fwd_of(NormParams p, int num_sms, cudaStream_t stream) {
+cudaError_t launch_fwd_of(NormParams p, cudaStream_t stream) {
   // The output's form and alignment only decide how it is stored: every form
   // comes from the same sums.
   const bool vec = aligned16(p.x, p.ldx) && aligned16(p.gain, 0) && (!p.res || aligned16(p.res, p.ldr)) &&
@@ -484,8 +482,8 @@ cudaError_t launch_fwd_of(NormParams p, int num_sms, cudaStream_t stream) {
   p.out_vec = p.q ? reinterpret_cast<uintptr_t>(p.q) % 8 == 0 && p.ldq % 8 == 0
                   : p.shifted ? like_x(p.y, p.ldy) : aligned16(p.y, p.ldy);
   if (p.q)
-    return vec || p.shifted ? launch_fwd<BF16, 8, true>(p, num_sms, stream) : launch_fwd<BF16, 1, true>(p, num_sms, stream);
-  return vec || p.shifted ? launch_fwd<BF16, 8, false>(p, num_sms, stream) : launch_fwd<BF16, 1, false>(p, num_sms, stream);
+    return vec || p.shifted ? launch_fwd<BF16, 8, true>(p, stream) : launch_fwd<BF16, 1, true>(p, stream);
+  return vec || p.shifted ? launch_fwd<BF16, 8, false>(p, stream) : launch_fwd<BF16, 1, false>(p, stream);
 }
 
 // Columns a row of the register kernel may have.
@@ -496,10 +494,10 @@ bool back_vec(const NormBackParams& p) {
          (!p.dtotal || aligned16(p.dtotal, p.lddt));
 }
 
-template <bool BF16, int VEC, int VPT, int MAXT>
+template <bool BF16, int VEC, int VPT, int MAXT, int MINB>
 cudaError_t launch_back_regs(const NormBackParams& p, cudaStream_t stream) {
   const int chunks = (p.n + VEC - 1) / VEC;
-  norm_back_kernel<BF16, VEC, VPT, MAXT>
+  norm_back_kernel<BF16, VEC, VPT, MAXT, MINB>
       <<<static_cast<unsigned>(p.ctas), static_cast<unsigned>((chunks + 32 * VPT - 1) / (32 * VPT) * 32), 0, stream>>>(p);
   return cudaGetLastError();
 }
@@ -509,11 +507,13 @@ cudaError_t launch_back(const NormBackParams& p, cudaStream_t stream) {
   const bool vec = back_vec(p);
   cudaError_t e;
   if (vec && p.n <= kBackRegs16) {
-    e = p.n <= 4096   ? launch_back_regs<BF16, 8, 1, 512>(p, stream)
-        : p.n <= 8192 ? launch_back_regs<BF16, 8, 2, 512>(p, stream)
-                      : launch_back_regs<BF16, 8, 4, 512>(p, stream);
+    e = p.n <= 2048   ? launch_back_regs<BF16, 8, 1, 256, 4>(p, stream)
+        : p.n <= 4096 ? launch_back_regs<BF16, 8, 1, 512, 2>(p, stream)
+        : p.n <= 8192 ? launch_back_regs<BF16, 8, 2, 512, 1>(p, stream)
+                      : launch_back_regs<BF16, 8, 4, 512, 1>(p, stream);
   } else if (!vec && p.n <= kBackRegs2) {
-    e = p.n <= 1024 ? launch_back_regs<BF16, 1, 1, 1024>(p, stream) : launch_back_regs<BF16, 1, 8, 1024>(p, stream);
+    e = p.n <= 1024 ? launch_back_regs<BF16, 1, 1, 1024, 1>(p, stream)
+                    : launch_back_regs<BF16, 1, 8, 1024, 1>(p, stream);
   } else {
     norm_back_dot_kernel<BF16><<<static_cast<unsigned>(p.m), 1024, 0, stream>>>(p);
     e = cudaGetLastError();
@@ -523,25 +523,34 @@ cudaError_t launch_back(const NormBackParams& p, cudaStream_t stream) {
     e = cudaGetLastError();
   }
   if (e != cudaSuccess || !p.partials) return e;
-  norm_dgain_kernel<<<static_cast<unsigned>((p.n + 31) / 32), 1024, 0, stream>>>(p.partials, p.ctas, p.n, p.dgain);
-  return cudaGetLastError();
+  // launched while the rows are still worked on; it waits for their end
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((p.n + 31) / 32));
+  cfg.blockDim = dim3(1024);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, norm_dgain_kernel, static_cast<const float*>(p.partials), p.ctas, p.n, p.dgain);
 }
 
 }  // namespace
 
-cudaError_t launch_norm(const NormParams& p, int num_sms, cudaStream_t stream) {
-  return p.is_bf16 ? launch_fwd_of<true>(p, num_sms, stream) : launch_fwd_of<false>(p, num_sms, stream);
+cudaError_t launch_norm(const NormParams& p, cudaStream_t stream) {
+  return p.is_bf16 ? launch_fwd_of<true>(p, stream) : launch_fwd_of<false>(p, stream);
 }
 
-int norm_back_ctas(long long m, int num_sms) {
-  // two CTAs an SM; of few rows one, or the partials outweigh the rows
-  const long long most = m >= 8ll * num_sms ? 2ll * num_sms : num_sms;
+int norm_back_ctas(long long m, int n, int num_sms) {
+  // as many as are resident; of few rows one an SM, or the partials outweigh the rows
+  const long long most = m >= 8ll * num_sms ? (n <= 4096 ? 2ll : 1ll) * num_sms : num_sms;
   return static_cast<int>(m < most ? m : most);
 }
 
 size_t norm_back_workspace(long long m, int n, int num_sms) {
   // the partials of the gain's gradient, then each row's mean
-  return (static_cast<size_t>(norm_back_ctas(m, num_sms)) * static_cast<size_t>(n) + static_cast<size_t>(m)) *
+  return (static_cast<size_t>(norm_back_ctas(m, n, num_sms)) * static_cast<size_t>(n) + static_cast<size_t>(m)) *
          sizeof(float);
 }
 

@@ -77,7 +77,7 @@ fgemm_status_t fgemm_rms_norm(fgemm_handle_t h, int64_t M, int64_t N, const void
   if (!h) return no_handle();
   p.y = static_cast<uint16_t*>(y);
   p.ldy = ldy;
-  return launched(h, fgemm::launch_norm(p, fgemm::handle_sms(h), fgemm::handle_stream(h)));
+  return launched(h, fgemm::launch_norm(p, fgemm::handle_stream(h)));
 }
 
 fgemm_status_t fgemm_rms_norm_mx(fgemm_handle_t h, int64_t M, int64_t N, const void* x, int64_t ldx,
@@ -98,7 +98,7 @@ fgemm_status_t fgemm_rms_norm_mx(fgemm_handle_t h, int64_t M, int64_t N, const v
   p.scales = static_cast<uint8_t*>(scales);
   p.lds = lds;
   p.mx_format = format;
-  return launched(h, fgemm::launch_norm(p, fgemm::handle_sms(h), fgemm::handle_stream(h)));
+  return launched(h, fgemm::launch_norm(p, fgemm::handle_stream(h)));
 }
 
 size_t fgemm_rms_norm_backward_workspace(fgemm_handle_t h, int64_t M, int64_t N) {
@@ -143,7 +143,7 @@ fgemm_status_t fgemm_rms_norm_backward(fgemm_handle_t h, int64_t M, int64_t N, c
   p.lddt = lddt;
   p.lddx = lddx;
   p.is_bf16 = dtype == FGEMM_BF16;
-  p.ctas = fgemm::norm_back_ctas(M, sms);
+  p.ctas = fgemm::norm_back_ctas(M, static_cast<int>(N), sms);
   p.partials = dgain ? static_cast<float*>(workspace) : nullptr;
   p.dots = static_cast<float*>(workspace) + static_cast<size_t>(p.ctas) * static_cast<size_t>(N);
   return launched(h, fgemm::launch_norm_back(p, fgemm::handle_stream(h)));
