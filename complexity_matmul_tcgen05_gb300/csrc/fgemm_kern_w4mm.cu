@@ -20,8 +20,8 @@
 // may begin before the pre-pass ends (programmatic dependent launch): its
 // codes are on their way by then.
 //
-// Roles: warp 0 TMA, warp 1 MMA issue, warps 4.. expand the codes, the last 4
-// or 8 warps fold.  Every wait is bounded; a wait that runs out latches the
+// Roles: warp 0 loads the codes, warp 2 A, warp 1 issues the MMAs, warps 4.. expand
+// the codes, the last 4 or 8 warps fold.  Every wait is bounded; a wait that runs out latches the
 // error word and all roles leave.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -40,23 +40,30 @@ namespace {
 constexpr int kRows = 128;   // rows of W of a tile
 constexpr int kBlock = 128;  // k of one pipeline step: 64 bytes of codes a row
 constexpr int kThreads = 512;
-constexpr int kAStages = 4;        // operand stages in tensor memory, 64 columns each
 constexpr int kCodeBytes = kRows * 64;
 
-template <int MT>
+// Most rows of A a tile takes: the accumulators of a step's groups and the
+// expanded codes of at least two steps fit in tensor memory.
+constexpr int kMostRows[3] = {32, 64, 128};  // groups of 32, 64, 128
+
+template <int MT, int GROUPS>  // groups of a step
 struct Cfg {
-  static constexpr int kFoldWarps = MT == 128 ? 8 : 4;
+  static constexpr int kFoldWarps = MT >= 64 ? 8 : 4;
+  static constexpr int kCols = MT == 128 ? 64 : MT < 32 ? MT : 32;  // of A's rows, a fold warp's
   static constexpr int kExpandWarps = 12 - kFoldWarps;
-  static constexpr int kDStages = MT == 128 ? 2 : 4;
-  static constexpr int kXBytes = MT * 256;       // A's rows of one step
-  static constexpr int kSxBytes = 4 * MT * 4;    // sums of at most four groups
+  // A stage of tensor memory: 64 columns of expanded codes, and GROUPS
+  // accumulators.
+  static constexpr int kStageCols = 64 + GROUPS * MT;
+  static constexpr int kStages = 512 / kStageCols < 4 ? 512 / kStageCols : 4;
+  static constexpr int kXBytes = MT * 256;            // A's rows of one step
+  static constexpr int kSxBytes = GROUPS * MT * 4;    // sums of its groups
   static constexpr int kXStages = MT == 128 ? 4 : 6;
   static constexpr int kCodeStages = MT == 128 ? 8 : 10;
-  static constexpr int kBars = 2 * kCodeStages + 2 * kXStages + 2 * kAStages + 2 * kDStages + 1;
+  static constexpr int kBars = 2 * kCodeStages + 2 * kXStages + 3 * kStages + 1;
   static constexpr int kSmem = 1024 + kCodeStages * kCodeBytes + kXStages * (kXBytes + kSxBytes) + 8 * kBars + 16;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(MT * kRows * 4 <= kCodeStages * kCodeBytes + kXStages * kXBytes, "the sums reuse the rings");
-  static_assert(kAStages * 64 + kDStages * MT <= 512, "tensor memory");
+  static_assert(kStages >= 2, "tensor memory");
 };
 
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
@@ -81,6 +88,23 @@ __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 32 TMEM lanes x N consecutive 32-bit columns, N = 16 or 32.
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
+  if constexpr (N == 16)
+    ptx::tmem_ld_32x32b_x16(taddr, r);
+  else
+    ptx::tmem_ld_32x32b_x32(taddr, r);
+}
+template <int N>
+__device__ __forceinline__ void tmem_ready(uint32_t (&r)[N]) {
+  ptx::tmem_wait_ld();
+  if constexpr (N == 16)
+    ptx::tmem_regs_ready16(r);
+  else
+    ptx::tmem_regs_ready(r);
+}
 
 // Contiguous copy global -> shared of a multiple of 16 bytes, counted on `bar`.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -140,8 +164,8 @@ struct Ring {
 
 template <bool BF16, int MT, int GC>  // GC: group / 32
 __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant__ W4Params p) {
-  using C = Cfg<MT>;
   constexpr int GROUPS = 4 / GC;  // groups of a step
+  using C = Cfg<MT, GROUPS>;
   constexpr int FW = C::kFoldWarps, EW = C::kExpandWarps;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
@@ -160,10 +184,9 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
   auto x_full = [&](int s) { return bar0 + 8u * (2 * C::kCodeStages + s); };
   auto x_empty = [&](int s) { return bar0 + 8u * (2 * C::kCodeStages + C::kXStages + s); };
   constexpr int kABar = 2 * C::kCodeStages + 2 * C::kXStages;
-  auto a_full = [&](int s) { return bar0 + 8u * (kABar + s); };
-  auto a_empty = [&](int s) { return bar0 + 8u * (kABar + kAStages + s); };
-  auto d_full = [&](int s) { return bar0 + 8u * (kABar + 2 * kAStages + s); };
-  auto d_empty = [&](int s) { return bar0 + 8u * (kABar + 2 * kAStages + C::kDStages + s); };
+  auto a_full = [&](int s) { return bar0 + 8u * (kABar + s); };                    // codes expanded
+  auto d_full = [&](int s) { return bar0 + 8u * (kABar + C::kStages + s); };       // products done
+  auto s_empty = [&](int s) { return bar0 + 8u * (kABar + 2 * C::kStages + s); };  // products read
   const uint32_t drain = bar0 + 8u * (C::kBars - 1);
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + kBar + 8 * C::kBars);
 
@@ -182,15 +205,12 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
     }
     for (int s = 0; s < C::kXStages; ++s) {
       ptx::mbar_init(x_full(s), 1);
-      ptx::mbar_init(x_empty(s), 1 + FW);
+      ptx::mbar_init(x_empty(s), FW);
     }
-    for (int s = 0; s < kAStages; ++s) {
+    for (int s = 0; s < C::kStages; ++s) {
       ptx::mbar_init(a_full(s), 4);
-      ptx::mbar_init(a_empty(s), 1);
-    }
-    for (int s = 0; s < C::kDStages; ++s) {
       ptx::mbar_init(d_full(s), 1);
-      ptx::mbar_init(d_empty(s), FW);
+      ptx::mbar_init(s_empty(s), FW);
     }
     ptx::mbar_init(drain, 1);
     ptx::fence_mbar_init();
@@ -203,61 +223,51 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t d_at = tmem + kAStages * 64;
 
-  uint64_t sum[MT == 128 ? 32 : MT / 2];  // fold warps: columns of A's rows in pairs
+  uint64_t sum[C::kCols / 2];  // fold warps: rows of A in pairs
 #pragma unroll
   for (int i = 0; i < static_cast<int>(sizeof(sum) / 8); ++i) sum[i] = 0;
 
   if (warp == 0) {
-    // ---------------------------------------------------------- TMA
+    // ---------------------------------------------------------- codes
     if (lane == 0) {
       ptx::prefetch_tmap(&p.tmap_w);
-      ptx::prefetch_tmap(&p.tmap_x);
       const int row0 = glu ? tile * 64 : tile * 128, row1 = glu ? p.n_out + tile * 64 : tile * 128 + 64;
       Ring<C::kCodeStages> rc;
-      Ring<C::kXStages> rx;
-      int done_c = b0, done_x = b0;
-      bool ok = true;
-      auto load_codes = [&]() {
+      int b = b0;
+      for (; b < b1; ++b, rc.next()) {
+        if (!wait(code_empty(rc.s), rc.ph ^ 1u, p, 0)) break;
         ptx::mbar_arrive_expect_tx(code_full(rc.s), kCodeBytes);
-        ptx::tma_load_2d(code_at(rc.s), &p.tmap_w, done_c * 64, row0, code_full(rc.s));
-        ptx::tma_load_2d(code_at(rc.s) + kCodeBytes / 2, &p.tmap_w, done_c * 64, row1, code_full(rc.s));
-        rc.next();
-        ++done_c;
-      };
-      for (int i = 0; i < C::kCodeStages && done_c < b1; ++i) load_codes();
-      // the packed A is there once the pre-pass has ended
-      asm volatile("griddepcontrol.wait;" ::: "memory");
-      ptx::fence_proxy_async_global();
-      while (ok && done_x < b1) {
-        if (!wait(x_empty(rx.s), rx.ph ^ 1u, p, 0)) {
-          ok = false;
-          break;
-        }
-        ptx::mbar_arrive_expect_tx(x_full(rx.s), C::kXBytes + GROUPS * MT * 4);
-        ptx::tma_load_2d(x_at(rx.s), &p.tmap_x, done_x * kBlock, m0, x_full(rx.s));
-        ptx::tma_load_2d(x_at(rx.s) + C::kXBytes / 2, &p.tmap_x, done_x * kBlock + 64, m0, x_full(rx.s));
-        for (int i = 0; i < GROUPS; ++i)
-          bulk_load(sx_at(rx.s) + i * MT * 4, p.sx + (static_cast<long long>(done_x) * GROUPS + i) * p.m_pad + m0,
-                    MT * 4, x_full(rx.s));
-        rx.next();
-        ++done_x;
-        if (done_c < b1) {
-          if (!wait(code_empty(rc.s), rc.ph ^ 1u, p, 0)) {
-            ok = false;
-            break;
-          }
-          load_codes();
-        }
+        ptx::tma_load_2d(code_at(rc.s), &p.tmap_w, b * 64, row0, code_full(rc.s));
+        ptx::tma_load_2d(code_at(rc.s) + kCodeBytes / 2, &p.tmap_w, b * 64, row1, code_full(rc.s));
       }
       // Whatever another role did, the copies in flight land before the CTA
       // goes on: the stages loaded last.
-      for (int i = 0; i < C::kCodeStages && done_c - i > b0; ++i) {
+      for (int i = 0; i < C::kCodeStages && b - i > b0; ++i) {
         if (--rc.s < 0) rc.s = C::kCodeStages - 1, rc.ph ^= 1u;
         if (!ptx::mbar_try_wait(code_full(rc.s), rc.ph)) wait_slow(code_full(rc.s), rc.ph, p, kErrTimeout, false);
       }
-      for (int i = 0; i < C::kXStages && done_x - i > b0; ++i) {
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ---------------------------------------------------------- packed A
+    if (lane == 0) {
+      ptx::prefetch_tmap(&p.tmap_x);
+      // it is there once the pre-pass has ended
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      ptx::fence_proxy_async_global();
+      Ring<C::kXStages> rx;
+      int b = b0;
+      for (; b < b1; ++b, rx.next()) {
+        if (!wait(x_empty(rx.s), rx.ph ^ 1u, p, 0)) break;
+        ptx::mbar_arrive_expect_tx(x_full(rx.s), C::kXBytes + GROUPS * MT * 4);
+        ptx::tma_load_2d(x_at(rx.s), &p.tmap_x, b * kBlock, m0, x_full(rx.s));
+        ptx::tma_load_2d(x_at(rx.s) + C::kXBytes / 2, &p.tmap_x, b * kBlock + 64, m0, x_full(rx.s));
+        for (int i = 0; i < GROUPS; ++i)
+          bulk_load(sx_at(rx.s) + i * MT * 4, p.sx + (static_cast<long long>(b) * GROUPS + i) * p.m_pad + m0, MT * 4,
+                    x_full(rx.s));
+      }
+      for (int i = 0; i < C::kXStages && b - i > b0; ++i) {
         if (--rx.s < 0) rx.s = C::kXStages - 1, rx.ph ^= 1u;
         if (!ptx::mbar_try_wait(x_full(rx.s), rx.ph)) wait_slow(x_full(rx.s), rx.ph, p, kErrTimeout, false);
       }
@@ -268,34 +278,23 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
     if (lane == 0) {
       // fp32 accumulator, fp16 operands, both K-major, N = MT, M = 128
       constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(MT >> 3) << 17) | ((128u >> 4) << 24);
+      const uint64_t desc0 = ptx::sdesc(x_at(0), 16, 1024);
       Ring<C::kXStages> rx;
-      Ring<kAStages> ra;
-      Ring<C::kDStages> rd;
-      bool ok = true;
-      for (int b = b0; ok && b < b1; ++b) {
-        if (!wait(x_full(rx.s), rx.ph, p, 1) || !wait(a_full(ra.s), ra.ph, p, 1)) break;
+      Ring<C::kStages> rs;
+      // One thread issues everything, so its instructions a step count: one
+      // commit tells the fold warps, and they hand back all that the step used.
+      for (int b = b0; b < b1; ++b) {
+        if (!wait(x_full(rx.s), rx.ph, p, 1) || !wait(a_full(rs.s), rs.ph, p, 1)) break;
         ptx::tc_fence_after();
-        for (int grp = 0; grp < GROUPS; ++grp) {
-          if (!wait(d_empty(rd.s), rd.ph ^ 1u, p, 1)) {
-            ok = false;
-            break;
-          }
-          ptx::tc_fence_after();
+        const uint64_t desc = desc0 + static_cast<uint32_t>(rx.s * (C::kXBytes >> 4));
+        const uint32_t stage = tmem + rs.s * C::kStageCols;
 #pragma unroll
-          for (int i = 0; i < 2 * GC; ++i) {
-            const int k16 = grp * 2 * GC + i;  // of the step's eight
-            const uint64_t bd = ptx::sdesc(x_at(rx.s) + (k16 >> 2) * (C::kXBytes / 2), 16, 1024) +
-                                static_cast<uint64_t>((k16 & 3) * 2);
-            mma_f16_ts(d_at + rd.s * MT, tmem + ra.s * 64 + k16 * 8, bd, idesc, i != 0 ? 1u : 0u);
-          }
-          ptx::mma_commit(d_full(rd.s));
-          rd.next();
-        }
-        if (!ok) break;
-        ptx::mma_commit(a_empty(ra.s));
-        ptx::mma_commit(x_empty(rx.s));
+        for (int k16 = 0; k16 < 8; ++k16)
+          mma_f16_ts(stage + 64 + (k16 / (2 * GC)) * MT, stage + k16 * 8,
+                     desc + ((k16 >> 2) * (C::kXBytes >> 5) + (k16 & 3) * 2), idesc, k16 % (2 * GC) != 0 ? 1u : 0u);
+        ptx::mma_commit(d_full(rs.s));
         rx.next();
-        ra.next();
+        rs.next();
       }
       ptx::mma_commit(drain);
       if (!ptx::mbar_try_wait(drain, 0)) wait_slow(drain, 0, p, kErrTimeout | (1u << 24), false);
@@ -311,17 +310,19 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
     constexpr int SETS = EW / 4;  // sets of four warps, which take steps in turn
     const int set = (warp - 4) >> 2;
     Ring<C::kCodeStages> rc;
-    Ring<kAStages> ra;
-    for (int b = b0; b < b1; ++b, rc.next(), ra.next()) {
+    Ring<C::kStages> rs;
+    for (int b = b0; b < b1; ++b, rc.next(), rs.next()) {
       if (SETS > 1 && (b - b0) % SETS != set) continue;
       if (!wait_warp(code_full(rc.s), rc.ph, p, 3)) break;
       uint4 w[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c)
         w[c] = *reinterpret_cast<const uint4*>(base_ptr + kCodes + rc.s * kCodeBytes + sr * 64 + ((c ^ sw) << 4));
-      if (!wait_warp(a_empty(ra.s), ra.ph ^ 1u, p, 3)) break;
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(code_empty(rc.s));
+      if (!wait_warp(s_empty(rs.s), rs.ph ^ 1u, p, 3)) break;
       ptx::tc_fence_after();
-      const uint32_t to = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + ra.s * 64;
+      const uint32_t to = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + rs.s * C::kStageCols;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t e[32];
@@ -336,95 +337,82 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
         }
         tmem_st_32x32b_x32(to + h * 32, e);
       }
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(code_empty(rc.s));
       tmem_wait_st();
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(a_full(ra.s));
+      if (lane == 0) ptx::mbar_arrive(a_full(rs.s));
     }
   } else if (warp >= 4 + EW) {
     // ---------------------------------------------------------- fold
-    constexpr int COLS = MT == 128 ? 64 : MT;   // of A's rows, a warp's
-    constexpr int BATCH = COLS < 32 ? COLS : 32;
-    const int r = (warp & 3) * 32 + lane, col0 = MT == 128 ? ((warp - 4 - EW) >> 2) * 64 : 0;
+    constexpr int COLS = C::kCols, PART = COLS < 32 ? COLS : 32;  // PART: columns in registers at a time
+    const int r = (warp & 3) * 32 + lane, col0 = ((warp - 4 - EW) >> 2) * COLS;
     const long long j = min(w4_column(p, tile, r, kRows), p.n - 1);
     const uint16_t* const s_row = p.scales + j * p.lds;
     const uint8_t* const z_row = p.zeros + j * p.ldz;
     const int groups = (p.k + GC * 32 - 1) / (GC * 32);
-    const int g0 = b0 * GROUPS, g1 = b1 * GROUPS;
-    // scales and zero points, four groups ahead
-    uint16_t s_next[4];
-    uint8_t z_next[4] = {8, 8, 8, 8};
-    auto fetch = [&](int g) {
+    // scales and zero points of the groups of AHEAD steps
+    constexpr int AHEAD = GROUPS == 1 ? 4 : GROUPS == 2 ? 2 : 1, KEEP = AHEAD * GROUPS;
+    uint16_t s_next[KEEP];
+    uint8_t z_next[KEEP];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int at = min(g + i, groups - 1);  // past the last group A is zero
+    for (int i = 0; i < KEEP; ++i) z_next[i] = 8;
+    auto fetch = [&](int b) {
+#pragma unroll
+      for (int i = 0; i < KEEP; ++i) {
+        const int at = min(b * GROUPS + i, groups - 1);  // past the last group A is zero
         s_next[i] = s_row[at];
         if (p.zeros) z_next[i] = z_row[at];
       }
     };
-    if (g0 < g1) fetch(g0);
+    fetch(b0);
+    float s[KEEP], z[KEEP];
     Ring<C::kXStages> rx;
-    Ring<C::kDStages> rd;
-    bool ok = true;
-    for (int g = g0; ok && g < g1; g += 4) {
-      float s[4], z[4];
+    Ring<C::kStages> rs;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b, rx.next(), rs.next()) {
+      if ((b - b0) % AHEAD == 0) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s[i] = w4_f32<BF16>(s_next[i]);
-        z[i] = 8388608.0f - __uint_as_float(0x4B000000u | z_next[i]);  // minus the zero point
+        for (int i = 0; i < KEEP; ++i) {
+          s[i] = w4_f32<BF16>(s_next[i]);
+          z[i] = 8388608.0f - __uint_as_float(0x4B000000u | z_next[i]);  // minus the zero point
+        }
+        fetch(b + AHEAD);
+      } else {
+#pragma unroll
+        for (int i = 0; i + GROUPS < KEEP; ++i) s[i] = s[i + GROUPS], z[i] = z[i + GROUPS];
       }
-      if (g + 4 < g1) fetch(g + 4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (g + i >= g1) break;
-        const int grp = i % GROUPS;  // g0 is a multiple of GROUPS, and so is g
-        if (grp == 0 && !wait_warp(x_full(rx.s), rx.ph, p, 2)) {
-          ok = false;
+      {
+        const bool x = ptx::mbar_try_wait(x_full(rx.s), rx.ph), d = ptx::mbar_try_wait(d_full(rs.s), rs.ph);
+        if (!__all_sync(0xFFFFFFFFu, x && d) &&
+            !(wait_warp(x_full(rx.s), rx.ph, p, 2) && wait_warp(d_full(rs.s), rs.ph, p, 2)))
           break;
-        }
-        if (!wait_warp(d_full(rd.s), rd.ph, p, 2)) {
-          ok = false;
-          break;
-        }
-        ptx::tc_fence_after();
-        const uint32_t from = d_at + (static_cast<uint32_t>((warp & 3) * 32) << 16) + rd.s * MT + col0;
-        const uint64_t s2 = pair(s[i], s[i]), z2 = pair(z[i], z[i]);
-        const ulonglong2* const sx =
-            reinterpret_cast<const ulonglong2*>(base_ptr + kSx + rx.s * C::kSxBytes + (grp * MT + col0) * 4);
+      }
+      ptx::tc_fence_after();
+      const uint32_t from = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + rs.s * C::kStageCols + 64 + col0;
 #pragma unroll
-        for (int c = 0; c < COLS; c += BATCH) {
-          uint32_t acc[BATCH];
-          if constexpr (BATCH == 32) {
-            ptx::tmem_ld_32x32b_x32(from + c, acc);
-            ptx::tmem_wait_ld();
-            ptx::tmem_regs_ready(acc);
-          } else {
-            ptx::tmem_ld_32x32b_x16(from + c, acc);
-            ptx::tmem_wait_ld();
-            ptx::tmem_regs_ready16(acc);
-          }
-          if (c + BATCH == COLS) {  // all of it is in registers: hand the accumulator back
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(d_empty(rd.s));
-          }
-#pragma unroll
-          for (int q = 0; q < BATCH / 4; ++q) {
-            const ulonglong2 x = sx[c / 4 + q];
-            uint64_t* const to = sum + (c + 4 * q) / 2;
-            to[0] = fma2(s2, fma2(z2, x.x, pair(__uint_as_float(acc[4 * q]), __uint_as_float(acc[4 * q + 1]))), to[0]);
-            to[1] = fma2(s2, fma2(z2, x.y, pair(__uint_as_float(acc[4 * q + 2]), __uint_as_float(acc[4 * q + 3]))), to[1]);
-          }
-        }
-        rd.next();
-        if (grp == GROUPS - 1) {
+      for (int i = 0; i < GROUPS * COLS / PART; ++i) {
+        const int grp = i / (COLS / PART), c0 = i % (COLS / PART) * PART;
+        uint32_t acc[PART];
+        tmem_ld<PART>(from + grp * MT + c0, acc);
+        tmem_ready<PART>(acc);
+        if (i + 1 == GROUPS * COLS / PART) {  // all of the step has been read
+          ptx::tc_fence_before();
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(x_empty(rx.s));
-          rx.next();
+          if (lane == 0) ptx::mbar_arrive(s_empty(rs.s));
+        }
+        const uint64_t s2 = pair(s[grp], s[grp]), z2 = pair(z[grp], z[grp]);
+        const ulonglong2* const sx =
+            reinterpret_cast<const ulonglong2*>(base_ptr + kSx + rx.s * C::kSxBytes + (grp * MT + col0 + c0) * 4);
+#pragma unroll
+        for (int q = 0; q < PART / 4; ++q) {
+          const ulonglong2 x = sx[q];
+          uint64_t* const to = sum + c0 / 2 + 2 * q;
+          to[0] = fma2(s2, fma2(z2, x.x, pair(__uint_as_float(acc[4 * q]), __uint_as_float(acc[4 * q + 1]))), to[0]);
+          to[1] = fma2(s2, fma2(z2, x.y, pair(__uint_as_float(acc[4 * q + 2]), __uint_as_float(acc[4 * q + 3]))), to[1]);
         }
       }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(x_empty(rx.s));
     }
   }
 
@@ -436,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
   if (warp == 1) ptx::tmem_dealloc(tmem, 512);
   float* const part = reinterpret_cast<float*>(base_ptr);
   if (warp >= 4 + EW) {
-    const int r = (warp & 3) * 32 + lane, col0 = MT == 128 ? ((warp - 4 - EW) >> 2) * 64 : 0;
+    const int r = (warp & 3) * 32 + lane, col0 = ((warp - 4 - EW) >> 2) * C::kCols;
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(sum) / 8); ++i) {
       float lo, hi;
@@ -566,21 +554,26 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const __grid_constant__ W4
   }
 }
 
-int m_tile(long long m) { return m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128; }
+int m_tile(long long m, int group) {
+  const int most = kMostRows[group / 64];
+  int t = 16;
+  while (t < m && t < most) t *= 2;
+  return t;
+}
 
 template <bool BF16, int MT, int GC>
 cudaError_t launch_main(const W4Params& p, const cudaLaunchConfig_t& cfg) {
   auto kernel = w4mm_kernel<BF16, MT, GC>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<MT>::kSmem);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<MT, 4 / GC>::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t c = cfg;
-  c.dynamicSmemBytes = Cfg<MT>::kSmem;
+  c.dynamicSmemBytes = Cfg<MT, 4 / GC>::kSmem;
   return cudaLaunchKernelEx(&c, kernel, p);
 }
 
 template <bool BF16, int GC>
 cudaError_t launch_of(W4Params p, int num_sms, cudaStream_t stream) {
-  const int mt = m_tile(p.m);
+  const int mt = m_tile(p.m, p.group);
   const int per_tile = p.epi == kEpiSwiglu ? kRows / 2 : kRows;
   const long long tiles = (p.n_out + per_tile - 1) / per_tile, tiles_m = (p.m + mt - 1) / mt;
   const int blocks = (p.k + kBlock - 1) / kBlock;
@@ -611,12 +604,15 @@ cudaError_t launch_of(W4Params p, int num_sms, cudaStream_t stream) {
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = p.slices > 1 ? 2 : 1;
-  switch (mt) {
-    case 16: return launch_main<BF16, 16, GC>(p, cfg);
-    case 32: return launch_main<BF16, 32, GC>(p, cfg);
-    case 64: return launch_main<BF16, 64, GC>(p, cfg);
-    default: return launch_main<BF16, 128, GC>(p, cfg);
+  if (mt == 16) return launch_main<BF16, 16, GC>(p, cfg);
+  if (mt == 32) return launch_main<BF16, 32, GC>(p, cfg);
+  if constexpr (GC >= 2) {
+    if (mt == 64) return launch_main<BF16, 64, GC>(p, cfg);
   }
+  if constexpr (GC >= 4) {
+    if (mt == 128) return launch_main<BF16, 128, GC>(p, cfg);
+  }
+  return cudaErrorInvalidValue;
 }
 
 // The workspace: packed A, then the groups' sums, then the rows' units.
@@ -627,7 +623,8 @@ struct Layout {
 Layout layout(long long m, long long k, int group) {
   Layout l;
   l.k_pad = (k + kBlock - 1) / kBlock * kBlock;
-  l.m_pad = (m + m_tile(m) - 1) / m_tile(m) * m_tile(m);
+  const int mt = m_tile(m, group);
+  l.m_pad = (m + mt - 1) / mt * mt;
   l.x = 0;
   l.sx = static_cast<size_t>(m) * l.k_pad * 2;  // rows of a multiple of 256 bytes
   l.unit = l.sx + static_cast<size_t>(l.k_pad / group) * l.m_pad * 4;
@@ -653,7 +650,7 @@ cudaError_t launch_w4mm(const W4Params& all, void* workspace, int num_sms, cudaS
   if (!encode_map_2d(&p.tmap_w, p.w, 1, static_cast<uint64_t>(p.k + 1) / 2, static_cast<uint64_t>(p.n),
                      static_cast<uint64_t>(p.n > 1 ? p.ldw : ((p.k + 1) / 2 + 15) / 16 * 16), 64, 64) ||
       !encode_map_2d(&p.tmap_x, p.x, 2, static_cast<uint64_t>(l.k_pad), static_cast<uint64_t>(p.m),
-                     static_cast<uint64_t>(l.k_pad) * 2, 64, static_cast<uint32_t>(m_tile(p.m))))
+                     static_cast<uint64_t>(l.k_pad) * 2, 64, static_cast<uint32_t>(m_tile(p.m, p.group))))
     return cudaErrorInvalidValue;
   switch ((p.is_bf16 ? 4 : 0) + p.group / 64) {
     case 0: return launch_of<false, 1>(p, num_sms, stream);

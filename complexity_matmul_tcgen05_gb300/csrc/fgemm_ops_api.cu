@@ -150,7 +150,7 @@ fgemm_status_t fgemm_rms_norm_backward(fgemm_handle_t h, int64_t M, int64_t N, c
 }
 
 size_t fgemm_matmul_w4_workspace(int64_t M, int64_t K, int32_t group) {
-  if (M <= 0 || K <= 0 || M > (int64_t{1} << 22) || K > (int64_t{1} << 30) || (group != 32 && group != 64 && group != 128)) return 0;
+  if (M <= 0 || K <= 0 || M > (int64_t{1} << 20) || K > (int64_t{1} << 30) || (group != 32 && group != 64 && group != 128)) return 0;
   return fgemm::w4_workspace(M, K, group);
 }
 
@@ -159,8 +159,8 @@ fgemm_status_t fgemm_matmul_w4(fgemm_handle_t h, int64_t M, int64_t N, int64_t K
                                int64_t ldz, int32_t group, void* C, int64_t ldc, fgemm_dtype_t dtype,
                                const fgemm_epilogue_t* epi, void* workspace, size_t workspace_bytes) {
   if (!is_16bit(dtype)) return bad_arg(h, "dtype must be FGEMM_F16 or FGEMM_BF16");
-  if (M < 0 || N < 0 || K < 0 || M > (int64_t{1} << 22) || N > kMaxDim || K > (int64_t{1} << 30))
-    return bad_arg(h, "sizes must be in 0 .. 2^31 - 1024, M in 0 .. 2^22, K in 0 .. 2^30");
+  if (M < 0 || N < 0 || K < 0 || M > (int64_t{1} << 20) || N > kMaxDim || K > (int64_t{1} << 30))
+    return bad_arg(h, "sizes must be in 0 .. 2^31 - 1024, M in 0 .. 2^20, K in 0 .. 2^30");
   if (group != 32 && group != 64 && group != 128) return bad_arg(h, "group must be 32, 64 or 128");
   const int32_t kind = epi ? epi->kind : FGEMM_EPI_NONE;
   if (kind < FGEMM_EPI_NONE || kind > FGEMM_EPI_SWIGLU) return bad_arg(h, "unknown epilogue kind");

@@ -386,7 +386,7 @@ fgemm_status_t fgemm_rms_norm_backward(fgemm_handle_t h, int64_t M, int64_t N, c
 /*
  * C = epi(alpha * A * W^T + bias) with 4-bit weights and group scales:
  *   W[j][k] = (code[j][k] - zero[j][k / group]) * scale[j][k / group]
- *   A, lda       M x K of dtype, M at most 2^22, K at most 2^30.
+ *   A, lda       M x K of dtype, M at most 2^20, K at most 2^30.
  *   W, ldw       N x ceil(K / 2) bytes, ldw in bytes: two codes (0 .. 15) to
  *                a byte along K, the even k in the low half. (N x K, unlike
  *                B of fgemm_matmul: codes are read along K.)
