@@ -20,8 +20,8 @@
 // may begin before the pre-pass ends (programmatic dependent launch): its
 // codes are on their way by then.
 //
-// Roles: warp 0 loads the codes, warp 2 A, warp 1 issues the MMAs, warps 4.. expand
-// the codes, the last 4 or 8 warps fold.  Every wait is bounded; a wait that runs out latches the
+// Roles: warp 0 loads the codes, warp 2 A, warps 1 and 3 issue the MMAs, warps 4..
+// expand the codes, the last 4 or 8 warps fold.  Every wait is bounded; a wait that runs out latches the
 // error word and all roles leave.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -54,7 +54,7 @@ struct Cfg {
   // A stage of tensor memory: 64 columns of expanded codes, and GROUPS
   // accumulators.
   static constexpr int kStageCols = 64 + GROUPS * MT;
-  static constexpr int kStages = 512 / kStageCols < 4 ? 512 / kStageCols : 4;
+  static constexpr int kStages = 512 / kStageCols < 4 ? 2 : 4;
   static constexpr int kXBytes = MT * 256;            // A's rows of one step
   static constexpr int kSxBytes = GROUPS * MT * 4;    // sums of its groups
   static constexpr int kXStages = MT == 128 ? 4 : 6;
@@ -63,7 +63,7 @@ struct Cfg {
   static constexpr int kSmem = 1024 + kCodeStages * kCodeBytes + kXStages * (kXBytes + kSxBytes) + 8 * kBars + 16;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(MT * kRows * 4 <= kCodeStages * kCodeBytes + kXStages * kXBytes, "the sums reuse the rings");
-  static_assert(kStages >= 2, "tensor memory");
+  static_assert(kStages == 2 || kStages == 4, "tensor memory");  // even: two warps issue in turn
 };
 
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
       ptx::mbar_init(d_full(s), 1);
       ptx::mbar_init(s_empty(s), FW);
     }
-    ptx::mbar_init(drain, 1);
+    ptx::mbar_init(drain, 2);
     ptx::fence_mbar_init();
   }
   if (warp == 1) {
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp == 1 || warp == 3) {
     // ---------------------------------------------------------- MMA
     if (lane == 0) {
       // fp32 accumulator, fp16 operands, both K-major, N = MT, M = 128
@@ -281,9 +281,13 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
       const uint64_t desc0 = ptx::sdesc(x_at(0), 16, 1024);
       Ring<C::kXStages> rx;
       Ring<C::kStages> rs;
-      // One thread issues everything, so its instructions a step count: one
-      // commit tells the fold warps, and they hand back all that the step used.
-      for (int b = b0; b < b1; ++b) {
+      // A step's products are issued by one thread, whose time counts (16 rows:
+      // 590 clocks for the 8 products, 390 to tell the fold warps and to find
+      // the next step ready): one commit a step, on which the fold warps hand
+      // back all that it used, and two warps that take steps in turn.
+      const int turn = warp >> 1;
+      if (turn) rx.next(), rs.next();
+      for (int b = b0 + turn; b < b1; b += 2) {
         if (!wait(x_full(rx.s), rx.ph, p, 1) || !wait(a_full(rs.s), rs.ph, p, 1)) break;
         ptx::tc_fence_after();
         const uint64_t desc = desc0 + static_cast<uint32_t>(rx.s * (C::kXBytes >> 4));
@@ -293,8 +297,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
           mma_f16_ts(stage + 64 + (k16 / (2 * GC)) * MT, stage + k16 * 8,
                      desc + ((k16 >> 2) * (C::kXBytes >> 5) + (k16 & 3) * 2), idesc, k16 % (2 * GC) != 0 ? 1u : 0u);
         ptx::mma_commit(d_full(rs.s));
-        rx.next();
-        rs.next();
+        rx.next(), rx.next();
+        rs.next(), rs.next();
       }
       ptx::mma_commit(drain);
       if (!ptx::mbar_try_wait(drain, 0)) wait_slow(drain, 0, p, kErrTimeout | (1u << 24), false);
