@@ -25,6 +25,13 @@
 // An infinite or NaN x makes acc - z sx meaningless: an output that is not
 // finite is computed again term by term (w4_exact).
 //
+// What bounds it: latency, from the codes' arrival to the tile's last sum, with
+// 1.9 instructions a clock (254 a warp for 4096 weights).  5 x 28672 x 4096,
+// SwiGLU, bf16, groups of 128: 19.2 us, 3.2 TB/s; one row 4096 x 4096: 6.7 us.
+// Measured on the first of these on the way: codes turned into 1 + q/16 with
+// a ring a warp 34.3 us, two teams to a CTA 27.4, codes as subnormals 21.9,
+// A loaded once and scales folded a group at a time 19.2.
+//
 // mma.sync with the codes as the 16-row operand and 8 rows of A as the other:
 // the operand goes from the ring in shared memory through registers, where
 // it is expanded, into the tensor core, with no second trip through shared
@@ -50,9 +57,9 @@ constexpr int kW4Threads = kW4Teams * kW4Warps * 32;
 constexpr int kW4Rows = 32;    // rows of W (columns of C) of a tile
 constexpr int kW4Block = 128;  // k of one ring slot: 64 bytes of codes a row
 constexpr int kW4Stages = 3;
-// Of A in shared memory; finer groups have more scales beside it, more rows more sums.
-template <int NT, int GC>
-constexpr int kW4ABytes = ((GC > 1 ? 64 : 48) - (NT > 1 ? 16 : 0)) * 1024;
+// Of A in shared memory; finer groups have more scales beside it.
+template <int GC>
+constexpr int kW4ABytes = (GC > 1 ? 64 : 48) * 1024;
 
 // 16 bytes global -> shared; bytes past `valid` (0..16) are zero and not read.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int valid) {
@@ -71,7 +78,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The few-rows kernel: tiles of 32 rows of W against all (at most 16) rows
+// The few-rows kernel: tiles of 32 rows of W against all (at most 8) rows
 // of A.
 //
 // A sits in shared memory for as long as the CTA lives (when it fits; else a
@@ -82,7 +89,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 // when their sums meet, while the blocks of the next tile are already on
 // their way.  With few tiles, the CTAs of a cluster take a slice of K each and
 // add their sums through distributed shared memory, in rank order.
-template <bool BF16, int NT, int GC>  // GC: group / 32
+template <bool BF16, int GC>  // GC: group / 32
 __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant__ W4Params p) {
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr int R = kW4Rows / 16;
@@ -107,8 +114,8 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
                              (threadIdx.x >> 5) * (kW4Stages * kScales);  // [group][row]: scale, zero point
   unsigned char* const a_at = smem + kW4Teams * kW4Warps * kW4Stages * (kSlot + kScales * 8);
   const int a_pitch = p.chunk * 2;
-  float2* const sx_at = reinterpret_cast<float2*>(a_at + static_cast<size_t>(a_pitch) * mt);  // [group of the chunk][8 NT]
-  float* const red = reinterpret_cast<float*>(sx_at + p.chunk / G * (8 * NT)) + team * ((kW4Warps + 2) * kW4Rows * mt);  // [warp][row of A][row]
+  float2* const sx_at = reinterpret_cast<float2*>(a_at + static_cast<size_t>(a_pitch) * mt);  // [group of the chunk][8]
+  float* const red = reinterpret_cast<float*>(sx_at + p.chunk / G * 8) + team * ((kW4Warps + 2) * kW4Rows * mt);  // [warp][row of A][row]
   float* const part = red + kW4Warps * kW4Rows * mt;  // [2][row of A][row], read by the cluster
   const int w_bytes = (p.k + 1) / 2 - k_lo / 2;  // of a row, from this CTA's first
   const int groups = (p.k + G - 1) / G;
@@ -252,7 +259,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
             s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
           }
           const int e = w4_shift<BF16>(most);
-          if (run % (G / 8) == 0) sx_at[run / (G / 8) * (8 * NT) + m] = make_float2(s, w4_pow2(24 - e));
+          if (run % (G / 8) == 0) sx_at[run / (G / 8) * 8 + m] = make_float2(s, w4_pow2(24 - e));
           const float even = w4_pow2(e), odd = even * 0.0625f;
           uint32_t o[4];
 #pragma unroll
@@ -286,12 +293,11 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
   int slot_i = 0, side = 0;
   // A's rows as the tensor core's columns; those past mt repeat the last one
   // and their sums go nowhere.  Run 4 c + t of a block is at 4 (c ^ row % 2) + t.
-  const unsigned char* a_row[NT][2];  // by c % 2
+  const unsigned char* a_row[2];  // by c % 2
+  {
+    const int m = min(g, mt - 1);
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int m = min(8 * n + g, mt - 1);
-#pragma unroll
-    for (int c = 0; c < 2; ++c) a_row[n][c] = a_at + m * a_pitch + ((4 * (c ^ (m & 1)) + t) << 4);
+    for (int c = 0; c < 2; ++c) a_row[c] = a_at + m * a_pitch + ((4 * (c ^ (m & 1)) + t) << 4);
   }
 
   // A team without a last tile goes along where the CTA or the cluster meets.
@@ -299,13 +305,11 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
   for (int tile = first_tile; meets ? tile - team * (gridDim.x / slices) < p.tiles : tile < p.tiles;
        tile += tile_step, side ^= 1) {
     const bool live = tile < p.tiles;
-    float sum[R][NT][4];
+    float sum[R][4];
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sum[r][n][i] = 0.0f;
+      for (int i = 0; i < 4; ++i) sum[r][i] = 0.0f;
 
     for (int chunk0 = 0; chunk0 < blocks; chunk0 += chunk_blocks) {
       if (!resident) {
@@ -322,20 +326,15 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
         slot_i = slot_i + 1 == kW4Stages ? 0 : slot_i + 1;
 #pragma unroll
         for (int grp = 0; grp < GROUPS; ++grp) {
-          float acc[R][NT][4];
+          float acc[R][4];
 #pragma unroll
           for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) acc[r][n][i] = 0.0f;
+            for (int i = 0; i < 4; ++i) acc[r][i] = 0.0f;
 #pragma unroll
           for (int cc = 0; cc < GC; ++cc) {
             const int c = grp * GC + cc;
-            uint4 x[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-              x[n] = *reinterpret_cast<const uint4*>(a_row[n][c & 1] + b * 256 + (c >> 1) * 128);
+            const uint4 x = *reinterpret_cast<const uint4*>(a_row[c & 1] + b * 256 + (c >> 1) * 128);
             const unsigned char* at = slot + ((c ^ ((g >> 1) & 3)) << 4);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
@@ -344,28 +343,20 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
               w4_expand(*reinterpret_cast<const uint32_t*>(at + r * 1024 + 512), hi);
               // the lower kind of codes in one product, the upper in the other
               const uint32_t a0[4] = {lo[0], hi[0], lo[2], hi[2]}, a1[4] = {lo[1], hi[1], lo[3], hi[3]};
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                mma16816(acc[r][n], a0, x[n].x, x[n].z);
-                mma16816(acc[r][n], a1, x[n].y, x[n].w);
-              }
+              mma16816(acc[r], a0, x.x, x.z);
+              mma16816(acc[r], a1, x.y, x.w);
             }
           }
-          float4 sx[NT];  // sum and unit of acc, of two rows of A
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-            sx[n] = *reinterpret_cast<const float4*>(sx_at + (b * GROUPS + grp) * (8 * NT) + 8 * n + 2 * t);
+          // sum and unit of acc, of two rows of A
+          const float4 sx = *reinterpret_cast<const float4*>(sx_at + (b * GROUPS + grp) * 8 + 2 * t);
 #pragma unroll
           for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const float2 sz = scales[grp * kW4Rows + r * 16 + h * 8];
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                float* to = sum[r][n] + 2 * h;
-                to[0] = fmaf(sz.x, fmaf(-sz.y, sx[n].x, acc[r][n][2 * h] * sx[n].y), to[0]);
-                to[1] = fmaf(sz.x, fmaf(-sz.y, sx[n].z, acc[r][n][2 * h + 1] * sx[n].w), to[1]);
-              }
+              float* to = sum[r] + 2 * h;
+              to[0] = fmaf(sz.x, fmaf(-sz.y, sx.x, acc[r][2 * h] * sx.y), to[0]);
+              to[1] = fmaf(sz.x, fmaf(-sz.y, sx.z, acc[r][2 * h + 1] * sx.w), to[1]);
             }
         }
       }
@@ -373,17 +364,15 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
 
     // the warps' sums are added in warp order, then the CTAs' in rank order
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int i = 0; i < 2; ++i)
+      if (2 * t + i < mt) {
+        float* const to = red + (warp * mt + 2 * t + i) * kW4Rows + g;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (8 * n + 2 * t + i < mt) {
-          float* const to = red + (warp * mt + 8 * n + 2 * t + i) * kW4Rows + g;
-#pragma unroll
-          for (int r = 0; r < R; ++r) {
-            to[r * 16] = sum[r][n][i];
-            to[r * 16 + 8] = sum[r][n][i + 2];
-          }
+        for (int r = 0; r < R; ++r) {
+          to[r * 16] = sum[r][i];
+          to[r * 16 + 8] = sum[r][i + 2];
         }
+      }
     ptx::named_bar_sync(1 + team, kW4Warps * 32);
     const bool glu = p.epi == kEpiSwiglu;
     const int outs_log2 = glu ? 4 : 5;  // columns of C of a tile
@@ -433,7 +422,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
   if (slices > 1) ptx::cluster_sync();  // no CTA leaves while its sums may be read
 }
 
-template <bool BF16, int NT, int GC>
+template <bool BF16, int GC>
 cudaError_t launch_w4_few(W4Params p, int num_sms, cudaStream_t stream) {
   const int per_tile = p.epi == kEpiSwiglu ? kW4Rows / 2 : kW4Rows;
   p.tiles = (p.n_out + per_tile - 1) / per_tile;
@@ -441,7 +430,7 @@ cudaError_t launch_w4_few(W4Params p, int num_sms, cudaStream_t stream) {
   // K is cut into slices, a CTA of a cluster each: while there are SMs without
   // a tile and every warp keeps a block, and until A's slice fits
   int slices = 1;
-  const int most_chunk = kW4ABytes<NT, GC> / (2 * p.m) / 256 * 256;
+  const int most_chunk = kW4ABytes<GC> / (2 * p.m) / 256 * 256;
   while (slices < 8 && blocks >= 2 * slices * kW4Warps && static_cast<long long>(p.tiles) * slices * 2 <= num_sms * kW4Teams)
     slices *= 2;
   while (slices < 8 && (blocks + slices - 1) / slices * kW4Block > most_chunk) slices *= 2;
@@ -449,9 +438,9 @@ cudaError_t launch_w4_few(W4Params p, int num_sms, cudaStream_t stream) {
   p.slice = ((blocks + slices - 1) / slices * kW4Block + 255) / 256 * 256;
   p.chunk = p.slice < most_chunk ? (p.slice > 0 ? p.slice : 256) : most_chunk;
   const size_t smem = static_cast<size_t>(kW4Teams * kW4Warps) * kW4Stages * kW4Rows * (64 + 4 / GC * 8) +
-                      static_cast<size_t>(p.chunk) * 2 * p.m + static_cast<size_t>(p.chunk / (GC * 32)) * 8 * NT * 8 +
+                      static_cast<size_t>(p.chunk) * 2 * p.m + static_cast<size_t>(p.chunk / (GC * 32)) * 8 * 8 +
                       static_cast<size_t>(kW4Teams * (kW4Warps + 2)) * kW4Rows * p.m * 4;
-  auto kernel = w4_kernel<BF16, NT, GC>;
+  auto kernel = w4_kernel<BF16, GC>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const int clusters = num_sms / slices;
@@ -472,9 +461,9 @@ cudaError_t launch_w4_few(W4Params p, int num_sms, cudaStream_t stream) {
 
 template <bool BF16>
 cudaError_t launch_w4_type(const W4Params& p, int num_sms, cudaStream_t stream) {
-  return p.group == 32   ? launch_w4_few<BF16, 1, 1>(p, num_sms, stream)
-         : p.group == 64 ? launch_w4_few<BF16, 1, 2>(p, num_sms, stream)
-                         : launch_w4_few<BF16, 1, 4>(p, num_sms, stream);
+  return p.group == 32   ? launch_w4_few<BF16, 1>(p, num_sms, stream)
+         : p.group == 64 ? launch_w4_few<BF16, 2>(p, num_sms, stream)
+                         : launch_w4_few<BF16, 4>(p, num_sms, stream);
 }
 
 }  // namespace
