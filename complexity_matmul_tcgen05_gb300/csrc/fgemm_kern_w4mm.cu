@@ -113,6 +113,17 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
+// 16 bytes of a ring's stage.  Volatile: the read stays between the wait for
+// the stage and the arrival that hands it back.
+__device__ __forceinline__ uint4 ring_read(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+
 // Two fp32 multiply-adds in one instruction.
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
@@ -323,9 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
       uint4 w[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        w[c] = *reinterpret_cast<const uint4*>(base_ptr + kCodes + rc.s * kCodeBytes + sr * 64 + ((c ^ sw) << 4));
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(code_empty(rc.s));
+        w[c] = ring_read(code_at(rc.s) + sr * 64 + ((c ^ sw) << 4));
       if (!wait_warp(s_empty(rs.s), rs.ph ^ 1u, p, 3)) break;
       ptx::tc_fence_after();
       const uint32_t to = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + rs.s * C::kStageCols;
@@ -346,7 +355,13 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
       tmem_wait_st();
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(a_full(rs.s));
+      // The codes' stage goes back only now that what was made of it has been
+      // stored: handed back behind the reads, before the wait for the operand's
+      // stage, it was overwritten while rows of it were still to be read.
+      if (lane == 0) {
+        ptx::mbar_arrive(a_full(rs.s));
+        ptx::mbar_arrive(code_empty(rc.s));
+      }
     }
   } else if (warp >= 4 + EW) {
     // ---------------------------------------------------------- fold
@@ -407,14 +422,15 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
           if (lane == 0) ptx::mbar_arrive(s_empty(rs.s));
         }
         const uint64_t s2 = pair(s[grp], s[grp]), z2 = pair(z[grp], z[grp]);
-        const ulonglong2* const sx =
-            reinterpret_cast<const ulonglong2*>(base_ptr + kSx + rx.s * C::kSxBytes + (grp * MT + col0 + c0) * 4);
+        const uint32_t sx = sx_at(rx.s) + (grp * MT + col0 + c0) * 4;
 #pragma unroll
         for (int q = 0; q < PART / 4; ++q) {
-          const ulonglong2 x = sx[q];
+          const uint4 x = ring_read(sx + q * 16);
           uint64_t* const to = sum + c0 / 2 + 2 * q;
-          to[0] = fma2(s2, fma2(z2, x.x, pair(__uint_as_float(acc[4 * q]), __uint_as_float(acc[4 * q + 1]))), to[0]);
-          to[1] = fma2(s2, fma2(z2, x.y, pair(__uint_as_float(acc[4 * q + 2]), __uint_as_float(acc[4 * q + 3]))), to[1]);
+          const uint64_t x0 = pair(__uint_as_float(x.x), __uint_as_float(x.y));
+          const uint64_t x1 = pair(__uint_as_float(x.z), __uint_as_float(x.w));
+          to[0] = fma2(s2, fma2(z2, x0, pair(__uint_as_float(acc[4 * q]), __uint_as_float(acc[4 * q + 1]))), to[0]);
+          to[1] = fma2(s2, fma2(z2, x1, pair(__uint_as_float(acc[4 * q + 2]), __uint_as_float(acc[4 * q + 3]))), to[1]);
         }
       }
       __syncwarp();
