@@ -20,7 +20,7 @@
 // may begin before the pre-pass ends (programmatic dependent launch): its
 // codes are on their way by then.
 //
-// Roles: warp 0 loads the codes, warp 2 A, warps 1 and 3 issue the MMAs, warps 4..
+// Roles: warp 0 loads the codes, warp 2 A, warp 1 or warps 1 and 3 issue the MMAs, warps 4..
 // expand the codes, the last 4 or 8 warps fold.  Every wait is bounded; a wait that runs out latches the
 // error word and all roles leave.
 #include <cuda_bf16.h>
@@ -63,7 +63,13 @@ struct Cfg {
   static constexpr int kSmem = 1024 + kCodeStages * kCodeBytes + kXStages * (kXBytes + kSxBytes) + 8 * kBars + 16;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(MT * kRows * 4 <= kCodeStages * kCodeBytes + kXStages * kXBytes, "the sums reuse the rings");
-  static_assert(kStages == 2 || kStages == 4, "tensor memory");  // even: two warps issue in turn
+  static_assert(kStages == 2 || kStages == 4, "tensor memory");
+  // Warps that issue the products, a step each in turn: two when four steps are
+  // under way, one when it is two.  One against two, 8192 x 16384: four steps,
+  // 16 rows (groups of 128) 42.6 -> 32.6 us, 32 rows (64) 45.7 -> 43.6, 64 rows
+  // (128) 46.5 -> 46.2; two steps, 32 rows (32) 53.9 -> 56.7, 64 rows (64) 53.5 ->
+  // 55.3, 128 rows (128) 63.0 -> 65.0.
+  static constexpr int kIssuers = kStages == 4 ? 2 : 1;
 };
 
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
@@ -223,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
       ptx::mbar_init(d_full(s), 1);
       ptx::mbar_init(s_empty(s), FW);
     }
-    ptx::mbar_init(drain, 2);
+    ptx::mbar_init(drain, C::kIssuers);
     ptx::fence_mbar_init();
   }
   if (warp == 1) {
@@ -284,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
       }
     }
     __syncwarp();
-  } else if (warp == 1 || warp == 3) {
+  } else if (warp == 1 || (C::kIssuers == 2 && warp == 3)) {
     // ---------------------------------------------------------- MMA
     if (lane == 0) {
       // fp32 accumulator, fp16 operands, both K-major, N = MT, M = 128
@@ -295,12 +301,10 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
       // A step's products are issued by one thread, whose time counts (16 rows:
       // 590 clocks for the 8 products, 390 to tell the fold warps and to find
       // the next step ready): one commit a step, on which the fold warps hand
-      // back all that it used, and two warps that take steps in turn.  One warp
-      // against two, 8192 x 16384: 16 rows 43.7 -> 31.2 us, 48 rows (groups of
-      // 64) 55.7 -> 53.3, 128 rows 63.8 -> 61.0; no size lost.
+      // back all that it used, and one or two warps (kIssuers).
       const int turn = warp >> 1;
       if (turn) rx.next(), rs.next();
-      for (int b = b0 + turn; b < b1; b += 2) {
+      for (int b = b0 + turn; b < b1; b += C::kIssuers) {
         if (!wait(x_full(rx.s), rx.ph, p, 1) || !wait(a_full(rs.s), rs.ph, p, 1)) break;
         ptx::tc_fence_after();
         const uint64_t desc = desc0 + static_cast<uint32_t>(rx.s * (C::kXBytes >> 4));
@@ -310,8 +314,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
           mma_f16_ts(stage + 64 + (k16 / (2 * GC)) * MT, stage + k16 * 8,
                      desc + ((k16 >> 2) * (C::kXBytes >> 5) + (k16 & 3) * 2), idesc, k16 % (2 * GC) != 0 ? 1u : 0u);
         ptx::mma_commit(d_full(rs.s));
-        rx.next(), rx.next();
-        rs.next(), rs.next();
+#pragma unroll
+        for (int i = 0; i < C::kIssuers; ++i) rx.next(), rs.next();
       }
       ptx::mma_commit(drain);
       if (!ptx::mbar_try_wait(drain, 0)) wait_slow(drain, 0, p, kErrTimeout | (1u << 24), false);
