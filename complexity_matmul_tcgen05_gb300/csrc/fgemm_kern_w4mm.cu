@@ -120,7 +120,9 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 
 // 16 bytes of a ring's stage.  Volatile: the read stays between the wait for
-// the stage and the arrival that hands it back.
+// the stage and the arrival that hands it back.  Before that arrival the reader
+// needs fence.proxy.async: the barrier orders a copy's writes before reads, but
+// not reads of the generic proxy before the next copy's writes.
 __device__ __forceinline__ uint4 ring_read(uint32_t at) {
   uint4 v;
   asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -358,10 +360,12 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
       }
       tmem_wait_st();
       ptx::tc_fence_before();
+      ptx::fence_proxy_async_smem();
       __syncwarp();
-      // The codes' stage goes back only now that what was made of it has been
-      // stored: handed back behind the reads, before the wait for the operand's
-      // stage, it was overwritten while rows of it were still to be read.
+      // The codes' stage goes back when what was made of it has been stored.
+      // Handed back right behind the reads, without the fence and before the
+      // wait for the operand's stage, it was overwritten while rows of it were
+      // still to be read.
       if (lane == 0) {
         ptx::mbar_arrive(a_full(rs.s));
         ptx::mbar_arrive(code_empty(rc.s));
@@ -437,6 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
           to[1] = fma2(s2, fma2(z2, x1, pair(__uint_as_float(acc[4 * q + 2]), __uint_as_float(acc[4 * q + 3]))), to[1]);
         }
       }
+      ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(x_empty(rx.s));
     }
