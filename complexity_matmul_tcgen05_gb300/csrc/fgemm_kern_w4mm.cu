@@ -20,6 +20,12 @@
 // may begin before the pre-pass ends (programmatic dependent launch): its
 // codes are on their way by then.
 //
+// What bounds it: the fold's chain (products done -> tensor memory -> scale, add
+// -> room for the next), not the tensor pipe (31 % active) nor memory.  Measured:
+// 48 x 8192 x 8192 fp16, groups of 64, 34 us; 2048 x 4096 x 14336 bf16, groups of
+// 128, 361 us, 666 TFLOP/s.  Expanding ahead of the products, with rings of their
+// own for operand and accumulators, gave 361.0 against 361.5.
+//
 // Roles: warp 0 loads the codes, warp 2 A, warp 1 or warps 1 and 3 issue the MMAs, warps 4..
 // expand the codes, the last 4 or 8 warps fold.  Every wait is bounded; a wait that runs out latches the
 // error word and all roles leave.
