@@ -22,11 +22,10 @@
 //
 // What bounds it: the fold's chain (products done -> tensor memory -> scale, add
 // -> room for the next), not the tensor pipe (31 % active) nor memory.  Measured:
-// 48 x 8192 x 8192 fp16, groups of 64, 34 us; 2048 x 4096 x 14336 bf16, groups of
-// 128, 361 us, 666 TFLOP/s.  Expanding ahead of the products, with rings of their
-// own for operand and accumulators, gave 361.0 against 361.5.
+// 48 x 8192 x 8192 fp16, groups of 64, 32 us; 2048 x 4096 x 14336 bf16, groups of
+// 128, 340 us, 708 TFLOP/s.
 //
-// Roles: warp 0 loads the codes, warp 2 A, warp 1 or warps 1 and 3 issue the MMAs, warps 4..
+// Roles: warp 0 loads the codes, warp 2 A, warps 1 and 3 issue the MMAs, warps 4..
 // expand the codes, the last 4 or 8 warps fold.  Every wait is bounded; a wait that runs out latches the
 // error word and all roles leave.
 #include <cuda_bf16.h>
@@ -48,8 +47,8 @@ constexpr int kBlock = 128;  // k of one pipeline step: 64 bytes of codes a row
 constexpr int kThreads = 512;
 constexpr int kCodeBytes = kRows * 64;
 
-// Most rows of A a tile takes: the accumulators of a step's groups and the
-// expanded codes of at least two steps fit in tensor memory.
+// Most rows of A a tile takes: the accumulators of two steps' groups fit in
+// tensor memory beside the expanded codes.
 constexpr int kMostRows[3] = {32, 64, 128};  // groups of 32, 64, 128
 
 template <int MT, int GROUPS>  // groups of a step
@@ -57,25 +56,33 @@ struct Cfg {
   static constexpr int kFoldWarps = MT >= 64 ? 8 : 4;
   static constexpr int kCols = MT == 128 ? 64 : MT < 32 ? MT : 32;  // of A's rows, a fold warp's
   static constexpr int kExpandWarps = 12 - kFoldWarps;
-  // A stage of tensor memory: 64 columns of expanded codes, and GROUPS
-  // accumulators.
-  static constexpr int kStageCols = 64 + GROUPS * MT;
-  static constexpr int kStages = 512 / kStageCols < 4 ? 2 : 4;
+  // Tensor memory: four stages of 64 columns of expanded codes, then two or
+  // four of GROUPS accumulators each.  Where it is two, the codes' stages go
+  // back on their own as soon as they have been multiplied (kAhead), so that
+  // codes are expanded while both accumulators are multiplied or folded; where
+  // it is four, both go back together: 8192 x 16384, 32 rows (groups of 64) 43.3 us
+  // on their own against 41.1 together, 16 rows (128) 32.1 against 31.4.
+  static constexpr int kAStages = 4;
+  static constexpr int kDCols = GROUPS * MT;
+  static constexpr int kDAt = kAStages * 64;
+  static constexpr int kDStages = (512 - kDAt) / kDCols < 4 ? 2 : 4;
   static constexpr int kXBytes = MT * 256;            // A's rows of one step
   static constexpr int kSxBytes = GROUPS * MT * 4;    // sums of its groups
   static constexpr int kXStages = MT == 128 ? 4 : 6;
   static constexpr int kCodeStages = MT == 128 ? 8 : 10;
-  static constexpr int kBars = 2 * kCodeStages + 2 * kXStages + 3 * kStages + 1;
+  static constexpr int kBars = 2 * kCodeStages + 2 * kXStages + 2 * kAStages + 2 * kDStages + 1;
   static constexpr int kSmem = 1024 + kCodeStages * kCodeBytes + kXStages * (kXBytes + kSxBytes) + 8 * kBars + 16;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(MT * kRows * 4 <= kCodeStages * kCodeBytes + kXStages * kXBytes, "the sums reuse the rings");
-  static_assert(kStages == 2 || kStages == 4, "tensor memory");
-  // Warps that issue the products, a step each in turn: two when four steps are
-  // under way, one when it is two.  One against two, 8192 x 16384: four steps,
-  // 16 rows (groups of 128) 42.6 -> 32.6 us, 32 rows (64) 45.7 -> 43.6, 64 rows
-  // (128) 46.5 -> 46.2; two steps, 32 rows (32) 53.9 -> 56.7, 64 rows (64) 53.5 ->
-  // 55.3, 128 rows (128) 63.0 -> 65.0.
-  static constexpr int kIssuers = kStages == 4 ? 2 : 1;
+  static constexpr bool kAhead = kDStages < kAStages;
+  // Warps that issue the products, a step each in turn.  Two accumulators,
+  // codes' stages and accumulators handed back together and one warp / on
+  // their own and one warp / on their own and two warps: 2048 x 4096 x 14336
+  // (groups of 128) 361 / 361 / 340 us, 8192 x 16384 with 128 rows (64) 107 / 103 /
+  // 101, 32 rows (32) 60 / 58 / 54.  Four, on their own, one warp against two: 16
+  // rows (128) 46.3 / 32.1, 32 rows (64) 52.5 / 43.3.
+  static constexpr int kIssuers = 2;
+  static_assert(kDAt + kDStages * kDCols <= 512 && kDStages % kIssuers == 0, "tensor memory");
 };
 
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
@@ -209,9 +216,11 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
   auto x_full = [&](int s) { return bar0 + 8u * (2 * C::kCodeStages + s); };
   auto x_empty = [&](int s) { return bar0 + 8u * (2 * C::kCodeStages + C::kXStages + s); };
   constexpr int kABar = 2 * C::kCodeStages + 2 * C::kXStages;
-  auto a_full = [&](int s) { return bar0 + 8u * (kABar + s); };                    // codes expanded
-  auto d_full = [&](int s) { return bar0 + 8u * (kABar + C::kStages + s); };       // products done
-  auto s_empty = [&](int s) { return bar0 + 8u * (kABar + 2 * C::kStages + s); };  // products read
+  constexpr int kDBar = kABar + 2 * C::kAStages;
+  auto a_full = [&](int s) { return bar0 + 8u * (kABar + s); };                 // codes expanded
+  auto a_empty = [&](int s) { return bar0 + 8u * (kABar + C::kAStages + s); };  // multiplied
+  auto d_full = [&](int s) { return bar0 + 8u * (kDBar + s); };                 // products done
+  auto d_empty = [&](int s) { return bar0 + 8u * (kDBar + C::kDStages + s); };  // products read
   const uint32_t drain = bar0 + 8u * (C::kBars - 1);
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + kBar + 8 * C::kBars);
 
@@ -232,10 +241,13 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
       ptx::mbar_init(x_full(s), 1);
       ptx::mbar_init(x_empty(s), FW);
     }
-    for (int s = 0; s < C::kStages; ++s) {
+    for (int s = 0; s < C::kAStages; ++s) {
       ptx::mbar_init(a_full(s), 4);
+      ptx::mbar_init(a_empty(s), 1);
+    }
+    for (int s = 0; s < C::kDStages; ++s) {
       ptx::mbar_init(d_full(s), 1);
-      ptx::mbar_init(s_empty(s), FW);
+      ptx::mbar_init(d_empty(s), FW);
     }
     ptx::mbar_init(drain, C::kIssuers);
     ptx::fence_mbar_init();
@@ -300,30 +312,36 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
     __syncwarp();
   } else if (warp == 1 || (C::kIssuers == 2 && warp == 3)) {
     // ---------------------------------------------------------- MMA
+    // (The condition as `warp == 1 || warp == 3` becomes one comparison, and the
+    // loop behind it slower: 2048 x 4096 x 14336 351 us instead of 340, 8192 x 16384
+    // with 32 rows 42 instead of 36.)
     if (lane == 0) {
       // fp32 accumulator, fp16 operands, both K-major, N = MT, M = 128
       constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(MT >> 3) << 17) | ((128u >> 4) << 24);
       const uint64_t desc0 = ptx::sdesc(x_at(0), 16, 1024);
       Ring<C::kXStages> rx;
-      Ring<C::kStages> rs;
+      Ring<C::kAStages> ra;
+      Ring<C::kDStages> rd;
       // A step's products are issued by one thread, whose time counts (16 rows:
       // 590 clocks for the 8 products, 390 to tell the fold warps and to find
       // the next step ready): one commit a step, on which the fold warps hand
-      // back all that it used, and one or two warps (kIssuers).
+      // back what it used, and two warps.
       const int turn = warp >> 1;
-      if (turn) rx.next(), rs.next();
+      if (turn) rx.next(), ra.next(), rd.next();
       for (int b = b0 + turn; b < b1; b += C::kIssuers) {
-        if (!wait(x_full(rx.s), rx.ph, p, 1) || !wait(a_full(rs.s), rs.ph, p, 1)) break;
+        if (!wait(x_full(rx.s), rx.ph, p, 1) || !wait(a_full(ra.s), ra.ph, p, 1) ||
+            (C::kAhead && !wait(d_empty(rd.s), rd.ph ^ 1u, p, 1)))
+          break;
         ptx::tc_fence_after();
         const uint64_t desc = desc0 + static_cast<uint32_t>(rx.s * (C::kXBytes >> 4));
-        const uint32_t stage = tmem + rs.s * C::kStageCols;
+        const uint32_t a = tmem + ra.s * 64, d = tmem + C::kDAt + rd.s * C::kDCols;
 #pragma unroll
         for (int k16 = 0; k16 < 8; ++k16)
-          mma_f16_ts(stage + 64 + (k16 / (2 * GC)) * MT, stage + k16 * 8,
+          mma_f16_ts(d + (k16 / (2 * GC)) * MT, a + k16 * 8,
                      desc + ((k16 >> 2) * (C::kXBytes >> 5) + (k16 & 3) * 2), idesc, k16 % (2 * GC) != 0 ? 1u : 0u);
-        ptx::mma_commit(d_full(rs.s));
+        ptx::mma_commit(d_full(rd.s));
 #pragma unroll
-        for (int i = 0; i < C::kIssuers; ++i) rx.next(), rs.next();
+        for (int i = 0; i < C::kIssuers; ++i) rx.next(), ra.next(), rd.next();
       }
       ptx::mma_commit(drain);
       if (!ptx::mbar_try_wait(drain, 0)) wait_slow(drain, 0, p, kErrTimeout | (1u << 24), false);
@@ -339,17 +357,17 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
     constexpr int SETS = EW / 4;  // sets of four warps, which take steps in turn
     const int set = (warp - 4) >> 2;
     Ring<C::kCodeStages> rc;
-    Ring<C::kStages> rs;
-    for (int b = b0; b < b1; ++b, rc.next(), rs.next()) {
+    Ring<C::kAStages> ra;
+    for (int b = b0; b < b1; ++b, rc.next(), ra.next()) {
       if (SETS > 1 && (b - b0) % SETS != set) continue;
       if (!wait_warp(code_full(rc.s), rc.ph, p, 3)) break;
       uint4 w[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c)
         w[c] = ring_read(code_at(rc.s) + sr * 64 + ((c ^ sw) << 4));
-      if (!wait_warp(s_empty(rs.s), rs.ph ^ 1u, p, 3)) break;
+      if (!wait_warp(C::kAhead ? a_empty(ra.s) : d_empty(ra.s), ra.ph ^ 1u, p, 3)) break;
       ptx::tc_fence_after();
-      const uint32_t to = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + rs.s * C::kStageCols;
+      const uint32_t to = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + ra.s * 64;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t e[32];
@@ -373,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
       // wait for the operand's stage, it was overwritten while rows of it were
       // still to be read.
       if (lane == 0) {
-        ptx::mbar_arrive(a_full(rs.s));
+        ptx::mbar_arrive(a_full(ra.s));
         ptx::mbar_arrive(code_empty(rc.s));
       }
     }
@@ -402,9 +420,10 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
     fetch(b0);
     float s[KEEP], z[KEEP];
     Ring<C::kXStages> rx;
-    Ring<C::kStages> rs;
+    Ring<C::kAStages> ra;
+    Ring<C::kDStages> rd;
 #pragma unroll 1
-    for (int b = b0; b < b1; ++b, rx.next(), rs.next()) {
+    for (int b = b0; b < b1; ++b, rx.next(), ra.next(), rd.next()) {
       if ((b - b0) % AHEAD == 0) {
 #pragma unroll
         for (int i = 0; i < KEEP; ++i) {
@@ -417,13 +436,19 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
         for (int i = 0; i + GROUPS < KEEP; ++i) s[i] = s[i + GROUPS], z[i] = z[i + GROUPS];
       }
       {
-        const bool x = ptx::mbar_try_wait(x_full(rx.s), rx.ph), d = ptx::mbar_try_wait(d_full(rs.s), rs.ph);
+        const bool x = ptx::mbar_try_wait(x_full(rx.s), rx.ph), d = ptx::mbar_try_wait(d_full(rd.s), rd.ph);
         if (!__all_sync(0xFFFFFFFFu, x && d) &&
-            !(wait_warp(x_full(rx.s), rx.ph, p, 2) && wait_warp(d_full(rs.s), rs.ph, p, 2)))
+            !(wait_warp(x_full(rx.s), rx.ph, p, 2) && wait_warp(d_full(rd.s), rd.ph, p, 2)))
           break;
       }
       ptx::tc_fence_after();
-      const uint32_t from = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + rs.s * C::kStageCols + 64 + col0;
+      if (C::kAhead && warp == 4 + EW) {  // the step's operand has been multiplied; one warp says so
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(a_empty(ra.s));
+      }
+      const uint32_t from =
+          tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + C::kDAt + rd.s * C::kDCols + col0;
 #pragma unroll
       for (int i = 0; i < GROUPS * COLS / PART; ++i) {
         const int grp = i / (COLS / PART), c0 = i % (COLS / PART) * PART;
@@ -433,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
         if (i + 1 == GROUPS * COLS / PART) {  // all of the step has been read
           ptx::tc_fence_before();
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(s_empty(rs.s));
+          if (lane == 0) ptx::mbar_arrive(d_empty(rd.s));
         }
         const uint64_t s2 = pair(s[grp], s[grp]), z2 = pair(z[grp], z[grp]);
         const uint32_t sx = sx_at(rx.s) + (grp * MT + col0 + c0) * 4;
