@@ -616,10 +616,12 @@ __device__ Threshold find_threshold(const S& slice, SampleShared& sh, cg::cluste
       lo = top - lo > width ? top - width : lo;
       hi = top;
     }
+    // sel_bin, sel_before and range have been read: the next round, or the next
+    // search, writes sel_bin before its first barrier
+    __syncthreads();
     if (lo >= hi) break;
     const int bits = 32 - __clz(hi - lo);
     shift = bits > 10 ? bits - 10 : 0;
-    __syncthreads();
   }
   res.key = lo;
   return res;
