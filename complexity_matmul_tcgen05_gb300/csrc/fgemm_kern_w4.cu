@@ -61,6 +61,34 @@ constexpr int kW4Stages = 3;
 template <int GC>
 constexpr int kW4ABytes = (GC > 1 ? 64 : 48) * 1024;
 
+// Shared memory of a CTA: the rings of codes and of scales, A's `chunk` values
+// of m rows with the sums of their groups (64 bytes a group whatever m is, as
+// much as A itself for one row in groups of 32), the warps' and teams' sums.
+constexpr size_t kW4MostSmem = 227 * 1024;
+template <int GC>
+constexpr size_t w4_few_fixed(int m) {
+  return static_cast<size_t>(kW4Teams * kW4Warps) * kW4Stages * kW4Rows * (64 + 4 / GC * 8) +
+         static_cast<size_t>(kW4Teams * (kW4Warps + 2)) * kW4Rows * m * 4;
+}
+template <int GC>
+constexpr size_t w4_few_smem(int m, int chunk) {
+  return w4_few_fixed<GC>(m) + static_cast<size_t>(chunk) * 2 * m + static_cast<size_t>(chunk / (GC * 32)) * 64;
+}
+// Most k of A a CTA keeps: A's own bound, and what is left beside the rest.
+template <int GC>
+constexpr int w4_most_chunk(int m) {
+  const size_t left = (kW4MostSmem - w4_few_fixed<GC>(m)) * (GC * 32) / (2 * m * GC * 32 + 64);
+  const size_t own = kW4ABytes<GC> / (2 * m);
+  return static_cast<int>((left < own ? left : own) / 256 * 256);
+}
+template <int GC>
+constexpr bool w4_few_fits() {
+  for (int m = 1; m <= kW4FewRows; ++m)
+    if (w4_most_chunk<GC>(m) < 8 * kW4Block || w4_few_smem<GC>(m, w4_most_chunk<GC>(m)) > kW4MostSmem) return false;
+  return true;
+}
+static_assert(w4_few_fits<1>() && w4_few_fits<2>() && w4_few_fits<4>(), "shared memory, for every number of rows");
+
 // 16 bytes global -> shared; bytes past `valid` (0..16) are zero and not read.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid) : "memory");
@@ -430,16 +458,14 @@ cudaError_t launch_w4_few(W4Params p, int num_sms, cudaStream_t stream) {
   // K is cut into slices, a CTA of a cluster each: while there are SMs without
   // a tile and every warp keeps a block, and until A's slice fits
   int slices = 1;
-  const int most_chunk = kW4ABytes<GC> / (2 * p.m) / 256 * 256;
+  const int most_chunk = w4_most_chunk<GC>(p.m);
   while (slices < 8 && blocks >= 2 * slices * kW4Warps && static_cast<long long>(p.tiles) * slices * 2 <= num_sms * kW4Teams)
     slices *= 2;
   while (slices < 8 && (blocks + slices - 1) / slices * kW4Block > most_chunk) slices *= 2;
   p.slices = slices;
   p.slice = ((blocks + slices - 1) / slices * kW4Block + 255) / 256 * 256;
   p.chunk = p.slice < most_chunk ? (p.slice > 0 ? p.slice : 256) : most_chunk;
-  const size_t smem = static_cast<size_t>(kW4Teams * kW4Warps) * kW4Stages * kW4Rows * (64 + 4 / GC * 8) +
-                      static_cast<size_t>(p.chunk) * 2 * p.m + static_cast<size_t>(p.chunk / (GC * 32)) * 8 * 8 +
-                      static_cast<size_t>(kW4Teams * (kW4Warps + 2)) * kW4Rows * p.m * 4;
+  const size_t smem = w4_few_smem<GC>(p.m, p.chunk);
   auto kernel = w4_kernel<BF16, GC>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;

@@ -1,11 +1,13 @@
 """The operators of a token step at the edges of what their documentation
 admits: long K with few rows, ties behind a long top-k, activations and rows
 far from 1, infinities, in-place outputs."""
+import numpy as np
 import pytest
 import torch
 
+import token_reference as ref
 from complexity_matmul_tcgen05_gb300 import fgemm
-from test_token_ops_gpu import DEV, TYPES, check_sample, gen, rand
+from test_token_ops_gpu import DEV, TYPES, check_sample, gen, rand, w4_inputs, within
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +36,59 @@ def test_sample_top_p_behind_a_long_top_k(kind, dtype):
         for _ in range(20):
             again = fgemm.sample(x, u, **kw)
             assert torch.equal(again[0], token) and torch.equal(again[1], prob)
+
+
+# ----------------------------------------------------------------------- w4
+
+
+def w4_terms(A, W, scales, zeros, group):
+    """(C, magnitude, lost) in 64 bits: the product, the sum of its terms'
+    magnitudes |A| |q - z| |s|, and what operands of 11 bits drop of a group's
+    small values: 2^-35 of its largest for each term."""
+    k = A.shape[1]
+    at = np.arange(k) // group
+    s = scales[:, at]
+    z = np.full_like(s, 8.0) if zeros is None else zeros.astype(np.float64)[:, at]
+    q = ref.w4_codes(W, k) - z
+    lost = np.zeros((A.shape[0], W.shape[0]))
+    for k0 in range(0, k, group):
+        most = np.max(np.abs(A[:, k0:k0 + group]), axis=1)
+        lost += np.outer(most, np.sum(np.abs(q[:, k0:k0 + group] * s[:, k0:k0 + group]), axis=1))
+    return A @ (q * s).T, np.abs(A) @ np.abs(q * s).T, lost * 2.0 ** -35
+
+
+def w4_close(C, A, W, scales, zeros, group, cols=None):
+    """C is the product to what its own terms allow, nothing wider: a product
+    step adds 16 terms and the running sum, each cut to 24 bits; then one
+    addition a group, and at most 32 over warps, slices and the epilogue."""
+    if cols is not None:
+        C, W, scales = C[:, cols], W[cols], scales[cols]
+        zeros = None if zeros is None else zeros[cols]
+    k = A.shape[1]
+    want, mag, lost = w4_terms(ref.f64(A), W.cpu().numpy(), ref.f64(scales), None if zeros is None else zeros.cpu().numpy(),
+                               group)
+    within("w4 terms", C, want, (17 / 16 * group + k / group + 32) * ref.U32 * mag + lost + ref.store(want, A.dtype))
+
+
+@pytest.mark.parametrize("k", [20736, 22016, 24576, 45056, 180224])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_w4_one_row_of_a_long_k(k, zeros):
+    n = 64 if k > 100000 else 8192  # many columns: K is cut only as far as A has to be
+    A, W, s, z, _ = w4_inputs(1, n, k, "bf16", 32, zeros, k)
+    C = fgemm.matmul_w4(A, W, s, zeros=z, group=32)
+    w4_close(C, A, W, s, z, 32, torch.arange(0, n, n // 64, device=DEV))
+
+
+@pytest.mark.parametrize("m,k,group", [(8, 28672, 32), (8, 33000, 32), (5, 53248, 128), (8, 53248, 128), (7, 40000, 64),
+                                       (1, 200000, 32), (2, 140000, 64)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_w4_few_rows_whose_a_is_loaded_in_parts(m, k, group, dtype):
+    """K above what eight CTAs keep of A in shared memory."""
+    n = 100  # an odd number of tiles, the last of them ragged
+    A, W, s, z, bias = w4_inputs(m, n, k, dtype, group, True, m + k)
+    C = fgemm.matmul_w4(A, W, s, zeros=z, group=group)
+    w4_close(C, A, W, s, z, group)
+    C = fgemm.matmul_w4(A, W, s, zeros=z, group=group, bias=bias, epilogue="swiglu")
+    want, bound = ref.w4(ref.f64(A), W.cpu().numpy(), ref.f64(s), z.cpu().numpy(), group, 1.0, ref.f64(bias), "swiglu",
+                         A.dtype)
+    within("w4 swiglu", C, want, bound)
