@@ -170,7 +170,10 @@ fgemm_status_t set_msg(fgemm_handle_t h, fgemm_status_t s, const std::string& te
   return s;
 }
 
+// The error is told here; the runtime's own record of it must not be found by
+// the next call that asks whether its launch went well.
 fgemm_status_t cuda_fail(fgemm_handle_t h, cudaError_t e, const char* what) {
+  cudaGetLastError();
   std::string t = std::string(what) + ": " + cudaGetErrorString(e);
   return set_msg(h, FGEMM_ERR_CUDA, t);
 }

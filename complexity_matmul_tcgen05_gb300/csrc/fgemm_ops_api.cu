@@ -25,7 +25,9 @@ fgemm_status_t no_handle() { return bad(nullptr, FGEMM_ERR_INVALID_ARG, "handle 
 fgemm_status_t nothing(fgemm_handle_t h) { return h ? FGEMM_OK : no_handle(); }
 
 fgemm_status_t launched(fgemm_handle_t h, cudaError_t e) {
-  return e == cudaSuccess ? FGEMM_OK : bad(h, FGEMM_ERR_CUDA, cudaGetErrorString(e));
+  if (e == cudaSuccess) return FGEMM_OK;
+  cudaGetLastError();  // told here, not again by the next call's launch
+  return bad(h, FGEMM_ERR_CUDA, cudaGetErrorString(e));
 }
 
 bool off(const void* p, uintptr_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }

@@ -43,6 +43,7 @@ void* g_scratch_addr[kMaxDevices] = {nullptr};
 int g_num_sms[kMaxDevices] = {0};
 
 fgemm_status_t fail(fgemm_status_t s, const std::string& text) {
+  if (s == FGEMM_ERR_CUDA) cudaGetLastError();  // told here, not again by the next call's launch
   fgemm::set_thread_message(text);
   return s;
 }

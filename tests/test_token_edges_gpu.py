@@ -1,6 +1,8 @@
 """The operators of a token step at the edges of what their documentation
 admits: long K with few rows, ties behind a long top-k, activations and rows
 far from 1, infinities, in-place outputs."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -92,3 +94,25 @@ def test_w4_few_rows_whose_a_is_loaded_in_parts(m, k, group, dtype):
     want, bound = ref.w4(ref.f64(A), W.cpu().numpy(), ref.f64(s), z.cpu().numpy(), group, 1.0, ref.f64(bias), "swiglu",
                          A.dtype)
     within("w4 swiglu", C, want, bound)
+
+
+# ------------------------------------------------------------------- errors
+
+
+def test_an_error_is_reported_once():
+    """A call that failed leaves nothing behind for the next one to report."""
+    x, gain = torch.randn(3, 64, device=DEV).half(), torch.ones(64, device=DEV).half()
+    want = fgemm.rms_norm(x, gain)[0]
+    torch.cuda.synchronize()
+    rt = ctypes.CDLL("libcudart.so.13")
+    h, L = fgemm.default_handle(), fgemm.lib()
+    side = torch.cuda.Stream()
+    stream, graph = ctypes.c_void_p(side.cuda_stream), ctypes.c_void_p()
+    assert rt.cudaStreamBeginCapture(stream, 2) == 0  # relaxed
+    L.fgemm_set_stream(h._h, stream)
+    failed = L.fgemm_get_error(h._h)  # it would wait for a stream that is being captured
+    rt.cudaStreamEndCapture(stream, ctypes.byref(graph))
+    rt.cudaGetLastError()  # torch's own copy of the runtime
+    assert failed == fgemm.ERR_CUDA
+    assert torch.equal(fgemm.rms_norm(x, gain)[0], want)
+    assert h.get_error() == fgemm.OK
