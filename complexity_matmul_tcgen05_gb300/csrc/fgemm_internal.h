@@ -420,8 +420,7 @@ struct W4Params {
   // (tcgen05) of each, k of A kept in shared memory
   int tiles, slices, slice, chunk;
   uint16_t* x;   // m x k_pad packed A
-  float* sx;     // groups x m_pad sums
-  float* unit;   // m units
+  float* units;  // groups x m_pad
   int k_pad;
   long long m_pad;
 };

@@ -9,28 +9,29 @@
 //
 // The codes are never turned into weights: the scale of a group is applied to
 // the fp32 sums of its codes,
-//   sum_k (q - z) s x = s (acc - z sx),   acc = sum_k q x,   sx = sum_k x,
-// so no weight is rounded, and scales and zero points cost a few operations a
-// group instead of one a weight.
+//   sum_k (q - z) s x = s acc,   acc = sum_k (q - z) x,
+// so no weight is rounded, and scales cost a few operations a group instead of
+// one a weight.
 //
 // A code is a 16-bit operand of the tensor cores as it stands: four bits at
 // the bottom of an fp16 number are the subnormal q 2^-24, four bits above them
 // q 2^-20, both exact, so one logical operation makes two operands and one
-// shift serves four.  The factor 2^4 between the two kinds goes into A.  For
-// that, A too is held as fp16, scaled by a power of two for each row and group
-// (the largest value below 2^15; 2^11 for the k whose codes are the upper
-// kind), bf16 as well: its 8 significant bits fit, and what falls below fp16's
-// range is under 2^-35 of the group's largest value, less than the fp32 sums
-// resolve.
-// An infinite or NaN x makes acc - z sx meaningless: an output that is not
-// finite is computed again term by term (w4_exact).
+// shift serves four.  The zero point is taken off there, two codes at a time,
+// and exactly.  (Taken off the group's sum, as z sum_k x, it left 2^-24 of z
+// times an activation whose weight is 0: with one of them 2^20 times the rest,
+// hundreds of times the error of the sum itself.)  The factor 2^4 between the two kinds
+// goes into A.  For that, A too is held as fp16, scaled by a power of two for
+// each row and group (the largest value below 2^15; 2^11 for the k whose codes
+// are the upper kind), bf16 as well: its 8 significant bits fit, and what falls
+// below fp16's range is under 2^-35 of the group's largest value.
+// An output that is not finite is computed again term by term (w4_exact).
 //
-// What bounds it: latency, from the codes' arrival to the tile's last sum, with
-// 1.9 instructions a clock (254 a warp for 4096 weights).  5 x 28672 x 4096,
-// SwiGLU, bf16, groups of 128: 19.2 us, 3.2 TB/s; one row 4096 x 4096: 6.7 us.
-// Measured on the first of these on the way: codes turned into 1 + q/16 with
-// a ring a warp 34.3 us, two teams to a CTA 27.4, codes as subnormals 21.9,
-// A loaded once and scales folded a group at a time 19.2.
+// What bounds it: latency, from the codes' arrival to the tile's last sum.
+// 5 x 28672 x 4096, SwiGLU, bf16, groups of 128: 20.6 us, 3.0 TB/s; one row 4096 x
+// 4096: 6.7 us.  Measured on the first of these on the way: codes turned into
+// 1 + q/16 with a ring a warp 34.3 us, two teams to a CTA 27.4, codes as
+// subnormals 21.9, A loaded once and scales folded a group at a time 19.2, the
+// zero point off each code 20.6.
 //
 // mma.sync with the codes as the 16-row operand and 8 rows of A as the other:
 // the operand goes from the ring in shared memory through registers, where
@@ -62,8 +63,8 @@ template <int GC>
 constexpr int kW4ABytes = (GC > 1 ? 64 : 48) * 1024;
 
 // Shared memory of a CTA: the rings of codes and of scales, A's `chunk` values
-// of m rows with the sums of their groups (64 bytes a group whatever m is, as
-// much as A itself for one row in groups of 32), the warps' and teams' sums.
+// of m rows with the units of their groups (32 bytes a group whatever m is,
+// half as much as A itself for one row in groups of 32), the warps' and teams' sums.
 constexpr size_t kW4MostSmem = 227 * 1024;
 template <int GC>
 constexpr size_t w4_few_fixed(int m) {
@@ -72,12 +73,12 @@ constexpr size_t w4_few_fixed(int m) {
 }
 template <int GC>
 constexpr size_t w4_few_smem(int m, int chunk) {
-  return w4_few_fixed<GC>(m) + static_cast<size_t>(chunk) * 2 * m + static_cast<size_t>(chunk / (GC * 32)) * 64;
+  return w4_few_fixed<GC>(m) + static_cast<size_t>(chunk) * 2 * m + static_cast<size_t>(chunk / (GC * 32)) * 32;
 }
 // Most k of A a CTA keeps: A's own bound, and what is left beside the rest.
 template <int GC>
 constexpr int w4_most_chunk(int m) {
-  const size_t left = (kW4MostSmem - w4_few_fixed<GC>(m)) * (GC * 32) / (2 * m * GC * 32 + 64);
+  const size_t left = (kW4MostSmem - w4_few_fixed<GC>(m)) * (GC * 32) / (2 * m * GC * 32 + 32);
   const size_t own = kW4ABytes<GC> / (2 * m);
   return static_cast<int>((left < own ? left : own) / 256 * 256);
 }
@@ -111,7 +112,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 //
 // A sits in shared memory for as long as the CTA lives (when it fits; else a
 // chunk of K at a time), its values already in the order in which expand()
-// pairs codes, with the sums sx of each group beside it.  The codes stream
+// pairs codes, with the unit of each group beside it.  The codes stream
 // through a ring of the warp's own: warp w of a team takes the blocks w,
 // w + 8, ... of 128 k of a tile, so warps wait for each other once a tile,
 // when their sums meet, while the blocks of the next tile are already on
@@ -134,16 +135,16 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
   const int blocks = k_hi > k_lo ? (k_hi - k_lo + kW4Block - 1) / kW4Block : 0;
   const int chunk_blocks = p.chunk / kW4Block;
 
-  // shared memory: the warps' rings of codes and of scales, A, sx, the warps'
+  // shared memory: the warps' rings of codes and of scales, A, its units, the warps'
   // sums, the teams' sums
   constexpr int kSlot = kW4Rows * 64, kScales = kW4Rows * GROUPS;
   unsigned char* const ring = smem + (threadIdx.x >> 5) * (kW4Stages * kSlot);
   float2* const scale_ring = reinterpret_cast<float2*>(smem + kW4Teams * kW4Warps * kW4Stages * kSlot) +
-                             (threadIdx.x >> 5) * (kW4Stages * kScales);  // [group][row]: scale, zero point
+                             (threadIdx.x >> 5) * (kW4Stages * kScales);  // [group][row]: scale, w4_zero
   unsigned char* const a_at = smem + kW4Teams * kW4Warps * kW4Stages * (kSlot + kScales * 8);
   const int a_pitch = p.chunk * 2;
-  float2* const sx_at = reinterpret_cast<float2*>(a_at + static_cast<size_t>(a_pitch) * mt);  // [group of the chunk][8]
-  float* const red = reinterpret_cast<float*>(sx_at + p.chunk / G * 8) + team * ((kW4Warps + 2) * kW4Rows * mt);  // [warp][row of A][row]
+  float* const unit_at = reinterpret_cast<float*>(a_at + static_cast<size_t>(a_pitch) * mt);  // [group of the chunk][8]
+  float* const red = unit_at + p.chunk / G * 8 + team * ((kW4Warps + 2) * kW4Rows * mt);  // [warp][row of A][row]
   float* const part = red + kW4Warps * kW4Rows * mt;  // [2][row of A][row], read by the cluster
   const int w_bytes = (p.k + 1) / 2 - k_lo / 2;  // of a row, from this CTA's first
   const int groups = (p.k + G - 1) / G;
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
 #pragma unroll
     for (int i = 0; i < GROUPS; ++i)
       scale_ring[before * kScales + i * kW4Rows + lane] =
-          make_float2(w4_f32<BF16>(s_next[i]), __uint_as_float(0x4B000000u | z_next[i]) - 8388608.0f);
+          make_float2(w4_f32<BF16>(s_next[i]), __uint_as_float(w4_zero(z_next[i])));
     if (load_tile < p.tiles) {
       const int block = load_chunk + load_b, byte = block * (kW4Block / 2);
       // 16-byte chunk c of row r at chunk c ^ (r >> 1 & 3)
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
     return x;
   };
   // A's rows of one chunk into shared memory as scaled fp16, each run of 8
-  // values in the order 0 4 1 5 2 6 3 7, and for each group its scale and sum.
+  // values in the order 0 4 1 5 2 6 3 7, and for each group its unit.
   // The G / 8 lanes that hold a group agree on its largest value.
   // begin(), once, runs between the first loads and their use.
   const int runs = p.chunk / 8;  // of a row of the chunk, a multiple of 32: a warp is in one row
@@ -275,19 +276,13 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
           const uint32_t pair = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
                                          __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
           uint32_t most = max(pair & 0xFFFFu, pair >> 16);
-          float v[8], s = 0.0f;
+          float v[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            v[j] = w4_f32<BF16>(static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1))));
-            s += v[j];
-          }
+          for (int j = 0; j < 8; ++j) v[j] = w4_f32<BF16>(static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1))));
 #pragma unroll
-          for (int o = 1; o < G / 8; o <<= 1) {
-            most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-            s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-          }
+          for (int o = 1; o < G / 8; o <<= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
           const int e = w4_shift<BF16>(most);
-          if (run % (G / 8) == 0) sx_at[run / (G / 8) * 8 + m] = make_float2(s, w4_pow2(24 - e));
+          if (run % (G / 8) == 0) unit_at[run / (G / 8) * 8 + m] = w4_pow2(24 - kW4Up - e);
           const float even = w4_pow2(e), odd = even * 0.0625f;
           uint32_t o[4];
 #pragma unroll
@@ -355,10 +350,14 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
 #pragma unroll
         for (int grp = 0; grp < GROUPS; ++grp) {
           float acc[R][4];
+          uint32_t zero[R][2];
 #pragma unroll
-          for (int r = 0; r < R; ++r)
+          for (int r = 0; r < R; ++r) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[r][i] = 0.0f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) zero[r][h] = __float_as_uint(scales[grp * kW4Rows + r * 16 + h * 8].y);
+          }
 #pragma unroll
           for (int cc = 0; cc < GC; ++cc) {
             const int c = grp * GC + cc;
@@ -367,24 +366,24 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
 #pragma unroll
             for (int r = 0; r < R; ++r) {
               uint32_t lo[4], hi[4];
-              w4_expand(*reinterpret_cast<const uint32_t*>(at + r * 1024), lo);
-              w4_expand(*reinterpret_cast<const uint32_t*>(at + r * 1024 + 512), hi);
+              w4_expand(*reinterpret_cast<const uint32_t*>(at + r * 1024), zero[r][0], lo);
+              w4_expand(*reinterpret_cast<const uint32_t*>(at + r * 1024 + 512), zero[r][1], hi);
               // the lower kind of codes in one product, the upper in the other
               const uint32_t a0[4] = {lo[0], hi[0], lo[2], hi[2]}, a1[4] = {lo[1], hi[1], lo[3], hi[3]};
               mma16816(acc[r], a0, x.x, x.z);
               mma16816(acc[r], a1, x.y, x.w);
             }
           }
-          // sum and unit of acc, of two rows of A
-          const float4 sx = *reinterpret_cast<const float4*>(sx_at + (b * GROUPS + grp) * 8 + 2 * t);
+          // unit of acc, of two rows of A
+          const float2 unit = *reinterpret_cast<const float2*>(unit_at + (b * GROUPS + grp) * 8 + 2 * t);
 #pragma unroll
           for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const float2 sz = scales[grp * kW4Rows + r * 16 + h * 8];
+              const float scale = scales[grp * kW4Rows + r * 16 + h * 8].x;
               float* to = sum[r] + 2 * h;
-              to[0] = fmaf(sz.x, fmaf(-sz.y, sx.x, acc[r][2 * h] * sx.y), to[0]);
-              to[1] = fmaf(sz.x, fmaf(-sz.y, sx.z, acc[r][2 * h + 1] * sx.w), to[1]);
+              to[0] = fmaf(scale, acc[r][2 * h] * unit.x, to[0]);
+              to[1] = fmaf(scale, acc[r][2 * h + 1] * unit.y, to[1]);
             }
         }
       }
@@ -436,6 +435,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
           for (int w = 0; w < kW4Warps; ++w) s += red[w * mt * kW4Rows + at];
         }
         const long long col = j + static_cast<long long>(h) * p.n_out;
+        s *= static_cast<float>(1 << kW4Up);
         if (!isfinite(s)) s = w4_exact<BF16>(p, i, col);
         v[h] = p.alpha * s + (p.bias ? w4_f32<BF16>(p.bias[col]) : 0.0f);
       }

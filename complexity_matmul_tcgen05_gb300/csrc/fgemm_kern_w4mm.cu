@@ -4,19 +4,19 @@
 //
 //   C[i][j] = epi(alpha * sum_k A[i][k] (q[j][k] - z[j][k/G]) s[j][k/G] + bias[j])
 //
-// As there, codes are never turned into weights: with acc = sum_k q x and
-// sx = sum_k x over a group, the group's part is s (acc - z sx), added to a
-// running fp32 sum.  A tile is 128 rows of W (the tensor core's rows) by MT
-// rows of A.  Its codes go TMA -> shared memory -> registers, where a logical
-// operation makes two fp16 operands (the subnormals q 2^-24 and q 2^-20) ->
-// tensor memory; the product of a group is 2 to 8 MMAs into an accumulator of
+// As there, codes are never turned into weights: with acc = sum_k (q - z) x
+// over a group, the group's part is s acc, added to a running fp32 sum.  A tile
+// is 128 rows of W (the tensor core's rows) by MT rows of A.  Its codes go TMA
+// -> shared memory -> registers, where a logical operation makes two fp16
+// operands (the subnormals q 2^-24 and q 2^-20) and a subtraction takes z off
+// -> tensor memory; the product of a group is 2 to 8 MMAs into an accumulator of
 // its own, which the fold warps read once, scale and add in registers.  So a
-// weight costs about one ALU operation and nothing is rounded but the output;
-// the fold costs 2 fp32 operations for every group, row and column, against
-// 2 G of the product.
+// weight costs about one and a half ALU operations and nothing is rounded but
+// the output; the fold costs 2 fp32 operations for every group, row and column
+// (the unit of the row's group, the column's scale), against 2 G of the product.
 //
 // A pre-pass (w4_pack_kernel) writes A as scaled fp16 in the order of the
-// codes' pairs, with sx of each group.  The main kernel is launched so that it
+// codes' pairs, with the unit of each group.  The main kernel is launched so that it
 // may begin before the pre-pass ends (programmatic dependent launch): its
 // codes are on their way by then.
 //
@@ -67,11 +67,11 @@ struct Cfg {
   static constexpr int kDAt = kAStages * 64;
   static constexpr int kDStages = (512 - kDAt) / kDCols < 4 ? 2 : 4;
   static constexpr int kXBytes = MT * 256;            // A's rows of one step
-  static constexpr int kSxBytes = GROUPS * MT * 4;    // sums of its groups
+  static constexpr int kUnitBytes = GROUPS * MT * 4;  // units of its groups
   static constexpr int kXStages = MT == 128 ? 4 : 6;
   static constexpr int kCodeStages = MT == 128 ? 8 : 10;
   static constexpr int kBars = 2 * kCodeStages + 2 * kXStages + 2 * kAStages + 2 * kDStages + 1;
-  static constexpr int kSmem = 1024 + kCodeStages * kCodeBytes + kXStages * (kXBytes + kSxBytes) + 8 * kBars + 16;
+  static constexpr int kSmem = 1024 + kCodeStages * kCodeBytes + kXStages * (kXBytes + kUnitBytes) + 8 * kBars + 16;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(MT * kRows * 4 <= kCodeStages * kCodeBytes + kXStages * kXBytes, "the sums reuse the rings");
   static constexpr bool kAhead = kDStages < kAStages;
@@ -151,6 +151,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
   uint64_t d;
   asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
@@ -203,13 +208,13 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
   const uint32_t raw = ptx::smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const base_ptr = smem_raw + (base - raw);
-  // X stages first (1024-byte atoms), then codes, sums, barriers
+  // X stages first (1024-byte atoms), then codes, units, barriers
   auto x_at = [&](int s) { return base + s * C::kXBytes; };
   constexpr int kCodes = C::kXStages * C::kXBytes;
-  constexpr int kSx = kCodes + C::kCodeStages * kCodeBytes;
-  constexpr int kBar = kSx + C::kXStages * C::kSxBytes;
+  constexpr int kUnits = kCodes + C::kCodeStages * kCodeBytes;
+  constexpr int kBar = kUnits + C::kXStages * C::kUnitBytes;
   auto code_at = [&](int s) { return base + kCodes + s * kCodeBytes; };
-  auto sx_at = [&](int s) { return base + kSx + s * C::kSxBytes; };
+  auto unit_at = [&](int s) { return base + kUnits + s * C::kUnitBytes; };
   const uint32_t bar0 = base + kBar;
   auto code_full = [&](int s) { return bar0 + 8u * s; };
   auto code_empty = [&](int s) { return bar0 + 8u * (C::kCodeStages + s); };
@@ -301,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
         ptx::tma_load_2d(x_at(rx.s), &p.tmap_x, b * kBlock, m0, x_full(rx.s));
         ptx::tma_load_2d(x_at(rx.s) + C::kXBytes / 2, &p.tmap_x, b * kBlock + 64, m0, x_full(rx.s));
         for (int i = 0; i < GROUPS; ++i)
-          bulk_load(sx_at(rx.s) + i * MT * 4, p.sx + (static_cast<long long>(b) * GROUPS + i) * p.m_pad + m0, MT * 4,
+          bulk_load(unit_at(rx.s) + i * MT * 4, p.units + (static_cast<long long>(b) * GROUPS + i) * p.m_pad + m0, MT * 4,
                     x_full(rx.s));
       }
       for (int i = 0; i < C::kXStages && b - i > b0; ++i) {
@@ -356,10 +361,26 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
     const int sw = (sr >> 1) & 3;
     constexpr int SETS = EW / 4;  // sets of four warps, which take steps in turn
     const int set = (warp - 4) >> 2;
+    // zero points of this lane's row, fetched a step of its own ahead
+    const uint8_t* const z_row = p.zeros + min(w4_column(p, tile, r, kRows), p.n - 1) * p.ldz;
+    const int groups = (p.k + GC * 32 - 1) / (GC * 32);
+    uint8_t z_next[GROUPS];
+#pragma unroll
+    for (int i = 0; i < GROUPS; ++i) z_next[i] = 8;
+    auto fetch = [&](int b) {
+#pragma unroll
+      for (int i = 0; i < GROUPS; ++i)
+        if (p.zeros) z_next[i] = z_row[min(b * GROUPS + i, groups - 1)];  // past the last group A is zero
+    };
+    fetch(b0 + set);
     Ring<C::kCodeStages> rc;
     Ring<C::kAStages> ra;
     for (int b = b0; b < b1; ++b, rc.next(), ra.next()) {
       if (SETS > 1 && (b - b0) % SETS != set) continue;
+      uint32_t zero[GROUPS];
+#pragma unroll
+      for (int i = 0; i < GROUPS; ++i) zero[i] = w4_zero(z_next[i]);
+      fetch(b + SETS);
       if (!wait_warp(code_full(rc.s), rc.ph, p, 3)) break;
       uint4 w[4];
 #pragma unroll
@@ -376,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           uint32_t o[4];
-          w4_expand(q[i], o);
+          w4_expand(q[i], zero[(2 * h + i / 4) / GC], o);
 #pragma unroll
           for (int j = 0; j < 4; ++j) e[4 * i + j] = o[j];
         }
@@ -401,24 +422,18 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
     const int r = (warp & 3) * 32 + lane, col0 = ((warp - 4 - EW) >> 2) * COLS;
     const long long j = min(w4_column(p, tile, r, kRows), p.n - 1);
     const uint16_t* const s_row = p.scales + j * p.lds;
-    const uint8_t* const z_row = p.zeros + j * p.ldz;
     const int groups = (p.k + GC * 32 - 1) / (GC * 32);
-    // scales and zero points of the groups of AHEAD steps
+    // scales of the groups of AHEAD steps
     constexpr int AHEAD = GROUPS == 1 ? 4 : GROUPS == 2 ? 2 : 1, KEEP = AHEAD * GROUPS;
     uint16_t s_next[KEEP];
-    uint8_t z_next[KEEP];
-#pragma unroll
-    for (int i = 0; i < KEEP; ++i) z_next[i] = 8;
     auto fetch = [&](int b) {
 #pragma unroll
       for (int i = 0; i < KEEP; ++i) {
-        const int at = min(b * GROUPS + i, groups - 1);  // past the last group A is zero
-        s_next[i] = s_row[at];
-        if (p.zeros) z_next[i] = z_row[at];
+        s_next[i] = s_row[min(b * GROUPS + i, groups - 1)];  // past the last group A is zero
       }
     };
     fetch(b0);
-    float s[KEEP], z[KEEP];
+    float s[KEEP];
     Ring<C::kXStages> rx;
     Ring<C::kAStages> ra;
     Ring<C::kDStages> rd;
@@ -426,14 +441,11 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
     for (int b = b0; b < b1; ++b, rx.next(), ra.next(), rd.next()) {
       if ((b - b0) % AHEAD == 0) {
 #pragma unroll
-        for (int i = 0; i < KEEP; ++i) {
-          s[i] = w4_f32<BF16>(s_next[i]);
-          z[i] = 8388608.0f - __uint_as_float(0x4B000000u | z_next[i]);  // minus the zero point
-        }
+        for (int i = 0; i < KEEP; ++i) s[i] = w4_f32<BF16>(s_next[i]);
         fetch(b + AHEAD);
       } else {
 #pragma unroll
-        for (int i = 0; i + GROUPS < KEEP; ++i) s[i] = s[i + GROUPS], z[i] = z[i + GROUPS];
+        for (int i = 0; i + GROUPS < KEEP; ++i) s[i] = s[i + GROUPS];
       }
       {
         const bool x = ptx::mbar_try_wait(x_full(rx.s), rx.ph), d = ptx::mbar_try_wait(d_full(rd.s), rd.ph);
@@ -460,16 +472,16 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(d_empty(rd.s));
         }
-        const uint64_t s2 = pair(s[grp], s[grp]), z2 = pair(z[grp], z[grp]);
-        const uint32_t sx = sx_at(rx.s) + (grp * MT + col0 + c0) * 4;
+        const uint64_t s2 = pair(s[grp], s[grp]);
+        const uint32_t units = unit_at(rx.s) + (grp * MT + col0 + c0) * 4;
 #pragma unroll
         for (int q = 0; q < PART / 4; ++q) {
-          const uint4 x = ring_read(sx + q * 16);
+          const uint4 x = ring_read(units + q * 16);
           uint64_t* const to = sum + c0 / 2 + 2 * q;
-          const uint64_t x0 = pair(__uint_as_float(x.x), __uint_as_float(x.y));
-          const uint64_t x1 = pair(__uint_as_float(x.z), __uint_as_float(x.w));
-          to[0] = fma2(s2, fma2(z2, x0, pair(__uint_as_float(acc[4 * q]), __uint_as_float(acc[4 * q + 1]))), to[0]);
-          to[1] = fma2(s2, fma2(z2, x1, pair(__uint_as_float(acc[4 * q + 2]), __uint_as_float(acc[4 * q + 3]))), to[1]);
+          const uint64_t u0 = pair(__uint_as_float(x.x), __uint_as_float(x.y));
+          const uint64_t u1 = pair(__uint_as_float(x.z), __uint_as_float(x.w));
+          to[0] = fma2(s2, mul2(u0, pair(__uint_as_float(acc[4 * q]), __uint_as_float(acc[4 * q + 1]))), to[0]);
+          to[1] = fma2(s2, mul2(u1, pair(__uint_as_float(acc[4 * q + 2]), __uint_as_float(acc[4 * q + 3]))), to[1]);
         }
       }
       ptx::fence_proxy_async_smem();
@@ -495,7 +507,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
       part[(col0 + 2 * i + 1) * kRows + r] = hi;
     }
   }
-  // the scales of A's rows come from the pre-pass, too
+  // no CTA ends before the pre-pass: what follows in the stream may write A and
+  // the workspace
   asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncthreads();
   __syncwarp();
@@ -507,7 +520,6 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
     const long long j = static_cast<long long>(tile) * (8 << oct_log2) + o;
     const int row = glu ? o * 2 : o;
     if (j >= p.n_out) continue;
-    const float unit = p.unit[m0 + i];
     float v[2][8];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -527,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         const long long col = j + q + static_cast<long long>(h) * p.n_out;
-        float s = v[h][q] * unit;
+        float s = v[h][q] * static_cast<float>(1 << kW4Up);
         if (j + q < p.n_out) {
           if (!isfinite(s)) s = w4_exact<BF16>(p, m0 + i, col);
           v[h][q] = p.alpha * s + (p.bias ? w4_f32<BF16>(p.bias[col]) : 0.0f);
@@ -558,15 +570,13 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
 }
 
 // A's row blockIdx.x as scaled fp16 in the order of the codes' pairs, with the
-// sums of its groups in the same units and the unit.
+// units of its groups.
 template <bool BF16, int GC>
 __global__ void __launch_bounds__(256) w4_pack_kernel(const __grid_constant__ W4Params p) {
   constexpr int LANES = GC * 4;  // of a group: 8 values each
-  __shared__ uint32_t most_of[8];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const long long m = blockIdx.x;
   const int runs = p.k_pad / 8;  // a multiple of 16
-  uint32_t most = 0;
   auto fetch = [&](int run) {
     const int k0 = run * 8;
     const uint16_t* const src = p.a + m * p.lda + k0;
@@ -577,34 +587,22 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const __grid_constant__ W4
       if (k0 + j < p.k) w[j >> 1] |= static_cast<uint32_t>(src[j]) << (16 * (j & 1));
     return make_uint4(w[0], w[1], w[2], w[3]);
   };
-  for (int run = threadIdx.x; run < runs; run += 256) {
-    const uint4 x = fetch(run);
-    const uint32_t two = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
-                                  __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
-    most = max(most, max(two & 0xFFFFu, two >> 16));
-  }
-  most = __reduce_max_sync(0xFFFFFFFFu, most);
-  if ((threadIdx.x & 31) == 0) most_of[threadIdx.x >> 5] = most;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < 8; ++w) most = max(most, most_of[w]);
-  const int e = w4_shift<BF16>(most);
-  const float even = w4_pow2(e), odd = even * 0.0625f;
-  if (threadIdx.x == 0) p.unit[m] = w4_pow2(24 - e);
   for (int run0 = threadIdx.x & ~31; run0 < runs; run0 += 256) {
     const int run = run0 + (threadIdx.x & 31);
     const uint4 x = run < runs ? fetch(run) : make_uint4(0, 0, 0, 0);
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    float v[8], s = 0.0f;
+    const uint32_t two = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                                  __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+    uint32_t most = max(two & 0xFFFFu, two >> 16);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[j] = w4_f32<BF16>(static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1))));
-      s += v[j];
-    }
-#pragma unroll
-    for (int o = 1; o < LANES; o <<= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    for (int o = 1; o < LANES; o <<= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
     if (run >= runs) continue;
-    if (run % LANES == 0) p.sx[static_cast<long long>(run / LANES) * p.m_pad + m] = s * even * 0x1p-24f;
+    const int e = w4_shift<BF16>(most);
+    const float even = w4_pow2(e), odd = even * 0.0625f;
+    if (run % LANES == 0) p.units[static_cast<long long>(run / LANES) * p.m_pad + m] = w4_pow2(24 - kW4Up - e);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = w4_f32<BF16>(static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1))));
     uint32_t out[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -677,9 +675,9 @@ cudaError_t launch_of(W4Params p, int num_sms, cudaStream_t stream) {
   return cudaErrorInvalidValue;
 }
 
-// The workspace: packed A, then the groups' sums, then the rows' units.
+// The workspace: packed A, then the groups' units.
 struct Layout {
-  size_t x, sx, unit, end;
+  size_t x, units, end;
   long long k_pad, m_pad;
 };
 Layout layout(long long m, long long k, int group) {
@@ -688,9 +686,8 @@ Layout layout(long long m, long long k, int group) {
   const int mt = m_tile(m, group);
   l.m_pad = (m + mt - 1) / mt * mt;
   l.x = 0;
-  l.sx = static_cast<size_t>(m) * l.k_pad * 2;  // rows of a multiple of 256 bytes
-  l.unit = l.sx + static_cast<size_t>(l.k_pad / group) * l.m_pad * 4;
-  l.end = l.unit + static_cast<size_t>(l.m_pad) * 4;
+  l.units = static_cast<size_t>(m) * l.k_pad * 2;  // rows of a multiple of 256 bytes
+  l.end = l.units + static_cast<size_t>(l.k_pad / group) * l.m_pad * 4;
   return l;
 }
 
@@ -705,8 +702,7 @@ cudaError_t launch_w4mm(const W4Params& all, void* workspace, int num_sms, cudaS
   const Layout l = layout(p.m, p.k, p.group);
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
   p.x = reinterpret_cast<uint16_t*>(ws + l.x);
-  p.sx = reinterpret_cast<float*>(ws + l.sx);
-  p.unit = reinterpret_cast<float*>(ws + l.unit);
+  p.units = reinterpret_cast<float*>(ws + l.units);
   p.k_pad = static_cast<int>(l.k_pad);
   p.m_pad = l.m_pad;
   if (!encode_map_2d(&p.tmap_w, p.w, 1, static_cast<uint64_t>(p.k + 1) / 2, static_cast<uint64_t>(p.n),

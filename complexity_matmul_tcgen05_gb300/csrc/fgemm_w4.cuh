@@ -28,15 +28,31 @@ __device__ __forceinline__ float w4_f32(uint16_t v) {
   return __half2float(__ushort_as_half(v));
 }
 
-// The eight codes of a word as fp16 pairs: p[i] holds code i in its low half
-// and code i + 4 in its high half, times 2^-24 for even i and 2^-20 for odd.
-__device__ __forceinline__ void w4_expand(uint32_t w, uint32_t (&p)[4]) {
-  const uint32_t v = w >> 8;
-  p[0] = w & 0x000F000Fu;
-  p[1] = w & 0x00F000F0u;
-  p[2] = v & 0x000F000Fu;
-  p[3] = v & 0x00F000F0u;
+__device__ __forceinline__ uint32_t w4_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+__device__ __forceinline__ __half2 w4_half2(uint32_t bits) { return *reinterpret_cast<const __half2*>(&bits); }
+
+// A zero point (0 .. 255) in both kinds of codes: times 2^-24 in the low half,
+// times 2^-20 in the high half.
+__device__ __forceinline__ uint32_t w4_zero(uint32_t z) {
+  return w4_bits(__hmul2(w4_half2(z | z << 16), w4_half2(0x4C003C00u)));  // (1, 16)
 }
+
+// The eight codes of a word less their zero point, as fp16 pairs: p[i] holds
+// code i in its low half and code i + 4 in its high half, times 2^-24 for even i
+// and 2^-20 for odd.  Codes and differences are fp16 numbers: nothing is rounded.
+__device__ __forceinline__ void w4_expand(uint32_t w, uint32_t zero, uint32_t (&p)[4]) {
+  const __half2 lower = __low2half2(w4_half2(zero)), upper = __high2half2(w4_half2(zero));
+  const uint32_t v = w >> 8;
+  p[0] = w4_bits(__hsub2(w4_half2(w & 0x000F000Fu), lower));
+  p[1] = w4_bits(__hsub2(w4_half2(w & 0x00F000F0u), upper));
+  p[2] = w4_bits(__hsub2(w4_half2(v & 0x000F000Fu), lower));
+  p[3] = w4_bits(__hsub2(w4_half2(v & 0x00F000F0u), upper));
+}
+
+// What a product of expanded codes and a group's scaled A counts: the kernels
+// hold their sums in units of 2^kW4Up, so that the unit of values near the end
+// of fp32, 2^(24 - e - kW4Up), is still a number.
+constexpr int kW4Up = 12;
 
 __device__ __forceinline__ float w4_silu(float v) { return v / (1.0f + __expf(-v)); }
 
@@ -69,7 +85,8 @@ __device__ __forceinline__ float w4_pow2(int e) {
 }
 
 // The power of two that brings values whose largest magnitude has these bits
-// below 2^15 (0 for zeros; at most 2^120, which fp32 holds).
+// below 2^15 (0 for zeros; at most 2^120, which fp32 holds; at least 2^-113, or
+// 2^-114 for values that are not finite).
 template <bool BF16>
 __device__ __forceinline__ int w4_shift(uint32_t most) {
   const int field = static_cast<int>(most) >> (BF16 ? 7 : 10);

@@ -96,6 +96,42 @@ def test_w4_few_rows_whose_a_is_loaded_in_parts(m, k, group, dtype):
     within("w4 swiglu", C, want, bound)
 
 
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("m,n,k", [(1, 33, 100), (3, 64, 1023), (8, 96, 4096), (9, 128, 257), (17, 64, 700), (40, 72, 4096),
+                                   (65, 40, 300), (150, 136, 2304)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_w4_to_what_its_terms_allow(m, n, k, dtype, group, zeros):
+    A, W, s, z, _ = w4_inputs(m, n, k, dtype, group, False, m + n + k)
+    if zeros:  # a byte, not four bits
+        z = torch.randint(0, 256, s.shape, generator=gen(k), device=DEV, dtype=torch.uint8)
+        s = s / 16
+    C = fgemm.matmul_w4(A, W, s, zeros=z, group=group)
+    w4_close(C, A, W, s, z, group)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("m", [1, 4, 8, 9, 40, 150])
+@pytest.mark.parametrize("dtype,small,large", [("bf16", 1.0, 2.0 ** 20), ("bf16", 1.0, 1e30), ("f16", 0.02, 60000.0)])
+def test_w4_large_activations_of_codes_at_the_zero_point(m, group, dtype, small, large):
+    """A weight of 0 takes nothing of its activation, however large."""
+    n, k = 72, 1024
+    A, W, s, _, _ = w4_inputs(m, n, k, dtype, group, False, m + group)
+    z = torch.randint(0, 16, s.shape, generator=gen(m), device=DEV, dtype=torch.uint8)
+    A = (A * small).contiguous()
+    # one such activation in a row, in the first half of K; a whole group of them for the largest
+    hot = (torch.arange(m, device=DEV) * 131 + 64) % (k // 2)
+    width = group if large > 2.0 ** 34 else 1
+    q = torch.stack((W & 15, W >> 4), 2).flatten(1)
+    for i, h in enumerate(hot.tolist()):
+        h = h // width * width
+        A[i, h:h + width] = large
+        q[:, h:h + width] = z[:, h // group, None]
+    W = q[:, 0::2] | (q[:, 1::2] << 4)
+    C = fgemm.matmul_w4(A, W, s, zeros=z, group=group)
+    w4_close(C, A, W, s, z, group)
+
+
 # ------------------------------------------------------------------- errors
 
 
