@@ -24,7 +24,8 @@
 // each row and group (the largest value below 2^15; 2^11 for the k whose codes
 // are the upper kind), bf16 as well: its 8 significant bits fit, and what falls
 // below fp16's range is under 2^-35 of the group's largest value.
-// An output that is not finite is computed again term by term (w4_exact).
+// Where a CTA has met an infinite scale, outputs that are not finite are computed
+// again term by term (w4_exact).
 //
 // What bounds it: latency, from the codes' arrival to the tile's last sum.
 // 5 x 28672 x 4096, SwiGLU, bf16, groups of 128: 20.6 us, 3.0 TB/s; one row 4096 x
@@ -64,12 +65,13 @@ constexpr int kW4ABytes = (GC > 1 ? 64 : 48) * 1024;
 
 // Shared memory of a CTA: the rings of codes and of scales, A's `chunk` values
 // of m rows with the units of their groups (32 bytes a group whatever m is,
-// half as much as A itself for one row in groups of 32), the warps' and teams' sums.
+// half as much as A itself for one row in groups of 32), the warps' and teams'
+// sums, a word.
 constexpr size_t kW4MostSmem = 227 * 1024;
 template <int GC>
 constexpr size_t w4_few_fixed(int m) {
   return static_cast<size_t>(kW4Teams * kW4Warps) * kW4Stages * kW4Rows * (64 + 4 / GC * 8) +
-         static_cast<size_t>(kW4Teams * (kW4Warps + 2)) * kW4Rows * m * 4;
+         static_cast<size_t>(kW4Teams * (kW4Warps + 2)) * kW4Rows * m * 4 + 16;
 }
 template <int GC>
 constexpr size_t w4_few_smem(int m, int chunk) {
@@ -144,8 +146,12 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
   unsigned char* const a_at = smem + kW4Teams * kW4Warps * kW4Stages * (kSlot + kScales * 8);
   const int a_pitch = p.chunk * 2;
   float* const unit_at = reinterpret_cast<float*>(a_at + static_cast<size_t>(a_pitch) * mt);  // [group of the chunk][8]
-  float* const red = unit_at + p.chunk / G * 8 + team * ((kW4Warps + 2) * kW4Rows * mt);  // [warp][row of A][row]
+  float* const sums_at = unit_at + p.chunk / G * 8;
+  float* const red = sums_at + team * ((kW4Warps + 2) * kW4Rows * mt);  // [warp][row of A][row]
   float* const part = red + kW4Warps * kW4Rows * mt;  // [2][row of A][row], read by the cluster
+  int* const wild = reinterpret_cast<int*>(sums_at + kW4Teams * ((kW4Warps + 2) * kW4Rows * mt));  // an infinite scale was met
+  if (threadIdx.x == 0) *wild = 0;
+  __syncthreads();
   const int w_bytes = (p.k + 1) / 2 - k_lo / 2;  // of a row, from this CTA's first
   const int groups = (p.k + G - 1) / G;
   const int tile_step = gridDim.x / slices * kW4Teams;
@@ -208,9 +214,11 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
   auto issue = [&]() {
     const int before = load_slot == 0 ? kW4Stages - 1 : load_slot - 1;  // the slot of the block issued last
 #pragma unroll
-    for (int i = 0; i < GROUPS; ++i)
-      scale_ring[before * kScales + i * kW4Rows + lane] =
-          make_float2(w4_f32<BF16>(s_next[i]), __uint_as_float(w4_zero(z_next[i])));
+    for (int i = 0; i < GROUPS; ++i) {
+      const float s = w4_f32<BF16>(s_next[i]);
+      if (isinf(s)) *wild = 1;
+      scale_ring[before * kScales + i * kW4Rows + lane] = make_float2(s, __uint_as_float(w4_zero(z_next[i])));
+    }
     if (load_tile < p.tiles) {
       const int block = load_chunk + load_b, byte = block * (kW4Block / 2);
       // 16-byte chunk c of row r at chunk c ^ (r >> 1 & 3)
@@ -436,7 +444,12 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
         }
         const long long col = j + static_cast<long long>(h) * p.n_out;
         s *= static_cast<float>(1 << kW4Up);
-        if (!isfinite(s)) s = w4_exact<BF16>(p, i, col);
+        if (!isfinite(s)) {
+          int met = *wild;
+          for (int q = 0; q < slices && slices > 1; ++q)
+            met |= __float_as_int(ld_cluster_f32(ptx::mapa(ptx::smem_u32(wild), q)));
+          if (met) s = w4_exact<BF16>(p, i, col);
+        }
         v[h] = p.alpha * s + (p.bias ? w4_f32<BF16>(p.bias[col]) : 0.0f);
       }
       const float out = glu ? w4_silu(v[0]) * v[1] : p.epi == kEpiSilu ? w4_silu(v[0]) : v[0];

@@ -21,9 +21,11 @@
 // codes are on their way by then.
 //
 // What bounds it: the fold's chain (products done -> tensor memory -> scale, add
-// -> room for the next), not the tensor pipe (31 % active) nor memory.  Measured:
-// 48 x 8192 x 8192 fp16, groups of 64, 32 us; 2048 x 4096 x 14336 bf16, groups of
-// 128, 340 us, 708 TFLOP/s.
+// -> room for the next), not the tensor pipe nor memory.  Measured: 48 x 8192 x
+// 8192 fp16, groups of 64, 30.3 us; 2048 x 4096 x 14336 bf16, groups of 128, 311
+// us, 774 TFLOP/s.  (With the zero point taken off the group's sum in the fold, as
+// z sum_k x: 32.4 and 341 us; but 128 x 8192 x 16384 in groups of 32 takes 241 us
+// against 223.)
 //
 // Roles: warp 0 loads the codes, warp 2 A, warps 1 and 3 issue the MMAs, warps 4..
 // expand the codes, the last 4 or 8 warps fold.  Every wait is bounded; a wait that runs out latches the
@@ -73,7 +75,7 @@ struct Cfg {
   static constexpr int kBars = 2 * kCodeStages + 2 * kXStages + 2 * kAStages + 2 * kDStages + 1;
   static constexpr int kSmem = 1024 + kCodeStages * kCodeBytes + kXStages * (kXBytes + kUnitBytes) + 8 * kBars + 16;
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  static_assert(MT * kRows * 4 <= kCodeStages * kCodeBytes + kXStages * kXBytes, "the sums reuse the rings");
+  static_assert(MT * kRows * 4 + kRows * 4 <= kCodeStages * kCodeBytes + kXStages * kXBytes, "the sums reuse the rings");
   static constexpr bool kAhead = kDStages < kAStages;
   // Warps that issue the products, a step each in turn.  Two accumulators,
   // codes' stages and accumulators handed back together and one warp / on
@@ -198,6 +200,42 @@ struct Ring {
     }
   }
 };
+
+// The outputs of a tile in columns with an infinite scale, term by term
+// (w4_exact).  Only where an output is infinite: there every weight's sign, and
+// every code at the zero point, counts.  `flags`: a word for each of the tile's rows.
+template <bool BF16>
+static __device__ __noinline__ void store_wild(const W4Params& p, int tile, int m0, int mt, int rank, int* flags) {
+  const bool glu = p.epi == kEpiSwiglu;
+  const int groups = (p.k + p.group - 1) / p.group;
+  for (int r = threadIdx.x; r < kRows; r += kThreads) flags[r] = 0;
+  __syncthreads();
+  {
+    constexpr int kEach = kThreads / kRows;  // threads a row
+    const int r = threadIdx.x / kEach;
+    const uint16_t* const s = p.scales + min(w4_column(p, tile, r, kRows), p.n - 1) * p.lds;
+    for (int g = threadIdx.x % kEach; g < groups; g += kEach)
+      if ((s[g] & 0x7FFF) == (BF16 ? 0x7F80 : 0x7C00)) flags[r] = 1;
+  }
+  __syncthreads();
+  // (the elements that this thread has stored before)
+  const int oct_log2 = glu ? 3 : 4;
+  for (int e = threadIdx.x + rank * kThreads; e < (mt << oct_log2); e += kThreads * p.slices) {
+    const int i = e >> oct_log2, o = (e & ((1 << oct_log2) - 1)) * 8;
+    for (int q = 0; q < 8; ++q) {
+      const long long j = static_cast<long long>(tile) * (8 << oct_log2) + o + q;
+      const int row = (glu ? o * 2 : o) + q;
+      if (j >= p.n_out || !(flags[row] || (glu && flags[row + 8]))) continue;
+      float v[2];
+      for (int h = 0; h < (glu ? 2 : 1); ++h) {
+        const long long col = j + static_cast<long long>(h) * p.n_out;
+        v[h] = p.alpha * w4_exact<BF16>(p, m0 + i, col) + (p.bias ? w4_f32<BF16>(p.bias[col]) : 0.0f);
+      }
+      const float y = glu ? w4_silu(v[0]) * v[1] : p.epi == kEpiSilu ? w4_silu(v[0]) : v[0];
+      p.c[(m0 + i) * p.ldc + j] = BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(y)) : __half_as_ushort(__float2half_rn(y));
+    }
+  }
+}
 
 template <bool BF16, int MT, int GC>  // GC: group / 32
 __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant__ W4Params p) {
@@ -515,6 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
   if (slices > 1) ptx::cluster_sync();
   const int mt = min(MT, p.m - m0);
   const int oct_log2 = glu ? 3 : 4;  // eights of columns of C of a tile
+  bool infinite = false;
   for (int e = threadIdx.x + rank * kThreads; e < (mt << oct_log2); e += kThreads * slices) {
     const int i = e >> oct_log2, o = (e & ((1 << oct_log2) - 1)) * 8;
     const long long j = static_cast<long long>(tile) * (8 << oct_log2) + o;
@@ -539,9 +578,9 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         const long long col = j + q + static_cast<long long>(h) * p.n_out;
-        float s = v[h][q] * static_cast<float>(1 << kW4Up);
+        const float s = v[h][q] * static_cast<float>(1 << kW4Up);
         if (j + q < p.n_out) {
-          if (!isfinite(s)) s = w4_exact<BF16>(p, m0 + i, col);
+          infinite |= isinf(s);
           v[h][q] = p.alpha * s + (p.bias ? w4_f32<BF16>(p.bias[col]) : 0.0f);
         }
       }
@@ -565,7 +604,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
         if (j + q < p.n_out) dst[q] = static_cast<uint16_t>(out[q >> 1] >> (16 * (q & 1)));
     }
   }
-  __syncwarp();
+  if (__syncthreads_or(infinite))
+    store_wild<BF16>(p, tile, m0, mt, rank, reinterpret_cast<int*>(base_ptr + MT * kRows * 4));
   if (slices > 1) ptx::cluster_sync();  // no CTA leaves while its sums may be read
 }
 

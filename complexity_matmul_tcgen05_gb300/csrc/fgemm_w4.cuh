@@ -51,17 +51,22 @@ __device__ __forceinline__ void w4_expand(uint32_t w, uint32_t zero, uint32_t (&
 
 // What a product of expanded codes and a group's scaled A counts: the kernels
 // hold their sums in units of 2^kW4Up, so that the unit of values near the end
-// of fp32, 2^(24 - e - kW4Up), is still a number.
-constexpr int kW4Up = 12;
+// of fp32, 2^(24 - e - kW4Up), is still a number, and so is the sum of a group
+// (255 x 128 x 2^128 at most) before its scale.
+constexpr int kW4Up = 16;
 
 __device__ __forceinline__ float w4_silu(float v) { return v / (1.0f + __expf(-v)); }
 
 
-// Column j of W against row i of A, term by term.
+// Column j of W against row i of A, term by term: for columns with an infinite
+// scale, whose weights are infinite or, at the zero point, not numbers.
+// Everything else follows from the products themselves: an infinity or a NaN in
+// A goes through the tensor core as such, and finite values do not overflow
+// before their sum does.
 template <bool BF16>
 static __device__ __noinline__ float w4_exact(const W4Params& p, long long i, long long j) {
   float sum = 0.0f;
-  for (int k = 0; k < p.k; ++k) {
+  for (int k = 0; k < p.k && sum == sum; ++k) {
     const int q = (p.w[j * p.ldw + (k >> 1)] >> (4 * (k & 1))) & 15;
     const int g = k / p.group;
     const float z = p.zeros ? static_cast<float>(p.zeros[j * p.ldz + g]) : 8.0f;

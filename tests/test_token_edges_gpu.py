@@ -2,6 +2,7 @@
 admits: long K with few rows, ties behind a long top-k, activations and rows
 far from 1, infinities, in-place outputs."""
 import ctypes
+import math
 
 import numpy as np
 import pytest
@@ -130,6 +131,89 @@ def test_w4_large_activations_of_codes_at_the_zero_point(m, group, dtype, small,
     W = q[:, 0::2] | (q[:, 1::2] << 4)
     C = fgemm.matmul_w4(A, W, s, zeros=z, group=group)
     w4_close(C, A, W, s, z, group)
+
+
+@pytest.mark.parametrize("m", [1, 5, 20, 140])
+def test_w4_large_finite_rows(m):
+    A, W, s, z, _ = w4_inputs(m, 72, 600, "bf16", 64, True, m)
+    A = A.contiguous()
+    for i in range(0, m, 2):
+        A[i] = (A[i].float() * 2.0 ** 122).to(A.dtype)
+    s = (s.float() * 2.0 ** -8).to(s.dtype)
+    assert torch.all(torch.isfinite(A))
+    C = fgemm.matmul_w4(A, W, s, zeros=z, group=64)
+    w4_close(C, A, W, s, z, 64)
+
+
+@pytest.mark.parametrize("m", [1, 5, 20, 140])
+def test_w4_large_groups_with_small_scales(m):
+    """Sums of a group beyond fp32 whose scale brings them back."""
+    n, k, group = 40, 512, 128
+    A, W, s, _, _ = w4_inputs(m, n, k, "bf16", group, False, m)
+    A = torch.full_like(A, 2.0 ** 127)
+    z = torch.full(s.shape, 255, device=DEV, dtype=torch.uint8)
+    s = (s.float() * 2.0 ** -15).to(s.dtype)
+    C = fgemm.matmul_w4(A, W, s, zeros=z, group=group)
+    assert torch.all(torch.isfinite(C))
+    w4_close(C, A, W, s, z, group)
+
+
+@pytest.mark.parametrize("k", [300, 4072])  # one CTA a tile, and slices of K
+@pytest.mark.parametrize("m", [1, 3, 9, 200])
+def test_w4_infinite_and_nan_scales(m, k):
+    n = 48
+    A, W, s, z, _ = w4_inputs(m, n, k, "bf16", 64, True, 5)
+    A, s = torch.nn.functional.pad(A.abs() + 0.5, (0, -k % 8))[:, :k], s.clone()  # rows of whole 16 bytes
+    s[3, 1] = math.inf
+    s[17, 4] = -math.inf
+    s[40, 2] = math.nan
+    z[3, 1] = z[17, 4] = 20  # every weight of the group is infinite, with one sign
+    z[20, 0], s[20, 0] = 7, math.inf  # some are 0 times infinity
+    C = fgemm.matmul_w4(A, W, s, zeros=z, group=64)
+    q = torch.stack((W & 15, W >> 4), 2).flatten(1)[:, :k].double()
+    at = torch.arange(k, device=DEV) // 64
+    want = (A.double().cpu() @ ((q - z.double()[:, at]) * s.double()[:, at]).T.cpu())
+    got = C.double().cpu()
+    bad = ~torch.isfinite(want)
+    assert torch.equal(torch.isnan(got), torch.isnan(want)) and bool(bad[:, [3, 17, 20, 40]].all())
+    assert torch.equal(got[bad & ~torch.isnan(want)], want[bad & ~torch.isnan(want)])
+    ok = torch.tensor([j for j in range(n) if j not in (3, 17, 20, 40)], device=DEV)
+    w4_close(C, A, W, s, z, 64, ok)
+    # a gate with such a column spoils its own output and no other
+    C = fgemm.matmul_w4(A, W, s, zeros=z, group=64, epilogue="swiglu")
+    lost = torch.tensor([j in (3, 17, 20, 16) for j in range(n // 2)], device=DEV)
+    assert torch.all(torch.isfinite(C[:, ~lost]))
+    assert torch.all(torch.isnan(C[:, [20, 16]]))
+
+
+@pytest.mark.parametrize("kind", ["nan", "inf", "large"])
+@pytest.mark.parametrize("m", [8, 256])
+def test_w4_time_of_rows_that_are_not_finite(m, kind):
+    """Rows of a batch that diverged, or that pad it, take what others take."""
+    n = k = 4096
+    A, W, s, _, _ = w4_inputs(m, n, k, "bf16", 128, False, m)
+    B = A.clone()
+    if kind == "nan":
+        B[:, 1::7] = math.nan
+    elif kind == "inf":
+        B[:, -1] = math.inf
+    else:
+        B = (B.float() * 2.0 ** 122).to(B.dtype)
+
+    def us(X):
+        times = []
+        for _ in range(8):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(5):
+                fgemm.matmul_w4(X, W, s)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b) * 200)
+        return sorted(times)[2]
+
+    us(A)
+    assert us(B) < 4 * us(A)
 
 
 # ------------------------------------------------------------------- errors
