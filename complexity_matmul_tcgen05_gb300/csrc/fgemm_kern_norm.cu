@@ -8,6 +8,10 @@
 // The norm is taken of t as stored (16 bits): the next layer's residual, the
 // backward pass and a recomputation all read that t, and all see the same
 // norm.  Squares, sums, r and y are fp32.
+// bf16 reaches further than fp32's squares do.  Where the sum of a row's squares
+// overflows, or is so small with eps that squares were lost, the row is scaled
+// by a power of two and summed again, and y formed from the scaled values
+// (far_row).
 // MX output (blocks of 32 along the row): the scale is 2^e with
 // e = floor(log2 max|y|) - emax (8 for E4M3, 15 for E5M2) held to E8M0's
 // range, the elements y / 2^e rounded to nearest even, those past the
@@ -223,6 +227,58 @@ __device__ __forceinline__ void total_chunk(const NormParams& p, Chunk<VEC>& t, 
   }
 }
 
+// Whether a bf16 row's sum of squares is none: overflown (or infinite, or a
+// NaN), or so small that squares below fp32's range count (each is off by
+// 2^-150 at most).
+__device__ __forceinline__ bool is_far(float sum, const NormParams& p) {
+  return !(sum < INFINITY) || sum / static_cast<float>(p.n) + p.eps < 0x1p-120f;
+}
+
+// Such a row, read again element by element from the total (or x and the
+// residual) behind the barrier of its sum: rare, so it is kept out of the
+// kernels' registers.  A thread reads and writes the same columns in all passes
+// (y may be x).
+template <bool MX>
+__device__ __noinline__ void far_row(const NormParams& p, long long row, int lane, int tpr) {
+  __shared__ float red[32];
+  __shared__ uint32_t red_most[32];
+  auto value = [&](int c) {
+    Chunk<1> t;
+    if (p.total)
+      load_chunk<1>(t, p.total + row * p.ldt, c, p.n);
+    else
+      total_chunk<true, 1>(p, t, row, c);
+    return t.w[0];
+  };
+  if (tpr == 32) __syncwarp();  // the row's total, stored by other threads
+  uint32_t most = 0;
+  for (long long c = lane; c < p.n; c += tpr) most = max(most, value(static_cast<int>(c)) & 0x7FFFu);
+  most = __reduce_max_sync(0xFFFFFFFFu, most);
+  if (tpr > 32) {
+    if ((threadIdx.x & 31) == 0) red_most[threadIdx.x >> 5] = most;
+    __syncthreads();
+    most = __reduce_max_sync(0xFFFFFFFFu, (threadIdx.x & 31) < (tpr >> 5) ? red_most[threadIdx.x & 31] : 0u);
+  }
+  // the largest magnitude to about 2^40; nothing helps zeros, infinities and NaN
+  const int k = most == 0 || most >= 0x7F80u ? 0 : min(120, 40 + 127 - static_cast<int>(most >> 7));
+  const float a = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+  float sum = 0.0f;
+  for (long long c = lane; c < p.n; c += tpr) {
+    const float e = to_f32<true>(value(static_cast<int>(c))) * a;
+    sum = fmaf(e, e, sum);
+  }
+  sum = row_sum(sum, tpr, red);
+  const float r = 1.0f / sqrtf(sum / static_cast<float>(p.n) + p.eps * a * a);
+  if (lane == 0 && p.inv_rms) p.inv_rms[row] = r * a;
+  for (long long c0 = lane & ~31; c0 < p.n; c0 += tpr) {
+    const int c = c0 + (lane & 31) < p.n ? static_cast<int>(c0) + (lane & 31) : p.n;
+    Chunk<1> t;
+    // (what a takes below bf16's range has a y below it)
+    t.w[0] = to_16<true>(to_f32<true>(value(c)) * a);
+    finish_chunk<true, 1, MX>(p, t, r, row, c);
+  }
+}
+
 // One row on tpr = blockDim.x / rows_per_cta threads, VPT chunks a thread in
 // registers.
 template <bool BF16, int VEC, int VPT, bool MX, int MAXT>
@@ -249,6 +305,10 @@ __global__ void __launch_bounds__(MAXT) norm_kernel(const __grid_constant__ Norm
     }
   }
   sum = row_sum(sum, tpr, red);
+  if (BF16 && is_far(sum, p)) {
+    far_row<MX>(p, row, lane, tpr);
+    return;
+  }
   const float r = 1.0f / sqrtf(sum / static_cast<float>(p.n) + p.eps);
   if (lane == 0 && p.inv_rms) p.inv_rms[row] = r;
   if (MX && p.shifted) {  // chunks would straddle blocks of 32: element by element
@@ -275,7 +335,7 @@ __global__ void __launch_bounds__(MAXT) norm_kernel(const __grid_constant__ Norm
 // Rows that do not fit in registers: one row a CTA, read twice (the second
 // time mostly from L2).
 template <bool BF16, int VEC, bool MX>
-__global__ void __launch_bounds__(1024) norm_long_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(1024, 2) norm_long_kernel(const __grid_constant__ NormParams p) {
   __shared__ float red[32];
   const long long row = blockIdx.x;
   float sum = 0.0f;
@@ -291,6 +351,10 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const __grid_constant__
     }
   }
   sum = row_sum(sum, blockDim.x, red);
+  if (BF16 && is_far(sum, p)) {
+    far_row<MX>(p, row, threadIdx.x, blockDim.x);
+    return;
+  }
   const float r = 1.0f / sqrtf(sum / static_cast<float>(p.n) + p.eps);
   if (threadIdx.x == 0 && p.inv_rms) p.inv_rms[row] = r;
   for (long long c = threadIdx.x & ~31; c * VEC < p.n; c += blockDim.x) {

@@ -343,7 +343,9 @@ fgemm_status_t fgemm_plan_ex(fgemm_handle_t h, int64_t M, int64_t N, int64_t K,
  *             residual itself).
  *   y         M x N, ldy (may be x itself).
  *   inv_rms   NULL or M entries: written, for the backward pass.
- * A row whose inv is infinite (all zeros with eps 0) gives NaN.
+ * Squares of bf16 values may leave fp32's range: y follows the formula all the
+ * same, and inv_rms is what fp32 holds of inv (infinite below 2^-128 with eps 0).
+ * A row of zeros with eps 0 gives NaN.
  */
 fgemm_status_t fgemm_rms_norm(fgemm_handle_t h, int64_t M, int64_t N, const void* x, int64_t ldx,
                               const void* residual, int64_t ldr, const void* gain, float eps,

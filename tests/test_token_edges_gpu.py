@@ -10,7 +10,7 @@ import torch
 
 import token_reference as ref
 from complexity_matmul_tcgen05_gb300 import fgemm
-from test_token_ops_gpu import DEV, TYPES, check_sample, gen, rand, w4_inputs, within
+from test_token_ops_gpu import DEV, TYPES, check_mx, check_sample, gen, padded, rand, w4_inputs, within
 
 pytestmark = pytest.mark.gpu
 
@@ -214,6 +214,49 @@ def test_w4_time_of_rows_that_are_not_finite(m, kind):
 
     us(A)
     assert us(B) < 4 * us(A)
+
+
+# --------------------------------------------------------------------- norm
+
+FAR = [3e38, 1e20, 1e18, 1e-18, 1e-25, 1e-38, 2.0 ** -130]
+
+
+@pytest.mark.parametrize("layout", ["tight", "shifted", "odd"])
+@pytest.mark.parametrize("n", [7, 64, 1000, 4096, 16392, 70000])
+def test_norm_of_rows_far_from_one(n, layout):
+    """bf16 holds values whose squares fp32 does not."""
+    t = torch.bfloat16
+    g = gen(n)
+    rows = len(FAR)
+    scale = torch.tensor(FAR, device=DEV, dtype=torch.float64)[:, None]
+    x = (torch.rand((rows, n), generator=g, device=DEV, dtype=torch.float64) * 2 - 1)
+    x[:, 0] = 1
+    x = (x * scale).to(t)
+    gain = (1 + 0.3 * rand(g, n)).to(t)
+    assert torch.all(torch.isfinite(x))
+    if layout == "shifted":
+        x = padded(x, 16 - n % 8, 3)
+    elif layout == "odd":
+        x = padded(x, 1 if n % 2 == 0 else 2, 1)
+    zero = torch.zeros_like(x)
+    for eps in (0.0, 1e-6):
+        inv64, y64 = ref.norm(ref.f64(x), ref.f64(gain), float(np.float32(eps)))
+        for residual in (None, zero):
+            y, total, inv = fgemm.rms_norm(x, gain, residual=residual, eps=eps)
+            assert torch.equal(total, x)
+            with np.errstate(over="ignore"):
+                want = torch.from_numpy(inv64).float()
+            fits = torch.isfinite(want)
+            within("inv_rms", inv.cpu()[fits], inv64[fits.numpy()],
+                   (inv64 * (ref.norm_chain(n) / 2 + 6) * ref.U32 + 2.0 ** -149)[fits.numpy()])
+            assert torch.all(torch.isinf(inv.cpu()[~fits]))
+            # (2^-140: products of fp32 numbers near its end)
+            within("y", y, y64, ref.store(y64, t) + ref.norm_bound(y64, n) + 2.0 ** -140)
+            for fmt in ("e4m3", "e5m2"):
+                q, scales, total2, inv2 = fgemm.rms_norm_mx(x, gain, residual=residual, eps=eps, fmt=fmt)
+                assert torch.equal(total2, total) and torch.equal(inv2, inv)
+                if eps == 0.0:
+                    check_mx(q, scales, y64, ref.norm_bound(y64, n), fmt)
 
 
 # ------------------------------------------------------------------- errors
