@@ -420,15 +420,16 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_back_kernel(const __grid_cons
     }
     if (row + gridDim.x < p.m) fetch(row + gridDim.x);
     dot = row_sum(dot, tpr, red[side]) * inv_n;
-    const float rd = rr * rr * dot;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       float o[VEC];
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        // r (a - u mean(a u)) with u = t r
-        o[i] = fmaf(-elem<BF16, VEC>(tc[v], i), rd, rr * (elem<BF16, VEC>(dc[v], i) * elem<BF16, VEC>(g[v], i)));
-        if (p.dtotal) o[i] += elem<BF16, VEC>(dt[v], i);
+        // r (a - u mean(a u)) with u = t r, in this order: r^2 leaves fp32's range
+        // where r does not
+        const float u = elem<BF16, VEC>(tc[v], i) * rr;
+        const float w = fmaf(-u, dot, elem<BF16, VEC>(dc[v], i) * elem<BF16, VEC>(g[v], i));
+        o[i] = p.dtotal ? fmaf(rr, w, elem<BF16, VEC>(dt[v], i)) : rr * w;
       }
       Chunk<VEC> c;
 #pragma unroll

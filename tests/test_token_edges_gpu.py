@@ -259,6 +259,30 @@ def test_norm_of_rows_far_from_one(n, layout):
                     check_mx(q, scales, y64, ref.norm_bound(y64, n), fmt)
 
 
+@pytest.mark.parametrize("layout", ["tight", "shifted"])
+@pytest.mark.parametrize("n", [64, 1000, 4096, 8200, 16400])
+def test_norm_backward_of_rows_far_from_one(n, layout):
+    t = torch.bfloat16
+    g = gen(n + 1)
+    far = [1e37, 1e20, 1.0, 1e-18, 1e-25, 1e-36]
+    rows = len(far)
+    scale = torch.tensor(far, device=DEV, dtype=torch.float64)[:, None]
+    total = (rand(g, rows, n).double() * scale).to(t)
+    dy, gain = (0.2 * rand(g, rows, n)).to(t), (1 + 0.3 * rand(g, n)).to(t)
+    dy[-1] *= 2.0 ** -30  # dx is dy / rms: within bf16
+    dt = (0.1 * rand(g, rows, n).double() / scale.clamp(1e-30, 1e30)).to(t)
+    inv = (1 / total.double().square().mean(1).sqrt()).float()
+    if layout == "shifted":
+        total, dy, dt = (padded(v, 8, 1) for v in (total, dy, dt))
+    for dtotal in (None, dt):
+        dx, dgain = fgemm.rms_norm_backward(dy, total, gain, inv, dtotal=dtotal)
+        args = [ref.f64(v) for v in (dy, total, gain, inv, dtotal)]
+        dx64, dg64 = ref.norm_backward(*args)
+        ex, eg = ref.norm_backward_bound(*args, 1, rows)
+        within("dx", dx, dx64, ref.store(dx64, t) + ex + 2.0 ** -140)
+        within("dgain", dgain, dg64, eg + np.abs(dg64) * ref.U32)
+
+
 # ------------------------------------------------------------------- errors
 
 
