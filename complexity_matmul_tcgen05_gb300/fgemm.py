@@ -770,7 +770,8 @@ def sample(logits: torch.Tensor, u: torch.Tensor, *, temperature: float | torch.
             one.append(off)
             each.append(_vector(value, name, rows, dtype, dev))
         else:
-            one.append(value)
+            # (ctypes would take the lower 32 bits of a top_k beyond them)
+            one.append(min(max(value, -1), 0x7FFFFFFF) if name == "top_k" else value)
             each.append(None)
     lp, ld = _rows(logits, "logits", (rows, vocab), logits.dtype, dev)
     up = _vector(u, "u", rows, torch.float32, dev)

@@ -41,6 +41,16 @@ def test_sample_top_p_behind_a_long_top_k(kind, dtype):
             assert torch.equal(again[0], token) and torch.equal(again[1], prob)
 
 
+@pytest.mark.parametrize("top_k", [(1 << 31) + 7, (1 << 32) + 1, 1 << 40, -(1 << 31) - 1, -(1 << 32) + 1])
+def test_sample_top_k_beyond_32_bits(top_k):
+    """All of them keep every token: above the vocabulary, or not above 0."""
+    g = gen(32)
+    x, u = rand(g, 5, 300), torch.rand(5, generator=g, device=DEV)
+    want = fgemm.sample(x, u)
+    got = fgemm.sample(x, u, top_k=top_k)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 # ----------------------------------------------------------------------- w4
 
 
