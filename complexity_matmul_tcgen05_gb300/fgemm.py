@@ -609,7 +609,16 @@ def _on(t: torch.Tensor, name: str, handle: Handle | None):
     return L, h._h, dev
 
 
-def _norm_operands(x, gain, residual, total, inv_rms, eps, handle):
+def _like(x: torch.Tensor) -> torch.Tensor:
+    """New memory of x's shape and type whose rows lie behind 16-byte boundaries
+    as x's do, so that the kernel takes the same sums."""
+    m, n = x.shape
+    ld = n + (x.stride(0) - n) % 8 if m > 1 else max(n, 1)
+    shift = x.data_ptr() % 16 // x.element_size()
+    return torch.empty(m * ld + shift, dtype=x.dtype, device=x.device).as_strided((m, n), (ld, 1), shift)
+
+
+def _norm_operands(x, gain, residual, total, inv_rms, eps, handle, out=None):
     """The arguments both forms of the norm share, in the order of the C calls
     (through total's leading dimension), with the outputs they return."""
     L, h, dev = _on(x, "x", handle)
@@ -618,12 +627,12 @@ def _norm_operands(x, gain, residual, total, inv_rms, eps, handle):
     dt = _dtype_code(t)
     xp, ldx = _rows(x, "x", shape, t, dev)
     gp = _vector(gain, "gain", n, t, dev)
-    if residual is None and total is None:
+    if residual is None and total is None and (out is None or out.data_ptr() != xp):
         total, rp, ldr, tp, ldt = x, None, 0, None, 0
     else:
         rp, ldr = _rows(residual, "residual", shape, t, dev)
         if total is None:
-            total = torch.empty_like(x)
+            total = torch.empty_like(x) if residual is not None else _like(x)
         tp, ldt = _rows(total, "total", shape, t, dev)
     if inv_rms is None:
         inv_rms = torch.empty(m, dtype=torch.float32, device=x.device)
@@ -637,13 +646,14 @@ def rms_norm(x: torch.Tensor, gain: torch.Tensor, *, residual: torch.Tensor | No
              out: torch.Tensor | None = None, total: torch.Tensor | None = None,
              inv_rms: torch.Tensor | None = None, handle: Handle | None = None):
     """(y, total, inv_rms) of fgemm_rms_norm: total = x + residual rounded to
-    x's type (x itself, not copied, without a residual), y = total * inv_rms *
-    gain with inv_rms = 1 / sqrt(mean(total^2) + eps) per row (fp32).
+    x's type (without a residual x itself, or a copy where out takes its place),
+    y = total * inv_rms * gain with inv_rms = 1 / sqrt(mean(total^2) + eps) per
+    row (fp32).
 
     x and residual are M x N fp16 or bf16, gain has N entries.  out, total and
     inv_rms, if given, are written (out and total may be x, total may be the
     residual)."""
-    L, h, dev, args, total, inv_rms, ip = _norm_operands(x, gain, residual, total, inv_rms, eps, handle)
+    L, h, dev, args, total, inv_rms, ip = _norm_operands(x, gain, residual, total, inv_rms, eps, handle, out)
     if out is None:
         out = torch.empty_like(x)
     yp, ldy = _rows(out, "out", x.shape, x.dtype, dev)

@@ -293,6 +293,20 @@ def test_norm_backward_of_rows_far_from_one(n, layout):
         within("dgain", dgain, dg64, eg + np.abs(dg64) * ref.U32)
 
 
+@pytest.mark.parametrize("rows,n,layout", [(3, 256, "tight"), (1, 100, "tight"), (3, 100, "shifted"), (2, 70000, "tight")])
+def test_norm_in_place_keeps_the_total(rows, n, layout):
+    """y over x: the total that comes back, which the backward pass takes, is x as it was."""
+    g = gen(n)
+    x, gain = rand(g, rows, n).bfloat16(), (1 + 0.3 * rand(g, n)).bfloat16()
+    if layout == "shifted":
+        x = padded(x, 8, 1)
+    want = fgemm.rms_norm(x, gain)
+    before = x.clone()
+    y, total, inv = fgemm.rms_norm(x, gain, out=x)
+    assert y is x and torch.equal(y, want[0]) and torch.equal(inv, want[2])
+    assert torch.equal(total, before)
+
+
 # ------------------------------------------------------------------- errors
 
 
