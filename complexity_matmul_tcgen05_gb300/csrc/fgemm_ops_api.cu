@@ -74,6 +74,7 @@ fgemm_status_t fgemm_rms_norm(fgemm_handle_t h, int64_t M, int64_t N, const void
   fgemm_status_t s = rms_forward(h, p, M, N, x, ldx, residual, ldr, gain, eps, dtype, total, ldt, inv_rms);
   if (s != FGEMM_OK || M == 0) return s;
   if (!y) return bad_arg(h, "y must not be NULL");
+  if (y == total) return bad_arg(h, "y and total must not be the same memory");
   if (ldy < N) return bad_arg(h, "a leading dimension is below the row length");
   if (off(y, 2)) return bad(h, FGEMM_ERR_ALIGNMENT, "16-bit data must be 2-byte aligned, inv_rms 4-byte");
   if (!h) return no_handle();

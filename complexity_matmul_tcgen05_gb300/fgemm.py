@@ -651,7 +651,7 @@ def rms_norm(x: torch.Tensor, gain: torch.Tensor, *, residual: torch.Tensor | No
     row (fp32).
 
     x and residual are M x N fp16 or bf16, gain has N entries.  out, total and
-    inv_rms, if given, are written (out and total may be x, total may be the
+    inv_rms, if given, are written (out or total may be x, total may be the
     residual)."""
     L, h, dev, args, total, inv_rms, ip = _norm_operands(x, gain, residual, total, inv_rms, eps, handle, out)
     if out is None:

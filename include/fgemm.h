@@ -341,7 +341,7 @@ fgemm_status_t fgemm_plan_ex(fgemm_handle_t h, int64_t M, int64_t N, int64_t K,
  *   residual  NULL or M x N, ldr.  gain  N entries.  eps finite, >= 0.
  *   total     NULL or M x N, ldt: written (the next residual; may be x or
  *             residual itself).
- *   y         M x N, ldy (may be x itself).
+ *   y         M x N, ldy (may be x itself, but not the memory of total).
  *   inv_rms   NULL or M entries: written, for the backward pass.
  * Squares of bf16 values may leave fp32's range: y follows the formula all the
  * same, and inv_rms is what fp32 holds of inv (infinite below 2^-128 with eps 0).

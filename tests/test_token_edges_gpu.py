@@ -307,6 +307,13 @@ def test_norm_in_place_keeps_the_total(rows, n, layout):
     assert torch.equal(total, before)
 
 
+def test_norm_refuses_one_memory_for_both_outputs():
+    x, gain = torch.randn(3, 64, device=DEV).half(), torch.ones(64, device=DEV).half()
+    for kw in (dict(out=x, total=x), dict(out=x, total=x, residual=x.clone())):
+        with pytest.raises(fgemm.FgemmError):
+            fgemm.rms_norm(x, gain, **kw)
+
+
 # ------------------------------------------------------------------- errors
 
 
