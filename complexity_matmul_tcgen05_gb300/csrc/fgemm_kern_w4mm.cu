@@ -22,14 +22,14 @@
 //
 // What bounds it: the fold's chain (products done -> tensor memory -> scale, add
 // -> room for the next), not the tensor pipe nor memory.  Measured: 48 x 8192 x
-// 8192 fp16, groups of 64, 30.3 us; 2048 x 4096 x 14336 bf16, groups of 128, 311
-// us, 774 TFLOP/s.  (With the zero point taken off the group's sum in the fold, as
+// 8192 fp16, groups of 64, 30.3 us; 2048 x 4096 x 14336 bf16, groups of 128, 310
+// us, 775 TFLOP/s.  (With the zero point taken off the group's sum in the fold, as
 // z sum_k x: 32.4 and 341 us; but 128 x 8192 x 16384 in groups of 32 takes 241 us
 // against 223.)
 //
 // Roles: warp 0 loads the codes, warp 2 A, warps 1 and 3 issue the MMAs, warps 4..
-// expand the codes, the last 4 or 8 warps fold.  Every wait is bounded; a wait that runs out latches the
-// error word and all roles leave.
+// expand the codes, the last 4 or 8 warps fold.  Every wait is bounded; a wait
+// that runs out latches the error word and all roles leave.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -62,8 +62,8 @@ struct Cfg {
   // four of GROUPS accumulators each.  Where it is two, the codes' stages go
   // back on their own as soon as they have been multiplied (kAhead), so that
   // codes are expanded while both accumulators are multiplied or folded; where
-  // it is four, both go back together: 8192 x 16384, 32 rows (groups of 64) 43.3 us
-  // on their own against 41.1 together, 16 rows (128) 32.1 against 31.4.
+  // it is four, both go back together: 8192 x 16384, 16 rows, groups of 32 / 64 / 128
+  // 48.0 / 36.3 / 33.9 us on their own against 45.7 / 36.1 / 33.0 together.
   static constexpr int kAStages = 4;
   static constexpr int kDCols = GROUPS * MT;
   static constexpr int kDAt = kAStages * 64;
@@ -77,12 +77,10 @@ struct Cfg {
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(MT * kRows * 4 + kRows * 4 <= kCodeStages * kCodeBytes + kXStages * kXBytes, "the sums reuse the rings");
   static constexpr bool kAhead = kDStages < kAStages;
-  // Warps that issue the products, a step each in turn.  Two accumulators,
-  // codes' stages and accumulators handed back together and one warp / on
-  // their own and one warp / on their own and two warps: 2048 x 4096 x 14336
-  // (groups of 128) 361 / 361 / 340 us, 8192 x 16384 with 128 rows (64) 107 / 103 /
-  // 101, 32 rows (32) 60 / 58 / 54.  Four, on their own, one warp against two: 16
-  // rows (128) 46.3 / 32.1, 32 rows (64) 52.5 / 43.3.
+  // Warps that issue the products, a step each in turn.  One against two:
+  // 2048 x 4096 x 14336 (groups of 128) 357 / 310 us, 8192 x 16384 with 128 rows (64)
+  // 102.9 / 95.6, 32 rows (32) 63.2 / 59.9; with four accumulators 16 rows (128)
+  // 46.2 / 33.0, 32 rows (64) 52.0 / 40.3.
   static constexpr int kIssuers = 2;
   static_assert(kDAt + kDStages * kDCols <= 512 && kDStages % kIssuers == 0, "tensor memory");
 };
@@ -355,9 +353,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
     __syncwarp();
   } else if (warp == 1 || (C::kIssuers == 2 && warp == 3)) {
     // ---------------------------------------------------------- MMA
-    // (The condition as `warp == 1 || warp == 3` becomes one comparison, and the
-    // loop behind it slower: 2048 x 4096 x 14336 351 us instead of 340, 8192 x 16384
-    // with 32 rows 42 instead of 36.)
+    // (The condition as `warp == 1 || warp == 3` becomes one comparison; the loop
+    // behind it was 3 to 18 % slower then.)
     if (lane == 0) {
       // fp32 accumulator, fp16 operands, both K-major, N = MT, M = 128
       constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(MT >> 3) << 17) | ((128u >> 4) << 24);
@@ -365,10 +362,9 @@ __global__ void __launch_bounds__(kThreads, 1) w4mm_kernel(const __grid_constant
       Ring<C::kXStages> rx;
       Ring<C::kAStages> ra;
       Ring<C::kDStages> rd;
-      // A step's products are issued by one thread, whose time counts (16 rows:
-      // 590 clocks for the 8 products, 390 to tell the fold warps and to find
-      // the next step ready): one commit a step, on which the fold warps hand
-      // back what it used, and two warps.
+      // A step's products are issued by one thread, whose time counts: one
+      // commit a step, on which the fold warps hand back what it used, and two
+      // warps (kIssuers).
       const int turn = warp >> 1;
       if (turn) rx.next(), ra.next(), rd.next();
       for (int b = b0 + turn; b < b1; b += C::kIssuers) {
