@@ -13,17 +13,15 @@
 // so no weight is rounded, and scales cost a few operations a group instead of
 // one a weight.
 //
-// A code is a 16-bit operand of the tensor cores as it stands: four bits at
-// the bottom of an fp16 number are the subnormal q 2^-24, four bits above them
-// q 2^-20, both exact, so one logical operation makes two operands and one
-// shift serves four.  The zero point is taken off there, two codes at a time,
-// and exactly.  (Taken off the group's sum, as z sum_k x, it left 2^-24 of z
-// times an activation whose weight is 0: with one of them 2^20 times the rest,
-// hundreds of times the error of the sum itself.)  The factor 2^4 between the two kinds
-// goes into A.  For that, A too is held as fp16, scaled by a power of two for
-// each row and group (the largest value below 2^15; 2^11 for the k whose codes
-// are the upper kind), bf16 as well: its 8 significant bits fit, and what falls
-// below fp16's range is under 2^-35 of the group's largest value.
+// A code is an fp16 number as it stands: four bits at the bottom of one are the
+// subnormal q 2^-24, four bits above them q 2^-20, so one logical operation and one
+// multiply-add make two operands (q - z) 2^-9, exactly, and one shift serves four
+// (w4_expand).  (The zero point taken off the group's sum, as z sum_k x, left 2^-24
+// of z times an activation whose weight is 0: with one of them 2^20 times the rest,
+// hundreds of times the error of the sum itself.)  A too is held as fp16, scaled
+// by a power of two for each row and group (the largest value below 2^15), bf16
+// as well: its 8 significant bits fit, and what falls below fp16's range is under
+// 2^-39 of the group's largest value.
 // Where a CTA has met an infinite scale, outputs that are not finite are computed
 // again term by term (w4_exact).
 //
@@ -290,12 +288,11 @@ __global__ void __launch_bounds__(kW4Threads, 1) w4_kernel(const __grid_constant
 #pragma unroll
           for (int o = 1; o < G / 8; o <<= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
           const int e = w4_shift<BF16>(most);
-          if (run % (G / 8) == 0) unit_at[run / (G / 8) * 8 + m] = w4_pow2(24 - kW4Up - e);
-          const float even = w4_pow2(e), odd = even * 0.0625f;
+          if (run % (G / 8) == 0) unit_at[run / (G / 8) * 8 + m] = w4_unit(e);
+          const float f = w4_pow2(e);
           uint32_t o[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float f = j & 1 ? odd : even;
             const __half2 h = __floats2half2_rn(v[j] * f, v[j + 4] * f);
             o[j] = *reinterpret_cast<const uint32_t*>(&h);
           }

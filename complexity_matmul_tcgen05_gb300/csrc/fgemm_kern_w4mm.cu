@@ -7,9 +7,8 @@
 // As there, codes are never turned into weights: with acc = sum_k (q - z) x
 // over a group, the group's part is s acc, added to a running fp32 sum.  A tile
 // is 128 rows of W (the tensor core's rows) by MT rows of A.  Its codes go TMA
-// -> shared memory -> registers, where a logical operation makes two fp16
-// operands (the subnormals q 2^-24 and q 2^-20) and a subtraction takes z off
-// -> tensor memory; the product of a group is 2 to 8 MMAs into an accumulator of
+// -> shared memory -> registers, where a logical operation and a multiply-add
+// make two fp16 operands (q - z) 2^-9 -> tensor memory; the product of a group is 2 to 8 MMAs into an accumulator of
 // its own, which the fold warps read once, scale and add in registers.  So a
 // weight costs about one and a half ALU operations and nothing is rounded but
 // the output; the fold costs 2 fp32 operations for every group, row and column
@@ -22,10 +21,10 @@
 //
 // What bounds it: the fold's chain (products done -> tensor memory -> scale, add
 // -> room for the next), not the tensor pipe nor memory.  Measured: 48 x 8192 x
-// 8192 fp16, groups of 64, 30.3 us; 2048 x 4096 x 14336 bf16, groups of 128, 310
-// us, 775 TFLOP/s.  (With the zero point taken off the group's sum in the fold, as
-// z sum_k x: 32.4 and 341 us; but 128 x 8192 x 16384 in groups of 32 takes 241 us
-// against 223.)
+// 8192 fp16, groups of 64, 32.1 us; 2048 x 4096 x 14336 bf16, groups of 128, 317
+// us, 758 TFLOP/s.  (With the zero point taken off the group's sum in the fold, as
+// z sum_k x: 32.4 and 341 us; but 128 x 8192 x 16384 in groups of 32 takes 242 us
+// against 223.  With subnormal operands: 30.3 and 310.)
 //
 // Roles: warp 0 loads the codes, warp 2 A, warps 1 and 3 issue the MMAs, warps 4..
 // expand the codes, the last 4 or 8 warps fold.  Every wait is bounded; a wait
@@ -63,7 +62,7 @@ struct Cfg {
   // back on their own as soon as they have been multiplied (kAhead), so that
   // codes are expanded while both accumulators are multiplied or folded; where
   // it is four, both go back together: 8192 x 16384, 16 rows, groups of 32 / 64 / 128
-  // 48.0 / 36.3 / 33.9 us on their own against 45.7 / 36.1 / 33.0 together.
+  // 47.6 / 36.1 / 33.9 us on their own against 45.7 / 35.9 / 33.2 together.
   static constexpr int kAStages = 4;
   static constexpr int kDCols = GROUPS * MT;
   static constexpr int kDAt = kAStages * 64;
@@ -78,9 +77,9 @@ struct Cfg {
   static_assert(MT * kRows * 4 + kRows * 4 <= kCodeStages * kCodeBytes + kXStages * kXBytes, "the sums reuse the rings");
   static constexpr bool kAhead = kDStages < kAStages;
   // Warps that issue the products, a step each in turn.  One against two:
-  // 2048 x 4096 x 14336 (groups of 128) 357 / 310 us, 8192 x 16384 with 128 rows (64)
-  // 102.9 / 95.6, 32 rows (32) 63.2 / 59.9; with four accumulators 16 rows (128)
-  // 46.2 / 33.0, 32 rows (64) 52.0 / 40.3.
+  // 2048 x 4096 x 14336 (groups of 128) 346 / 317 us, 8192 x 16384 with 128 rows (64)
+  // 110.8 / 104.5, 32 rows (32) 61.5 / 60.0; with four accumulators 16 rows (128)
+  // 45.1 / 33.2, 32 rows (64) 49.7 / 40.6.
   static constexpr int kIssuers = 2;
   static_assert(kDAt + kDStages * kDCols <= 512 && kDStages % kIssuers == 0, "tensor memory");
 };
@@ -634,15 +633,14 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const __grid_constant__ W4
     for (int o = 1; o < LANES; o <<= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
     if (run >= runs) continue;
     const int e = w4_shift<BF16>(most);
-    const float even = w4_pow2(e), odd = even * 0.0625f;
-    if (run % LANES == 0) p.units[static_cast<long long>(run / LANES) * p.m_pad + m] = w4_pow2(24 - kW4Up - e);
+    const float f = w4_pow2(e);
+    if (run % LANES == 0) p.units[static_cast<long long>(run / LANES) * p.m_pad + m] = w4_unit(e);
     float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = w4_f32<BF16>(static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1))));
     uint32_t out[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float f = j & 1 ? odd : even;
       const __half2 h = __floats2half2_rn(v[j] * f, v[j + 4] * f);
       out[j] = *reinterpret_cast<const uint32_t*>(&h);
     }

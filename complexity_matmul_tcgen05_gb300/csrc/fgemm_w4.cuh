@@ -31,27 +31,29 @@ __device__ __forceinline__ float w4_f32(uint16_t v) {
 __device__ __forceinline__ uint32_t w4_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 __device__ __forceinline__ __half2 w4_half2(uint32_t bits) { return *reinterpret_cast<const __half2*>(&bits); }
 
-// A zero point (0 .. 255) in both kinds of codes: times 2^-24 in the low half,
-// times 2^-20 in the high half.
+// -z 2^-9 of a zero point (0 .. 255) as an fp16 pair.
 __device__ __forceinline__ uint32_t w4_zero(uint32_t z) {
-  return w4_bits(__hmul2(w4_half2(z | z << 16), w4_half2(0x4C003C00u)));  // (1, 16)
+  return w4_bits(__hmul2(w4_half2(z | z << 16), w4_half2(0xF800F800u)));  // z 2^-24 times -2^15
 }
 
-// The eight codes of a word less their zero point, as fp16 pairs: p[i] holds
-// code i in its low half and code i + 4 in its high half, times 2^-24 for even i
-// and 2^-20 for odd.  Codes and differences are fp16 numbers: nothing is rounded.
+// The eight codes of a word less their zero point as fp16 pairs: p[i] holds
+// (q - z) 2^-9 of code i in its low half and of code i + 4 in its high half.
+// Four bits at the bottom of an fp16 number are the subnormal q 2^-24, four
+// bits above them q 2^-20; one multiply-add takes either to (q - z) 2^-9,
+// exactly.  The results are normal numbers: the tensor core aligns its sums by
+// the operands' exponent fields, and kept only 16 to 20 bits below the largest
+// term when it was given the subnormals (25 now).
 __device__ __forceinline__ void w4_expand(uint32_t w, uint32_t zero, uint32_t (&p)[4]) {
-  const __half2 lower = __low2half2(w4_half2(zero)), upper = __high2half2(w4_half2(zero));
+  const __half2 lower = w4_half2(0x78007800u), upper = w4_half2(0x68006800u), z = w4_half2(zero);  // 2^15, 2^11
   const uint32_t v = w >> 8;
-  p[0] = w4_bits(__hsub2(w4_half2(w & 0x000F000Fu), lower));
-  p[1] = w4_bits(__hsub2(w4_half2(w & 0x00F000F0u), upper));
-  p[2] = w4_bits(__hsub2(w4_half2(v & 0x000F000Fu), lower));
-  p[3] = w4_bits(__hsub2(w4_half2(v & 0x00F000F0u), upper));
+  p[0] = w4_bits(__hfma2(w4_half2(w & 0x000F000Fu), lower, z));
+  p[1] = w4_bits(__hfma2(w4_half2(w & 0x00F000F0u), upper, z));
+  p[2] = w4_bits(__hfma2(w4_half2(v & 0x000F000Fu), lower, z));
+  p[3] = w4_bits(__hfma2(w4_half2(v & 0x00F000F0u), upper, z));
 }
 
-// What a product of expanded codes and a group's scaled A counts: the kernels
-// hold their sums in units of 2^kW4Up, so that the unit of values near the end
-// of fp32, 2^(24 - e - kW4Up), is still a number, and so is the sum of a group
+// The kernels hold their sums in units of 2^kW4Up, so that the unit of values near the end
+// of fp32, 2^(9 - e - kW4Up), is still a number, and so is the sum of a group
 // (255 x 128 x 2^128 at most) before its scale.
 constexpr int kW4Up = 16;
 
@@ -89,13 +91,16 @@ __device__ __forceinline__ float w4_pow2(int e) {
   return __uint_as_float(static_cast<uint32_t>(min(max(e + 127, 0), 255)) << 23);
 }
 
+// What a product of expanded codes and A scaled by 2^e counts, in units of 2^kW4Up.
+__device__ __forceinline__ float w4_unit(int e) { return w4_pow2(9 - kW4Up - e); }
+
 // The power of two that brings values whose largest magnitude has these bits
-// below 2^15 (0 for zeros; at most 2^120, which fp32 holds; at least 2^-113, or
-// 2^-114 for values that are not finite).
+// below 2^15 (0 for zeros; at most 2^119, whose unit fp32 holds; at least 2^-113,
+// or 2^-114 for values that are not finite).
 template <bool BF16>
 __device__ __forceinline__ int w4_shift(uint32_t most) {
   const int field = static_cast<int>(most) >> (BF16 ? 7 : 10);
-  return most == 0 ? 0 : min(120, 14 - (field - (BF16 ? 127 : 15)));
+  return most == 0 ? 0 : min(119, 14 - (field - (BF16 ? 127 : 15)));
 }
 
 }  // namespace fgemm

@@ -403,7 +403,7 @@ fgemm_status_t fgemm_rms_norm_backward(fgemm_handle_t h, int64_t M, int64_t N, c
  * Codes less their zero points are multiplied as they are and the scale is
  * applied to fp32 sums of a group: no weight is rounded, and a weight of 0
  * takes nothing of its activation, however large. Each value of A is held to
- * within 2^-35 of the largest of its row in its group.
+ * within 2^-39 of the largest of its row in its group.
  * A and W 16-byte aligned, lda a multiple of 8, ldw of 16, else
  * FGEMM_ERR_ALIGNMENT. K == 0: C = epi(bias).
  */

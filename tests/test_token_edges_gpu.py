@@ -56,8 +56,8 @@ def test_sample_top_k_beyond_32_bits(top_k):
 
 def w4_terms(A, W, scales, zeros, group):
     """(C, magnitude, lost) in 64 bits: the product, the sum of its terms'
-    magnitudes |A| |q - z| |s|, and what operands of 11 bits drop of a group's
-    small values: 2^-35 of its largest for each term."""
+    magnitudes |A| |q - z| |s|, and what fp16's range drops of a group's small
+    values: 2^-39 of its largest for each term."""
     k = A.shape[1]
     at = np.arange(k) // group
     s = scales[:, at]
@@ -67,7 +67,7 @@ def w4_terms(A, W, scales, zeros, group):
     for k0 in range(0, k, group):
         most = np.max(np.abs(A[:, k0:k0 + group]), axis=1)
         lost += np.outer(most, np.sum(np.abs(q[:, k0:k0 + group] * s[:, k0:k0 + group]), axis=1))
-    return A @ (q * s).T, np.abs(A) @ np.abs(q * s).T, lost * 2.0 ** -35
+    return A @ (q * s).T, np.abs(A) @ np.abs(q * s).T, lost * 2.0 ** -39
 
 
 def w4_close(C, A, W, scales, zeros, group, cols=None):
@@ -119,6 +119,34 @@ def test_w4_to_what_its_terms_allow(m, n, k, dtype, group, zeros):
         s = s / 16
     C = fgemm.matmul_w4(A, W, s, zeros=z, group=group)
     w4_close(C, A, W, s, z, group)
+
+
+@pytest.mark.parametrize("m", [1, 9])
+@pytest.mark.parametrize("first,second,third", [(0, 2, 4), (1, 3, 5), (0, 1, 7), (3, 8, 12)])
+def test_w4_terms_that_cancel_leave_the_rest(first, second, third, m):
+    """L - L + x, all with weights of one step: x comes back whole, as long as
+    24 bits hold it beside L."""
+    k, x = 64, 1 + 513 / 1024
+    for log_l in range(0, 13):
+        A = torch.zeros((m, k), device=DEV, dtype=torch.float16)
+        A[:, [first, second]] = 2.0 ** log_l
+        A[:, third] = x
+        q = torch.full((8, k), 8, device=DEV, dtype=torch.uint8)
+        q[:, first], q[:, second], q[:, third] = 9, 7, 9
+        C = fgemm.matmul_w4(A, q[:, 0::2] | (q[:, 1::2] << 4), torch.ones((8, 1), device=DEV).half(), group=64)
+        assert torch.all(C == x), log_l
+
+
+@pytest.mark.parametrize("m,n,k,group", [(26, 65, 213, 32), (142, 359, 290, 128), (7, 125, 46, 64), (174, 323, 22, 32),
+                                         (56, 129, 877, 32), (4, 509, 2266, 64), (35, 261, 3, 64), (278, 120, 45, 32),
+                                         (1, 96, 4096, 128), (100, 65, 4096, 128)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_w4_small_terms_beside_large_ones(m, n, k, group, dtype):
+    A, W, s, _, _ = w4_inputs(m, n, k, "f16", group, False, m + n)
+    hot = torch.rand(A.shape, generator=gen(m), device=DEV) < 0.01
+    A = torch.nn.functional.pad(torch.where(hot, A * 64, A / 128), (0, -k % 8)).to(TYPES[dtype])[:, :k]
+    C = fgemm.matmul_w4(A, W, s.to(A.dtype), group=group)
+    w4_close(C, A, W, s.to(A.dtype), None, group)
 
 
 @pytest.mark.parametrize("group", [32, 64, 128])
