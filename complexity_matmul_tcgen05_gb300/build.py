@@ -36,6 +36,11 @@ SOURCES = [
     "fgemm_kern_w4.cu",
     "fgemm_kern_w4mm.cu",
     "fgemm_kern_sample.cu",
+    "fgemm_cache_api.cu",
+    "fgemm_kern_rotary.cu",
+    "fgemm_kern_decode.cu",
+    "fgemm_kern_prompt.cu",
+    "fgemm_kern_logprobs.cu",
 ]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE,

@@ -1,0 +1,47 @@
+// fgemm_attn.cuh -- what the kernels around a key-value cache share: 16-bit
+// conversions and the place of a token in a paged cache.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+namespace fgemm {
+namespace attn {
+
+template <bool BF16>
+__device__ __forceinline__ float lo_f32(uint32_t w) {
+  if (BF16) return __uint_as_float(w << 16);
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(w & 0xFFFFu)));
+}
+template <bool BF16>
+__device__ __forceinline__ float hi_f32(uint32_t w) {
+  if (BF16) return __uint_as_float(w & 0xFFFF0000u);
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(w >> 16)));
+}
+
+template <bool BF16>
+__device__ __forceinline__ float to_f32(uint16_t bits) {
+  return lo_f32<BF16>(bits);
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint16_t to_16(float v) {
+  if (BF16) return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+  return __half_as_ushort(__float2half_rn(v));
+}
+
+// Two values in one word, lo in the low half, each rounded to nearest even.
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if (BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+}  // namespace attn
+}  // namespace fgemm

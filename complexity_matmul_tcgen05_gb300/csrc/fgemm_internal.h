@@ -452,6 +452,69 @@ struct SampleParams {
 };
 cudaError_t launch_sample(const SampleParams& p, int num_sms, cudaStream_t stream);
 
+// A tensor of heads: token t, head i at p + t * ld + i * hs.
+struct Heads {
+  uint16_t* p;
+  long long ld, hs;
+};
+
+// Rotary positions and the write into a paged cache (fgemm_kern_rotary.cu).
+struct RotaryParams {
+  Heads q, k, v, out;
+  uint16_t* k_cache;
+  uint16_t* v_cache;
+  long long k_page, k_token, k_head, v_page, v_token, v_head;
+  const int* positions;
+  const int* slots;
+  const float* inv_freq;
+  long long tokens, cache_slots;
+  int heads, kv_heads, dim, rot, interleaved, page_size, is_bf16;
+};
+cudaError_t launch_rotary(const RotaryParams& p, int num_sms, cudaStream_t stream);
+
+// Attention of one token a sequence over a paged cache (fgemm_kern_decode.cu).
+struct DecodeParams {
+  Heads q, out;
+  const uint16_t* k_cache;
+  const uint16_t* v_cache;
+  long long k_page, k_token, k_head, v_page, v_token, v_head, pages;
+  const int* page_table;
+  const int* lengths;
+  float* lse;  // or null
+  long long ld_table;
+  int seqs, heads, kv_heads, dim, page_size, table_pages, window, is_bf16;
+  float scale;
+};
+size_t decode_workspace(int seqs, int heads, int kv_heads, int dim, int num_sms);
+cudaError_t launch_decode(const DecodeParams& p, void* workspace, int num_sms, cudaStream_t stream);
+
+// Attention over packed prompts (fgemm_kern_prompt.cu).
+struct PromptParams {
+  Heads q, k, v, out;
+  const int* starts;
+  const int* k_starts;
+  float* lse;  // or null
+  long long tokens, k_tokens;
+  int seqs, heads, kv_heads, dim, causal, window, is_bf16;
+  float scale;
+  unsigned int* err;           // device error word
+  unsigned long long spin_ns;  // bound of every wait
+};
+cudaError_t launch_prompt(const PromptParams& p, int num_sms, cudaStream_t stream);
+
+// Log probabilities (fgemm_kern_logprobs.cu).
+struct LogprobParams {
+  const void* logits;
+  long long ld;
+  const int* tokens;
+  float* logprob;
+  float* entropy;  // or null
+  int* top_tokens;
+  float* top_logprobs;
+  int rows, vocab, type, top;  // type: 0 f16, 1 bf16, 2 f32
+};
+cudaError_t launch_logprobs(const LogprobParams& p, int num_sms, cudaStream_t stream);
+
 // One-level Winograd variant on the single-CTA kernel (bn = 128 or 256): the
 // Strassen kernel with up to four source blocks per formed operand; `tab`
 // must be the Winograd table.

@@ -40,6 +40,13 @@ class Sampling(ctypes.Structure):
                 ("top_ps", ctypes.c_void_p), ("min_ps", ctypes.c_void_p)]
 
 
+class KvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("k_page", ctypes.c_int64), ("k_token", ctypes.c_int64),
+                ("k_head", ctypes.c_int64), ("v_page", ctypes.c_int64), ("v_token", ctypes.c_int64),
+                ("v_head", ctypes.c_int64)]
+
+
 class FgemmError(RuntimeError):
     def __init__(self, status: int, message: str):
         self.status = status
@@ -113,6 +120,17 @@ def lib() -> ctypes.CDLL:
         L.fgemm_matmul_w4_workspace.argtypes = [i64, i64, i32]
         L.fgemm_matmul_w4_workspace.restype = size
         L.fgemm_sample.argtypes = [vp, i64, i64, vp, i64, i32, vp, ctypes.POINTER(Sampling), vp, vp]
+        heads = [vp, i64, i64]
+        cache_p = ctypes.POINTER(KvCache)
+        L.fgemm_rotary_cache.argtypes = [vp, i64, i32, i32, i32] + 3 * heads + [vp, vp, vp, i32, i32, st] + heads + \
+            [cache_p]
+        L.fgemm_attention_paged_workspace.argtypes = [vp, i64, i32, i32, i32]
+        L.fgemm_attention_paged_workspace.restype = size
+        L.fgemm_attention_paged.argtypes = [vp, i64, i32, i32, i32] + heads + [cache_p, vp, i64, i64, vp, f32, i32,
+                                                                               st] + heads + [vp, vp, size]
+        L.fgemm_attention.argtypes = [vp, i64, i64, i64, i32, i32, i32] + 3 * heads + [vp, vp, i32, i32, f32, st] + \
+            heads + [vp]
+        L.fgemm_logprobs.argtypes = [vp, i64, i64, vp, i64, i32, vp, i32, vp, vp, vp, vp]
         L.fgemm_plan.argtypes = [vp, i64, i64, i64, st, epi_p, ctypes.POINTER(st),
                                  ctypes.POINTER(i32), ctypes.POINTER(i32),
                                  ctypes.POINTER(ctypes.c_double)]
@@ -177,7 +195,8 @@ def lib() -> ctypes.CDLL:
                      "fgemm_set_split_mode", "fgemm_set_lcma_formation", "fgemm_call_launches", "fgemm_matmul_host", "fgemm_matmul_host_ex", "fgemm_matmul_rms", "fgemm_matmul_mx",
                      "fgemm_mx_to_bf16", "fgemm_strassen_static_get_error",
                      "fgemm_strassen_static_selftest_timeout", "fgemm_rms_norm", "fgemm_rms_norm_mx",
-                     "fgemm_rms_norm_backward", "fgemm_matmul_w4", "fgemm_sample"):
+                     "fgemm_rms_norm_backward", "fgemm_matmul_w4", "fgemm_sample", "fgemm_rotary_cache",
+                     "fgemm_attention_paged", "fgemm_attention", "fgemm_logprobs"):
             getattr(L, name).restype = st
         _lib = L
         return L
@@ -593,14 +612,14 @@ def _vector(t: torch.Tensor | None, name: str, n: int, dtype, dev: int) -> int |
     return t.data_ptr()
 
 
-def _on(t: torch.Tensor, name: str, handle: Handle | None):
+def _on(t: torch.Tensor, name: str, handle: Handle | None, dims: int = 2):
     """(library, handle pointer, device index) of a call whose main operand is
     t; the handle is set to the current stream of t's device."""
     dev = t.get_device()
     if dev < 0:
         raise FgemmError(ERR_INVALID_ARG, f"{name} must be a CUDA tensor")
-    if t.dim() != 2:
-        raise FgemmError(ERR_INVALID_ARG, f"{name} must be 2-D")
+    if t.dim() != dims:
+        raise FgemmError(ERR_INVALID_ARG, f"{name} must be {dims}-D")
     h = handle if handle is not None else default_handle()
     if dev != h.device:
         raise FgemmError(ERR_INVALID_ARG, f"{name} is on cuda:{dev}, the handle on cuda:{h.device}")
@@ -792,3 +811,171 @@ def sample(logits: torch.Tensor, u: torch.Tensor, *, temperature: float | torch.
     if s != OK:
         _check(s, h)
     return token, prob
+
+
+# ---------------------------------- operators around a key-value cache
+
+
+def _heads(t: torch.Tensor, name: str, shape, dtype, dev: int) -> tuple[int, int, int]:
+    """(address, token stride, head stride) of a tokens x heads x dim operand on
+    device dev, checked."""
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev:
+        raise FgemmError(ERR_INVALID_ARG, f"{name} must be a {tuple(shape)} {dtype} tensor on cuda:{dev}")
+    ld, hs, unit = t.stride()
+    if unit != 1 and shape[2] > 1:
+        raise FgemmError(ERR_INVALID_ARG, f"the values of a head of {name} must be adjacent")
+    return t.data_ptr(), ld, hs
+
+
+def _cache(k: torch.Tensor, v: torch.Tensor, kv_heads: int | None, dim: int, dtype, dev: int) -> KvCache:
+    """The C view of a paged cache, checked; kv_heads None: any number."""
+    for t, name in ((k, "k_cache"), (v, "v_cache")):
+        if t.dim() != 4 or t.dtype != dtype or t.get_device() != dev or t.shape[3] != dim or t.shape != k.shape or \
+                (kv_heads is not None and t.shape[2] != kv_heads):
+            raise FgemmError(ERR_INVALID_ARG, f"{name} must be a pages x page size x key heads x {dim} {dtype} tensor "
+                                              f"on cuda:{dev}")
+        if t.stride(3) != 1 and dim > 1:
+            raise FgemmError(ERR_INVALID_ARG, f"the values of a head of {name} must be adjacent")
+    return KvCache(k.data_ptr(), v.data_ptr(), k.shape[0], k.shape[1], *k.stride()[:3], *v.stride()[:3])
+
+
+def rotary_cache(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
+                 inv_freq: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, *, interleaved: bool = False,
+                 out: torch.Tensor | None = None, handle: Handle | None = None) -> torch.Tensor:
+    """The queries with rotary positions (fgemm_rotary_cache); the keys with
+    theirs and the values go into the cache.
+
+    q is T x heads x dim, k and v T x key heads x dim (fp16 or bf16; parts of one
+    projection's output do), positions and slots T int32 entries, inv_freq rot / 2
+    fp32 entries (radians a position).  The first rot values of a head turn in
+    pairs (i, i + rot / 2), or (2 i, 2 i + 1) if interleaved.  k_cache and v_cache are
+    pages x page size x key heads x dim; slot = page * page size + token in the
+    page, tokens with a slot outside the cache (-1) are not written.  out, if
+    given, is written (it may be q)."""
+    L, h, dev = _on(q, "q", handle, 3)
+    t = q.dtype
+    dt = _dtype_code(t)
+    n, heads, dim = q.shape
+    kv = (n, k.shape[1] if k.dim() == 3 else 1, dim)
+    qa = _heads(q, "q", q.shape, t, dev)
+    ka = _heads(k, "k", kv, t, dev)
+    va = _heads(v, "v", kv, t, dev)
+    pp = _vector(positions, "positions", n, torch.int32, dev)
+    sp = _vector(slots, "slots", n, torch.int32, dev)
+    half = inv_freq.shape[0] if inv_freq.dim() == 1 else 0
+    fp = _vector(inv_freq, "inv_freq", half, torch.float32, dev)
+    cache = _cache(k_cache, v_cache, kv[1], dim, t, dev)
+    if out is None:
+        out = torch.empty((n, heads, dim), dtype=t, device=q.device)
+    oa = _heads(out, "out", q.shape, t, dev)
+    s = L.fgemm_rotary_cache(h, n, heads, kv[1], dim, *qa, *ka, *va, pp, sp, fp, 2 * half, 1 if interleaved else 0, dt,
+                             *oa, ctypes.byref(cache))
+    if s != OK:
+        _check(s, h)
+    return out
+
+
+def attention_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                    lengths: torch.Tensor, *, scale: float | None = None, window: int = 0,
+                    out: torch.Tensor | None = None, handle: Handle | None = None):
+    """(out, lse) of fgemm_attention_paged: attention of one new token of each
+    sequence, q (sequences x heads x dim), over the lengths[s] tokens (int32,
+    the new one among them) that the pages page_table[s] (int32) of the cache
+    hold (k_cache and v_cache: pages x page size x key heads x dim).
+
+    scale None: 1 / sqrt(dim); window 0: every token, else the last `window`.
+    lse is the natural logarithm of each row's sum (sequences x heads, fp32); a
+    sequence of length 0 gives zeros and -inf.  out, if given, is written (it
+    may be q)."""
+    L, h, dev = _on(q, "q", handle, 3)
+    t = q.dtype
+    dt = _dtype_code(t)
+    n, heads, dim = q.shape
+    cache = _cache(k_cache, v_cache, None, dim, t, dev)
+    kv_heads = k_cache.shape[2]
+    qa = _heads(q, "q", q.shape, t, dev)
+    pages = page_table.shape[1] if page_table.dim() == 2 else 0
+    tp, ldt = _rows(page_table, "page_table", (n, pages), torch.int32, dev)
+    lp = _vector(lengths, "lengths", n, torch.int32, dev)
+    if out is None:
+        out = torch.empty((n, heads, dim), dtype=t, device=q.device)
+    oa = _heads(out, "out", q.shape, t, dev)
+    lse = torch.empty((n, heads), dtype=torch.float32, device=q.device)
+    size = L.fgemm_attention_paged_workspace(h, n, heads, kv_heads, dim)
+    work = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
+    s = L.fgemm_attention_paged(h, n, heads, kv_heads, dim, *qa, ctypes.byref(cache), tp, ldt, pages, lp,
+                                dim ** -0.5 if scale is None else scale, window, dt, *oa, lse.data_ptr(),
+                                None if work is None else work.data_ptr(), size)
+    if s != OK:
+        _check(s, h)
+    return out, lse
+
+
+def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, starts: torch.Tensor, *,
+              k_starts: torch.Tensor | None = None, causal: bool = True, window: int = 0, scale: float | None = None,
+              out: torch.Tensor | None = None, lse: torch.Tensor | None = None, handle: Handle | None = None):
+    """(out, lse) of fgemm_attention over packed prompts: sequence s has the
+    queries starts[s] .. starts[s + 1] - 1 of q (T x heads x dim) and the keys and
+    values k_starts[s] .. k_starts[s + 1] - 1 of k and v (T_k x key heads x dim);
+    its queries are the last of its keys' positions.  starts and k_starts (None:
+    starts) are ascending int32 vectors of sequences + 1 entries.
+
+    causal: keys up to a query's own position, the last `window` of them if
+    window > 0.  scale None: 1 / sqrt(dim).  lse is the natural logarithm of each
+    row's sum (T x heads, fp32).  A query that sees no key gives zeros and -inf;
+    rows of no sequence are left as they are.  out and lse, if given, are
+    written."""
+    L, h, dev = _on(q, "q", handle, 3)
+    t = q.dtype
+    dt = _dtype_code(t)
+    n, heads, dim = q.shape
+    kv = (k.shape[0], k.shape[1], dim) if k.dim() == 3 else (0, 1, dim)
+    qa = _heads(q, "q", q.shape, t, dev)
+    ka = _heads(k, "k", kv, t, dev)
+    va = _heads(v, "v", kv, t, dev)
+    seqs = starts.shape[0] - 1 if starts.dim() == 1 else -1
+    if seqs < 0:
+        raise FgemmError(ERR_INVALID_ARG, "starts must be a vector of sequences + 1 entries")
+    sp = _vector(starts, "starts", seqs + 1, torch.int32, dev)
+    kp = _vector(k_starts, "k_starts", seqs + 1, torch.int32, dev)
+    if out is None:
+        out = torch.empty((n, heads, dim), dtype=t, device=q.device)
+    oa = _heads(out, "out", q.shape, t, dev)
+    if lse is None:
+        lse = torch.empty((n, heads), dtype=torch.float32, device=q.device)
+    elif lse.shape != (n, heads) or lse.dtype != torch.float32 or lse.get_device() != dev or not lse.is_contiguous():
+        raise FgemmError(ERR_INVALID_ARG, f"lse must be a contiguous {(n, heads)} float32 tensor on cuda:{dev}")
+    s = L.fgemm_attention(h, seqs, n, kv[0], heads, kv[1], dim, *qa, *ka, *va, sp, kp, 1 if causal else 0, window,
+                          dim ** -0.5 if scale is None else scale, dt, *oa, lse.data_ptr())
+    if s != OK:
+        _check(s, h)
+    return out, lse
+
+
+def logprobs(logits: torch.Tensor, tokens: torch.Tensor, *, top: int = 0, handle: Handle | None = None):
+    """(logprob, entropy, top_tokens, top_logprobs) of fgemm_logprobs: for each
+    row of logits (rows x vocab, fp16, bf16 or fp32) the log probability of the
+    given token (int32), the entropy (both fp32, natural logarithms), and the
+    `top` (0 to 32) most probable tokens (rows x top, int32, ties by the lower
+    index) with their log probabilities (fp32).
+
+    A token outside the vocabulary has -inf; where fewer than `top` logits are
+    above -inf the rest is token -1 with -inf."""
+    L, h, dev = _on(logits, "logits", handle)
+    rows, vocab = logits.shape
+    code = LOGIT_TYPES.get(logits.dtype)
+    if code is None:
+        raise FgemmError(ERR_INVALID_ARG, f"logits must be float16, bfloat16 or float32, not {logits.dtype}")
+    if not 0 <= top <= 32:
+        raise FgemmError(ERR_INVALID_ARG, "top must be in 0 .. 32")
+    lp, ld = _rows(logits, "logits", (rows, vocab), logits.dtype, dev)
+    tp = _vector(tokens, "tokens", rows, torch.int32, dev)
+    logprob = torch.empty(rows, dtype=torch.float32, device=logits.device)
+    entropy = torch.empty(rows, dtype=torch.float32, device=logits.device)
+    top_tokens = torch.empty((rows, top), dtype=torch.int32, device=logits.device)
+    top_logprobs = torch.empty((rows, top), dtype=torch.float32, device=logits.device)
+    s = L.fgemm_logprobs(h, rows, vocab, lp, ld, code, tp, top, logprob.data_ptr(), entropy.data_ptr(),
+                         top_tokens.data_ptr() if top else None, top_logprobs.data_ptr() if top else None)
+    if s != OK:
+        _check(s, h)
+    return logprob, entropy, top_tokens, top_logprobs

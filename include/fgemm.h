@@ -451,6 +451,127 @@ fgemm_status_t fgemm_sample(fgemm_handle_t h, int64_t rows, int64_t vocab, const
                             int32_t logits_type, const float* u, const fgemm_sampling_t* how, int32_t* token,
                             float* prob);
 
+/* ------------------------------------------------------------------------
+ * Operators of a token step around a key-value cache. Tensors of heads are
+ * T x heads x dim of dtype with two strides in elements: ld from one token to
+ * the next, hs from one head to the next (a projection's output row by row:
+ * hs = dim; head by head: hs >= T * ld); values of a head are adjacent. dim is
+ * a multiple of 8 up to FGEMM_MAX_HEAD_DIM, addresses are 16-byte aligned and
+ * strides multiples of 8 and at least dim, else FGEMM_ERR_INVALID_ARG or
+ * FGEMM_ERR_ALIGNMENT (a stride over a single token or head is not looked at). heads is a
+ * multiple of kv_heads and query head i reads key head i / (heads / kv_heads).
+ * As the operators above they allocate nothing, keep nothing in the handle and
+ * do not synchronise. What is read on the device (lengths, starts, pages,
+ * slots) is held to the sizes given here before it is used.
+ * ------------------------------------------------------------------------ */
+#define FGEMM_MAX_HEAD_DIM 128
+
+/* A paged cache: token t of page p, head i of its keys is
+ * k + p * k_page + t * k_token + i * k_head, values likewise. Strides in
+ * elements, multiples of 8 and at least dim; pages * page_size < 2^31. */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t pages;
+  int32_t page_size; /* tokens of a page, any number from 1 */
+  int64_t k_page, k_token, k_head;
+  int64_t v_page, v_token, v_head;
+} fgemm_kv_cache_t;
+
+/*
+ * Rotary positions of queries and keys, and the write of keys and values into
+ * a paged cache. For token t and i < rot / 2, with
+ * angle = positions[t] * inv_freq[i] (formed in 64 bits), a pair (a, b) becomes
+ *   (a cos - b sin, b cos + a sin)       in fp32, rounded once;
+ * pairs are values i and i + rot / 2 of a head, or 2 i and 2 i + 1 where
+ * interleaved is not 0; values from rot on stay as they are.
+ *   q, out     T x heads x dim; out may be q itself.
+ *   k, v       T x kv_heads x dim.
+ *   positions  T entries.
+ *   slots      T entries: page * page_size + token in the page, each slot once
+ *              at most. Tokens with a slot outside the cache are not written.
+ *   inv_freq   rot / 2 entries, radians a position (may be NULL for rot 0).
+ *   rot        even, 0 .. dim.
+ */
+fgemm_status_t fgemm_rotary_cache(fgemm_handle_t h, int64_t T, int32_t heads, int32_t kv_heads, int32_t dim,
+                                  const void* q, int64_t ldq, int64_t hsq, const void* k, int64_t ldk, int64_t hsk,
+                                  const void* v, int64_t ldv, int64_t hsv, const int32_t* positions,
+                                  const int32_t* slots, const float* inv_freq, int32_t rot, int32_t interleaved,
+                                  fgemm_dtype_t dtype, void* out, int64_t ldo, int64_t hso,
+                                  const fgemm_kv_cache_t* cache);
+
+/*
+ * Attention of one new token of each of `seqs` sequences over a paged cache.
+ * Sequence s has lengths[s] tokens (the new one among them), token j in slot
+ * j % page_size of page page_table[s][j / page_size]. With
+ * x_j = scale * (q . k_j) over the tokens j that are seen, window of them at most
+ * (window 0: all; else the last `window`):
+ *   out = sum_j e^(x_j - lse) v_j,   lse = log sum_j e^(x_j).
+ * A row that sees nothing (length 0) gets zeros and lse = -infinity.
+ *   q, out      seqs x heads x dim; out may be q itself.
+ *   page_table  seqs rows of `table_pages` entries, ld_table >= table_pages apart.
+ *               Pages outside the cache count as not there: their tokens are not
+ *               seen. Lengths beyond the table are held to it, below 0 to 0.
+ *   lengths     seqs entries.
+ *   scale       positive and finite.  window  not negative.
+ *   lse         NULL or seqs x heads fp32 entries (natural logarithm).
+ *   workspace   at least fgemm_attention_paged_workspace(h, seqs, heads,
+ *               kv_heads, dim) bytes of device memory, 16-byte aligned, left with
+ *               nothing of use. Calls that may run at the same time need one each.
+ * Sums are fp32 and their order depends on the sizes, the lengths and the SM
+ * count only; weights are rounded to dtype before they meet the values.
+ */
+size_t fgemm_attention_paged_workspace(fgemm_handle_t h, int64_t seqs, int32_t heads, int32_t kv_heads, int32_t dim);
+fgemm_status_t fgemm_attention_paged(fgemm_handle_t h, int64_t seqs, int32_t heads, int32_t kv_heads, int32_t dim,
+                                     const void* q, int64_t ldq, int64_t hsq, const fgemm_kv_cache_t* cache,
+                                     const int32_t* page_table, int64_t ld_table, int64_t table_pages,
+                                     const int32_t* lengths, float scale, int32_t window, fgemm_dtype_t dtype,
+                                     void* out, int64_t ldo, int64_t hso, float* lse, void* workspace,
+                                     size_t workspace_bytes);
+
+/*
+ * Attention over packed prompts. Sequence s has queries starts[s] ..
+ * starts[s + 1] - 1 and keys k_starts[s] .. k_starts[s + 1] - 1; its queries are
+ * the last of its keys' positions: with n queries and m keys, query i stands at
+ * position m - n + i. It sees every key of its sequence, or with causal not 0
+ * those up to its position, or with window > 0 (causal only) the last `window`
+ * of these. Formulas and rows that see nothing as fgemm_attention_paged.
+ *   q, out    T x heads x dim.  k, v  T_k x kv_heads x dim. out overlaps none of them.
+ *   starts    seqs + 1 ascending entries in 0 .. T.  k_starts  the same in
+ *             0 .. T_k, or NULL: starts.
+ *   lse       NULL or T x heads fp32 entries.
+ * Rows of out and lse that belong to no sequence are left as they were. A value
+ * that is not finite reaches only the queries that see its key.
+ */
+fgemm_status_t fgemm_attention(fgemm_handle_t h, int64_t seqs, int64_t T, int64_t T_k, int32_t heads,
+                               int32_t kv_heads, int32_t dim, const void* q, int64_t ldq, int64_t hsq,
+                               const void* k, int64_t ldk, int64_t hsk, const void* v, int64_t ldv, int64_t hsv,
+                               const int32_t* starts, const int32_t* k_starts, int32_t causal, int32_t window,
+                               float scale, fgemm_dtype_t dtype, void* out, int64_t ldo, int64_t hso, float* lse);
+
+/*
+ * Log probability of a given token in each row of logits, the row's entropy
+ * and its most probable tokens. For a row x with largest value m (a NaN counts
+ * as -infinity), z = sum_i e^(x_i - m), log p_i = x_i - m - log z:
+ *   logprob = log p_token,   entropy = -sum_i p_i log p_i   (natural logarithms)
+ *   top_tokens, top_logprobs: the `top` largest, ties by the lower index.
+ * A token outside 0 .. vocab - 1 has logprob -infinity. Tokens at -infinity are
+ * no alternatives: what is left over of `top` gets token -1 and -infinity, so a
+ * row with nothing above -infinity (as fgemm_sample: token -1) has logprob
+ * -infinity and entropy 0. A row that holds +infinity shares its probability
+ * among those entries.
+ *   logits, ld    rows x vocab of logits_type (as fgemm_sample).
+ *   tokens        rows entries.
+ *   logprob       rows entries.  entropy  rows entries or NULL.
+ *   top           0 .. FGEMM_LOGPROBS_MAX_TOP.  top_tokens, top_logprobs
+ *                 rows x top entries (NULL for top 0).
+ * vocab above FGEMM_SAMPLE_MAX_VOCAB -> FGEMM_ERR_UNSUPPORTED.
+ */
+#define FGEMM_LOGPROBS_MAX_TOP 32
+fgemm_status_t fgemm_logprobs(fgemm_handle_t h, int64_t rows, int64_t vocab, const void* logits, int64_t ld,
+                              int32_t logits_type, const int32_t* tokens, int32_t top, float* logprob,
+                              float* entropy, int32_t* top_tokens, float* top_logprobs);
+
 /* Synchronises the handle's stream, then returns and clears the latched
  * device error (FGEMM_OK, FGEMM_ERR_TIMEOUT or FGEMM_ERR_CUDA). */
 fgemm_status_t fgemm_get_error(fgemm_handle_t h);
