@@ -236,6 +236,13 @@ def test_paged_special_values():
     assert bool(torch.isnan(out[3]).all()) and bool(torch.isnan(lse[3]).all())
 
 
+def test_paged_only_nan_keys():
+    q, k, v, table, n, _, _ = paged_inputs(gen(5), [1, 300], 2, 1, 64, 16, torch.bfloat16)
+    k.fill_(NAN)
+    out, lse = fgemm.attention_paged(q, k, v, table, n)
+    assert bool(torch.isnan(out).all()) and bool(torch.isnan(lse).all())
+
+
 def test_paged_long_context_and_repeatable():
     lengths = [70001, 3, 20000]
     q, k, v, table, n, keys, values = paged_inputs(gen(6), lengths, 8, 2, 64, 64, torch.bfloat16)
