@@ -500,6 +500,7 @@ struct PromptParams {
   unsigned int* err;           // device error word
   unsigned long long spin_ns;  // bound of every wait
 };
+long long prompt_ctas(long long tokens, int seqs, int heads);  // of a launch
 cudaError_t launch_prompt(const PromptParams& p, int num_sms, cudaStream_t stream);
 
 // Log probabilities (fgemm_kern_logprobs.cu).

@@ -1,74 +1,637 @@
-// fgemm_kern_prompt.cu -- attention over packed prompts: one warp a query and
-// head, keys one after the other with the running maximum and sum of the
-// softmax.
+// fgemm_kern_prompt.cu -- attention over packed prompts, on tcgen05.
+//
+//   S = Q K^T (fp32),  x = scale S,  w = 2^(x log2 e - r),  O = w V,
+//   out = O / sum w,  lse = (r + log2 sum w) ln 2
+//
+// One pass over the keys of a tile of 128 queries, 128 keys a step: S goes from
+// the tensor core to tensor memory, a thread takes one row of it (a query) to
+// registers, so the maximum and the sum of a row need no other thread, and
+// writes the weights, rounded to 16 bits, over S in tensor memory, from where
+// they are an operand of the product with the values. The reference r follows
+// the row's maximum only when that is more than 8 above it: the weights stay
+// below 2^8 (fp16: below 2^14, so that small ones keep their bits) and O is
+// seldom scaled.
+//
+// A CTA has two tiles of queries (256 rows) of one head. While the tensor core
+// works on one tile's products the threads of the other tile form its weights.
+// Warps 0-3 and 4-7 are the two tiles' rows, warp 8 loads (TMA, a ring of key
+// and value tiles), warp 9 issues the products, warps 10 and 11 look after the
+// values of steps in which not every row sees every key.
+//
+// Those are the steps on the diagonal, at a window's edge and at the end of a
+// sequence. A weight there may be 0 because its key is hidden, and 0 times a
+// value that is not finite would be NaN: the two warps clear the values behind the
+// sequence's end (another sequence's) and look for others that are not finite.
+// If there are any, the step's product is taken row by row over the keys that
+// each row sees (product_by_rows), without the tensor core.
+//
+// Every wait is bounded; a wait that runs out latches the error word and all roles
+// leave.
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include <cstdint>
 
 #include "fgemm_attn.cuh"
 #include "fgemm_internal.h"
+#include "fgemm_ptx.cuh"
 
 namespace fgemm {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 namespace {
 
 using namespace attn;
 
-__device__ __forceinline__ int held(int v, long long lo, long long hi) {
-  return static_cast<int>(min(max(static_cast<long long>(v), lo), hi));
+constexpr int kTile = 128;            // queries of a tile, keys of a step
+constexpr int kRows = 2 * kTile;      // queries of a CTA
+constexpr int kThreads = 384;
+constexpr float kSlack = 8.0f;        // log2 of how far the maximum may be above the reference
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+template <int DP>  // values of a head, padded: 64 or 128
+struct Cfg {
+  static constexpr int kBytes = kTile * DP * 2;  // of a tile of queries, keys or values
+  static constexpr int kStages = DP == 128 ? 5 : 8;
+  static constexpr int kBars = 2 + 3 * kStages + 7;
+  static constexpr int kBarAt = (2 + kStages) * kBytes;
+  static constexpr int kSmem = 1024 + kBarAt + 8 * kBars + 8 * kStages + 16;
+  static constexpr int kOAt = 256;  // tensor memory: scores of the two tiles, then their outputs
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+struct Args {
+  CUtensorMap q, k, v;
+  PromptParams p;
+  int slots;  // of 256 queries, over all sequences
+};
+
+// ------------------------------------------------------------------- PTX
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(128) prompt_rows_kernel(const __grid_constant__ PromptParams p) {
-  const int lane = threadIdx.x & 31, head = blockIdx.y;
-  const long long t = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (t >= p.tokens) return;
-  int lo = 0, hi = p.seqs;  // the last sequence that starts at or before t
+// D[tmem] (+)= A[tmem] * B[smem desc].
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x16(uint32_t at, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_x8(uint32_t at, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// Eight columns, with the wait for them.
+__device__ __forceinline__ void tmem_ld_x8(uint32_t at, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// ----------------------------------------------------------------- waits
+
+// Waits for a phase; gives up when another role has (the error word) or when
+// the time limit runs out, and then latches `code`.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, unsigned int* err, unsigned long long spin_ns,
+                                       uint32_t code, bool honor) {
+  const uint64_t t0 = ptx::globaltimer();
+#pragma unroll 1
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (ptx::mbar_try_wait(bar, parity)) return true;
+    if (honor && *reinterpret_cast<volatile unsigned int*>(err) != 0u) return false;
+    if (ptx::globaltimer() - t0 > spin_ns) {
+      atomicCAS(err, 0u, code);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const PromptParams& p, int role) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  return wait_slow(bar, parity, p.err, p.spin_ns,
+                   kErrTimeout | (static_cast<uint32_t>(role) << 24) | (blockIdx.x & 0xFFFFFFu), true);
+}
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const PromptParams& p, int role) {
+  return __all_sync(0xFFFFFFFFu, wait(bar, parity, p, role));
+}
+__device__ __forceinline__ void wait_out(uint32_t bar, uint32_t parity, const PromptParams& p, int role) {
+  if (!ptx::mbar_try_wait(bar, parity))
+    wait_slow(bar, parity, p.err, p.spin_ns, kErrTimeout | (static_cast<uint32_t>(role) << 24), false);
+}
+
+// ------------------------------------------------------------------ tiles
+
+__device__ __forceinline__ int held(int v, int lo, long long hi) {
+  return static_cast<int>(min(max(static_cast<long long>(v), static_cast<long long>(lo)), hi));
+}
+
+// The sequence of slot `slot`. Sequence i begins at slot floor(start_i / 256) + i,
+// which leaves it at least ceil(length / 256) slots before the next one begins.
+// All lanes of a warp search together. -1: the slot lies before the first.
+__device__ __forceinline__ int sequence_of(const PromptParams& p, int slot) {
+  const int lane = threadIdx.x & 31;
+  auto first = [&](int i) { return held(p.starts[i], 0, p.tokens) / kRows + i; };
+  int lo = 0, hi = p.seqs;  // the last i in [lo, hi) with first(i) <= slot, if first(lo) is
   while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (p.starts[mid] <= t) lo = mid; else hi = mid;
+    const int step = (hi - lo + 31) / 32, i = lo + lane * step;
+    const bool ok = lane == 0 || (i < hi && first(i) <= slot);
+    const int n = __ffs(~__ballot_sync(0xFFFFFFFFu, ok)) - 1;  // lanes from 0 on that hold it
+    const int at = lo + ((n < 0 ? 32 : n) - 1) * step;
+    hi = min(hi, at + step);
+    lo = at;
   }
-  // (empty sequences start where the next one does: the last of them holds t)
-  const int q0 = held(p.starts[lo], 0, p.tokens), q1 = held(p.starts[lo + 1], q0, p.tokens);
-  if (t < q0 || t >= q1) return;
-  const int k0 = held(p.k_starts[lo], 0, p.k_tokens), k1 = held(p.k_starts[lo + 1], k0, p.k_tokens);
-  const long long at = (k1 - k0) - (q1 - q0) + (t - q0);  // the query's position
-  const long long last = p.causal ? min(at + 1, static_cast<long long>(k1 - k0)) : k1 - k0;
-  const long long first = p.window > 0 ? max(0LL, at + 1 - p.window) : 0;
-  const int kv = head / (p.heads / p.kv_heads);
-  const bool mine = lane * 4 < p.dim;
-  float q[4] = {}, o[4] = {}, m = -INFINITY, l = 0.0f;
-  if (mine)
-    for (int i = 0; i < 4; ++i) q[i] = to_f32<BF16>(p.q.p[t * p.q.ld + head * p.q.hs + lane * 4 + i]);
-  for (long long j = k0 + first; j < k0 + last; ++j) {
-    float x = 0.0f;
-    if (mine)
-      for (int i = 0; i < 4; ++i) x += q[i] * to_f32<BF16>(p.k.p[j * p.k.ld + kv * p.k.hs + lane * 4 + i]);
-    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
-    x *= p.scale;
-    const float to = fmaxf(m, x);
-    const float keep = to == -INFINITY ? 1.0f : expf(m - to), w = x == -INFINITY ? 0.0f : expf(x - to);
-    m = to;
-    l = l * keep + w;
-    if (mine)
-      for (int i = 0; i < 4; ++i) o[i] = o[i] * keep + w * to_f32<BF16>(p.v.p[j * p.v.ld + kv * p.v.hs + lane * 4 + i]);
+  return first(lo) <= slot ? lo : -1;
+}
+
+// A tile of queries: its rows, the keys that its first and its last row see,
+// and the steps that these lie in.
+struct Tile {
+  int rows;              // 0: none
+  int hi_first, lo_last; // end of the first row's keys, begin of the last row's
+  int from, to;          // steps
+  __device__ __forceinline__ bool active(int j) const { return j >= from && j < to; }
+  // whether some row does not see some key of step j
+  __device__ __forceinline__ bool masked(int j) const { return (j + 1) * kTile > hi_first || j * kTile < lo_last; }
+};
+// Keys [lo, hi) that a query at position `at` sees.
+__device__ __forceinline__ int key_end(const PromptParams& p, int at, int keys) {
+  return p.causal ? max(0, min(at + 1, keys)) : keys;
+}
+__device__ __forceinline__ int key_begin(const PromptParams& p, int at) {
+  return p.window > 0 ? max(0, at + 1 - p.window) : 0;
+}
+__device__ __forceinline__ Tile tile_of(const PromptParams& p, int row0, int queries, int keys) {
+  Tile t;
+  t.rows = min(kTile, queries - row0);
+  t.hi_first = t.lo_last = t.from = t.to = 0;
+  if (t.rows <= 0) {
+    t.rows = 0;
+    return t;
   }
-  if (mine)
-    for (int i = 0; i < 4; ++i)
-      p.out.p[t * p.out.ld + head * p.out.hs + lane * 4 + i] = to_16<BF16>(l == 0.0f ? 0.0f : o[i] / l);
-  if (p.lse && lane == 0) p.lse[t * p.heads + head] = l == 0.0f ? -INFINITY : m + logf(l);
+  const int at0 = keys - queries + row0, at1 = at0 + t.rows - 1;
+  t.hi_first = key_end(p, at0, keys);
+  t.lo_last = key_begin(p, at1);
+  const int lo = key_begin(p, at0), hi = key_end(p, at1, keys);
+  if (lo < hi) {
+    t.from = lo / kTile;
+    t.to = (hi + kTile - 1) / kTile;
+  }
+  return t;
+}
+
+// O (+)= w V of one step for the rows of a warp, over the keys [lo, hi) of the
+// step that each row sees; all lanes together. w is read from tensor memory.
+template <bool BF16, int DP>
+__device__ __noinline__ void product_by_rows(uint32_t w_at, uint32_t o_at, uint32_t values, int lo, int hi, bool first) {
+#pragma unroll 1
+  for (int d = 0; d < DP / 8; ++d) {
+    float acc[8] = {};
+#pragma unroll 1
+    for (int c = 0; c < kTile; c += 16) {
+      uint32_t w[8];
+      tmem_ld_x8(w_at + c / 2, w);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const int key = c + k;
+        if (key < lo || key >= hi) continue;
+        const float f = k & 1 ? hi_f32<BF16>(w[k >> 1]) : lo_f32<BF16>(w[k >> 1]);
+        uint32_t v[4];
+        asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                     : "r"(values + (d >> 3) * (kTile * 128) + key * 128 + (((d & 7) ^ (key & 7)) << 4))
+                     : "memory");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[2 * i] += f * lo_f32<BF16>(v[i]);
+          acc[2 * i + 1] += f * hi_f32<BF16>(v[i]);
+        }
+      }
+      __syncwarp();
+    }
+    uint32_t o[8];
+    if (!first) tmem_ld_x8(o_at + d * 8, o);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(first ? acc[i] : __uint_as_float(o[i]) + acc[i]);
+    tmem_st_x8(o_at + d * 8, o);
+    tmem_wait_st();
+  }
+}
+
+template <bool BF16, int DP>
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ Args a) {
+  using C = Cfg<DP>;
+  const PromptParams& p = a.p;
+  const int head = blockIdx.x % p.heads;
+  // the last slots first: with a causal mask they have the most keys
+  const int slot = a.slots - 1 - static_cast<int>(blockIdx.x / p.heads);
+  const int seq = sequence_of(p, slot);
+  if (seq < 0) return;
+  const int q0 = held(p.starts[seq], 0, p.tokens), queries = held(p.starts[seq + 1], q0, p.tokens) - q0;
+  const int k0 = held(p.k_starts[seq], 0, p.k_tokens), keys = held(p.k_starts[seq + 1], k0, p.k_tokens) - k0;
+  const int row0 = (slot - (q0 / kRows + seq)) * kRows;
+  if (row0 >= queries) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = ptx::smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const base_ptr = smem_raw + (base - raw);
+  auto q_at = [&](int t) { return base + t * C::kBytes; };
+  auto ring_at = [&](int s) { return base + (2 + s) * C::kBytes; };
+  const uint32_t bar0 = base + C::kBarAt;
+  auto q_full = [&](int t) { return bar0 + 8u * t; };
+  auto full = [&](int s) { return bar0 + 8u * (2 + s); };
+  auto empty = [&](int s) { return bar0 + 8u * (2 + C::kStages + s); };
+  auto v_ok = [&](int s) { return bar0 + 8u * (2 + 2 * C::kStages + s); };  // values looked after
+  constexpr int kMore = 2 + 3 * C::kStages;
+  auto s_full = [&](int t) { return bar0 + 8u * (kMore + t); };        // scores are there
+  auto w_full = [&](int t) { return bar0 + 8u * (kMore + 2 + t); };    // weights are there
+  auto o_full = [&](int t) { return bar0 + 8u * (kMore + 4 + t); };    // outputs are there
+  const uint32_t drain = bar0 + 8u * (kMore + 6);
+  // of the value tiles in the ring, by each of the warps that look: not all of it is finite
+  volatile int* const wild = reinterpret_cast<volatile int*>(base_ptr + C::kBarAt + 8 * C::kBars);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + C::kBarAt + 8 * C::kBars + 8 * C::kStages);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      ptx::mbar_init(full(s), 1);
+      ptx::mbar_init(empty(s), 1);
+      ptx::mbar_init(v_ok(s), 2);
+    }
+    for (int t = 0; t < 2; ++t) {
+      ptx::mbar_init(q_full(t), 1);
+      ptx::mbar_init(s_full(t), 1);
+      ptx::mbar_init(w_full(t), 4);
+      ptx::mbar_init(o_full(t), 1);
+    }
+    ptx::mbar_init(drain, 1);
+    ptx::fence_mbar_init();
+  }
+  if (warp == 9) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  Tile tiles[2] = {tile_of(p, row0, queries, keys), tile_of(p, row0 + kTile, queries, keys)};
+  // the steps of both (the second tile's begin no later than the first's end)
+  const bool one = tiles[0].from < tiles[0].to, two = tiles[1].from < tiles[1].to;
+  const int from = one ? tiles[0].from : tiles[1].from;
+  const int to = two ? max(tiles[0].to, tiles[1].to) : tiles[0].to;
+  auto stage_of = [&](int n) { return n % C::kStages; };
+  auto phase_of = [&](int n) { return static_cast<uint32_t>(n / C::kStages) & 1u; };
+  // of v_ok, which only the ring's values pass: with an odd number of stages
+  // every other tile of a stage
+  auto v_phase_of = [&](int n) { return static_cast<uint32_t>(n / (C::kStages % 2 ? 2 * C::kStages : C::kStages)) & 1u; };
+  auto by_rows = [&](int s) { return (wild[2 * s] | wild[2 * s + 1]) != 0; };
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ loads
+    if (lane == 0 && from < to) {
+      ptx::prefetch_tmap(&a.q);
+      ptx::prefetch_tmap(&a.k);
+      ptx::prefetch_tmap(&a.v);
+      const int kv = head / (p.heads / p.kv_heads);
+      for (int t = 0; t < 2; ++t)
+        if (tiles[t].from < tiles[t].to) {
+          ptx::mbar_arrive_expect_tx(q_full(t), C::kBytes);
+          for (int x = 0; x < DP; x += 64)
+            tma_load_3d(q_at(t) + x * (kTile * 2), &a.q, x, head, q0 + row0 + t * kTile, q_full(t));
+        }
+      const int count = 2 * (to - from);
+      int n = 0;
+      for (; n < count; ++n) {
+        const int s = stage_of(n);
+        if (!wait(empty(s), phase_of(n) ^ 1u, p, 0)) break;
+        ptx::mbar_arrive_expect_tx(full(s), C::kBytes);
+        const CUtensorMap* const map = n & 1 ? &a.v : &a.k;
+        for (int x = 0; x < DP; x += 64)
+          tma_load_3d(ring_at(s) + x * (kTile * 2), map, x, kv, k0 + (from + n / 2) * kTile, full(s));
+      }
+      // Whatever another role did, the copies in flight land before the CTA ends.
+      for (int i = max(0, n - C::kStages); i < n; ++i) wait_out(full(stage_of(i)), phase_of(i), p, 0);
+      for (int t = 0; t < 2; ++t)
+        if (tiles[t].from < tiles[t].to) wait_out(q_full(t), 0, p, 0);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // --------------------------------------------------------- products
+    if (lane == 0 && from < to) {
+      constexpr uint32_t fmt = BF16 ? 1u : 0u;
+      // fp32 accumulator, M = 128; scores: both operands K-major, N = 128;
+      // outputs: the values MN-major (bit 16), N = DP
+      constexpr uint32_t i_s = (1u << 4) | (fmt << 7) | (fmt << 10) | ((kTile >> 3) << 17) | ((kTile >> 4) << 24);
+      constexpr uint32_t i_o =
+          (1u << 4) | (fmt << 7) | (fmt << 10) | (1u << 16) | ((DP >> 3) << 17) | ((kTile >> 4) << 24);
+      uint32_t done[2] = {0, 0};  // steps of each tile whose weights were waited for
+      bool ok = true;
+      auto scores = [&](int t, int j) {
+        const int n = 2 * (j - from);
+        if (j == tiles[t].from) ok = ok && wait(q_full(t), 0, p, 1);
+        ok = ok && wait(full(stage_of(n)), phase_of(n), p, 1);
+        if (!ok) return;
+        ptx::tc_fence_after();
+        const uint64_t ad = ptx::sdesc(q_at(t), 16, 1024), bd = ptx::sdesc(ring_at(stage_of(n)), 16, 1024);
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+          const uint64_t step = (k >> 2) * (kTile * 128 >> 4) + (k & 3) * 2;
+          ptx::mma_f16(tmem + t * kTile, ad + step, bd + step, i_s, k != 0 ? 1u : 0u);
+        }
+        ptx::mma_commit(s_full(t));
+      };
+      for (int t = 0; t < 2; ++t)
+        if (tiles[t].active(from)) scores(t, from);
+      if (ok) ptx::mma_commit(empty(stage_of(0)));
+      for (int j = from; ok && j < to; ++j) {
+        const int n = 2 * (j - from) + 1, s = stage_of(n);
+        for (int t = 0; ok && t < 2; ++t) {
+          if (tiles[t].active(j)) {
+            ok = wait(w_full(t), done[t]++ & 1u, p, 1) && wait(full(s), phase_of(n), p, 1) &&
+                 wait(v_ok(s), v_phase_of(n), p, 1);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            if (!by_rows(s)) {
+              const uint64_t bd = ptx::sdesc(ring_at(s), kTile * 128, 1024);
+#pragma unroll
+              for (int k = 0; k < kTile / 16; ++k)
+                mma_ts(tmem + C::kOAt + t * 128, tmem + t * kTile + k * 8, bd + k * 128, i_o,
+                       j != tiles[t].from || k != 0 ? 1u : 0u);
+            }
+            if (j + 1 == tiles[t].to) ptx::mma_commit(o_full(t));
+          }
+          if (tiles[t].active(j + 1)) scores(t, j + 1);
+        }
+        if (!ok) break;
+        ptx::mma_commit(empty(s));
+        if (j + 1 < to) ptx::mma_commit(empty(stage_of(n + 1)));
+      }
+      // Every product this thread issued is complete before tensor memory goes back.
+      ptx::mma_commit(drain);
+      wait_out(drain, 0, p, 1);
+    }
+    __syncwarp();
+  } else if (warp >= 10) {
+    // ----------------------------------------------- values that are hidden
+    const int thread = (warp - 10) * 32 + lane;
+    for (int j = from; j < to; ++j) {
+      const int n = 2 * (j - from) + 1, s = stage_of(n);
+      if (!wait_warp(full(s), phase_of(n), p, 3)) break;
+      uint32_t found = 0;
+      if ((tiles[0].active(j) && tiles[0].masked(j)) || (tiles[1].active(j) && tiles[1].masked(j))) {
+        const int count = min(kTile, keys - j * kTile);
+        constexpr uint32_t kExponent = BF16 ? 0x7F807F80u : 0x7C007C00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
+#pragma unroll 4
+        for (int e = thread; e < kTile * DP / 8; e += 64) {
+          const uint32_t at = ring_at(s) + e * 16;
+          if ((e >> 3) % kTile < count) {
+            uint32_t v[4];
+            asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                         : "r"(at)
+                         : "memory");
+            // an exponent of ones carries into its half's sign
+#pragma unroll
+            for (int i = 0; i < 4; ++i) found |= (v[i] & kExponent) + kOne;
+          } else {
+            asm volatile("st.volatile.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0u) : "memory");
+          }
+        }
+        ptx::fence_proxy_async_smem();
+      }
+      const bool any = __any_sync(0xFFFFFFFFu, (found & 0x80008000u) != 0u);
+      if (lane == 0) {
+        wild[2 * s + warp - 10] = any ? 1 : 0;
+        ptx::mbar_arrive(v_ok(s));
+      }
+    }
+  } else {
+    // ---------------------------------------------------------- weights
+    const int t = warp >> 2, row = (warp & 3) * 32 + lane;  // row of the tile
+    const Tile tile = t == 0 ? tiles[0] : tiles[1];
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + lanes + t * kTile, o_at = tmem + lanes + C::kOAt + t * 128;
+    const int at = keys - queries + row0 + t * kTile + row;
+    const int lo = key_begin(p, at), hi = key_end(p, at, keys);
+    const float to_log2 = p.scale * kLog2e;
+    const uint64_t to_log2_2 = pair(to_log2, to_log2);
+    constexpr float kLift = BF16 ? 0.0f : 6.0f;
+    float ref = -INFINITY, sum = 0.0f;
+    uint32_t turn = 0;
+    bool ok = true;
+    for (int j = tile.from; j < tile.to; ++j, ++turn) {
+      if (!(ok = wait_warp(s_full(t), turn & 1u, p, 2))) break;
+      ptx::tc_fence_after();
+      uint32_t s[4][32];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ptx::tmem_ld_32x32b_x32(s_at + i * 32, s[i]);
+      ptx::tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ptx::tmem_regs_ready(s[i]);
+      const bool masked = tile.masked(j);
+      const int key_lo = lo - j * kTile, key_hi = hi - j * kTile;
+      if (masked) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (i * 32 + c < key_lo || i * 32 + c >= key_hi) s[i][c] = 0xFF800000u;  // -inf
+      }
+      float most = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float m0 = __uint_as_float(s[i][0]), m1 = __uint_as_float(s[i][1]);
+#pragma unroll
+        for (int c = 2; c < 32; c += 2) {
+          m0 = fmaxf(m0, __uint_as_float(s[i][c]));
+          m1 = fmaxf(m1, __uint_as_float(s[i][c + 1]));
+        }
+        most = fmaxf(most, fmaxf(m0, m1));
+      }
+      most *= to_log2;
+      if (__any_sync(0xFFFFFFFFu, most > ref + kSlack)) {
+        const float next = most > ref + kSlack ? most : ref;
+        const float f = next == -INFINITY ? 1.0f : exp2_fast(ref - next);
+        ref = next;
+        sum *= f;
+        if (j != tile.from) {
+          // (the scores of this step are there, so the product before them is done)
+#pragma unroll 1
+          for (int d = 0; d < DP; d += 8) {
+            uint32_t o[8];
+            tmem_ld_x8(o_at + d, o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st_x8(o_at + d, o);
+          }
+        }
+      }
+      const float less = ref == -INFINITY ? 0.0f : kLift - ref;
+      const uint64_t less2 = pair(less, less);
+      uint64_t sum2 = pair(0.0f, 0.0f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t w[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          float x, y;
+          unpair(fma2(pair(__uint_as_float(s[i][2 * c]), __uint_as_float(s[i][2 * c + 1])), to_log2_2, less2), x, y);
+          x = exp2_fast(x);
+          y = exp2_fast(y);
+          sum2 = add2(sum2, pair(x, y));
+          w[c] = pack2<BF16>(x, y);
+        }
+        tmem_st_x16(s_at + i * 16, w);
+      }
+      tmem_wait_st();
+      float x, y;
+      unpair(sum2, x, y);
+      sum += x + y;
+      if ((tiles[0].active(j) && tiles[0].masked(j)) || (tiles[1].active(j) && tiles[1].masked(j))) {
+        const int n = 2 * (j - from) + 1, st = stage_of(n);
+        if (!(ok = wait_warp(full(st), phase_of(n), p, 2) && wait_warp(v_ok(st), v_phase_of(n), p, 2))) break;
+        if (by_rows(st)) {
+          product_by_rows<BF16, DP>(s_at, o_at, ring_at(st), key_lo, key_hi, j == tile.from);
+          ptx::fence_proxy_async_smem();
+        }
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(w_full(t));
+    }
+    // outputs: a row a thread
+    if (tile.rows > 0 && ok) {
+      const bool any = tile.from < tile.to;
+      if (any) ok = wait_warp(o_full(t), 0, p, 2);
+      if (ok) {
+        ptx::tc_fence_after();
+        const bool mine = row < tile.rows;
+        const long long token = static_cast<long long>(q0) + row0 + t * kTile + row;
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        uint16_t* const out = p.out.p + token * p.out.ld + head * p.out.hs;
+#pragma unroll 1
+        for (int d = 0; d < DP; d += 32) {
+          uint32_t o[32];
+          if (any) {
+            ptx::tmem_ld_32x32b_x32(o_at + d, o);
+            ptx::tmem_wait_ld();
+            ptx::tmem_regs_ready(o);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (sum != 0.0f)
+                w[e] = pack2<BF16>(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
+            if (mine && d + 8 * i < p.dim)
+              *reinterpret_cast<uint4*>(out + d + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        if (mine && p.lse)
+          p.lse[token * p.heads + head] = sum == 0.0f ? -INFINITY : (ref - kLift + log2f(sum)) * kLn2;
+      }
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == 9) ptx::tmem_dealloc(tmem, 512);
+}
+
+// A map of tokens x heads x dim in boxes of 64 values x 128 tokens of a head.
+bool encode(CUtensorMap* map, const Heads& t, long long tokens, int heads, int dim, bool bf16) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(t.hs) * 2, static_cast<cuuint64_t>(t.ld) * 2};
+  const cuuint32_t box[3] = {64, 1, kTile}, step[3] = {1, 1, 1};
+  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, t.p, dims, strides, box,
+             step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool BF16, int DP>
+cudaError_t launch_of(const Args& a, unsigned grid, cudaStream_t stream) {
+  auto kernel = prompt_kernel<BF16, DP>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<DP>::kSmem);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, kThreads, Cfg<DP>::kSmem, stream>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
+long long prompt_ctas(long long tokens, int seqs, int heads) { return (tokens / kRows + seqs) * heads; }
+
 cudaError_t launch_prompt(const PromptParams& p, int num_sms, cudaStream_t stream) {
   (void)num_sms;
-  const dim3 grid(static_cast<unsigned>((p.tokens + 3) / 4), static_cast<unsigned>(p.heads));
-  if (p.is_bf16)
-    prompt_rows_kernel<true><<<grid, 128, 0, stream>>>(p);
-  else
-    prompt_rows_kernel<false><<<grid, 128, 0, stream>>>(p);
-  return cudaGetLastError();
+  Args a;
+  a.p = p;
+  a.slots = static_cast<int>(p.tokens / kRows) + p.seqs;
+  if (!encode(&a.q, p.q, p.tokens, p.heads, p.dim, p.is_bf16)) return cudaErrorInvalidValue;
+  if (p.k_tokens == 0) {  // nothing is loaded
+    a.k = a.v = a.q;
+  } else if (!encode(&a.k, p.k, p.k_tokens, p.kv_heads, p.dim, p.is_bf16) ||
+             !encode(&a.v, p.v, p.k_tokens, p.kv_heads, p.dim, p.is_bf16)) {
+    return cudaErrorInvalidValue;
+  }
+  const unsigned grid = static_cast<unsigned>(prompt_ctas(p.tokens, p.seqs, p.heads));
+  if (p.dim > 64) return p.is_bf16 ? launch_of<true, 128>(a, grid, stream) : launch_of<false, 128>(a, grid, stream);
+  return p.is_bf16 ? launch_of<true, 64>(a, grid, stream) : launch_of<false, 64>(a, grid, stream);
 }
 
 }  // namespace fgemm
