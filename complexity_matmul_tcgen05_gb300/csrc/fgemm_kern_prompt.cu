@@ -5,17 +5,17 @@
 //
 // One pass over the keys of a tile of 128 queries, 128 keys a step: S goes from
 // the tensor core to tensor memory, a thread takes one row of it (a query) to
-// registers, so the maximum and the sum of a row need no other thread, and
-// writes the weights, rounded to 16 bits, over S in tensor memory, from where
-// they are an operand of the product with the values. The reference r follows
+// registers (two threads, half of the keys each), so a row's maximum and sum need
+// no others, and writes the weights, rounded to 16 bits, over S in tensor memory,
+// from where they are an operand of the product with the values. The reference r follows
 // the row's maximum only when that is more than 8 above it: the weights stay
 // below 2^8 (fp16: below 2^14, so that small ones keep their bits) and O is
 // seldom scaled.
 //
 // A CTA has two tiles of queries (256 rows) of one head. While the tensor core
 // works on one tile's products the threads of the other tile form its weights.
-// Warps 0-3 and 4-7 are the two tiles' rows, warp 8 loads (TMA, a ring of key
-// and value tiles), warp 9 issues the products, warps 10 and 11 look after the
+// Warps 0-7 and 8-15 are the two tiles' rows, warp 16 loads (TMA, a ring of key
+// and value tiles), warp 17 issues the products, warps 18 and 19 look after the
 // values of steps in which not every row sees every key.
 //
 // Those are the steps on the diagonal, at a window's edge and at the end of a
@@ -46,17 +46,22 @@ using namespace attn;
 
 constexpr int kTile = 128;            // queries of a tile, keys of a step
 constexpr int kRows = 2 * kTile;      // queries of a CTA
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
+constexpr int kLoad = 16, kIssue = 17, kLook = 18;  // warps (0 to 15: weights)
 constexpr float kSlack = 8.0f;        // log2 of how far the maximum may be above the reference
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int DP>  // values of a head, padded: 64 or 128
 struct Cfg {
   static constexpr int kBytes = kTile * DP * 2;  // of a tile of queries, keys or values
-  static constexpr int kStages = DP == 128 ? 5 : 8;
-  static constexpr int kBars = 2 + 3 * kStages + 7;
-  static constexpr int kBarAt = (2 + kStages) * kBytes;
-  static constexpr int kSmem = 1024 + kBarAt + 8 * kBars + 8 * kStages + 16;
+  // Rings of their own for keys and values: who passes over one of them waits for
+  // each of its tiles in turn. (In a ring of both, the warps that look after the
+  // values alone took a stage whose key tile was still on its way for the next one.)
+  static constexpr int kKeys = DP == 128 ? 3 : 4, kValues = DP == 128 ? 2 : 4;
+  static constexpr int kBars = 2 + 2 * kKeys + 3 * kValues + 7;
+  static constexpr int kBarAt = (2 + kKeys + kValues) * kBytes;
+  static constexpr int kMeetAt = kBarAt + 8 * kBars + 8 * kValues + 16;  // a float a row
+  static constexpr int kSmem = 1024 + kMeetAt + kRows * 4;
   static constexpr int kOAt = 256;  // tensor memory: scores of the two tiles, then their outputs
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
@@ -169,6 +174,21 @@ __device__ __forceinline__ void wait_out(uint32_t bar, uint32_t parity, const Pr
     wait_slow(bar, parity, p.err, p.spin_ns, kErrTimeout | (static_cast<uint32_t>(role) << 24), false);
 }
 
+// The meeting of two warps at barrier `id`: whether the predicate holds for any of
+// their threads. Shared memory written before it is visible behind it.
+__device__ __forceinline__ bool either(uint32_t id, bool predicate) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(predicate)), "r"(id)
+      : "memory");
+  return r != 0;
+}
+
 // ------------------------------------------------------------------ tiles
 
 __device__ __forceinline__ int held(int v, int lo, long long hi) {
@@ -229,12 +249,14 @@ __device__ __forceinline__ Tile tile_of(const PromptParams& p, int row0, int que
   return t;
 }
 
-// O (+)= w V of one step for the rows of a warp, over the keys [lo, hi) of the
-// step that each row sees; all lanes together. w is read from tensor memory.
+// O (+)= w V of one step for the rows of a warp and one half of the values of a
+// head, over the keys [lo, hi) of the step that each row sees; all lanes
+// together. w is read from tensor memory.
 template <bool BF16, int DP>
-__device__ __noinline__ void product_by_rows(uint32_t w_at, uint32_t o_at, uint32_t values, int lo, int hi, bool first) {
+__device__ __noinline__ void product_by_rows(uint32_t w_at, uint32_t o_at, uint32_t values, int lo, int hi, bool first,
+                                             int half) {
 #pragma unroll 1
-  for (int d = 0; d < DP / 8; ++d) {
+  for (int d = half * (DP / 16); d < (half + 1) * (DP / 16); ++d) {
     float acc[8] = {};
 #pragma unroll 1
     for (int c = 0; c < kTile; c += 16) {
@@ -287,37 +309,45 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const base_ptr = smem_raw + (base - raw);
   auto q_at = [&](int t) { return base + t * C::kBytes; };
-  auto ring_at = [&](int s) { return base + (2 + s) * C::kBytes; };
+  auto k_at = [&](int s) { return base + (2 + s) * C::kBytes; };
+  auto v_at = [&](int s) { return base + (2 + C::kKeys + s) * C::kBytes; };
   const uint32_t bar0 = base + C::kBarAt;
   auto q_full = [&](int t) { return bar0 + 8u * t; };
-  auto full = [&](int s) { return bar0 + 8u * (2 + s); };
-  auto empty = [&](int s) { return bar0 + 8u * (2 + C::kStages + s); };
-  auto v_ok = [&](int s) { return bar0 + 8u * (2 + 2 * C::kStages + s); };  // values looked after
-  constexpr int kMore = 2 + 3 * C::kStages;
+  auto k_full = [&](int s) { return bar0 + 8u * (2 + s); };
+  auto k_empty = [&](int s) { return bar0 + 8u * (2 + C::kKeys + s); };
+  constexpr int kVBar = 2 + 2 * C::kKeys;
+  auto v_full = [&](int s) { return bar0 + 8u * (kVBar + s); };
+  auto v_empty = [&](int s) { return bar0 + 8u * (kVBar + C::kValues + s); };
+  auto v_ok = [&](int s) { return bar0 + 8u * (kVBar + 2 * C::kValues + s); };  // looked after
+  constexpr int kMore = kVBar + 3 * C::kValues;
   auto s_full = [&](int t) { return bar0 + 8u * (kMore + t); };        // scores are there
   auto w_full = [&](int t) { return bar0 + 8u * (kMore + 2 + t); };    // weights are there
   auto o_full = [&](int t) { return bar0 + 8u * (kMore + 4 + t); };    // outputs are there
   const uint32_t drain = bar0 + 8u * (kMore + 6);
-  // of the value tiles in the ring, by each of the warps that look: not all of it is finite
+  // of the value tiles in their ring, by each of the warps that look: not all of it is finite
   volatile int* const wild = reinterpret_cast<volatile int*>(base_ptr + C::kBarAt + 8 * C::kBars);
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + C::kBarAt + 8 * C::kBars + 8 * C::kStages);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + C::kBarAt + 8 * C::kBars + 8 * C::kValues);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
-      ptx::mbar_init(full(s), 1);
-      ptx::mbar_init(empty(s), 1);
+    for (int s = 0; s < C::kKeys; ++s) {
+      ptx::mbar_init(k_full(s), 1);
+      ptx::mbar_init(k_empty(s), 1);
+    }
+    for (int s = 0; s < C::kValues; ++s) {
+      ptx::mbar_init(v_full(s), 1);
+      ptx::mbar_init(v_empty(s), 1);
       ptx::mbar_init(v_ok(s), 2);
     }
     for (int t = 0; t < 2; ++t) {
       ptx::mbar_init(q_full(t), 1);
       ptx::mbar_init(s_full(t), 1);
-      ptx::mbar_init(w_full(t), 4);
+      ptx::mbar_init(w_full(t), 8);
       ptx::mbar_init(o_full(t), 1);
     }
     ptx::mbar_init(drain, 1);
     ptx::fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == kIssue) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
     ptx::tmem_relinquish();
   }
@@ -331,14 +361,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   const bool one = tiles[0].from < tiles[0].to, two = tiles[1].from < tiles[1].to;
   const int from = one ? tiles[0].from : tiles[1].from;
   const int to = two ? max(tiles[0].to, tiles[1].to) : tiles[0].to;
-  auto stage_of = [&](int n) { return n % C::kStages; };
-  auto phase_of = [&](int n) { return static_cast<uint32_t>(n / C::kStages) & 1u; };
-  // of v_ok, which only the ring's values pass: with an odd number of stages
-  // every other tile of a stage
-  auto v_phase_of = [&](int n) { return static_cast<uint32_t>(n / (C::kStages % 2 ? 2 * C::kStages : C::kStages)) & 1u; };
+  // stage and phase of the n-th tile of a ring
+  auto k_stage = [&](int n) { return n % C::kKeys; };
+  auto k_phase = [&](int n) { return static_cast<uint32_t>(n / C::kKeys) & 1u; };
+  auto v_stage = [&](int n) { return n % C::kValues; };
+  auto v_phase = [&](int n) { return static_cast<uint32_t>(n / C::kValues) & 1u; };
   auto by_rows = [&](int s) { return (wild[2 * s] | wild[2 * s + 1]) != 0; };
 
-  if (warp == 8) {
+  if (warp == kLoad) {
     // ------------------------------------------------------------ loads
     if (lane == 0 && from < to) {
       ptx::prefetch_tmap(&a.q);
@@ -351,23 +381,32 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           for (int x = 0; x < DP; x += 64)
             tma_load_3d(q_at(t) + x * (kTile * 2), &a.q, x, head, q0 + row0 + t * kTile, q_full(t));
         }
-      const int count = 2 * (to - from);
-      int n = 0;
-      for (; n < count; ++n) {
-        const int s = stage_of(n);
-        if (!wait(empty(s), phase_of(n) ^ 1u, p, 0)) break;
-        ptx::mbar_arrive_expect_tx(full(s), C::kBytes);
-        const CUtensorMap* const map = n & 1 ? &a.v : &a.k;
+      // keys a step ahead of the values
+      const int count = to - from;
+      int nk = 0, nv = 0;
+      for (bool ok = true; ok && nv < count;) {
+        for (int more = nk == 0 ? 2 : 1; ok && more > 0 && nk < count; --more, ++nk) {
+          const int s = k_stage(nk);
+          if (!(ok = wait(k_empty(s), k_phase(nk) ^ 1u, p, 0))) break;
+          ptx::mbar_arrive_expect_tx(k_full(s), C::kBytes);
+          for (int x = 0; x < DP; x += 64)
+            tma_load_3d(k_at(s) + x * (kTile * 2), &a.k, x, kv, k0 + (from + nk) * kTile, k_full(s));
+        }
+        const int s = v_stage(nv);
+        if (!ok || !(ok = wait(v_empty(s), v_phase(nv) ^ 1u, p, 0))) break;
+        ptx::mbar_arrive_expect_tx(v_full(s), C::kBytes);
         for (int x = 0; x < DP; x += 64)
-          tma_load_3d(ring_at(s) + x * (kTile * 2), map, x, kv, k0 + (from + n / 2) * kTile, full(s));
+          tma_load_3d(v_at(s) + x * (kTile * 2), &a.v, x, kv, k0 + (from + nv) * kTile, v_full(s));
+        ++nv;
       }
       // Whatever another role did, the copies in flight land before the CTA ends.
-      for (int i = max(0, n - C::kStages); i < n; ++i) wait_out(full(stage_of(i)), phase_of(i), p, 0);
+      for (int i = max(0, nk - C::kKeys); i < nk; ++i) wait_out(k_full(k_stage(i)), k_phase(i), p, 0);
+      for (int i = max(0, nv - C::kValues); i < nv; ++i) wait_out(v_full(v_stage(i)), v_phase(i), p, 0);
       for (int t = 0; t < 2; ++t)
         if (tiles[t].from < tiles[t].to) wait_out(q_full(t), 0, p, 0);
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == kIssue) {
     // --------------------------------------------------------- products
     if (lane == 0 && from < to) {
       constexpr uint32_t fmt = BF16 ? 1u : 0u;
@@ -379,12 +418,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       uint32_t done[2] = {0, 0};  // steps of each tile whose weights were waited for
       bool ok = true;
       auto scores = [&](int t, int j) {
-        const int n = 2 * (j - from);
+        const int n = j - from;
         if (j == tiles[t].from) ok = ok && wait(q_full(t), 0, p, 1);
-        ok = ok && wait(full(stage_of(n)), phase_of(n), p, 1);
+        ok = ok && wait(k_full(k_stage(n)), k_phase(n), p, 1);
         if (!ok) return;
         ptx::tc_fence_after();
-        const uint64_t ad = ptx::sdesc(q_at(t), 16, 1024), bd = ptx::sdesc(ring_at(stage_of(n)), 16, 1024);
+        const uint64_t ad = ptx::sdesc(q_at(t), 16, 1024), bd = ptx::sdesc(k_at(k_stage(n)), 16, 1024);
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k) {
           const uint64_t step = (k >> 2) * (kTile * 128 >> 4) + (k & 3) * 2;
@@ -394,17 +433,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       };
       for (int t = 0; t < 2; ++t)
         if (tiles[t].active(from)) scores(t, from);
-      if (ok) ptx::mma_commit(empty(stage_of(0)));
+      if (ok) ptx::mma_commit(k_empty(0));
       for (int j = from; ok && j < to; ++j) {
-        const int n = 2 * (j - from) + 1, s = stage_of(n);
+        const int n = j - from, s = v_stage(n);
         for (int t = 0; ok && t < 2; ++t) {
           if (tiles[t].active(j)) {
-            ok = wait(w_full(t), done[t]++ & 1u, p, 1) && wait(full(s), phase_of(n), p, 1) &&
-                 wait(v_ok(s), v_phase_of(n), p, 1);
+            ok = wait(w_full(t), done[t]++ & 1u, p, 1) && wait(v_full(s), v_phase(n), p, 1) &&
+                 wait(v_ok(s), v_phase(n), p, 1);
             if (!ok) break;
             ptx::tc_fence_after();
             if (!by_rows(s)) {
-              const uint64_t bd = ptx::sdesc(ring_at(s), kTile * 128, 1024);
+              const uint64_t bd = ptx::sdesc(v_at(s), kTile * 128, 1024);
 #pragma unroll
               for (int k = 0; k < kTile / 16; ++k)
                 mma_ts(tmem + C::kOAt + t * 128, tmem + t * kTile + k * 8, bd + k * 128, i_o,
@@ -415,27 +454,27 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           if (tiles[t].active(j + 1)) scores(t, j + 1);
         }
         if (!ok) break;
-        ptx::mma_commit(empty(s));
-        if (j + 1 < to) ptx::mma_commit(empty(stage_of(n + 1)));
+        ptx::mma_commit(v_empty(s));
+        if (j + 1 < to) ptx::mma_commit(k_empty(k_stage(n + 1)));
       }
       // Every product this thread issued is complete before tensor memory goes back.
       ptx::mma_commit(drain);
       wait_out(drain, 0, p, 1);
     }
     __syncwarp();
-  } else if (warp >= 10) {
+  } else if (warp >= kLook) {
     // ----------------------------------------------- values that are hidden
-    const int thread = (warp - 10) * 32 + lane;
+    const int thread = (warp - kLook) * 32 + lane;
     for (int j = from; j < to; ++j) {
-      const int n = 2 * (j - from) + 1, s = stage_of(n);
-      if (!wait_warp(full(s), phase_of(n), p, 3)) break;
+      const int n = j - from, s = v_stage(n);
+      if (!wait_warp(v_full(s), v_phase(n), p, 3)) break;
       uint32_t found = 0;
       if ((tiles[0].active(j) && tiles[0].masked(j)) || (tiles[1].active(j) && tiles[1].masked(j))) {
         const int count = min(kTile, keys - j * kTile);
         constexpr uint32_t kExponent = BF16 ? 0x7F807F80u : 0x7C007C00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
 #pragma unroll 4
         for (int e = thread; e < kTile * DP / 8; e += 64) {
-          const uint32_t at = ring_at(s) + e * 16;
+          const uint32_t at = v_at(s) + e * 16;
           if ((e >> 3) % kTile < count) {
             uint32_t v[4];
             asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -453,16 +492,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       }
       const bool any = __any_sync(0xFFFFFFFFu, (found & 0x80008000u) != 0u);
       if (lane == 0) {
-        wild[2 * s + warp - 10] = any ? 1 : 0;
+        wild[2 * s + warp - kLook] = any ? 1 : 0;
         ptx::mbar_arrive(v_ok(s));
       }
     }
   } else {
     // ---------------------------------------------------------- weights
-    const int t = warp >> 2, row = (warp & 3) * 32 + lane;  // row of the tile
+    // Two threads a row, each with half of a step's keys: warps w and w + 4.
+    const int t = warp >> 3, half = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;  // row of the tile
     const Tile tile = t == 0 ? tiles[0] : tiles[1];
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + t * kTile, o_at = tmem + lanes + C::kOAt + t * 128;
+    const uint32_t meet = 1 + t * 4 + (warp & 3);  // barrier of the two warps
+    float* const meet_at = reinterpret_cast<float*>(base_ptr + C::kMeetAt) + t * kTile + row;
     const int at = keys - queries + row0 + t * kTile + row;
     const int lo = key_begin(p, at), hi = key_end(p, at, keys);
     const float to_log2 = p.scale * kLog2e;
@@ -471,37 +513,58 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     float ref = -INFINITY, sum = 0.0f;
     uint32_t turn = 0;
     bool ok = true;
+    // A wait that ran out is told to the other warp at the next meeting, so that
+    // both come to every one of them.
     for (int j = tile.from; j < tile.to; ++j, ++turn) {
-      if (!(ok = wait_warp(s_full(t), turn & 1u, p, 2))) break;
+      ok = ok && wait_warp(s_full(t), turn & 1u, p, 2);
       ptx::tc_fence_after();
-      uint32_t s[4][32];
+      uint32_t s[2][32];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) ptx::tmem_ld_32x32b_x32(s_at + i * 32, s[i]);
+      for (int i = 0; i < 2; ++i) ptx::tmem_ld_32x32b_x32(s_at + half * 64 + i * 32, s[i]);
       ptx::tmem_wait_ld();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) ptx::tmem_regs_ready(s[i]);
+      for (int i = 0; i < 2; ++i) ptx::tmem_regs_ready(s[i]);
       const bool masked = tile.masked(j);
       const int key_lo = lo - j * kTile, key_hi = hi - j * kTile;
       if (masked) {
+        const int a = key_lo - half * 64, b = key_hi - half * 64;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int c = 0; c < 32; ++c)
-            if (i * 32 + c < key_lo || i * 32 + c >= key_hi) s[i][c] = 0xFF800000u;  // -inf
+            if (i * 32 + c < a || i * 32 + c >= b) s[i][c] = 0xFF800000u;  // -inf
       }
-      float most = -INFINITY;
+      float most;
+      {
+        float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float m0 = __uint_as_float(s[i][0]), m1 = __uint_as_float(s[i][1]);
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int c = 2; c < 32; c += 2) {
-          m0 = fmaxf(m0, __uint_as_float(s[i][c]));
-          m1 = fmaxf(m1, __uint_as_float(s[i][c + 1]));
+          for (int c = 0; c < 32; c += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              m[e] = fmaxf(m[e], fmaxf(__uint_as_float(s[i][c + e]), __uint_as_float(s[i][c + e + 4])));
+        most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * to_log2;
+      }
+      // The meeting also says that both have read their scores: the weights go
+      // over those of the first half.
+      if (either(meet, !ok || most > ref + kSlack)) {
+        // the second half's maxima go to the first half's threads and theirs of
+        // both back; NaN: no (a row without a number has the maximum -inf here)
+        if (half) *meet_at = ok ? most : NAN;
+        ptx::named_bar_sync(meet, 64);
+        if (!half) {
+          const float theirs = *meet_at;
+          ok = ok && !__any_sync(0xFFFFFFFFu, isnan(theirs));
+          most = fmaxf(most, theirs);
+          *meet_at = ok ? most : NAN;
         }
-        most = fmaxf(most, fmaxf(m0, m1));
-      }
-      most *= to_log2;
-      if (__any_sync(0xFFFFFFFFu, most > ref + kSlack)) {
+        ptx::named_bar_sync(meet, 64);
+        if (half) {
+          most = *meet_at;
+          ok = ok && !__any_sync(0xFFFFFFFFu, isnan(most));
+        }
+        if (!ok) break;
         const float next = most > ref + kSlack ? most : ref;
         const float f = next == -INFINITY ? 1.0f : exp2_fast(ref - next);
         ref = next;
@@ -509,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         if (j != tile.from) {
           // (the scores of this step are there, so the product before them is done)
 #pragma unroll 1
-          for (int d = 0; d < DP; d += 8) {
+          for (int d = half * (DP / 2); d < (half + 1) * (DP / 2); d += 8) {
             uint32_t o[8];
             tmem_ld_x8(o_at + d, o);
 #pragma unroll
@@ -522,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       const uint64_t less2 = pair(less, less);
       uint64_t sum2 = pair(0.0f, 0.0f);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         uint32_t w[16];
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
@@ -533,17 +596,21 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           sum2 = add2(sum2, pair(x, y));
           w[c] = pack2<BF16>(x, y);
         }
-        tmem_st_x16(s_at + i * 16, w);
+        tmem_st_x16(s_at + half * 32 + i * 16, w);
       }
       tmem_wait_st();
       float x, y;
       unpair(sum2, x, y);
       sum += x + y;
       if ((tiles[0].active(j) && tiles[0].masked(j)) || (tiles[1].active(j) && tiles[1].masked(j))) {
-        const int n = 2 * (j - from) + 1, st = stage_of(n);
-        if (!(ok = wait_warp(full(st), phase_of(n), p, 2) && wait_warp(v_ok(st), v_phase_of(n), p, 2))) break;
+        const int n = j - from, st = v_stage(n);
+        ok = wait_warp(v_full(st), v_phase(n), p, 2) && wait_warp(v_ok(st), v_phase(n), p, 2);
+        if (either(meet, !ok)) {  // (the weights of both are there behind it)
+          ok = false;
+          break;
+        }
         if (by_rows(st)) {
-          product_by_rows<BF16, DP>(s_at, o_at, ring_at(st), key_lo, key_hi, j == tile.from);
+          product_by_rows<BF16, DP>(s_at, o_at, v_at(st), key_lo, key_hi, j == tile.from, half);
           ptx::fence_proxy_async_smem();
         }
       }
@@ -551,10 +618,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(w_full(t));
     }
-    // outputs: a row a thread
-    if (tile.rows > 0 && ok) {
+    // outputs: a row two threads, half of its values each
+    if (tile.rows > 0) {
       const bool any = tile.from < tile.to;
-      if (any) ok = wait_warp(o_full(t), 0, p, 2);
+      if (half) *meet_at = sum;
+      ptx::named_bar_sync(meet, 64);
+      if (!half) *meet_at = sum += *meet_at;
+      ptx::named_bar_sync(meet, 64);
+      if (half) sum = *meet_at;
+      if (any) ok = ok && wait_warp(o_full(t), 0, p, 2);
       if (ok) {
         ptx::tc_fence_after();
         const bool mine = row < tile.rows;
@@ -562,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         uint16_t* const out = p.out.p + token * p.out.ld + head * p.out.hs;
 #pragma unroll 1
-        for (int d = 0; d < DP; d += 32) {
+        for (int d = half * (DP / 2); d < (half + 1) * (DP / 2); d += 32) {
           uint32_t o[32];
           if (any) {
             ptx::tmem_ld_32x32b_x32(o_at + d, o);
@@ -580,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
               *reinterpret_cast<uint4*>(out + d + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
-        if (mine && p.lse)
+        if (mine && half == 0 && p.lse)
           p.lse[token * p.heads + head] = sum == 0.0f ? -INFINITY : (ref - kLift + log2f(sum)) * kLn2;
       }
     }
@@ -588,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  if (warp == 9) ptx::tmem_dealloc(tmem, 512);
+  if (warp == kIssue) ptx::tmem_dealloc(tmem, 512);
 }
 
 // A map of tokens x heads x dim in boxes of 64 values x 128 tokens of a head.
