@@ -14,13 +14,13 @@
 //
 // A CTA has two tiles of queries (256 rows) of one head. While the tensor core
 // works on one tile's products the threads of the other tile form its weights.
-// Warps 0-7 and 8-15 are the two tiles' rows, warp 16 loads (TMA, a ring of key
-// and value tiles), warp 17 issues the products, warps 18 and 19 look after the
-// values of steps in which not every row sees every key.
+// Warp 0 issues the products, warp 1 loads (TMA, rings of key and value tiles),
+// warps 2 and 3 look after the values of steps in which not every row sees every
+// key, warps 4-11 and 12-19 are the two tiles' rows.
 //
 // Those are the steps on the diagonal, at a window's edge and at the end of a
 // sequence. A weight there may be 0 because its key is hidden, and 0 times a
-// value that is not finite would be NaN: the two warps clear the values behind the
+// value that is not finite would be NaN: warps 2 and 3 clear the values behind the
 // sequence's end (another sequence's) and look for others that are not finite.
 // If there are any, the step's product is taken row by row over the keys that
 // each row sees (product_by_rows), without the tensor core.
@@ -47,7 +47,7 @@ using namespace attn;
 constexpr int kTile = 128;            // queries of a tile, keys of a step
 constexpr int kRows = 2 * kTile;      // queries of a CTA
 constexpr int kThreads = 640;
-constexpr int kLoad = 16, kIssue = 17, kLook = 18;  // warps (0 to 15: weights)
+constexpr int kIssue = 0, kLoad = 1, kLook = 2, kWeights = 4;  // warps
 constexpr float kSlack = 8.0f;        // log2 of how far the maximum may be above the reference
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -57,8 +57,8 @@ struct Cfg {
   // Rings of their own for keys and values: who passes over one of them waits for
   // each of its tiles in turn. (In a ring of both, the warps that look after the
   // values alone took a stage whose key tile was still on its way for the next one.)
-  static constexpr int kKeys = DP == 128 ? 3 : 4, kValues = DP == 128 ? 2 : 4;
-  static constexpr int kBars = 2 + 2 * kKeys + 3 * kValues + 7;
+  static constexpr int kValues = DP == 128 ? 2 : 4, kKeys = kValues + 1;
+  static constexpr int kBars = 2 + kKeys + 3 * kValues + 7;
   static constexpr int kBarAt = (2 + kKeys + kValues) * kBytes;
   static constexpr int kMeetAt = kBarAt + 8 * kBars + 8 * kValues + 16;  // a float a row
   static constexpr int kSmem = 1024 + kMeetAt + kRows * 4;
@@ -120,6 +120,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // Two fp32 operations in one instruction.
@@ -314,10 +320,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   const uint32_t bar0 = base + C::kBarAt;
   auto q_full = [&](int t) { return bar0 + 8u * t; };
   auto k_full = [&](int s) { return bar0 + 8u * (2 + s); };
-  auto k_empty = [&](int s) { return bar0 + 8u * (2 + C::kKeys + s); };
-  constexpr int kVBar = 2 + 2 * C::kKeys;
+  constexpr int kVBar = 2 + C::kKeys;
   auto v_full = [&](int s) { return bar0 + 8u * (kVBar + s); };
-  auto v_empty = [&](int s) { return bar0 + 8u * (kVBar + C::kValues + s); };
+  auto empty = [&](int s) { return bar0 + 8u * (kVBar + C::kValues + s); };  // a step is done
   auto v_ok = [&](int s) { return bar0 + 8u * (kVBar + 2 * C::kValues + s); };  // looked after
   constexpr int kMore = kVBar + 3 * C::kValues;
   auto s_full = [&](int t) { return bar0 + 8u * (kMore + t); };        // scores are there
@@ -329,13 +334,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + C::kBarAt + 8 * C::kBars + 8 * C::kValues);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kKeys; ++s) {
-      ptx::mbar_init(k_full(s), 1);
-      ptx::mbar_init(k_empty(s), 1);
-    }
+    for (int s = 0; s < C::kKeys; ++s) ptx::mbar_init(k_full(s), 1);
     for (int s = 0; s < C::kValues; ++s) {
       ptx::mbar_init(v_full(s), 1);
-      ptx::mbar_init(v_empty(s), 1);
+      ptx::mbar_init(empty(s), 1);
       ptx::mbar_init(v_ok(s), 2);
     }
     for (int t = 0; t < 2; ++t) {
@@ -381,23 +383,24 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           for (int x = 0; x < DP; x += 64)
             tma_load_3d(q_at(t) + x * (kTile * 2), &a.q, x, head, q0 + row0 + t * kTile, q_full(t));
         }
-      // keys a step ahead of the values
+      // Keys go a step ahead of the values. A step's end hands back its values and
+      // the keys of the next, whose scores it ended with; there is one stage more of
+      // keys for the first ones, which come back with the first step too.
       const int count = to - from;
+      auto load = [&](int n, uint32_t at, const CUtensorMap* map, uint32_t bar) {
+        ptx::mbar_arrive_expect_tx(bar, C::kBytes);
+        for (int x = 0; x < DP; x += 64) tma_load_3d(at + x * (kTile * 2), map, x, kv, k0 + (from + n) * kTile, bar);
+      };
       int nk = 0, nv = 0;
-      for (bool ok = true; ok && nv < count;) {
-        for (int more = nk == 0 ? 2 : 1; ok && more > 0 && nk < count; --more, ++nk) {
-          const int s = k_stage(nk);
-          if (!(ok = wait(k_empty(s), k_phase(nk) ^ 1u, p, 0))) break;
-          ptx::mbar_arrive_expect_tx(k_full(s), C::kBytes);
-          for (int x = 0; x < DP; x += 64)
-            tma_load_3d(k_at(s) + x * (kTile * 2), &a.k, x, kv, k0 + (from + nk) * kTile, k_full(s));
+      load(0, k_at(0), &a.k, k_full(0));
+      ++nk;
+      for (; nv < count; ++nv) {
+        if (!wait(empty(v_stage(nv)), v_phase(nv) ^ 1u, p, 0)) break;
+        if (nk < count) {
+          load(nk, k_at(k_stage(nk)), &a.k, k_full(k_stage(nk)));
+          ++nk;
         }
-        const int s = v_stage(nv);
-        if (!ok || !(ok = wait(v_empty(s), v_phase(nv) ^ 1u, p, 0))) break;
-        ptx::mbar_arrive_expect_tx(v_full(s), C::kBytes);
-        for (int x = 0; x < DP; x += 64)
-          tma_load_3d(v_at(s) + x * (kTile * 2), &a.v, x, kv, k0 + (from + nv) * kTile, v_full(s));
-        ++nv;
+        load(nv, v_at(v_stage(nv)), &a.v, v_full(v_stage(nv)));
       }
       // Whatever another role did, the copies in flight land before the CTA ends.
       for (int i = max(0, nk - C::kKeys); i < nk; ++i) wait_out(k_full(k_stage(i)), k_phase(i), p, 0);
@@ -408,6 +411,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     __syncwarp();
   } else if (warp == kIssue) {
     // --------------------------------------------------------- products
+    // One thread, whose time counts (the tensor core holds about eight products
+    // ahead): the tiles take turns, what else a step needs is waited for before its
+    // weights are, and a step has three commits. Issued by a thread a tile, the two
+    // tiles' products fell in step, 2.2 ms against 1.9.
     if (lane == 0 && from < to) {
       constexpr uint32_t fmt = BF16 ? 1u : 0u;
       // fp32 accumulator, M = 128; scores: both operands K-major, N = 128;
@@ -415,57 +422,50 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       constexpr uint32_t i_s = (1u << 4) | (fmt << 7) | (fmt << 10) | ((kTile >> 3) << 17) | ((kTile >> 4) << 24);
       constexpr uint32_t i_o =
           (1u << 4) | (fmt << 7) | (fmt << 10) | (1u << 16) | ((DP >> 3) << 17) | ((kTile >> 4) << 24);
-      uint32_t done[2] = {0, 0};  // steps of each tile whose weights were waited for
+      const uint64_t q_desc = ptx::sdesc(q_at(0), 16, 1024);
+      uint32_t turn[2] = {0, 0};
       bool ok = true;
-      auto scores = [&](int t, int j) {
-        const int n = j - from;
-        if (j == tiles[t].from) ok = ok && wait(q_full(t), 0, p, 1);
-        ok = ok && wait(k_full(k_stage(n)), k_phase(n), p, 1);
-        if (!ok) return;
-        ptx::tc_fence_after();
-        const uint64_t ad = ptx::sdesc(q_at(t), 16, 1024), bd = ptx::sdesc(k_at(k_stage(n)), 16, 1024);
+      for (int t = 0; t < 2; ++t) ok = ok && (tiles[t].from >= tiles[t].to || wait(q_full(t), 0, p, 1));
+      for (int j = from - 1; ok && j < to; ++j) {
+        // the product of step j with the values, then the scores of step j + 1
+        const int nv = j - from, nk = nv + 1, s = v_stage(max(nv, 0)), sk = k_stage(nk);
+        ok = (nv < 0 || (wait(v_full(s), v_phase(nv), p, 1) && wait(v_ok(s), v_phase(nv), p, 1))) &&
+             (j + 1 >= to || wait(k_full(sk), k_phase(nk), p, 1));
+        const uint64_t k_desc = ptx::sdesc(k_at(sk), 16, 1024), v_desc = ptx::sdesc(v_at(s), kTile * 128, 1024);
+        const bool skip = nv >= 0 && by_rows(s);
 #pragma unroll
-        for (int k = 0; k < DP / 16; ++k) {
-          const uint64_t step = (k >> 2) * (kTile * 128 >> 4) + (k & 3) * 2;
-          ptx::mma_f16(tmem + t * kTile, ad + step, bd + step, i_s, k != 0 ? 1u : 0u);
-        }
-        ptx::mma_commit(s_full(t));
-      };
-      for (int t = 0; t < 2; ++t)
-        if (tiles[t].active(from)) scores(t, from);
-      if (ok) ptx::mma_commit(k_empty(0));
-      for (int j = from; ok && j < to; ++j) {
-        const int n = j - from, s = v_stage(n);
-        for (int t = 0; ok && t < 2; ++t) {
-          if (tiles[t].active(j)) {
-            ok = wait(w_full(t), done[t]++ & 1u, p, 1) && wait(v_full(s), v_phase(n), p, 1) &&
-                 wait(v_ok(s), v_phase(n), p, 1);
-            if (!ok) break;
-            ptx::tc_fence_after();
-            if (!by_rows(s)) {
-              const uint64_t bd = ptx::sdesc(v_at(s), kTile * 128, 1024);
+        for (int t = 0; t < 2; ++t) {
+          const bool product = nv >= 0 && tiles[t].active(j);
+          if (product && ok) ok = wait(w_full(t), turn[t]++ & 1u, p, 1);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          if (product && !skip) {
+            const uint32_t more = j != tiles[t].from ? 1u : 0u;
 #pragma unroll
-              for (int k = 0; k < kTile / 16; ++k)
-                mma_ts(tmem + C::kOAt + t * 128, tmem + t * kTile + k * 8, bd + k * 128, i_o,
-                       j != tiles[t].from || k != 0 ? 1u : 0u);
-            }
-            if (j + 1 == tiles[t].to) ptx::mma_commit(o_full(t));
+            for (int k = 0; k < kTile / 16; ++k)
+              mma_ts(tmem + C::kOAt + t * 128, tmem + t * kTile + k * 8, v_desc + k * 128, i_o, k != 0 ? 1u : more);
           }
-          if (tiles[t].active(j + 1)) scores(t, j + 1);
+          if (tiles[t].active(j + 1)) {
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k) {
+              const uint32_t step = (k >> 2) * (kTile * 128 >> 4) + (k & 3) * 2;
+              ptx::mma_f16(tmem + t * kTile, q_desc + (t * (C::kBytes >> 4) + step), k_desc + step, i_s, k != 0 ? 1u : 0u);
+            }
+            ptx::mma_commit(s_full(t));
+          } else if (product && j + 1 == tiles[t].to) {
+            ptx::mma_commit(o_full(t));
+          }
         }
-        if (!ok) break;
-        ptx::mma_commit(v_empty(s));
-        if (j + 1 < to) ptx::mma_commit(k_empty(k_stage(n + 1)));
+        if (ok && nv >= 0) ptx::mma_commit(empty(s));
       }
       // Every product this thread issued is complete before tensor memory goes back.
       ptx::mma_commit(drain);
       wait_out(drain, 0, p, 1);
     }
     __syncwarp();
-  } else if (warp >= kLook) {
+  } else if (warp < kWeights) {
     // ----------------------------------------------- values that are hidden
-    const int thread = (warp - kLook) * 32 + lane;
-    for (int j = from; j < to; ++j) {
+        for (int j = from; j < to; ++j) {
       const int n = j - from, s = v_stage(n);
       if (!wait_warp(v_full(s), v_phase(n), p, 3)) break;
       uint32_t found = 0;
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const int count = min(kTile, keys - j * kTile);
         constexpr uint32_t kExponent = BF16 ? 0x7F807F80u : 0x7C007C00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
 #pragma unroll 4
-        for (int e = thread; e < kTile * DP / 8; e += 64) {
+        for (int e = (warp - kLook) * 32 + lane; e < kTile * DP / 8; e += 64) {
           const uint32_t at = v_at(s) + e * 16;
           if ((e >> 3) % kTile < count) {
             uint32_t v[4];
@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   } else {
     // ---------------------------------------------------------- weights
     // Two threads a row, each with half of a step's keys: warps w and w + 4.
-    const int t = warp >> 3, half = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;  // row of the tile
+    const int t = (warp - kWeights) >> 3, half = ((warp - kWeights) >> 2) & 1, row = (warp & 3) * 32 + lane;  // row of the tile
     const Tile tile = t == 0 ? tiles[0] : tiles[1];
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + t * kTile, o_at = tmem + lanes + C::kOAt + t * 128;
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           for (int c = 0; c < 32; c += 8)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              m[e] = fmaxf(m[e], fmaxf(__uint_as_float(s[i][c + e]), __uint_as_float(s[i][c + e + 4])));
+              m[e] = max3(m[e], __uint_as_float(s[i][c + e]), __uint_as_float(s[i][c + e + 4]));
         most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * to_log2;
       }
       // The meeting also says that both have read their scores: the weights go
