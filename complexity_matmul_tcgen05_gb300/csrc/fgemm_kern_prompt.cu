@@ -5,8 +5,7 @@
 //
 // One pass over the keys of a tile of 128 queries, 128 keys a step: S goes from
 // the tensor core to tensor memory, a thread takes one row of it (a query) to
-// registers (two threads, half of the keys each), so a row's maximum and sum need
-// no others, and writes the weights, rounded to 16 bits, over S in tensor memory,
+// registers, so a row's maximum and sum need no other thread, and writes the weights, rounded to 16 bits, over S in tensor memory,
 // from where they are an operand of the product with the values. The reference r follows
 // the row's maximum only when that is more than 8 above it: the weights stay
 // below 2^8 (fp16: below 2^14, so that small ones keep their bits) and O is
@@ -14,14 +13,14 @@
 //
 // A CTA has two tiles of queries (256 rows) of one head. While the tensor core
 // works on one tile's products the threads of the other tile form its weights.
-// Warp 0 issues the products, warp 1 loads (TMA, rings of key and value tiles),
-// warps 2 and 3 look after the values of steps in which not every row sees every
-// key, warps 4-11 and 12-19 are the two tiles' rows.
+// Warps 0 and 1 issue the products of a tile each, warp 2 loads (TMA, rings of key
+// and value tiles), warp 3 looks after the values of steps in which not every row
+// sees every key, warps 4-7 and 8-11 are the two tiles' rows.
 //
 // Those are the steps on the diagonal, at a window's edge and at the end of a
 // sequence. A weight there may be 0 because its key is hidden, and 0 times a
-// value that is not finite would be NaN: warps 2 and 3 clear the values behind the
-// sequence's end (another sequence's) and look for others that are not finite.
+// value that is not finite would be NaN: warp 3 clears the values behind the
+// sequence's end (another sequence's) and looks for others that are not finite.
 // If there are any, the step's product is taken row by row over the keys that
 // each row sees (product_by_rows), without the tensor core.
 //
@@ -46,8 +45,8 @@ using namespace attn;
 
 constexpr int kTile = 128;            // queries of a tile, keys of a step
 constexpr int kRows = 2 * kTile;      // queries of a CTA
-constexpr int kThreads = 640;
-constexpr int kIssue = 0, kLoad = 1, kLook = 2, kWeights = 4;  // warps
+constexpr int kThreads = 384;
+constexpr int kIssue = 0, kLoad = 2, kLook = 3, kWeights = 4;  // warps (two that issue)
 constexpr float kSlack = 8.0f;        // log2 of how far the maximum may be above the reference
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -58,10 +57,9 @@ struct Cfg {
   // each of its tiles in turn. (In a ring of both, the warps that look after the
   // values alone took a stage whose key tile was still on its way for the next one.)
   static constexpr int kValues = DP == 128 ? 2 : 4, kKeys = kValues + 1;
-  static constexpr int kBars = 2 + kKeys + 3 * kValues + 7;
+  static constexpr int kBars = 2 + kKeys + 3 * kValues + 11;
   static constexpr int kBarAt = (2 + kKeys + kValues) * kBytes;
-  static constexpr int kMeetAt = kBarAt + 8 * kBars + 8 * kValues + 16;  // a float a row
-  static constexpr int kSmem = 1024 + kMeetAt + kRows * 4;
+  static constexpr int kSmem = 1024 + kBarAt + 8 * kBars + 4 * kValues + 16;
   static constexpr int kOAt = 256;  // tensor memory: scores of the two tiles, then their outputs
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
@@ -148,7 +146,46 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
+// One lane of a warp whose lanes are all here; the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+// A value that is the same in all lanes, known as such to the compiler.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+
+// A ring position: stage and phase parity.
+template <int N>
+struct Ring {
+  int s = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == N) {
+      s = 0;
+      ph ^= 1u;
+    }
+  }
+};
+
 // ----------------------------------------------------------------- waits
+
+// One try that may sleep for up to about 20 us.
+__device__ __forceinline__ bool try_wait_long(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
+}
 
 // Waits for a phase; gives up when another role has (the error word) or when
 // the time limit runs out, and then latches `code`.
@@ -168,7 +205,8 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, unsigned i
   }
 }
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const PromptParams& p, int role) {
-  if (ptx::mbar_try_wait(bar, parity)) return true;
+  // (reading the clock first costs a wait about 400 clocks)
+  if (try_wait_long(bar, parity) || try_wait_long(bar, parity)) return true;
   return wait_slow(bar, parity, p.err, p.spin_ns,
                    kErrTimeout | (static_cast<uint32_t>(role) << 24) | (blockIdx.x & 0xFFFFFFu), true);
 }
@@ -178,21 +216,6 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const P
 __device__ __forceinline__ void wait_out(uint32_t bar, uint32_t parity, const PromptParams& p, int role) {
   if (!ptx::mbar_try_wait(bar, parity))
     wait_slow(bar, parity, p.err, p.spin_ns, kErrTimeout | (static_cast<uint32_t>(role) << 24), false);
-}
-
-// The meeting of two warps at barrier `id`: whether the predicate holds for any of
-// their threads. Shared memory written before it is visible behind it.
-__device__ __forceinline__ bool either(uint32_t id, bool predicate) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, %2, 64, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(predicate)), "r"(id)
-      : "memory");
-  return r != 0;
 }
 
 // ------------------------------------------------------------------ tiles
@@ -255,14 +278,12 @@ __device__ __forceinline__ Tile tile_of(const PromptParams& p, int row0, int que
   return t;
 }
 
-// O (+)= w V of one step for the rows of a warp and one half of the values of a
-// head, over the keys [lo, hi) of the step that each row sees; all lanes
-// together. w is read from tensor memory.
+// O (+)= w V of one step for the rows of a warp, over the keys [lo, hi) of the
+// step that each row sees; all lanes together. w is read from tensor memory.
 template <bool BF16, int DP>
-__device__ __noinline__ void product_by_rows(uint32_t w_at, uint32_t o_at, uint32_t values, int lo, int hi, bool first,
-                                             int half) {
+__device__ __noinline__ void product_by_rows(uint32_t w_at, uint32_t o_at, uint32_t values, int lo, int hi, bool first) {
 #pragma unroll 1
-  for (int d = half * (DP / 16); d < (half + 1) * (DP / 16); ++d) {
+  for (int d = 0; d < DP / 8; ++d) {
     float acc[8] = {};
 #pragma unroll 1
     for (int c = 0; c < kTile; c += 16) {
@@ -308,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   const int k0 = held(p.k_starts[seq], 0, p.k_tokens), keys = held(p.k_starts[seq + 1], k0, p.k_tokens) - k0;
   const int row0 = (slot - (q0 / kRows + seq)) * kRows;
   if (row0 >= queries) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
@@ -328,25 +349,29 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   auto s_full = [&](int t) { return bar0 + 8u * (kMore + t); };        // scores are there
   auto w_full = [&](int t) { return bar0 + 8u * (kMore + 2 + t); };    // weights are there
   auto o_full = [&](int t) { return bar0 + 8u * (kMore + 4 + t); };    // outputs are there
-  const uint32_t drain = bar0 + 8u * (kMore + 6);
-  // of the value tiles in their ring, by each of the warps that look: not all of it is finite
+  auto w_half = [&](int t) { return bar0 + 8u * (kMore + 6 + t); };    // those of the first half of the keys
+  auto go = [&](int t) { return bar0 + 8u * (kMore + 8 + t); };        // it is the tile's turn to issue
+  const uint32_t drain = bar0 + 8u * (kMore + 10);
+  // of the value tiles in their ring: 1 where not all of it is finite
   volatile int* const wild = reinterpret_cast<volatile int*>(base_ptr + C::kBarAt + 8 * C::kBars);
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + C::kBarAt + 8 * C::kBars + 8 * C::kValues);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + C::kBarAt + 8 * C::kBars + 4 * C::kValues);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kKeys; ++s) ptx::mbar_init(k_full(s), 1);
     for (int s = 0; s < C::kValues; ++s) {
       ptx::mbar_init(v_full(s), 1);
-      ptx::mbar_init(empty(s), 1);
-      ptx::mbar_init(v_ok(s), 2);
+      ptx::mbar_init(empty(s), 2);
+      ptx::mbar_init(v_ok(s), 1);
     }
     for (int t = 0; t < 2; ++t) {
       ptx::mbar_init(q_full(t), 1);
       ptx::mbar_init(s_full(t), 1);
-      ptx::mbar_init(w_full(t), 8);
+      ptx::mbar_init(w_full(t), 4);
+      ptx::mbar_init(w_half(t), 4);
+      ptx::mbar_init(go(t), 1);
       ptx::mbar_init(o_full(t), 1);
     }
-    ptx::mbar_init(drain, 1);
+    ptx::mbar_init(drain, 2);
     ptx::fence_mbar_init();
   }
   if (warp == kIssue) {
@@ -356,7 +381,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  // (all columns: the address is 0, known when this is compiled)
+  constexpr uint32_t tmem = 0;
 
   Tile tiles[2] = {tile_of(p, row0, queries, keys), tile_of(p, row0 + kTile, queries, keys)};
   // the steps of both (the second tile's begin no later than the first's end)
@@ -368,7 +394,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   auto k_phase = [&](int n) { return static_cast<uint32_t>(n / C::kKeys) & 1u; };
   auto v_stage = [&](int n) { return n % C::kValues; };
   auto v_phase = [&](int n) { return static_cast<uint32_t>(n / C::kValues) & 1u; };
-  auto by_rows = [&](int s) { return (wild[2 * s] | wild[2 * s + 1]) != 0; };
+  auto by_rows = [&](int s) { return wild[s] != 0; };
+
 
   if (warp == kLoad) {
     // ------------------------------------------------------------ loads
@@ -409,61 +436,90 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         if (tiles[t].from < tiles[t].to) wait_out(q_full(t), 0, p, 0);
     }
     __syncwarp();
-  } else if (warp == kIssue) {
+  } else if (warp < kIssue + 2) {
     // --------------------------------------------------------- products
-    // One thread, whose time counts (the tensor core holds about eight products
-    // ahead): the tiles take turns, what else a step needs is waited for before its
-    // weights are, and a step has three commits. Issued by a thread a tile, the two
-    // tiles' products fell in step, 2.2 ms against 1.9.
-    if (lane == 0 && from < to) {
+    // A thread a tile, in turns: a thread's waits and commits (about 100 clocks each)
+    // run under the other's products, of which the tensor core holds about eight.
+    // By one thread alone 16384 tokens took 1.75 ms; by two without turns, whose
+    // tiles fell in step, 2.2.
+    // All lanes go through the loop, so that what a product takes (descriptors,
+    // addresses) is known to be the warp's; one lane issues.
+    const int t = warp - kIssue;
+    const int first = uniform(from), last = uniform(to);
+    const int tile_from = uniform(t == 0 ? tiles[0].from : tiles[1].from);
+    const int tile_to = uniform(t == 0 ? tiles[0].to : tiles[1].to);
+    if (first < last) {
       constexpr uint32_t fmt = BF16 ? 1u : 0u;
       // fp32 accumulator, M = 128; scores: both operands K-major, N = 128;
       // outputs: the values MN-major (bit 16), N = DP
       constexpr uint32_t i_s = (1u << 4) | (fmt << 7) | (fmt << 10) | ((kTile >> 3) << 17) | ((kTile >> 4) << 24);
       constexpr uint32_t i_o =
           (1u << 4) | (fmt << 7) | (fmt << 10) | (1u << 16) | ((DP >> 3) << 17) | ((kTile >> 4) << 24);
-      const uint64_t q_desc = ptx::sdesc(q_at(0), 16, 1024);
-      uint32_t turn[2] = {0, 0};
-      bool ok = true;
-      for (int t = 0; t < 2; ++t) ok = ok && (tiles[t].from >= tiles[t].to || wait(q_full(t), 0, p, 1));
-      for (int j = from - 1; ok && j < to; ++j) {
+      const uint32_t s_to = tmem + t * kTile, o_to = tmem + C::kOAt + t * 128;
+      const uint64_t q_desc = ptx::sdesc(q_at(t), 16, 1024);
+      const bool leader = elect_one();
+      uint32_t turn = 0;
+      Ring<C::kKeys> rk;
+      Ring<C::kValues> rv;
+      bool ok = tile_from >= tile_to || wait_warp(q_full(t), 0, p, 1);
+      // (the first tile's first turn needs no word of the second)
+      uint32_t mine = t == 0 ? 1u : 0u;
+      for (int j = first - 1; ok && j < last; ++j, mine ^= 1u) {
         // the product of step j with the values, then the scores of step j + 1
-        const int nv = j - from, nk = nv + 1, s = v_stage(max(nv, 0)), sk = k_stage(nk);
-        ok = (nv < 0 || (wait(v_full(s), v_phase(nv), p, 1) && wait(v_ok(s), v_phase(nv), p, 1))) &&
-             (j + 1 >= to || wait(k_full(sk), k_phase(nk), p, 1));
-        const uint64_t k_desc = ptx::sdesc(k_at(sk), 16, 1024), v_desc = ptx::sdesc(v_at(s), kTile * 128, 1024);
-        const bool skip = nv >= 0 && by_rows(s);
+        const bool begun = j >= first, product = begun && j >= tile_from && j < tile_to;
+        const bool scores = j + 1 >= tile_from && j + 1 < tile_to, keys_too = j + 1 < last;
+        {
+          const bool a = !begun || ptx::mbar_try_wait(v_full(rv.s), rv.ph);
+          const bool b = !begun || ptx::mbar_try_wait(v_ok(rv.s), rv.ph);
+          const bool c = !keys_too || ptx::mbar_try_wait(k_full(rk.s), rk.ph);
+          ok = __all_sync(0xFFFFFFFFu, a && b && c) ||
+               ((!begun || (wait_warp(v_full(rv.s), rv.ph, p, 1) && wait_warp(v_ok(rv.s), rv.ph, p, 1))) &&
+                (!keys_too || wait_warp(k_full(rk.s), rk.ph, p, 1)));
+        }
+        ok = ok && (!product || wait_warp(w_half(t), turn, p, 1)) && wait_warp(go(t), mine, p, 1);
+        if (!ok) break;
+        const uint64_t k_desc = ptx::sdesc(k_at(rk.s), 16, 1024), v_desc = ptx::sdesc(v_at(rv.s), kTile * 128, 1024);
+        ptx::tc_fence_after();
+        if (product) {
+          const bool issue = leader && !by_rows(rv.s);
+          const uint32_t more = j != tile_from ? 1u : 0u;
+          if (issue) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const bool product = nv >= 0 && tiles[t].active(j);
-          if (product && ok) ok = wait(w_full(t), turn[t]++ & 1u, p, 1);
-          if (!ok) break;
-          ptx::tc_fence_after();
-          if (product && !skip) {
-            const uint32_t more = j != tiles[t].from ? 1u : 0u;
-#pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              mma_ts(tmem + C::kOAt + t * 128, tmem + t * kTile + k * 8, v_desc + k * 128, i_o, k != 0 ? 1u : more);
+            for (int k = 0; k < kTile / 32; ++k) mma_ts(o_to, s_to + k * 8, v_desc + k * 128, i_o, k != 0 ? 1u : more);
           }
-          if (tiles[t].active(j + 1)) {
+          if (!(ok = wait_warp(w_full(t), turn, p, 1))) break;
+          turn ^= 1u;
+          ptx::tc_fence_after();
+          if (issue) {
+#pragma unroll
+            for (int k = kTile / 32; k < kTile / 16; ++k) mma_ts(o_to, s_to + k * 8, v_desc + k * 128, i_o, 1u);
+          }
+        }
+        if (leader) {
+          if (scores) {
 #pragma unroll
             for (int k = 0; k < DP / 16; ++k) {
               const uint32_t step = (k >> 2) * (kTile * 128 >> 4) + (k & 3) * 2;
-              ptx::mma_f16(tmem + t * kTile, q_desc + (t * (C::kBytes >> 4) + step), k_desc + step, i_s, k != 0 ? 1u : 0u);
+              ptx::mma_f16(s_to, q_desc + step, k_desc + step, i_s, k != 0 ? 1u : 0u);
             }
             ptx::mma_commit(s_full(t));
-          } else if (product && j + 1 == tiles[t].to) {
+          } else if (product) {
             ptx::mma_commit(o_full(t));
           }
+          ptx::mbar_arrive(go(1 - t));
+          if (begun) ptx::mma_commit(empty(rv.s));
         }
-        if (ok && nv >= 0) ptx::mma_commit(empty(s));
+        rk.next();
+        if (begun) rv.next();
       }
-      // Every product this thread issued is complete before tensor memory goes back.
-      ptx::mma_commit(drain);
-      wait_out(drain, 0, p, 1);
+      // Every product of this warp is complete before tensor memory goes back.
+      if (leader) {
+        ptx::mma_commit(drain);
+        wait_out(drain, 0, p, 1);
+      }
     }
     __syncwarp();
-  } else if (warp < kWeights) {
+  } else if (warp == kLook) {
     // ----------------------------------------------- values that are hidden
         for (int j = from; j < to; ++j) {
       const int n = j - from, s = v_stage(n);
@@ -473,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const int count = min(kTile, keys - j * kTile);
         constexpr uint32_t kExponent = BF16 ? 0x7F807F80u : 0x7C007C00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
 #pragma unroll 4
-        for (int e = (warp - kLook) * 32 + lane; e < kTile * DP / 8; e += 64) {
+        for (int e = lane; e < kTile * DP / 8; e += 32) {
           const uint32_t at = v_at(s) + e * 16;
           if ((e >> 3) % kTile < count) {
             uint32_t v[4];
@@ -492,19 +548,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       }
       const bool any = __any_sync(0xFFFFFFFFu, (found & 0x80008000u) != 0u);
       if (lane == 0) {
-        wild[2 * s + warp - kLook] = any ? 1 : 0;
+        wild[s] = any ? 1 : 0;
         ptx::mbar_arrive(v_ok(s));
       }
     }
   } else {
     // ---------------------------------------------------------- weights
-    // Two threads a row, each with half of a step's keys: warps w and w + 4.
-    const int t = (warp - kWeights) >> 3, half = ((warp - kWeights) >> 2) & 1, row = (warp & 3) * 32 + lane;  // row of the tile
+    const int t = (warp - kWeights) >> 2, row = (warp & 3) * 32 + lane;  // row of the tile
     const Tile tile = t == 0 ? tiles[0] : tiles[1];
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + t * kTile, o_at = tmem + lanes + C::kOAt + t * 128;
-    const uint32_t meet = 1 + t * 4 + (warp & 3);  // barrier of the two warps
-    float* const meet_at = reinterpret_cast<float*>(base_ptr + C::kMeetAt) + t * kTile + row;
     const int at = keys - queries + row0 + t * kTile + row;
     const int lo = key_begin(p, at), hi = key_end(p, at, keys);
     const float to_log2 = p.scale * kLog2e;
@@ -513,58 +566,30 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     float ref = -INFINITY, sum = 0.0f;
     uint32_t turn = 0;
     bool ok = true;
-    // A wait that ran out is told to the other warp at the next meeting, so that
-    // both come to every one of them.
     for (int j = tile.from; j < tile.to; ++j, ++turn) {
-      ok = ok && wait_warp(s_full(t), turn & 1u, p, 2);
+      if (!(ok = wait_warp(s_full(t), turn & 1u, p, 2))) break;
       ptx::tc_fence_after();
-      uint32_t s[2][32];
+      uint32_t s[4][32];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) ptx::tmem_ld_32x32b_x32(s_at + half * 64 + i * 32, s[i]);
+      for (int i = 0; i < 4; ++i) ptx::tmem_ld_32x32b_x32(s_at + i * 32, s[i]);
       ptx::tmem_wait_ld();
 #pragma unroll
-      for (int i = 0; i < 2; ++i) ptx::tmem_regs_ready(s[i]);
-      const bool masked = tile.masked(j);
+      for (int i = 0; i < 4; ++i) ptx::tmem_regs_ready(s[i]);
       const int key_lo = lo - j * kTile, key_hi = hi - j * kTile;
-      if (masked) {
-        const int a = key_lo - half * 64, b = key_hi - half * 64;
+      if (tile.masked(j)) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int c = 0; c < 32; ++c)
-            if (i * 32 + c < a || i * 32 + c >= b) s[i][c] = 0xFF800000u;  // -inf
+            if (i * 32 + c < key_lo || i * 32 + c >= key_hi) s[i][c] = 0xFF800000u;  // -inf
       }
-      float most;
-      {
-        float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+      for (int c = 0; c < 32; c += 2)
 #pragma unroll
-          for (int c = 0; c < 32; c += 8)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              m[e] = max3(m[e], __uint_as_float(s[i][c + e]), __uint_as_float(s[i][c + e + 4]));
-        most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * to_log2;
-      }
-      // The meeting also says that both have read their scores: the weights go
-      // over those of the first half.
-      if (either(meet, !ok || most > ref + kSlack)) {
-        // the second half's maxima go to the first half's threads and theirs of
-        // both back; NaN: no (a row without a number has the maximum -inf here)
-        if (half) *meet_at = ok ? most : NAN;
-        ptx::named_bar_sync(meet, 64);
-        if (!half) {
-          const float theirs = *meet_at;
-          ok = ok && !__any_sync(0xFFFFFFFFu, isnan(theirs));
-          most = fmaxf(most, theirs);
-          *meet_at = ok ? most : NAN;
-        }
-        ptx::named_bar_sync(meet, 64);
-        if (half) {
-          most = *meet_at;
-          ok = ok && !__any_sync(0xFFFFFFFFu, isnan(most));
-        }
-        if (!ok) break;
+        for (int i = 0; i < 4; ++i) m[i] = max3(m[i], __uint_as_float(s[i][c]), __uint_as_float(s[i][c + 1]));
+      const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * to_log2;
+      if (__any_sync(0xFFFFFFFFu, most > ref + kSlack)) {
         const float next = most > ref + kSlack ? most : ref;
         const float f = next == -INFINITY ? 1.0f : exp2_fast(ref - next);
         ref = next;
@@ -572,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         if (j != tile.from) {
           // (the scores of this step are there, so the product before them is done)
 #pragma unroll 1
-          for (int d = half * (DP / 2); d < (half + 1) * (DP / 2); d += 8) {
+          for (int d = 0; d < DP; d += 8) {
             uint32_t o[8];
             tmem_ld_x8(o_at + d, o);
 #pragma unroll
@@ -583,9 +608,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       }
       const float less = ref == -INFINITY ? 0.0f : kLift - ref;
       const uint64_t less2 = pair(less, less);
-      uint64_t sum2 = pair(0.0f, 0.0f);
+      uint64_t sum2[2] = {pair(sum, 0.0f), pair(0.0f, 0.0f)};
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 4; ++i) {
         uint32_t w[16];
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
@@ -593,24 +618,28 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           unpair(fma2(pair(__uint_as_float(s[i][2 * c]), __uint_as_float(s[i][2 * c + 1])), to_log2_2, less2), x, y);
           x = exp2_fast(x);
           y = exp2_fast(y);
-          sum2 = add2(sum2, pair(x, y));
+          sum2[c & 1] = add2(sum2[c & 1], pair(x, y));
           w[c] = pack2<BF16>(x, y);
         }
-        tmem_st_x16(s_at + half * 32 + i * 16, w);
+        tmem_st_x16(s_at + i * 16, w);
+        if (i == 1) {  // the product with the first half of the values may begin
+          tmem_wait_st();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(w_half(t));
+        }
       }
       tmem_wait_st();
-      float x, y;
-      unpair(sum2, x, y);
-      sum += x + y;
+      {
+        float x, y;
+        unpair(add2(sum2[0], sum2[1]), x, y);
+        sum = x + y;
+      }
       if ((tiles[0].active(j) && tiles[0].masked(j)) || (tiles[1].active(j) && tiles[1].masked(j))) {
         const int n = j - from, st = v_stage(n);
-        ok = wait_warp(v_full(st), v_phase(n), p, 2) && wait_warp(v_ok(st), v_phase(n), p, 2);
-        if (either(meet, !ok)) {  // (the weights of both are there behind it)
-          ok = false;
-          break;
-        }
+        if (!(ok = wait_warp(v_full(st), v_phase(n), p, 2) && wait_warp(v_ok(st), v_phase(n), p, 2))) break;
         if (by_rows(st)) {
-          product_by_rows<BF16, DP>(s_at, o_at, v_at(st), key_lo, key_hi, j == tile.from, half);
+          product_by_rows<BF16, DP>(s_at, o_at, v_at(st), key_lo, key_hi, j == tile.from);
           ptx::fence_proxy_async_smem();
         }
       }
@@ -618,15 +647,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(w_full(t));
     }
-    // outputs: a row two threads, half of its values each
-    if (tile.rows > 0) {
+    // outputs: a row a thread
+    if (tile.rows > 0 && ok) {
       const bool any = tile.from < tile.to;
-      if (half) *meet_at = sum;
-      ptx::named_bar_sync(meet, 64);
-      if (!half) *meet_at = sum += *meet_at;
-      ptx::named_bar_sync(meet, 64);
-      if (half) sum = *meet_at;
-      if (any) ok = ok && wait_warp(o_full(t), 0, p, 2);
+      if (any) ok = wait_warp(o_full(t), 0, p, 2);
       if (ok) {
         ptx::tc_fence_after();
         const bool mine = row < tile.rows;
@@ -634,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         uint16_t* const out = p.out.p + token * p.out.ld + head * p.out.hs;
 #pragma unroll 1
-        for (int d = half * (DP / 2); d < (half + 1) * (DP / 2); d += 32) {
+        for (int d = 0; d < DP; d += 32) {
           uint32_t o[32];
           if (any) {
             ptx::tmem_ld_32x32b_x32(o_at + d, o);
@@ -652,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
               *reinterpret_cast<uint4*>(out + d + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
-        if (mine && half == 0 && p.lse)
+        if (mine && p.lse)
           p.lse[token * p.heads + head] = sum == 0.0f ? -INFINITY : (ref - kLift + log2f(sum)) * kLn2;
       }
     }
@@ -660,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  if (warp == kIssue) ptx::tmem_dealloc(tmem, 512);
+  if (warp == kIssue) ptx::tmem_dealloc(*tmem_slot, 512);
 }
 
 // A map of tokens x heads x dim in boxes of 64 values x 128 tokens of a head.
