@@ -524,29 +524,29 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         for (int j = from; j < to; ++j) {
       const int n = j - from, s = v_stage(n);
       if (!wait_warp(v_full(s), v_phase(n), p, 3)) break;
-      uint32_t found = 0;
+      uint32_t most = 0;  // magnitudes as integers, two halves
       if ((tiles[0].active(j) && tiles[0].masked(j)) || (tiles[1].active(j) && tiles[1].masked(j))) {
         const int count = min(kTile, keys - j * kTile);
-        constexpr uint32_t kExponent = BF16 ? 0x7F807F80u : 0x7C007C00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
-#pragma unroll 4
-        for (int e = lane; e < kTile * DP / 8; e += 32) {
-          const uint32_t at = v_at(s) + e * 16;
-          if ((e >> 3) % kTile < count) {
+        for (int x = 0; x < DP; x += 64) {
+          const uint32_t at = v_at(s) + x * (kTile * 2) + lane * 16;  // 4 rows at a time
+#pragma unroll 8
+          for (int r = lane >> 3; r < count; r += 4) {
             uint32_t v[4];
             asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                         : "r"(at)
-                         : "memory");
-            // an exponent of ones carries into its half's sign
+                         : "r"(at + (r >> 2) * 512));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) found |= (v[i] & kExponent) + kOne;
-          } else {
-            asm volatile("st.volatile.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0u) : "memory");
+            for (int i = 0; i < 4; ++i) most = __vmaxu2(most, v[i] & 0x7FFF7FFFu);
           }
+          if (count < kTile)
+            for (int r = count + ((lane >> 3) - count & 3); r < kTile; r += 4)
+              asm volatile("st.volatile.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + (r >> 2) * 512), "r"(0u)
+                           : "memory");
         }
         ptx::fence_proxy_async_smem();
       }
-      const bool any = __any_sync(0xFFFFFFFFu, (found & 0x80008000u) != 0u);
+      constexpr uint32_t kInf = BF16 ? 0x7F80u : 0x7C00u;
+      const bool any = __any_sync(0xFFFFFFFFu, (most & 0xFFFFu) >= kInf || (most >> 16) >= kInf);
       if (lane == 0) {
         wild[s] = any ? 1 : 0;
         ptx::mbar_arrive(v_ok(s));
