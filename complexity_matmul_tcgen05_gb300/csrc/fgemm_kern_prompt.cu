@@ -45,6 +45,7 @@ using namespace attn;
 
 constexpr int kTile = 128;            // queries of a tile, keys of a step
 constexpr int kRows = 2 * kTile;      // queries of a CTA
+constexpr int kEarly = 96;            // keys of a step whose weights are handed over first
 constexpr int kThreads = 384;
 constexpr int kIssue = 0, kLoad = 2, kLook = 3, kWeights = 4;  // warps (two that issue)
 constexpr float kSlack = 8.0f;        // log2 of how far the maximum may be above the reference
@@ -349,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   auto s_full = [&](int t) { return bar0 + 8u * (kMore + t); };        // scores are there
   auto w_full = [&](int t) { return bar0 + 8u * (kMore + 2 + t); };    // weights are there
   auto o_full = [&](int t) { return bar0 + 8u * (kMore + 4 + t); };    // outputs are there
-  auto w_half = [&](int t) { return bar0 + 8u * (kMore + 6 + t); };    // those of the first half of the keys
+  auto w_early = [&](int t) { return bar0 + 8u * (kMore + 6 + t); };    // those of the first keys
   auto go = [&](int t) { return bar0 + 8u * (kMore + 8 + t); };        // it is the tile's turn to issue
   const uint32_t drain = bar0 + 8u * (kMore + 10);
   // of the value tiles in their ring: 1 where not all of it is finite
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       ptx::mbar_init(q_full(t), 1);
       ptx::mbar_init(s_full(t), 1);
       ptx::mbar_init(w_full(t), 4);
-      ptx::mbar_init(w_half(t), 4);
+      ptx::mbar_init(w_early(t), 4);
       ptx::mbar_init(go(t), 1);
       ptx::mbar_init(o_full(t), 1);
     }
@@ -476,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                ((!begun || (wait_warp(v_full(rv.s), rv.ph, p, 1) && wait_warp(v_ok(rv.s), rv.ph, p, 1))) &&
                 (!keys_too || wait_warp(k_full(rk.s), rk.ph, p, 1)));
         }
-        ok = ok && (!product || wait_warp(w_half(t), turn, p, 1)) && wait_warp(go(t), mine, p, 1);
+        ok = ok && wait_warp(go(t), mine, p, 1) && (!product || wait_warp(w_early(t), turn, p, 1));
         if (!ok) break;
         const uint64_t k_desc = ptx::sdesc(k_at(rk.s), 16, 1024), v_desc = ptx::sdesc(v_at(rv.s), kTile * 128, 1024);
         ptx::tc_fence_after();
@@ -485,14 +486,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           const uint32_t more = j != tile_from ? 1u : 0u;
           if (issue) {
 #pragma unroll
-            for (int k = 0; k < kTile / 32; ++k) mma_ts(o_to, s_to + k * 8, v_desc + k * 128, i_o, k != 0 ? 1u : more);
+            for (int k = 0; k < kEarly / 16; ++k) mma_ts(o_to, s_to + k * 8, v_desc + k * 128, i_o, k != 0 ? 1u : more);
           }
           if (!(ok = wait_warp(w_full(t), turn, p, 1))) break;
           turn ^= 1u;
           ptx::tc_fence_after();
           if (issue) {
 #pragma unroll
-            for (int k = kTile / 32; k < kTile / 16; ++k) mma_ts(o_to, s_to + k * 8, v_desc + k * 128, i_o, 1u);
+            for (int k = kEarly / 16; k < kTile / 16; ++k) mma_ts(o_to, s_to + k * 8, v_desc + k * 128, i_o, 1u);
           }
         }
         if (leader) {
@@ -622,11 +623,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           w[c] = pack2<BF16>(x, y);
         }
         tmem_st_x16(s_at + i * 16, w);
-        if (i == 1) {  // the product with the first half of the values may begin
+        if (i == kEarly / 32 - 1) {  // the product with the first values may begin
           tmem_wait_st();
           ptx::tc_fence_before();
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(w_half(t));
+          if (lane == 0) ptx::mbar_arrive(w_early(t));
         }
       }
       tmem_wait_st();
