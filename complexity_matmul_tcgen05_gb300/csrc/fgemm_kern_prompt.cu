@@ -58,9 +58,10 @@ struct Cfg {
   // each of its tiles in turn. (In a ring of both, the warps that look after the
   // values alone took a stage whose key tile was still on its way for the next one.)
   static constexpr int kValues = DP == 128 ? 2 : 4, kKeys = kValues + 1;
-  static constexpr int kBars = 2 + kKeys + 3 * kValues + 11;
+  static constexpr int kBars = 20 + kKeys + 3 * kValues;
   static constexpr int kBarAt = (2 + kKeys + kValues) * kBytes;
-  static constexpr int kSmem = 1024 + kBarAt + 8 * kBars + 4 * kValues + 16;
+  static constexpr int kJobAt = kBarAt + (8 * kBars + 15) / 16 * 16;  // two jobs, an answer, flags
+  static constexpr int kSmem = 1024 + kJobAt + 2 * 32 + 16 + 4 * kValues + 16;
   static constexpr int kOAt = 256;  // tensor memory: scores of the two tiles, then their outputs
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
@@ -69,6 +70,7 @@ struct Args {
   CUtensorMap q, k, v;
   PromptParams p;
   int slots;  // of 256 queries, over all sequences
+  int wide;   // rows of out are on 32 bytes
 };
 
 // ------------------------------------------------------------------- PTX
@@ -125,6 +127,37 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// 32 bytes in one store.
+__device__ __forceinline__ void store32(void* at, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// Asks for a CTA of the grid that has not been launched: it will not be, and its
+// work is the asker's. The answer (16 bytes) is counted on `bar`.
+__device__ __forceinline__ void ask_for_cta(uint32_t answer, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   answer),
+               "r"(bar)
+               : "memory");
+}
+// Whether there was one, and its index.
+__device__ __forceinline__ bool answered_cta(uint32_t answer, unsigned& index) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(ok), "=r"(index)
+      : "r"(answer)
+      : "memory");
+  return ok != 0;
 }
 
 // Two fp32 operations in one instruction.
@@ -243,15 +276,16 @@ __device__ __forceinline__ int sequence_of(const PromptParams& p, int slot) {
   return first(lo) <= slot ? lo : -1;
 }
 
-// A tile of queries: its rows, the keys that its first and its last row see,
-// and the steps that these lie in.
+// A tile of queries: its rows, the steps that the keys of any row lie in, and of
+// these the ones whose keys every row sees.
 struct Tile {
-  int rows;              // 0: none
-  int hi_first, lo_last; // end of the first row's keys, begin of the last row's
-  int from, to;          // steps
-  __device__ __forceinline__ bool active(int j) const { return j >= from && j < to; }
-  // whether some row does not see some key of step j
-  __device__ __forceinline__ bool masked(int j) const { return (j + 1) * kTile > hi_first || j * kTile < lo_last; }
+  int rows;  // 0: none
+  int from, to;
+  int all_from, all_to;
+  // a step that it has and of which some row does not see some key
+  __device__ __forceinline__ bool masked(int j) const {
+    return j >= from && j < to && (j < all_from || j >= all_to);
+  }
 };
 // Keys [lo, hi) that a query at position `at` sees.
 __device__ __forceinline__ int key_end(const PromptParams& p, int at, int keys) {
@@ -263,21 +297,25 @@ __device__ __forceinline__ int key_begin(const PromptParams& p, int at) {
 __device__ __forceinline__ Tile tile_of(const PromptParams& p, int row0, int queries, int keys) {
   Tile t;
   t.rows = min(kTile, queries - row0);
-  t.hi_first = t.lo_last = t.from = t.to = 0;
+  t.from = t.to = t.all_from = t.all_to = 0;
   if (t.rows <= 0) {
     t.rows = 0;
     return t;
   }
   const int at0 = keys - queries + row0, at1 = at0 + t.rows - 1;
-  t.hi_first = key_end(p, at0, keys);
-  t.lo_last = key_begin(p, at1);
   const int lo = key_begin(p, at0), hi = key_end(p, at1, keys);
   if (lo < hi) {
     t.from = lo / kTile;
     t.to = (hi + kTile - 1) / kTile;
+    t.all_from = (key_begin(p, at1) + kTile - 1) / kTile;
+    t.all_to = key_end(p, at0, keys) / kTile;
   }
   return t;
 }
+
+// Columns of the weights of keys 16 k to 16 k + 15 of a step from its scores on: each
+// 32 keys' weights lie over the first half of their scores.
+__device__ __forceinline__ constexpr int weights_at(int k) { return (k >> 1) * 32 + (k & 1) * 8; }
 
 // O (+)= w V of one step for the rows of a warp, over the keys [lo, hi) of the
 // step that each row sees; all lanes together. w is read from tensor memory.
@@ -289,7 +327,7 @@ __device__ __noinline__ void product_by_rows(uint32_t w_at, uint32_t o_at, uint3
 #pragma unroll 1
     for (int c = 0; c < kTile; c += 16) {
       uint32_t w[8];
-      tmem_ld_x8(w_at + c / 2, w);
+      tmem_ld_x8(w_at + weights_at(c / 16), w);
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
         const int key = c + k;
@@ -317,20 +355,48 @@ __device__ __noinline__ void product_by_rows(uint32_t w_at, uint32_t o_at, uint3
   }
 }
 
+// A job: 256 rows of one head of one sequence, as the loading warp finds it.
+struct Job {
+  int head, q0, queries, k0, keys, row0;
+  int more;  // 0: there are no more
+  int pad;
+};
+
+// The job of CTA `index` of the grid; false if there is none (the slots are more than
+// the jobs). All lanes of a warp together.
+__device__ __forceinline__ bool job_of(const PromptParams& p, int slots, unsigned index, Job& job) {
+  job.head = static_cast<int>(index % static_cast<unsigned>(p.heads));
+  // the last slots first: with a causal mask they have the most keys
+  const int slot = slots - 1 - static_cast<int>(index / static_cast<unsigned>(p.heads));
+  const int seq = sequence_of(p, slot);
+  if (seq < 0) return false;
+  job.q0 = held(p.starts[seq], 0, p.tokens);
+  job.queries = held(p.starts[seq + 1], job.q0, p.tokens) - job.q0;
+  job.k0 = held(p.k_starts[seq], 0, p.k_tokens);
+  job.keys = held(p.k_starts[seq + 1], job.k0, p.k_tokens) - job.k0;
+  job.row0 = (slot - (job.q0 / kRows + seq)) * kRows;
+  return job.row0 < job.queries;
+}
+
+// The two tiles of a job and the steps of both (the second tile's begin no later
+// than the first's end).
+struct Tiles {
+  Tile t0, t1;
+  int from, to;
+  __device__ __forceinline__ Tiles(const PromptParams& p, const Job& job) {
+    t0 = tile_of(p, job.row0, job.queries, job.keys);
+    t1 = tile_of(p, job.row0 + kTile, job.queries, job.keys);
+    from = t0.from < t0.to ? t0.from : t1.from;
+    to = t1.from < t1.to ? max(t0.to, t1.to) : t0.to;
+  }
+  __device__ __forceinline__ const Tile& operator[](int t) const { return t == 0 ? t0 : t1; }
+};
+
 template <bool BF16, int DP>
 __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ Args a) {
   using C = Cfg<DP>;
   const PromptParams& p = a.p;
-  const int head = blockIdx.x % p.heads;
-  // the last slots first: with a causal mask they have the most keys
-  const int slot = a.slots - 1 - static_cast<int>(blockIdx.x / p.heads);
-  const int seq = sequence_of(p, slot);
-  if (seq < 0) return;
-  const int q0 = held(p.starts[seq], 0, p.tokens), queries = held(p.starts[seq + 1], q0, p.tokens) - q0;
-  const int k0 = held(p.k_starts[seq], 0, p.k_tokens), keys = held(p.k_starts[seq + 1], k0, p.k_tokens) - k0;
-  const int row0 = (slot - (q0 / kRows + seq)) * kRows;
-  if (row0 >= queries) return;
-  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
@@ -340,40 +406,66 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   auto k_at = [&](int s) { return base + (2 + s) * C::kBytes; };
   auto v_at = [&](int s) { return base + (2 + C::kKeys + s) * C::kBytes; };
   const uint32_t bar0 = base + C::kBarAt;
-  auto q_full = [&](int t) { return bar0 + 8u * t; };
-  auto k_full = [&](int s) { return bar0 + 8u * (2 + s); };
-  constexpr int kVBar = 2 + C::kKeys;
-  auto v_full = [&](int s) { return bar0 + 8u * (kVBar + s); };
-  auto empty = [&](int s) { return bar0 + 8u * (kVBar + C::kValues + s); };  // a step is done
-  auto v_ok = [&](int s) { return bar0 + 8u * (kVBar + 2 * C::kValues + s); };  // looked after
-  constexpr int kMore = kVBar + 3 * C::kValues;
-  auto s_full = [&](int t) { return bar0 + 8u * (kMore + t); };        // scores are there
-  auto w_full = [&](int t) { return bar0 + 8u * (kMore + 2 + t); };    // weights are there
-  auto o_full = [&](int t) { return bar0 + 8u * (kMore + 4 + t); };    // outputs are there
-  auto w_early = [&](int t) { return bar0 + 8u * (kMore + 6 + t); };    // those of the first keys
-  auto go = [&](int t) { return bar0 + 8u * (kMore + 8 + t); };        // it is the tile's turn to issue
-  const uint32_t drain = bar0 + 8u * (kMore + 10);
+  auto bar = [&](int i) { return bar0 + 8u * i; };
+  // by tile
+  auto q_full = [&](int t) { return bar(t); };
+  auto q_empty = [&](int t) { return bar(2 + t); };
+  auto s_full = [&](int t) { return bar(4 + t); };    // scores are there
+  auto w_early = [&](int t) { return bar(6 + t); };   // weights of the first keys are there
+  auto w_full = [&](int t) { return bar(8 + t); };    // all are
+  auto o_full = [&](int t) { return bar(10 + t); };   // outputs are there
+  auto go = [&](int t) { return bar(12 + t); };       // it is the tile's turn to issue
+  // of the two places for jobs
+  auto job_full = [&](int s) { return bar(14 + s); };
+  auto job_empty = [&](int s) { return bar(16 + s); };
+  const uint32_t taken = bar(18);  // the answer to a request for a job
+  const uint32_t drain = bar(19);
+  // of the rings
+  auto k_full = [&](int s) { return bar(20 + s); };
+  constexpr int kVBar = 20 + C::kKeys;
+  auto v_full = [&](int s) { return bar(kVBar + s); };
+  auto v_ok = [&](int s) { return bar(kVBar + C::kValues + s); };       // looked after
+  auto empty = [&](int s) { return bar(kVBar + 2 * C::kValues + s); };  // a step is done
+  const uint32_t answer = base + C::kJobAt + 2 * sizeof(Job);
   // of the value tiles in their ring: 1 where not all of it is finite
-  volatile int* const wild = reinterpret_cast<volatile int*>(base_ptr + C::kBarAt + 8 * C::kBars);
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + C::kBarAt + 8 * C::kBars + 4 * C::kValues);
+  volatile int* const wild = reinterpret_cast<volatile int*>(base_ptr + C::kJobAt + 2 * sizeof(Job) + 16);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + C::kJobAt + 2 * sizeof(Job) + 16 + 4 * C::kValues);
 
   if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      ptx::mbar_init(q_full(t), 1);
+      ptx::mbar_init(q_empty(t), 1);
+      ptx::mbar_init(s_full(t), 1);
+      ptx::mbar_init(w_early(t), 4);
+      ptx::mbar_init(w_full(t), 4);
+      ptx::mbar_init(o_full(t), 1);
+      ptx::mbar_init(go(t), 1);
+      ptx::mbar_init(job_full(t), 1);
+      ptx::mbar_init(job_empty(t), kThreads / 32 - 1);
+    }
+    ptx::mbar_init(taken, 1);
+    ptx::mbar_init(drain, 2);
     for (int s = 0; s < C::kKeys; ++s) ptx::mbar_init(k_full(s), 1);
     for (int s = 0; s < C::kValues; ++s) {
       ptx::mbar_init(v_full(s), 1);
-      ptx::mbar_init(empty(s), 2);
       ptx::mbar_init(v_ok(s), 1);
+      ptx::mbar_init(empty(s), 2);
     }
-    for (int t = 0; t < 2; ++t) {
-      ptx::mbar_init(q_full(t), 1);
-      ptx::mbar_init(s_full(t), 1);
-      ptx::mbar_init(w_full(t), 4);
-      ptx::mbar_init(w_early(t), 4);
-      ptx::mbar_init(go(t), 1);
-      ptx::mbar_init(o_full(t), 1);
-    }
-    ptx::mbar_init(drain, 2);
     ptx::fence_mbar_init();
+  }
+  volatile Job* const jobs = reinterpret_cast<volatile Job*>(base_ptr + C::kJobAt);
+  Job job = {};
+  bool any_more = true;
+  auto store_job = [&](int place, bool more) {
+    if (lane == 0) {
+      volatile Job& to = jobs[place];
+      to.head = job.head, to.q0 = job.q0, to.queries = job.queries, to.k0 = job.k0, to.keys = job.keys;
+      to.row0 = job.row0, to.more = more ? 1 : 0;
+    }
+  };
+  if (warp == kLoad) {  // the first job; an empty one if the CTA's slot is
+    if (!job_of(p, a.slots, blockIdx.x, job)) job.head = job.q0 = job.queries = job.k0 = job.keys = job.row0 = 0;
+    store_job(0, true);
   }
   if (warp == kIssue) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
@@ -385,95 +477,154 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   // (all columns: the address is 0, known when this is compiled)
   constexpr uint32_t tmem = 0;
 
-  Tile tiles[2] = {tile_of(p, row0, queries, keys), tile_of(p, row0 + kTile, queries, keys)};
-  // the steps of both (the second tile's begin no later than the first's end)
-  const bool one = tiles[0].from < tiles[0].to, two = tiles[1].from < tiles[1].to;
-  const int from = one ? tiles[0].from : tiles[1].from;
-  const int to = two ? max(tiles[0].to, tiles[1].to) : tiles[0].to;
-  // stage and phase of the n-th tile of a ring
-  auto k_stage = [&](int n) { return n % C::kKeys; };
-  auto k_phase = [&](int n) { return static_cast<uint32_t>(n / C::kKeys) & 1u; };
-  auto v_stage = [&](int n) { return n % C::kValues; };
-  auto v_phase = [&](int n) { return static_cast<uint32_t>(n / C::kValues) & 1u; };
-  auto by_rows = [&](int s) { return wild[s] != 0; };
-
+  // Jobs are numbered; number n lies in place n & 1, the first since before the
+  // barrier above. False: a wait ran out.
+  int number = 0;
+  auto job_there = [&](int role) {
+    return number == 0 || wait_warp(job_full(number & 1), ((number - 1) >> 1) & 1u, p, role);
+  };
+  auto job_read = [&]() {
+    const volatile Job& from = jobs[number & 1];
+    job.head = from.head, job.q0 = from.q0, job.queries = from.queries, job.k0 = from.k0, job.keys = from.keys;
+    job.row0 = from.row0;
+    return from.more != 0;
+  };
+  auto job_done = [&]() {  // by every warp but the loading one
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(job_empty(number & 1));
+    ++number;
+  };
 
   if (warp == kLoad) {
-    // ------------------------------------------------------------ loads
-    if (lane == 0 && from < to) {
+    // ------------------------------------------------------ jobs and loads
+    // The grid has a CTA a job; one that is done with its own takes over those of
+    // CTAs that have not been launched (a job ahead of its work), so the next job's
+    // loads and first scores run under this one's last steps.
+    if (lane == 0) {
       ptx::prefetch_tmap(&a.q);
       ptx::prefetch_tmap(&a.k);
       ptx::prefetch_tmap(&a.v);
-      const int kv = head / (p.heads / p.kv_heads);
-      for (int t = 0; t < 2; ++t)
-        if (tiles[t].from < tiles[t].to) {
-          ptx::mbar_arrive_expect_tx(q_full(t), C::kBytes);
+    }
+    uint32_t asked = 0;
+    bool ok = true;
+    // Asks for jobs until there is one or no more and leaves it for the others.
+    auto publish = [&]() {
+      bool found = false;
+      while (ok && any_more && !found) {
+        if (lane == 0) {
+          ptx::mbar_arrive_expect_tx(taken, 16);
+          ask_for_cta(answer, taken);
+        }
+        __syncwarp();
+        // (waited for to its end: the answer is on its way to this CTA's memory)
+        if (!wait_warp(taken, asked & 1u, p, 0)) {
+          wait_out(taken, asked & 1u, p, 0);
+          ok = false;
+        }
+        ++asked;
+        unsigned index = 0;
+        any_more = ok && answered_cta(answer, index);
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (any_more) found = job_of(p, a.slots, static_cast<unsigned>(uniform(static_cast<int>(index))), job);
+      }
+      ++number;
+      if (ok && number >= 2) ok = wait_warp(job_empty(number & 1), ((number - 2) >> 1) & 1u, p, 0);
+      if (ok) {
+        store_job(number & 1, found);
+        if (lane == 0) ptx::mbar_arrive(job_full(number & 1));
+      }
+      return ok && found;
+    };
+    Ring<C::kKeys> rk;
+    Ring<C::kValues> rv;
+    uint32_t q_turn[2] = {0, 0};
+    int nk = 0, nv = 0;  // tiles loaded so far
+    for (bool more = true; ok && more;) {
+      const Tiles tiles(p, job);
+      const int q0 = job.q0 + job.row0, q_head = job.head, k0 = job.k0 + tiles.from * kTile;
+      const int kv = job.head / (p.heads / p.kv_heads), count = tiles.to - tiles.from;
+      auto load = [&](int n, uint32_t at, const CUtensorMap* map, uint32_t full) {
+        if (lane == 0) {
+          ptx::mbar_arrive_expect_tx(full, C::kBytes);
           for (int x = 0; x < DP; x += 64)
-            tma_load_3d(q_at(t) + x * (kTile * 2), &a.q, x, head, q0 + row0 + t * kTile, q_full(t));
+            tma_load_3d(at + x * (kTile * 2), map, x, kv, k0 + n * kTile, full);
+        }
+      };
+      for (int t = 0; ok && t < 2; ++t)
+        if (tiles[t].from < tiles[t].to) {
+          ok = wait_warp(q_empty(t), (q_turn[t] & 1u) ^ 1u, p, 0);
+          if (ok && lane == 0) {
+            ptx::mbar_arrive_expect_tx(q_full(t), C::kBytes);
+            for (int x = 0; x < DP; x += 64)
+              tma_load_3d(q_at(t) + x * (kTile * 2), &a.q, x, q_head, q0 + t * kTile, q_full(t));
+          }
+          q_turn[t] += ok ? 1 : 0;
         }
       // Keys go a step ahead of the values. A step's end hands back its values and
       // the keys of the next, whose scores it ended with; there is one stage more of
-      // keys for the first ones, which come back with the first step too.
-      const int count = to - from;
-      auto load = [&](int n, uint32_t at, const CUtensorMap* map, uint32_t bar) {
-        ptx::mbar_arrive_expect_tx(bar, C::kBytes);
-        for (int x = 0; x < DP; x += 64) tma_load_3d(at + x * (kTile * 2), map, x, kv, k0 + (from + n) * kTile, bar);
-      };
-      int nk = 0, nv = 0;
-      load(0, k_at(0), &a.k, k_full(0));
-      ++nk;
-      for (; nv < count; ++nv) {
-        if (!wait(empty(v_stage(nv)), v_phase(nv) ^ 1u, p, 0)) break;
-        if (nk < count) {
-          load(nk, k_at(k_stage(nk)), &a.k, k_full(k_stage(nk)));
-          ++nk;
+      // keys for the first of a job, which come back with its first step.
+      if (count <= 0) more = publish();
+      for (int n = 0; ok && n < count; ++n) {
+        if (n == 0) load(0, k_at(rk.s), &a.k, k_full(rk.s)), rk.next(), ++nk;
+        if (!(ok = wait_warp(empty(rv.s), rv.ph ^ 1u, p, 0))) break;
+        if (n + 1 < count) load(n + 1, k_at(rk.s), &a.k, k_full(rk.s)), rk.next(), ++nk;
+        load(n, v_at(rv.s), &a.v, v_full(rv.s)), rv.next(), ++nv;
+        if (n == min(count, C::kValues) - 1) {  // the ring is full, or this job is loaded
+          more = publish();
         }
-        load(nv, v_at(v_stage(nv)), &a.v, v_full(v_stage(nv)));
       }
-      // Whatever another role did, the copies in flight land before the CTA ends.
-      for (int i = max(0, nk - C::kKeys); i < nk; ++i) wait_out(k_full(k_stage(i)), k_phase(i), p, 0);
-      for (int i = max(0, nv - C::kValues); i < nv; ++i) wait_out(v_full(v_stage(i)), v_phase(i), p, 0);
+    }
+    // Whatever another role did, the copies in flight land before the CTA ends.
+    if (lane == 0) {
+      for (int i = max(0, nk - C::kKeys); i < nk; ++i) wait_out(k_full(i % C::kKeys), (i / C::kKeys) & 1u, p, 0);
+      for (int i = max(0, nv - C::kValues); i < nv; ++i) wait_out(v_full(i % C::kValues), (i / C::kValues) & 1u, p, 0);
       for (int t = 0; t < 2; ++t)
-        if (tiles[t].from < tiles[t].to) wait_out(q_full(t), 0, p, 0);
+        if (q_turn[t] > 0) wait_out(q_full(t), (q_turn[t] - 1) & 1u, p, 0);
     }
     __syncwarp();
   } else if (warp < kIssue + 2) {
     // --------------------------------------------------------- products
     // A thread a tile, in turns: a thread's waits and commits (about 100 clocks each)
     // run under the other's products, of which the tensor core holds about eight.
-    // By one thread alone 16384 tokens took 1.75 ms; by two without turns, whose
-    // tiles fell in step, 2.2.
-    // All lanes go through the loop, so that what a product takes (descriptors,
-    // addresses) is known to be the warp's; one lane issues.
+    // By one thread alone 16384 tokens took 1.75 ms where this took 1.50; by two
+    // without turns, whose tiles fell in step, 2.2. All lanes go through the loop, so
+    // that what a product takes (descriptors, addresses) is known to be the warp's
+    // (1.68 ms without); one lane issues.
+    constexpr uint32_t fmt = BF16 ? 1u : 0u;
+    // fp32 accumulator, M = 128; scores: both operands K-major, N = 128;
+    // outputs: the values MN-major (bit 16), N = DP
+    constexpr uint32_t i_s = (1u << 4) | (fmt << 7) | (fmt << 10) | ((kTile >> 3) << 17) | ((kTile >> 4) << 24);
+    constexpr uint32_t i_o =
+        (1u << 4) | (fmt << 7) | (fmt << 10) | (1u << 16) | ((DP >> 3) << 17) | ((kTile >> 4) << 24);
     const int t = warp - kIssue;
-    const int first = uniform(from), last = uniform(to);
-    const int tile_from = uniform(t == 0 ? tiles[0].from : tiles[1].from);
-    const int tile_to = uniform(t == 0 ? tiles[0].to : tiles[1].to);
-    if (first < last) {
-      constexpr uint32_t fmt = BF16 ? 1u : 0u;
-      // fp32 accumulator, M = 128; scores: both operands K-major, N = 128;
-      // outputs: the values MN-major (bit 16), N = DP
-      constexpr uint32_t i_s = (1u << 4) | (fmt << 7) | (fmt << 10) | ((kTile >> 3) << 17) | ((kTile >> 4) << 24);
-      constexpr uint32_t i_o =
-          (1u << 4) | (fmt << 7) | (fmt << 10) | (1u << 16) | ((DP >> 3) << 17) | ((kTile >> 4) << 24);
-      const uint32_t s_to = tmem + t * kTile, o_to = tmem + C::kOAt + t * 128;
-      const uint64_t q_desc = ptx::sdesc(q_at(t), 16, 1024);
-      const bool leader = elect_one();
-      uint32_t turn = 0;
-      Ring<C::kKeys> rk;
-      Ring<C::kValues> rv;
-      bool ok = tile_from >= tile_to || wait_warp(q_full(t), 0, p, 1);
-      // (the first tile's first turn needs no word of the second)
-      uint32_t mine = t == 0 ? 1u : 0u;
-      for (int j = first - 1; ok && j < last; ++j, mine ^= 1u) {
+    const uint32_t s_to = tmem + t * kTile, o_to = tmem + C::kOAt + t * 128;
+    const uint64_t q_desc = ptx::sdesc(q_at(t), 16, 1024);
+    const bool leader = elect_one();
+    uint32_t turn = 0, q_turn = 0;
+    Ring<C::kKeys> rk;
+    Ring<C::kValues> rv;
+    // (the first tile's first turn needs no word of the second)
+    uint32_t mine = t == 0 ? 1u : 0u;
+    bool ok = true;
+    for (; ok && (ok = job_there(1)) && job_read(); job_done()) {
+      const Tiles tiles(p, job);
+      const int first = uniform(tiles.from), last = uniform(tiles.to);
+      const int tile_from = uniform(tiles[t].from), tile_to = uniform(tiles[t].to);
+      const int all_from = uniform(tiles[t].all_from), all_to = uniform(tiles[t].all_to);
+      if (tile_from < tile_to) {
+        if (!(ok = wait_warp(q_full(t), q_turn, p, 1))) break;
+        q_turn ^= 1u;
+      }
+      for (int j = first - 1; first < last && j < last; ++j, mine ^= 1u) {
         // the product of step j with the values, then the scores of step j + 1
         const bool begun = j >= first, product = begun && j >= tile_from && j < tile_to;
         const bool scores = j + 1 >= tile_from && j + 1 < tile_to, keys_too = j + 1 < last;
         {
-          const bool a = !begun || ptx::mbar_try_wait(v_full(rv.s), rv.ph);
-          const bool b = !begun || ptx::mbar_try_wait(v_ok(rv.s), rv.ph);
-          const bool c = !keys_too || ptx::mbar_try_wait(k_full(rk.s), rk.ph);
-          ok = __all_sync(0xFFFFFFFFu, a && b && c) ||
+          const bool x = !begun || ptx::mbar_try_wait(v_full(rv.s), rv.ph);
+          const bool y = !begun || ptx::mbar_try_wait(v_ok(rv.s), rv.ph);
+          const bool z = !keys_too || ptx::mbar_try_wait(k_full(rk.s), rk.ph);
+          ok = __all_sync(0xFFFFFFFFu, x && y && z) ||
                ((!begun || (wait_warp(v_full(rv.s), rv.ph, p, 1) && wait_warp(v_ok(rv.s), rv.ph, p, 1))) &&
                 (!keys_too || wait_warp(k_full(rk.s), rk.ph, p, 1)));
         }
@@ -482,18 +633,24 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const uint64_t k_desc = ptx::sdesc(k_at(rk.s), 16, 1024), v_desc = ptx::sdesc(v_at(rv.s), kTile * 128, 1024);
         ptx::tc_fence_after();
         if (product) {
-          const bool issue = leader && !by_rows(rv.s);
+          const bool issue = leader && ((j >= all_from && j < all_to) || wild[rv.s] == 0);
           const uint32_t more = j != tile_from ? 1u : 0u;
           if (issue) {
 #pragma unroll
-            for (int k = 0; k < kEarly / 16; ++k) mma_ts(o_to, s_to + k * 8, v_desc + k * 128, i_o, k != 0 ? 1u : more);
+            for (int n = 0; n < kEarly / 16; ++n) {
+              const int k = (n + 4) % 8;  // (the second half of the keys comes first)
+              mma_ts(o_to, s_to + weights_at(k), v_desc + k * 128, i_o, n != 0 ? 1u : more);
+            }
           }
           if (!(ok = wait_warp(w_full(t), turn, p, 1))) break;
           turn ^= 1u;
           ptx::tc_fence_after();
           if (issue) {
 #pragma unroll
-            for (int k = kEarly / 16; k < kTile / 16; ++k) mma_ts(o_to, s_to + k * 8, v_desc + k * 128, i_o, 1u);
+            for (int n = kEarly / 16; n < kTile / 16; ++n) {
+              const int k = (n + 4) % 8;
+              mma_ts(o_to, s_to + weights_at(k), v_desc + k * 128, i_o, 1u);
+            }
           }
         }
         if (leader) {
@@ -504,182 +661,230 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
               ptx::mma_f16(s_to, q_desc + step, k_desc + step, i_s, k != 0 ? 1u : 0u);
             }
             ptx::mma_commit(s_full(t));
+            if (j + 2 == tile_to) ptx::mma_commit(q_empty(t));
           } else if (product) {
             ptx::mma_commit(o_full(t));
           }
           ptx::mbar_arrive(go(1 - t));
           if (begun) ptx::mma_commit(empty(rv.s));
         }
-        rk.next();
+        if (keys_too) rk.next();
         if (begun) rv.next();
       }
-      // Every product of this warp is complete before tensor memory goes back.
-      if (leader) {
-        ptx::mma_commit(drain);
-        wait_out(drain, 0, p, 1);
-      }
+    }
+    // Every product of this warp is complete before tensor memory goes back.
+    if (leader) {
+      ptx::mma_commit(drain);
+      wait_out(drain, 0, p, 1);
     }
     __syncwarp();
   } else if (warp == kLook) {
     // ----------------------------------------------- values that are hidden
-        for (int j = from; j < to; ++j) {
-      const int n = j - from, s = v_stage(n);
-      if (!wait_warp(v_full(s), v_phase(n), p, 3)) break;
-      uint32_t most = 0;  // magnitudes as integers, two halves
-      if ((tiles[0].active(j) && tiles[0].masked(j)) || (tiles[1].active(j) && tiles[1].masked(j))) {
-        const int count = min(kTile, keys - j * kTile);
-        for (int x = 0; x < DP; x += 64) {
-          const uint32_t at = v_at(s) + x * (kTile * 2) + lane * 16;  // 4 rows at a time
+    Ring<C::kValues> rv;
+    bool ok = true;
+    for (; ok && (ok = job_there(3)) && job_read(); job_done()) {
+      const Tiles tiles(p, job);
+      for (int j = tiles.from; j < tiles.to; ++j, rv.next()) {
+        if (!(ok = wait_warp(v_full(rv.s), rv.ph, p, 3))) break;
+        uint32_t most = 0;  // magnitudes as integers, two halves
+        if (tiles.t0.masked(j) || tiles.t1.masked(j)) {
+          const int count = min(kTile, job.keys - j * kTile);
+          for (int x = 0; x < DP; x += 64) {
+            const uint32_t at = v_at(rv.s) + x * (kTile * 2) + lane * 16;  // 4 rows at a time
 #pragma unroll 8
-          for (int r = lane >> 3; r < count; r += 4) {
-            uint32_t v[4];
-            asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                         : "r"(at + (r >> 2) * 512));
+            for (int r = lane >> 3; r < count; r += 4) {
+              uint32_t v[4];
+              asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                           : "r"(at + (r >> 2) * 512));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) most = __vmaxu2(most, v[i] & 0x7FFF7FFFu);
+              for (int i = 0; i < 4; ++i) most = __vmaxu2(most, v[i] & 0x7FFF7FFFu);
+            }
+            if (count < kTile)
+              for (int r = count + (((lane >> 3) - count) & 3); r < kTile; r += 4)
+                asm volatile("st.volatile.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + (r >> 2) * 512), "r"(0u)
+                             : "memory");
           }
-          if (count < kTile)
-            for (int r = count + ((lane >> 3) - count & 3); r < kTile; r += 4)
-              asm volatile("st.volatile.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + (r >> 2) * 512), "r"(0u)
-                           : "memory");
+          ptx::fence_proxy_async_smem();
         }
-        ptx::fence_proxy_async_smem();
-      }
-      constexpr uint32_t kInf = BF16 ? 0x7F80u : 0x7C00u;
-      const bool any = __any_sync(0xFFFFFFFFu, (most & 0xFFFFu) >= kInf || (most >> 16) >= kInf);
-      if (lane == 0) {
-        wild[s] = any ? 1 : 0;
-        ptx::mbar_arrive(v_ok(s));
+        constexpr uint32_t kInf = BF16 ? 0x7F80u : 0x7C00u;
+        const bool any = __any_sync(0xFFFFFFFFu, (most & 0xFFFFu) >= kInf || (most >> 16) >= kInf);
+        if (lane == 0) {
+          wild[rv.s] = any ? 1 : 0;
+          ptx::mbar_arrive(v_ok(rv.s));
+        }
       }
     }
   } else {
     // ---------------------------------------------------------- weights
     const int t = (warp - kWeights) >> 2, row = (warp & 3) * 32 + lane;  // row of the tile
-    const Tile tile = t == 0 ? tiles[0] : tiles[1];
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + t * kTile, o_at = tmem + lanes + C::kOAt + t * 128;
-    const int at = keys - queries + row0 + t * kTile + row;
-    const int lo = key_begin(p, at), hi = key_end(p, at, keys);
     const float to_log2 = p.scale * kLog2e;
-    const uint64_t to_log2_2 = pair(to_log2, to_log2);
     constexpr float kLift = BF16 ? 0.0f : 6.0f;
-    float ref = -INFINITY, sum = 0.0f;
-    uint32_t turn = 0;
+    uint32_t turn = 0, o_turn = 0;
     bool ok = true;
-    for (int j = tile.from; j < tile.to; ++j, ++turn) {
-      if (!(ok = wait_warp(s_full(t), turn & 1u, p, 2))) break;
-      ptx::tc_fence_after();
-      uint32_t s[4][32];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) ptx::tmem_ld_32x32b_x32(s_at + i * 32, s[i]);
-      ptx::tmem_wait_ld();
-#pragma unroll
-      for (int i = 0; i < 4; ++i) ptx::tmem_regs_ready(s[i]);
-      const int key_lo = lo - j * kTile, key_hi = hi - j * kTile;
-      if (tile.masked(j)) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (i * 32 + c < key_lo || i * 32 + c >= key_hi) s[i][c] = 0xFF800000u;  // -inf
-      }
-      float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int c = 0; c < 32; c += 2)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) m[i] = max3(m[i], __uint_as_float(s[i][c]), __uint_as_float(s[i][c + 1]));
-      const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * to_log2;
-      if (__any_sync(0xFFFFFFFFu, most > ref + kSlack)) {
-        const float next = most > ref + kSlack ? most : ref;
-        const float f = next == -INFINITY ? 1.0f : exp2_fast(ref - next);
-        ref = next;
-        sum *= f;
-        if (j != tile.from) {
-          // (the scores of this step are there, so the product before them is done)
-#pragma unroll 1
-          for (int d = 0; d < DP; d += 8) {
-            uint32_t o[8];
-            tmem_ld_x8(o_at + d, o);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tmem_st_x8(o_at + d, o);
-          }
-        }
-      }
-      const float less = ref == -INFINITY ? 0.0f : kLift - ref;
-      const uint64_t less2 = pair(less, less);
-      uint64_t sum2[2] = {pair(sum, 0.0f), pair(0.0f, 0.0f)};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t w[16];
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          float x, y;
-          unpair(fma2(pair(__uint_as_float(s[i][2 * c]), __uint_as_float(s[i][2 * c + 1])), to_log2_2, less2), x, y);
-          x = exp2_fast(x);
-          y = exp2_fast(y);
-          sum2[c & 1] = add2(sum2[c & 1], pair(x, y));
-          w[c] = pack2<BF16>(x, y);
-        }
-        tmem_st_x16(s_at + i * 16, w);
-        if (i == kEarly / 32 - 1) {  // the product with the first values may begin
-          tmem_wait_st();
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(w_early(t));
-        }
-      }
-      tmem_wait_st();
+    // (What a step seldom needs of its job is read again there: registers are short.)
+    auto keys_seen = [&](int j, int& lo, int& hi) {  // of step j by this row
+      const volatile Job& of = jobs[number & 1];
+      const int keys = of.keys, at = keys - of.queries + of.row0 + t * kTile + row;
+      lo = key_begin(p, at) - j * kTile, hi = key_end(p, at, keys) - j * kTile;
+    };
+    int ahead = 0;  // value tiles before step 0 of the job
+    for (; ok && (ok = job_there(2)) && job_read(); job_done()) {
+      int tile_from, tile_to, all_from, all_to;
       {
-        float x, y;
-        unpair(add2(sum2[0], sum2[1]), x, y);
-        sum = x + y;
+        const Tiles tiles(p, job);
+        ahead -= tiles.from;
+        tile_from = tiles[t].from, tile_to = tiles[t].to, all_from = tiles[t].all_from, all_to = tiles[t].all_to;
       }
-      if ((tiles[0].active(j) && tiles[0].masked(j)) || (tiles[1].active(j) && tiles[1].masked(j))) {
-        const int n = j - from, st = v_stage(n);
-        if (!(ok = wait_warp(v_full(st), v_phase(n), p, 2) && wait_warp(v_ok(st), v_phase(n), p, 2))) break;
-        if (by_rows(st)) {
-          product_by_rows<BF16, DP>(s_at, o_at, v_at(st), key_lo, key_hi, j == tile.from);
-          ptx::fence_proxy_async_smem();
-        }
-      }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(w_full(t));
-    }
-    // outputs: a row a thread
-    if (tile.rows > 0 && ok) {
-      const bool any = tile.from < tile.to;
-      if (any) ok = wait_warp(o_full(t), 0, p, 2);
-      if (ok) {
+      float ref = -INFINITY, sum = 0.0f;
+      for (int j = tile_from; j < tile_to; ++j) {
+        if (!(ok = wait_warp(s_full(t), turn, p, 2))) break;
+        turn ^= 1u;
         ptx::tc_fence_after();
-        const bool mine = row < tile.rows;
-        const long long token = static_cast<long long>(q0) + row0 + t * kTile + row;
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        uint16_t* const out = p.out.p + token * p.out.ld + head * p.out.hs;
-#pragma unroll 1
-        for (int d = 0; d < DP; d += 32) {
-          uint32_t o[32];
-          if (any) {
-            ptx::tmem_ld_32x32b_x32(o_at + d, o);
-            ptx::tmem_wait_ld();
-            ptx::tmem_regs_ready(o);
+        // The scores in chunks of 32 keys: all for the maximum, then again, the last
+        // two first (they are still here), for the weights. Held at once they do not
+        // fit a thread's registers.
+        uint32_t s[2][32];
+        int lo = 0, hi = kTile;
+        if (j >= all_to || j < all_from) keys_seen(j, lo, hi);
+        auto chunk = [&](uint32_t (&x)[32], int c) {  // arrived: keys 32 c on
+          ptx::tmem_regs_ready(x);
+          if (j >= all_to) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * c + i >= hi) x[i] = 0xFF800000u;  // -inf
           }
+          if (j < all_from) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t w[4] = {0, 0, 0, 0};
+            for (int i = 0; i < 32; ++i)
+              if (32 * c + i < lo) x[i] = 0xFF800000u;
+          }
+        };
+        float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (sum != 0.0f)
-                w[e] = pack2<BF16>(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
-            if (mine && d + 8 * i < p.dim)
-              *reinterpret_cast<uint4*>(out + d + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int h = 0; h < 2; ++h) {
+          ptx::tmem_ld_32x32b_x32(s_at + h * 64, s[0]);
+          ptx::tmem_ld_32x32b_x32(s_at + h * 64 + 32, s[1]);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            chunk(s[i], 2 * h + i);
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+              m[2 * i] = max3(m[2 * i], __uint_as_float(s[i][c]), __uint_as_float(s[i][c + 1]));
+              m[2 * i + 1] = max3(m[2 * i + 1], __uint_as_float(s[i][c + 2]), __uint_as_float(s[i][c + 3]));
+            }
           }
         }
-        if (mine && p.lse)
-          p.lse[token * p.heads + head] = sum == 0.0f ? -INFINITY : (ref - kLift + log2f(sum)) * kLn2;
+        const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * to_log2;
+        if (__any_sync(0xFFFFFFFFu, most > ref + kSlack)) {
+          const float next = most > ref + kSlack ? most : ref;
+          const float f = next == -INFINITY ? 1.0f : exp2_fast(ref - next);
+          ref = next;
+          sum *= f;
+          if (j != tile_from) {
+            // (the scores of this step are there, so the product before them is done)
+#pragma unroll 1
+            for (int d = 0; d < DP; d += 8) {
+              uint32_t o[8];
+              tmem_ld_x8(o_at + d, o);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st_x8(o_at + d, o);
+            }
+          }
+        }
+        const uint64_t to_log2_2 = pair(to_log2, to_log2);
+        const float less = ref == -INFINITY ? 0.0f : kLift - ref;
+        const uint64_t less2 = pair(less, less);
+        uint64_t sum2[2] = {pair(sum, 0.0f), pair(0.0f, 0.0f)};
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int i = (n + 2) & 3;  // chunk
+          uint32_t (&x)[32] = s[i & 1];
+          if (n >= 2) {
+            ptx::tmem_wait_ld();
+            chunk(x, i);
+          }
+          uint32_t w[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            float u, v;
+            unpair(fma2(pair(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), to_log2_2, less2), u, v);
+            u = exp2_fast(u);
+            v = exp2_fast(v);
+            sum2[c & 1] = add2(sum2[c & 1], pair(u, v));
+            w[c] = pack2<BF16>(u, v);
+          }
+          if (n < 2) ptx::tmem_ld_32x32b_x32(s_at + (i & 1) * 32, x);
+          tmem_st_x16(s_at + i * 32, w);  // over its own scores
+          if (n == kEarly / 32 - 1) {  // the product with these values may begin
+            tmem_wait_st();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(w_early(t));
+          }
+        }
+        tmem_wait_st();
+        {
+          float x, y;
+          unpair(add2(sum2[0], sum2[1]), x, y);
+          sum = x + y;
+        }
+        if (j < all_from || j >= all_to) {
+          const int n = ahead + j, st = n % C::kValues;
+          const uint32_t ph = (n / C::kValues) & 1u;
+          if (!(ok = wait_warp(v_full(st), ph, p, 2) && wait_warp(v_ok(st), ph, p, 2))) break;
+          if (wild[st] != 0) {
+            product_by_rows<BF16, DP>(s_at, o_at, v_at(st), lo, hi, j == tile_from);
+            ptx::fence_proxy_async_smem();
+          }
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(w_full(t));
       }
+      // outputs: a row a thread
+      if (!ok) break;
+      const bool any = tile_from < tile_to;
+      if (any) {
+        if (!(ok = wait_warp(o_full(t), o_turn, p, 2))) break;
+        o_turn ^= 1u;
+        ptx::tc_fence_after();
+      }
+      job_read();
+      ahead += Tiles(p, job).to;
+      const int head = job.head, at = job.row0 + t * kTile + row;
+      const bool mine = at < job.queries;
+      const long long token = static_cast<long long>(job.q0) + at;
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      uint16_t* const out = p.out.p + token * p.out.ld + head * p.out.hs;
+#pragma unroll 1
+      for (int d = 0; d < DP; d += 32) {
+        uint32_t o[32], w[16];
+        if (any) {
+          ptx::tmem_ld_32x32b_x32(o_at + d, o);
+          ptx::tmem_wait_ld();
+          ptx::tmem_regs_ready(o);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          w[i] = sum == 0.0f ? 0u : pack2<BF16>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+        if (mine && a.wide) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (d + 16 * i < p.dim) store32(out + d + 16 * i, &w[8 * i]);
+        } else if (mine) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (d + 8 * i < p.dim)
+              *reinterpret_cast<uint4*>(out + d + 8 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+        __syncwarp();
+      }
+      if (mine && p.lse) p.lse[token * p.heads + head] = sum == 0.0f ? -INFINITY : (ref - kLift + log2f(sum)) * kLn2;
     }
   }
   ptx::tc_fence_before();
@@ -719,6 +924,7 @@ cudaError_t launch_prompt(const PromptParams& p, int num_sms, cudaStream_t strea
   Args a;
   a.p = p;
   a.slots = static_cast<int>(p.tokens / kRows) + p.seqs;
+  a.wide = reinterpret_cast<uintptr_t>(p.out.p) % 32 == 0 && p.out.ld % 16 == 0 && p.out.hs % 16 == 0 && p.dim % 16 == 0;
   if (!encode(&a.q, p.q, p.tokens, p.heads, p.dim, p.is_bf16)) return cudaErrorInvalidValue;
   if (p.k_tokens == 0) {  // nothing is loaded
     a.k = a.v = a.q;
