@@ -193,6 +193,11 @@ __device__ __forceinline__ bool elect_one() {
 // A value that is the same in all lanes, known as such to the compiler.
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 
+template <bool V>
+struct Constant {
+  static constexpr bool value = V;
+};
+
 // A ring position: stage and phase parity.
 template <int N>
 struct Ring {
@@ -739,45 +744,36 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         tile_from = tiles[t].from, tile_to = tiles[t].to, all_from = tiles[t].all_from, all_to = tiles[t].all_to;
       }
       float ref = -INFINITY, sum = 0.0f;
-      for (int j = tile_from; j < tile_to; ++j) {
-        if (!(ok = wait_warp(s_full(t), turn, p, 2))) break;
+      // One step; MASKED: not every row sees every key. (Two copies of the code: the
+      // one that runs again and again stays short enough for the instruction cache.)
+      auto step = [&](auto masked, int j) {
+        constexpr bool MASKED = decltype(masked)::value;
+        if (!(ok = wait_warp(s_full(t), turn, p, 2))) return;
         turn ^= 1u;
         ptx::tc_fence_after();
-        // The scores in chunks of 32 keys: all for the maximum, then again, the last
-        // two first (they are still here), for the weights. Held at once they do not
-        // fit a thread's registers.
-        uint32_t s[2][32];
+        // The scores in chunks of 32 keys, all for the maximum. For the weights they do
+        // not fit a thread's registers together: chunk 1 comes last, read again.
+        uint32_t s[4][32];
         int lo = 0, hi = kTile;
-        if (j >= all_to || j < all_from) keys_seen(j, lo, hi);
+        if (MASKED) keys_seen(j, lo, hi);
         auto chunk = [&](uint32_t (&x)[32], int c) {  // arrived: keys 32 c on
           ptx::tmem_regs_ready(x);
-          if (j >= all_to) {
+          if (MASKED) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (32 * c + i >= hi) x[i] = 0xFF800000u;  // -inf
-          }
-          if (j < all_from) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * c + i < lo) x[i] = 0xFF800000u;
+              if (32 * c + i < lo || 32 * c + i >= hi) x[i] = 0xFF800000u;  // -inf
           }
         };
         float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          ptx::tmem_ld_32x32b_x32(s_at + h * 64, s[0]);
-          ptx::tmem_ld_32x32b_x32(s_at + h * 64 + 32, s[1]);
-          ptx::tmem_wait_ld();
+        for (int i = 0; i < 4; ++i) ptx::tmem_ld_32x32b_x32(s_at + i * 32, s[i]);
+        ptx::tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            chunk(s[i], 2 * h + i);
+        for (int i = 0; i < 4; ++i) chunk(s[i], i);
 #pragma unroll
-            for (int c = 0; c < 32; c += 4) {
-              m[2 * i] = max3(m[2 * i], __uint_as_float(s[i][c]), __uint_as_float(s[i][c + 1]));
-              m[2 * i + 1] = max3(m[2 * i + 1], __uint_as_float(s[i][c + 2]), __uint_as_float(s[i][c + 3]));
-            }
-          }
-        }
+        for (int c = 0; c < 32; c += 2)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) m[i] = max3(m[i], __uint_as_float(s[i][c]), __uint_as_float(s[i][c + 1]));
         const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * to_log2;
         if (__any_sync(0xFFFFFFFFu, most > ref + kSlack)) {
           const float next = most > ref + kSlack ? most : ref;
@@ -803,10 +799,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
           const int i = (n + 2) & 3;  // chunk
-          uint32_t (&x)[32] = s[i & 1];
-          if (n >= 2) {
+          uint32_t (&x)[32] = s[n == 3 ? 2 : i];
+          if (n == 3) {
             ptx::tmem_wait_ld();
-            chunk(x, i);
+            chunk(x, 1);
           }
           uint32_t w[16];
 #pragma unroll
@@ -818,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             sum2[c & 1] = add2(sum2[c & 1], pair(u, v));
             w[c] = pack2<BF16>(u, v);
           }
-          if (n < 2) ptx::tmem_ld_32x32b_x32(s_at + (i & 1) * 32, x);
+          if (n == 0) ptx::tmem_ld_32x32b_x32(s_at + 32, x);
           tmem_st_x16(s_at + i * 32, w);  // over its own scores
           if (n == kEarly / 32 - 1) {  // the product with these values may begin
             tmem_wait_st();
@@ -833,10 +829,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           unpair(add2(sum2[0], sum2[1]), x, y);
           sum = x + y;
         }
-        if (j < all_from || j >= all_to) {
+        if (MASKED) {
           const int n = ahead + j, st = n % C::kValues;
           const uint32_t ph = (n / C::kValues) & 1u;
-          if (!(ok = wait_warp(v_full(st), ph, p, 2) && wait_warp(v_ok(st), ph, p, 2))) break;
+          if (!(ok = wait_warp(v_full(st), ph, p, 2) && wait_warp(v_ok(st), ph, p, 2))) return;
           if (wild[st] != 0) {
             product_by_rows<BF16, DP>(s_at, o_at, v_at(st), lo, hi, j == tile_from);
             ptx::fence_proxy_async_smem();
@@ -845,6 +841,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(w_full(t));
+      };
+      for (int j = tile_from; ok && j < tile_to; ++j) {
+        if (j >= all_from && j < all_to)
+          step(Constant<false>{}, j);
+        else
+          step(Constant<true>{}, j);
       }
       // outputs: a row a thread
       if (!ok) break;

@@ -445,6 +445,23 @@ def test_prompt_bad_starts_stay_inside():
     assert fgemm.default_handle().get_error() == fgemm.OK
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+def test_prompt_many_jobs_a_cta(dim):
+    """More rows than the SMs hold at once, of sequences of very different
+    lengths, right behind work that has emptied the caches: no wait runs out."""
+    lengths = [700, 0, 3, 900, 130, 1, 257, 0, 400, 2100]
+    q, k, v, starts, _ = prompt_inputs(gen(19), lengths, lengths, 32, 8, dim, torch.bfloat16)
+    for _ in range(3):
+        torch.zeros(1 << 27, device=DEV)
+        out, lse = fgemm.attention(q, k, v, ints(starts))
+    torch.cuda.synchronize()
+    assert fgemm.default_handle().get_error() == fgemm.OK
+    few = torch.tensor([0, 13, 31], device=DEV)  # heads that are looked at
+    for h in few.tolist():
+        check_prompt(q[:, h:h + 1], k[:, h // 4:h // 4 + 1], v[:, h // 4:h // 4 + 1], starts, starts, True, 0,
+                     out[:, h:h + 1], lse[:, h:h + 1], what="prompt jobs")
+
+
 def test_prompt_in_a_graph_and_on_two_streams():
     lengths = [300, 77]
     q, k, v, starts, _ = prompt_inputs(gen(18), lengths, lengths, 4, 2, 128, torch.bfloat16)
