@@ -7,9 +7,9 @@
 // One entry at m stays out of the sum: with log(1 + r) what is left to the other
 // tokens keeps its bits beside a probability near 1.
 //
-// One pass over the row: a thread takes 64 bytes at a time, follows the largest
-// value with its sums relative to it (they are scaled when a batch brings a larger
-// one), and the threads' sums meet at the row's end. d is held to -200 and above:
+// One pass over the row: a warp takes 2 KB at a time, follows the largest value with
+// its lanes' sums relative to it (they are scaled when a batch brings a larger one),
+// and the warps' sums meet at the row's end. d is held to -200 and above:
 // that leaves e^d 0 and the product with d too, for masked logits and NaN alike.
 //
 // The most probable tokens: the n-th largest of the threads' maxima is a value that
@@ -157,83 +157,133 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// A batch of vectors into the thread's sums.
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 template <int TYPE>
-__device__ __forceinline__ void add_batch(Part& s, const uint4 (&v)[kDeep]) {
+__device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b) {  // a number before a NaN
+  if (TYPE == 2) return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  if (TYPE == 1) {
+    const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  }
+  const __half2 m = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+
+// A warp's sums of what it has seen: the largest value m is the warp's, r and t are
+// a lane's share, without one entry at m (a lane has left it out).
+struct Running {
+  float m, r, t;
+  float mine;  // the lane's largest
+};
+
+// A batch of vectors of each lane of a warp. The lanes go the same ways: a branch
+// by a lane's own maximum was taken by some lane in nearly every batch.
+template <int TYPE>
+__device__ __forceinline__ void add_batch(Running& s, uint4 (&v)[kDeep]) {
   using R = Row<TYPE>;
-  float most = -INFINITY;
+  uint32_t w = v[0].x;
 #pragma unroll
-  for (int n = 0; n < kDeep; ++n)
+  for (int n = 0; n < kDeep; ++n) {
+    w = max_word<TYPE>(w, max_word<TYPE>(v[n].x, v[n].y));
+    w = max_word<TYPE>(w, max_word<TYPE>(v[n].z, v[n].w));
+  }
+  const float most = TYPE == 2 ? fmaxf(-INFINITY, __uint_as_float(w))
+                               : fmaxf(fmaxf(-INFINITY, lo_f32<TYPE == 1>(w)), hi_f32<TYPE == 1>(w));
+  s.mine = fmaxf(s.mine, most);
+  const bool above = most > s.m;
+  if (__any_sync(0xFFFFFFFFu, above)) {
+    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, most > -INFINITY ? ordered(most) : 0u);
+    const float m = __uint_as_float(top & 0x80000000u ? top & 0x7FFFFFFFu : ~top);
+    if (s.m > -INFINITY) {
+      const float d = s.m - m, f = exp2_fast(fmaxf(d, -200.0f) * kLog2e);
+      if ((threadIdx.x & 31) == 0) s.r += 1.0f;  // the entry at the old m counts now
+      s.t = f > 0.0f ? f * (s.t + d * s.r) : 0.0f;
+      s.r *= f;
+    }
+    s.m = m;
+    // one lane leaves out one entry at m
+    const uint32_t has = __ballot_sync(0xFFFFFFFFu, most == m);
+    if ((threadIdx.x & 31) == __ffs(has) - 1) {
+      bool out = false;
 #pragma unroll
-    for (int k = 0; k < R::kVec; ++k) most = fmaxf(most, R::elem(v[n], k));
-  if (most > s.m) {
-    // Sums go to the new largest value, which is among these logits: its entries
-    // are counted, one of them not.
-    const Part before = s;
-    s = Part{most, 0.0f, 0.0f};
-    s = join(s, before);
-    float count = 0.0f;
+      for (int n = 0; n < kDeep; ++n) {
+        uint32_t x[4] = {v[n].x, v[n].y, v[n].z, v[n].w};
 #pragma unroll
-    for (int n = 0; n < kDeep; ++n)
-#pragma unroll
-      for (int k = 0; k < R::kVec; ++k) {
-        const float x = R::elem(v[n], k);
-        const float d = fmaxf(x - most, -200.0f);
-        const float w = x == most ? 0.0f : exp2_fast(d * kLog2e);
-        count += x == most ? 1.0f : 0.0f;
-        s.r += w;
-        s.t = fmaf(w, d, s.t);
+        for (int k = 0; k < 4; ++k) {
+          if (TYPE == 2) {
+            const bool hit = !out && __uint_as_float(x[k]) == m;
+            x[k] = hit ? 0xFF800000u : x[k];
+            out |= hit;
+          } else {
+            constexpr uint32_t kLow = TYPE == 1 ? 0xFF80u : 0xFC00u;
+            const bool lo = !out && lo_f32<TYPE == 1>(x[k]) == m;
+            x[k] = lo ? (x[k] & 0xFFFF0000u) | kLow : x[k];
+            out |= lo;
+            const bool hi = !out && hi_f32<TYPE == 1>(x[k]) == m;
+            x[k] = hi ? (x[k] & 0xFFFFu) | kLow << 16 : x[k];
+            out |= hi;
+          }
+        }
+        v[n] = make_uint4(x[0], x[1], x[2], x[3]);
       }
-    s.r += count - 1.0f;
-  } else if (s.m == INFINITY) {
+    }
+    __syncwarp();
+  }
+  if (s.m == -INFINITY) return;
+  if (s.m == INFINITY) {
 #pragma unroll
     for (int n = 0; n < kDeep; ++n)
 #pragma unroll
       for (int k = 0; k < R::kVec; ++k) s.r += R::elem(v[n], k) == INFINITY ? 1.0f : 0.0f;
-  } else if (s.m > -INFINITY) {
-    const uint64_t less = pair(-s.m, -s.m);
-    uint64_t r2 = pair(0.0f, 0.0f), t2 = pair(0.0f, 0.0f);
-#pragma unroll
-    for (int n = 0; n < kDeep; ++n)
-#pragma unroll
-      for (int k = 0; k < R::kVec; k += 2) {
-        float d0, d1;
-        unpair(add2(pair(R::elem(v[n], k), R::elem(v[n], k + 1)), less), d0, d1);
-        d0 = fmaxf(d0, -200.0f);
-        d1 = fmaxf(d1, -200.0f);
-        const uint64_t w = pair(exp2_fast(d0 * kLog2e), exp2_fast(d1 * kLog2e));
-        r2 = add2(r2, w);
-        t2 = fma2(w, pair(d0, d1), t2);
-      }
-    float a, b;
-    unpair(r2, a, b);
-    s.r += a + b;
-    unpair(t2, a, b);
-    s.t += a + b;
+    return;
   }
+  const uint64_t less = pair(-s.m, -s.m), log2e = pair(kLog2e, kLog2e);
+  uint64_t r2 = pair(s.r, 0.0f), t2 = pair(s.t, 0.0f);
+#pragma unroll
+  for (int n = 0; n < kDeep; ++n)
+#pragma unroll
+    for (int k = 0; k < R::kVec; k += 2) {
+      float d0, d1, e0, e1;
+      unpair(add2(pair(R::elem(v[n], k), R::elem(v[n], k + 1)), less), d0, d1);
+      const uint64_t d = pair(fmaxf(d0, -200.0f), fmaxf(d1, -200.0f));
+      unpair(mul2(d, log2e), e0, e1);
+      const uint64_t w2 = pair(exp2_fast(e0), exp2_fast(e1));
+      r2 = add2(r2, w2);
+      t2 = fma2(w2, d, t2);
+    }
+  float a, b;
+  unpair(r2, a, b);
+  s.r = a + b;
+  unpair(t2, a, b);
+  s.t = a + b;
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t at) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster_f32(uint32_t at, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
 }
-__device__ __forceinline__ Key ld_cluster_key(uint32_t at) {
-  Key v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(at) : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster_key(uint32_t at, Key v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // A CTA of a cluster of `split` takes a part of row blockIdx.x / split.
 template <int TYPE>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __grid_constant__ LogprobParams p,
                                                                         int split) {
   using R = Row<TYPE>;
-  __shared__ Key list[kList];
+  __shared__ __align__(16) Key list[kList];
+  __shared__ __align__(16) Key theirs[kMostSplit * kMostTop];  // first CTA: every CTA's first tokens
   __shared__ Key sorted[kMostTop];
   __shared__ Key best[kWarps];
   __shared__ Part parts[kWarps];
-  __shared__ float sums[3];
+  __shared__ uint32_t least[kWarps], largest[kWarps];
+  __shared__ float sums[kMostSplit][3];  // first CTA: every CTA's
   __shared__ int listed;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = split > 1 ? static_cast<int>(ptx::cluster_ctarank()) : 0;
@@ -241,57 +291,85 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
   const R x(p, row);
   const int each = (x.vectors + split - 1) / split;
   const int v0 = min(x.vectors, rank * each), v1 = min(x.vectors, v0 + each);
+  if (split > 1) cluster_arrive();  // this CTA is there
   const int token = rank == 0 && threadIdx.x == 0 ? p.tokens[row] : 0;
   const float given = rank == 0 && threadIdx.x == 0 && token >= 0 && token < p.vocab ? x.one(token) : -INFINITY;
 
-  Part s{-INFINITY, 0.0f, 0.0f};
-  for (int v = v0 + threadIdx.x; v < v1; v += kThreads * kDeep) {
-    uint4 batch[kDeep];
+  // A warp takes kDeep x 32 vectors in a row; the next ones are on their way.
+  constexpr int kChunk = kDeep * 32;
+  auto fetch = [&](uint4 (&batch)[kDeep], int v) {
+    const int end = v + kChunk;  // (the same for the lanes: the warp's first vector)
+    if (end <= v1 && v * R::kVec >= x.skip && end * R::kVec <= x.skip + x.vocab) {
 #pragma unroll
-    for (int n = 0; n < kDeep; ++n) batch[n] = v + n * kThreads < v1 ? x.load(v + n * kThreads) : R::none();
-    add_batch<TYPE>(s, batch);
+      for (int n = 0; n < kDeep; ++n) batch[n] = reinterpret_cast<const uint4*>(x.base)[v + n * 32 + lane];
+    } else {
+#pragma unroll
+      for (int n = 0; n < kDeep; ++n) batch[n] = v + n * 32 + lane < v1 ? x.load(v + n * 32 + lane) : R::none();
+    }
+  };
+  Running seen{-INFINITY, 0.0f, 0.0f, -INFINITY};
+  {
+    uint4 batch[kDeep], next[kDeep];
+    int v = v0 + warp * kChunk;
+    if (v < v1) fetch(batch, v);
+    while (v < v1) {
+      v += kThreads * kDeep;
+      if (v < v1) fetch(next, v);
+      add_batch<TYPE>(seen, batch);
+#pragma unroll
+      for (int n = 0; n < kDeep; ++n) batch[n] = next[n];
+    }
   }
-  const float mine = s.m;
+  const float mine = seen.mine;
+  Part s{seen.m, seen.r, seen.t};
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1)
-    s = join(s, Part{__shfl_xor_sync(0xFFFFFFFFu, s.m, d), __shfl_xor_sync(0xFFFFFFFFu, s.r, d),
-                     __shfl_xor_sync(0xFFFFFFFFu, s.t, d)});
+  for (int d = 16; d > 0; d >>= 1) {
+    s.r += __shfl_xor_sync(0xFFFFFFFFu, s.r, d);
+    s.t += __shfl_xor_sync(0xFFFFFFFFu, s.t, d);
+  }
+  const int top = p.top;
+  const uint32_t my = mine > -INFINITY ? ordered(mine) : 0u;
   if (lane == 0) parts[warp] = s;
-  if (threadIdx.x == 0) listed = 0;
-  if (threadIdx.x < kMostTop) sorted[threadIdx.x] = 0;
+  if (top > 0) {
+    const uint32_t l = __reduce_min_sync(0xFFFFFFFFu, my), m = __reduce_max_sync(0xFFFFFFFFu, my);
+    if (lane == 0) least[warp] = l, largest[warp] = m;
+    if (threadIdx.x == 0) listed = 0;
+    if (threadIdx.x < kMostTop) sorted[threadIdx.x] = 0;
+  }
   __syncthreads();
 
-  const int top = p.top;
   if (top > 0) {
     // A value that at least `top` threads reach, if so many have one above -inf,
-    // and not many more: keys in [lo, hi), those from lo on are enough.
-    const uint32_t my = mine > -INFINITY ? ordered(mine) : 0u;
-    uint32_t lo = 1u, hi = 0xFFFFFFFFu;
-    if (__syncthreads_count(my >= lo) > top) {
-      while (hi - lo > 1) {
-        const uint32_t mid = lo + (hi - lo) / 2;
-        const int count = __syncthreads_count(my >= mid);
-        if (count < top) {
-          hi = mid;
-        } else {
-          lo = mid;
-          if (count <= 2 * top) break;
-        }
-      }
+    // and not many more: between the least and the largest of the threads'.
+    uint32_t lo = least[0], hi = largest[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) lo = min(lo, least[w]), hi = max(hi, largest[w]);
+    constexpr uint32_t kLowest = 0x00800000u;  // ordered(-FLT_MAX)
+    lo = max(lo, kLowest);
+    hi = max(hi, lo) + 1;
+    int reach = lo > kLowest ? kThreads : __syncthreads_count(my >= lo);
+    while (reach > 2 * top && hi - lo > 1) {
+      const uint32_t mid = lo + (hi - lo) / 2;
+      const int count = __syncthreads_count(my >= mid);
+      if (count < top)
+        hi = mid;
+      else
+        lo = mid, reach = count;
     }
     if (my >= lo) {
-      for (int v = v0 + threadIdx.x; v < v1; v += kThreads * kDeep) {
+      const float from = value_of(static_cast<Key>(lo) << 32);
+      for (int v = v0 + warp * kChunk + lane; v < v1; v += kThreads * kDeep) {
         uint4 batch[kDeep];
 #pragma unroll
-        for (int n = 0; n < kDeep; ++n) batch[n] = v + n * kThreads < v1 ? x.load(v + n * kThreads) : R::none();
+        for (int n = 0; n < kDeep; ++n) batch[n] = v + n * 32 < v1 ? x.load(v + n * 32) : R::none();
 #pragma unroll
         for (int n = 0; n < kDeep; ++n)
 #pragma unroll
           for (int k = 0; k < R::kVec; ++k) {
-            const Key key = key_of(R::elem(batch[n], k), (v + n * kThreads) * R::kVec - x.skip + k);
-            if (static_cast<uint32_t>(key >> 32) >= lo) {
+            const float value = R::elem(batch[n], k);
+            if (value >= from && value > -INFINITY) {
               const int at = atomicAdd(&listed, 1);
-              if (at < kList) list[at] = key;
+              if (at < kList) list[at] = key_of(value, (v + n * 32) * R::kVec - x.skip + k);
             }
           }
       }
@@ -333,43 +411,48 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
     }
   }
 
-  // The CTA's sums, then the cluster's in its first CTA.
+  // The CTA's sums; the cluster's meet in its first CTA, to which the others write.
   if (threadIdx.x == 0) {
     s = parts[0];
     for (int w = 1; w < kWarps; ++w) s = join(s, parts[w]);
-    sums[0] = s.m, sums[1] = s.r, sums[2] = s.t;
+    if (split == 1) sums[0][0] = s.m, sums[0][1] = s.r, sums[0][2] = s.t;
   }
   __syncthreads();
   if (split > 1) {
-    ptx::cluster_sync();
-    if (rank == 0) {
-      if (threadIdx.x == 0) {
-        for (int c = 1; c < split; ++c) {
-          const uint32_t at = ptx::mapa(ptx::smem_u32(sums), c);
-          s = join(s, Part{ld_cluster_f32(at), ld_cluster_f32(at + 4), ld_cluster_f32(at + 8)});
-        }
-        sums[0] = s.m, sums[1] = s.r, sums[2] = s.t;
-      }
-      Key key = 0;  // at most 8 x 32 of them
-      if (top > 0 && threadIdx.x < split * kMostTop) {
-        const uint32_t at = ptx::mapa(ptx::smem_u32(sorted + threadIdx.x % kMostTop), threadIdx.x / kMostTop);
-        key = ld_cluster_key(at);
-      }
-      list[threadIdx.x] = key;
-      __syncthreads();
+    cluster_wait();
+    if (threadIdx.x == 0) {
+      const uint32_t at = ptx::mapa(ptx::smem_u32(sums[rank]), 0);
+      st_cluster_f32(at, s.m);
+      st_cluster_f32(at + 4, s.r);
+      st_cluster_f32(at + 8, s.t);
+    }
+    if (threadIdx.x < top) st_cluster_key(ptx::mapa(ptx::smem_u32(theirs + rank * top + threadIdx.x), 0), sorted[threadIdx.x]);
+    __syncwarp();
+    cluster_arrive();
+    if (rank != 0) return;  // (what is over counts as arrived; nobody writes to this CTA)
+    cluster_wait();
+    if (threadIdx.x == 0) {
+      for (int c = 1; c < split; ++c) s = join(s, Part{sums[c][0], sums[c][1], sums[c][2]});
+      sums[0][0] = s.m, sums[0][1] = s.r, sums[0][2] = s.t;
+    }
+    if (top > 0) {
+      const int count = split * top;
+      const Key key = threadIdx.x < count ? theirs[threadIdx.x] : 0;
       if (threadIdx.x < kMostTop) sorted[threadIdx.x] = 0;
       __syncthreads();
       if (key != 0) {
         int before = 0;
-        for (int j = 0; j < split * kMostTop; ++j) before += list[j] > key;
+#pragma unroll 4
+        for (int j = 0; j < count; j += 2) {  // (split is even)
+          const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(theirs + j);
+          before += (two.x > key) + (two.y > key);
+        }
         if (before < top) sorted[before] = key;
       }
-      __syncthreads();
     }
-    ptx::cluster_sync();  // no CTA leaves while it may be read
-    if (rank != 0) return;
+    __syncthreads();
   }
-  const float m = sums[0], r = sums[1], t = sums[2], log_z = log1pf(r);
+  const float m = sums[0][0], r = sums[0][1], t = sums[0][2], log_z = log1pf(r);
   const auto log_p = [&](float v) { return !(v > -INFINITY) ? -INFINITY : v == m ? -log_z : v - m - log_z; };
   if (threadIdx.x == 0) {
     p.logprob[row] = m == -INFINITY ? -INFINITY : log_p(given);
