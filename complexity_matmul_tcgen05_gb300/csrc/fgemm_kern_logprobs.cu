@@ -272,6 +272,59 @@ __device__ __forceinline__ void st_cluster_key(uint32_t at, Key v) {
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
+// The first `top` of `count` different keys, in order, by all threads of a CTA; four
+// threads a key.
+__device__ __forceinline__ void rank_list(const Key* list, int count, Key* sorted, int top) {
+  for (int i = threadIdx.x / 4; i < (count + 7) / 8 * 8; i += kThreads / 4) {  // (whole warps)
+    const Key key = i < count ? list[i] : 0;
+    int before = 0;
+#pragma unroll 4
+    for (int j = threadIdx.x % 4; j < count; j += 4) before += list[j] > key;
+    before += __shfl_xor_sync(0xFFFFFFFFu, before, 1);
+    before += __shfl_xor_sync(0xFFFFFFFFu, before, 2);
+    if (i < count && before < top && threadIdx.x % 4 == 0) sorted[before] = key;
+  }
+}
+
+constexpr uint32_t kLowest = 0x00800000u;  // ordered(-FLT_MAX)
+
+// Of 32 EACH ordered values one that at least `top` of them reach and not many more,
+// by a warp; kLowest if fewer than `top` are above -inf.
+template <int EACH>
+__device__ __forceinline__ uint32_t search(const uint32_t* values, int top) {
+  uint32_t v[EACH];
+#pragma unroll
+  for (int i = 0; i < EACH; i += 4) {
+    const uint4 w = reinterpret_cast<const uint4*>(values)[(threadIdx.x & 31) * (EACH / 4) + i / 4];
+    v[i] = w.x, v[i + 1] = w.y, v[i + 2] = w.z, v[i + 3] = w.w;
+  }
+  uint32_t lo = 0xFFFFFFFFu, hi = 0;
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) lo = min(lo, v[i]), hi = max(hi, v[i]);
+  lo = max(__reduce_min_sync(0xFFFFFFFFu, lo), kLowest);
+  hi = max(__reduce_max_sync(0xFFFFFFFFu, hi), lo) + 1;
+  // at least `top` reach lo (or lo is kLowest), fewer reach hi; three borders at a time
+  uint32_t reach = 32 * EACH;
+  while (reach > 2u * top && hi - lo > 1) {
+    const uint32_t step = max((hi - lo) / 4, 1u), a = lo + step, b = min(a + step, hi), c = min(b + step, hi);
+    uint32_t count = 0;  // ten bits each
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) count += (v[i] >= a ? 1u : 0u) + (v[i] >= b ? 1u << 10 : 0u) + (v[i] >= c ? 1u << 20 : 0u);
+    count = __reduce_add_sync(0xFFFFFFFFu, count);
+    const uint32_t na = count & 1023u, nb = count >> 10 & 1023u, nc = count >> 20;
+    const uint32_t need = static_cast<uint32_t>(top);
+    if (nc >= need)
+      lo = c, reach = nc;
+    else if (nb >= need)
+      lo = b, hi = c, reach = nb;
+    else if (na >= need)
+      lo = a, hi = b, reach = na;
+    else
+      hi = a;
+  }
+  return lo;
+}
+
 // A CTA of a cluster of `split` takes a part of row blockIdx.x / split.
 template <int TYPE>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __grid_constant__ LogprobParams p,
@@ -282,7 +335,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
   __shared__ Key sorted[kMostTop];
   __shared__ Key best[kWarps];
   __shared__ Part parts[kWarps];
-  __shared__ uint32_t least[kWarps], largest[kWarps];
+  __shared__ __align__(16) uint32_t maxima[kThreads];
+  __shared__ uint32_t threshold;
+  __shared__ uint8_t lanes[kWarps][32];
   __shared__ float sums[kMostSplit][3];  // first CTA: every CTA's
   __shared__ int listed;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -331,58 +386,50 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
   const uint32_t my = mine > -INFINITY ? ordered(mine) : 0u;
   if (lane == 0) parts[warp] = s;
   if (top > 0) {
-    const uint32_t l = __reduce_min_sync(0xFFFFFFFFu, my), m = __reduce_max_sync(0xFFFFFFFFu, my);
-    if (lane == 0) least[warp] = l, largest[warp] = m;
+    maxima[threadIdx.x] = my;
     if (threadIdx.x == 0) listed = 0;
     if (threadIdx.x < kMostTop) sorted[threadIdx.x] = 0;
   }
   __syncthreads();
 
   if (top > 0) {
-    // A value that at least `top` threads reach, if so many have one above -inf,
-    // and not many more: between the least and the largest of the threads'.
-    uint32_t lo = least[0], hi = largest[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) lo = min(lo, least[w]), hi = max(hi, largest[w]);
-    constexpr uint32_t kLowest = 0x00800000u;  // ordered(-FLT_MAX)
-    lo = max(lo, kLowest);
-    hi = max(hi, lo) + 1;
-    int reach = lo > kLowest ? kThreads : __syncthreads_count(my >= lo);
-    while (reach > 2 * top && hi - lo > 1) {
-      const uint32_t mid = lo + (hi - lo) / 2;
-      const int count = __syncthreads_count(my >= mid);
-      if (count < top)
-        hi = mid;
-      else
-        lo = mid, reach = count;
+    if (warp == 0) {
+      const uint32_t from = search<kThreads / 32>(maxima, top);
+      if (lane == 0) threshold = from;
     }
-    if (my >= lo) {
-      const float from = value_of(static_cast<Key>(lo) << 32);
-      for (int v = v0 + warp * kChunk + lane; v < v1; v += kThreads * kDeep) {
-        uint4 batch[kDeep];
+    __syncthreads();
+    // The lanes with a maximum from there on: the warp reads their logits again,
+    // a vector a lane.
+    const uint32_t from = threshold;
+    const uint32_t has = __ballot_sync(0xFFFFFFFFu, my >= from);
+    if (has) {
+      const float least = value_of(static_cast<Key>(from) << 32);
+      uint8_t* const who = lanes[warp];
+      if (my >= from) who[__popc(has & ((1u << lane) - 1))] = static_cast<uint8_t>(lane);
+      __syncwarp();
+      const int first = v0 + warp * kChunk;  // vector `first + b kThreads kDeep + n 32 + lane`, b from 0, n below kDeep
+      const int per = first < v1 ? ((v1 - first + kThreads * kDeep - 1) / (kThreads * kDeep)) * kDeep : 0;
+      const int all = per * __popc(has);
+#pragma unroll 4
+      for (int e = lane; e < all; e += 32) {
+        const int i = e % per;
+        const int v = first + i / kDeep * (kThreads * kDeep) + i % kDeep * 32 + who[e / per];
+        if (v >= v1) continue;
+        const uint4 w = x.load(v);
 #pragma unroll
-        for (int n = 0; n < kDeep; ++n) batch[n] = v + n * 32 < v1 ? x.load(v + n * 32) : R::none();
-#pragma unroll
-        for (int n = 0; n < kDeep; ++n)
-#pragma unroll
-          for (int k = 0; k < R::kVec; ++k) {
-            const float value = R::elem(batch[n], k);
-            if (value >= from && value > -INFINITY) {
-              const int at = atomicAdd(&listed, 1);
-              if (at < kList) list[at] = key_of(value, (v + n * 32) * R::kVec - x.skip + k);
-            }
+        for (int k = 0; k < R::kVec; ++k) {
+          const float value = R::elem(w, k);
+          if (value >= least) {
+            const int at = atomicAdd(&listed, 1);
+            if (at < kList) list[at] = key_of(value, v * R::kVec - x.skip + k);
           }
+        }
       }
     }
     __syncthreads();
     const int count = listed;
     if (count <= kList) {
-      for (int i = threadIdx.x; i < count; i += kThreads) {
-        const Key key = list[i];
-        int before = 0;
-        for (int j = 0; j < count; ++j) before += list[j] > key;
-        if (before < top) sorted[before] = key;
-      }
+      rank_list(list, count, sorted, top);
     } else {
       Key last = ~0ull;
       for (int n = 0; n < top; ++n) {
@@ -436,19 +483,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
       sums[0][0] = s.m, sums[0][1] = s.r, sums[0][2] = s.t;
     }
     if (top > 0) {
-      const int count = split * top;
-      const Key key = threadIdx.x < count ? theirs[threadIdx.x] : 0;
+      // At least `top` keys reach the least of the CTAs' k-th ones, k = ceil(top / split):
+      // those are ranked.
+      const int k = (top + split - 1) / split - 1;
+      Key least = ~0ull;
+      for (int c = 0; c < split; ++c) least = min(least, theirs[c * top + k]);
+      const Key key = threadIdx.x < split * top ? theirs[threadIdx.x] : 0;
+      if (threadIdx.x == 0) listed = 0;
       if (threadIdx.x < kMostTop) sorted[threadIdx.x] = 0;
       __syncthreads();
-      if (key != 0) {
-        int before = 0;
-#pragma unroll 4
-        for (int j = 0; j < count; j += 2) {  // (split is even)
-          const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(theirs + j);
-          before += (two.x > key) + (two.y > key);
-        }
-        if (before < top) sorted[before] = key;
-      }
+      if (key != 0 && key >= least) list[atomicAdd(&listed, 1)] = key;
+      __syncthreads();
+      rank_list(list, listed, sorted, top);
     }
     __syncthreads();
   }
