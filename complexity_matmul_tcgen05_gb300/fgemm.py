@@ -588,6 +588,7 @@ def plan(M: int, N: int, K: int, dtype: torch.dtype = torch.bfloat16, epilogue: 
 # The raw handle of a device's current stream: torch.cuda.current_stream builds
 # an object around it, which costs as much as one of these kernels.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _rows(t: torch.Tensor | None, name: str, shape, dtype, dev: int) -> tuple[int | None, int]:
@@ -620,7 +621,7 @@ def _on(t: torch.Tensor, name: str, handle: Handle | None, dims: int = 2):
         raise FgemmError(ERR_INVALID_ARG, f"{name} must be a CUDA tensor")
     if t.dim() != dims:
         raise FgemmError(ERR_INVALID_ARG, f"{name} must be {dims}-D")
-    h = handle if handle is not None else default_handle()
+    h = handle if handle is not None else _handles.get(_current_device()) or default_handle()
     if dev != h.device:
         raise FgemmError(ERR_INVALID_ARG, f"{name} is on cuda:{dev}, the handle on cuda:{h.device}")
     L = _lib or lib()
@@ -829,14 +830,16 @@ def _heads(t: torch.Tensor, name: str, shape, dtype, dev: int) -> tuple[int, int
 
 def _cache(k: torch.Tensor, v: torch.Tensor, kv_heads: int | None, dim: int, dtype, dev: int) -> KvCache:
     """The C view of a paged cache, checked; kv_heads None: any number."""
-    for t, name in ((k, "k_cache"), (v, "v_cache")):
-        if t.dim() != 4 or t.dtype != dtype or t.get_device() != dev or t.shape[3] != dim or t.shape != k.shape or \
-                (kv_heads is not None and t.shape[2] != kv_heads):
-            raise FgemmError(ERR_INVALID_ARG, f"{name} must be a pages x page size x key heads x {dim} {dtype} tensor "
-                                              f"on cuda:{dev}")
-        if t.stride(3) != 1 and dim > 1:
-            raise FgemmError(ERR_INVALID_ARG, f"the values of a head of {name} must be adjacent")
-    return KvCache(k.data_ptr(), v.data_ptr(), k.shape[0], k.shape[1], *k.stride()[:3], *v.stride()[:3])
+    shape = k.shape
+    if len(shape) != 4 or v.shape != shape or shape[3] != dim or kv_heads not in (None, shape[2]) or \
+            k.dtype != dtype or v.dtype != dtype or k.get_device() != dev or v.get_device() != dev:
+        raise FgemmError(ERR_INVALID_ARG, f"k_cache and v_cache must be pages x page size x key heads x {dim} {dtype} "
+                                          f"tensors of one shape on cuda:{dev}")
+    k_page, k_token, k_head, k_unit = k.stride()
+    v_page, v_token, v_head, v_unit = v.stride()
+    if (k_unit != 1 or v_unit != 1) and dim > 1:
+        raise FgemmError(ERR_INVALID_ARG, "the values of a head of k_cache and v_cache must be adjacent")
+    return KvCache(k.data_ptr(), v.data_ptr(), shape[0], shape[1], k_page, k_token, k_head, v_page, v_token, v_head)
 
 
 def rotary_cache(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
@@ -866,7 +869,7 @@ def rotary_cache(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: t
     fp = _vector(inv_freq, "inv_freq", half, torch.float32, dev)
     cache = _cache(k_cache, v_cache, kv[1], dim, t, dev)
     if out is None:
-        out = torch.empty((n, heads, dim), dtype=t, device=q.device)
+        out = torch.empty_like(q)
     oa = _heads(out, "out", q.shape, t, dev)
     s = L.fgemm_rotary_cache(h, n, heads, kv[1], dim, *qa, *ka, *va, pp, sp, fp, 2 * half, 1 if interleaved else 0, dt,
                              *oa, ctypes.byref(cache))
@@ -898,7 +901,7 @@ def attention_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     tp, ldt = _rows(page_table, "page_table", (n, pages), torch.int32, dev)
     lp = _vector(lengths, "lengths", n, torch.int32, dev)
     if out is None:
-        out = torch.empty((n, heads, dim), dtype=t, device=q.device)
+        out = torch.empty_like(q)
     oa = _heads(out, "out", q.shape, t, dev)
     lse = torch.empty((n, heads), dtype=torch.float32, device=q.device)
     size = L.fgemm_attention_paged_workspace(h, n, heads, kv_heads, dim)
@@ -939,7 +942,7 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, starts: torch.T
     sp = _vector(starts, "starts", seqs + 1, torch.int32, dev)
     kp = _vector(k_starts, "k_starts", seqs + 1, torch.int32, dev)
     if out is None:
-        out = torch.empty((n, heads, dim), dtype=t, device=q.device)
+        out = torch.empty_like(q)
     oa = _heads(out, "out", q.shape, t, dev)
     if lse is None:
         lse = torch.empty((n, heads), dtype=torch.float32, device=q.device)
