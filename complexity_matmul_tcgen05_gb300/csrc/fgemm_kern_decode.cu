@@ -19,8 +19,10 @@
 // sums; the warps of a CTA meet once at the end of a sequence's part.
 //
 // The work of all sequences and key heads, in blocks of 64 tokens laid end to
-// end, is cut into equal shares, one a CTA, on the device: lengths are not known
-// to the host. A sequence whose blocks lie in more than one share is joined from
+// end, is cut into shares, one a CTA, on the device: lengths are not known to the
+// host. With equal shares the SMs ended at very different times (on average 85 %
+// through the kernel), so three quarters are cut equally among the CTAs that the
+// device holds and the rest into smaller shares for those that end first. A sequence whose blocks lie in more than one share is joined from
 // its parts, in their order, by a second kernel, launched so that it is there when
 // the first ends. Sums do not depend on timing.
 #include <cuda_runtime.h>
@@ -42,6 +44,8 @@ constexpr int kTokens = 16;                 // of a warp's block
 constexpr int kBlock = kWarps * kTokens;    // tokens of a share's block
 constexpr int kRows = 16;                   // query heads of a CTA
 constexpr int kCtasPerSm = 2;
+constexpr int kFew = 16;                    // blocks of a share that is not cut further
+constexpr int kMostScanned = 4096;          // sequences whose blocks the join adds up itself
 constexpr long long kMostTokens = (1LL << 31) - 4096;  // of a sequence: its blocks stay inside 32 bits
 constexpr float kSlack = 8.0f;              // log2 of how far the maximum may be above the reference
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -60,7 +64,9 @@ struct Cfg {
 struct Plan {
   long long* before;  // seqs + 1: blocks of the sequences before
   float* parts;       // two a CTA
-  int grid, tiles;    // CTAs; groups of kRows query heads of a key head
+  // CTAs that the device holds at once and, where there is enough for them, as many
+  // again that start when one of those ends; groups of kRows query heads of a key head
+  int grid, extra, tiles;
 };
 
 struct Span {
@@ -78,8 +84,23 @@ __device__ __forceinline__ int blocks_of(const DecodeParams& p, int s) {
   return (span_of(p, s).count + kBlock - 1) / kBlock;
 }
 
-// Blocks of a share.
-__device__ __forceinline__ long long share_of(long long total, int grid) { return max((total + grid - 1) / grid, 1LL); }
+// The shares: block ranges of CTAs, in the CTAs' order.
+struct Shares {
+  long long total, large, small;  // blocks: all; of one of the first `grid` CTAs; of one of the others
+  int grid;
+  __device__ __forceinline__ Shares(long long all, const Plan& plan) : total(all), grid(plan.grid) {
+    const long long even = max((total + grid - 1) / grid, 1LL);
+    large = plan.extra && even >= kFew ? even * 3 / 4 : even;
+    small = max((total - large * grid + plan.extra - 1) / max(plan.extra, 1), 4LL);
+  }
+  __device__ __forceinline__ long long begin(int cta) const {
+    return cta < grid ? cta * large : grid * large + (cta - grid) * small;
+  }
+  __device__ __forceinline__ int owner(long long block) const {
+    const long long first = grid * large;
+    return static_cast<int>(block < first ? block / large : grid + (block - first) / small);
+  }
+};
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -166,8 +187,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
       if (threadIdx.x == 0) plan.before[p.seqs] = sums[kThreads];
     }
   }
-  const long long total = sums[kThreads], share = share_of(total, plan.grid);
-  const long long b0 = blockIdx.x * share, b1 = min(b0 + share, total);
+  const long long total = sums[kThreads];
+  const Shares shares(total, plan);
+  const long long b0 = shares.begin(blockIdx.x), b1 = min(shares.begin(blockIdx.x + 1), total);
   if (b0 >= b1) return;
   // the sequence of block b0
   int seq;
@@ -403,56 +425,98 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
   }
 }
 
-// One CTA a query head: the parts of its unit in their order, shared by four
-// warps, or zeros where there is nothing.
+// One CTA a query head: the parts of its unit, warp w taking part w and every
+// kJoinWarps-th behind it, or zeros where there is nothing. What does not come from
+// the first kernel is done while that one runs.
+constexpr int kJoinWarps = 8, kJoinThreads = kJoinWarps * 32;
 template <bool BF16, int DP>
-__global__ void __launch_bounds__(kThreads) decode_join_kernel(const __grid_constant__ DecodeParams p,
-                                                               const __grid_constant__ Plan plan) {
+__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_constant__ DecodeParams p,
+                                                                   const __grid_constant__ Plan plan) {
   using C = Cfg<DP>;
-  __shared__ float4 outs[kWarps][32];
-  __shared__ float refs[kWarps], sums[kWarps];
+  __shared__ float4 outs[kJoinWarps][32];
+  __shared__ float refs[kJoinWarps], sums[kJoinWarps];
+  __shared__ long long blocks_sum[2][kJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int seq = blockIdx.x / p.heads, head = blockIdx.x % p.heads, group = p.heads / p.kv_heads;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const long long before = plan.before[seq], n = plan.before[seq + 1] - before, total = plan.before[p.seqs];
+  const int per_seq = p.kv_heads * plan.tiles;
+  long long before, total;
+  const long long blocks = blocks_of(p, seq);
+  if (p.seqs <= kMostScanned) {
+    long long all = 0, ahead = 0;
+    for (int s = threadIdx.x; s < p.seqs; s += kJoinThreads) {
+      const int n = blocks_of(p, s);
+      all += n;
+      ahead += s < seq ? n : 0;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      all += __shfl_xor_sync(0xFFFFFFFFu, all, d);
+      ahead += __shfl_xor_sync(0xFFFFFFFFu, ahead, d);
+    }
+    if (lane == 0) blocks_sum[0][warp] = all, blocks_sum[1][warp] = ahead;
+    __syncthreads();
+    total = before = 0;
+    for (int w = 0; w < kJoinWarps; ++w) total += blocks_sum[0][w], before += blocks_sum[1][w];
+    total *= per_seq;
+    before *= per_seq;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+  } else {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    before = plan.before[seq];
+    total = plan.before[p.seqs];
+  }
   uint16_t* const out = p.out.p + seq * p.out.ld + head * p.out.hs;
-  if (n == 0) {
+  if (blocks == 0) {
     if (threadIdx.x < p.dim / 8) reinterpret_cast<uint4*>(out)[threadIdx.x] = make_uint4(0, 0, 0, 0);
     if (p.lse && threadIdx.x == 0) p.lse[blockIdx.x] = -INFINITY;
     return;
   }
-  const int per_seq = p.kv_heads * plan.tiles;
   const int unit = head / group * plan.tiles + head % group / kRows, r = head % group % kRows;
-  const long long blocks = n / per_seq, u0 = before + unit * blocks, u1 = u0 + blocks;
-  const long long share = share_of(total, plan.grid);
-  const int c0 = static_cast<int>(u0 / share), c1 = static_cast<int>((u1 - 1) / share);
+  const long long u0 = before + unit * blocks, u1 = u0 + blocks;
+  const Shares shares(total, plan);
+  const int c0 = shares.owner(u0), c1 = shares.owner(u1 - 1);
   if (c0 == c1) return;
   float top = -INFINITY, z = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  const int count = c1 - c0 + 1, each = (count + kWarps - 1) / kWarps;
-  const int from = c0 + warp * each, upto = min(c1 + 1, from + each);
   auto part = [&](int c) { return plan.parts + (2LL * c + (c == c0 ? 1 : 0)) * C::kPart; };
-  for (int c = from + lane; c < upto; c += 32) top = fmaxf(top, part(c)[kRows * DP + r]);
+#pragma unroll 1
+  for (int c = c0 + warp; c <= c1; c += 4 * kJoinWarps) {
+    // four parts at once
+    float ref[4], sum[4];
+    float4 v[4];
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-#pragma unroll 4
-  for (int c = from; c < upto; ++c) {
-    const float* const x = part(c);
-    const float mr = x[kRows * DP + r];
-    const float4 v = lane * 4 < DP ? *reinterpret_cast<const float4*>(x + r * DP + lane * 4) : acc;
-    const float l = x[kRows * DP + kRows + r];
-    const float f = scale_of(mr, top);
-    z += f * l;
-    acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
+    for (int i = 0; i < 4; ++i) {
+      const int at = c + i * kJoinWarps;
+      ref[i] = -INFINITY, sum[i] = 0.0f, v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (at <= c1) {
+        const float* const x = part(at);
+        ref[i] = x[kRows * DP + r];
+        sum[i] = x[kRows * DP + kRows + r];
+        if (lane * 4 < DP) v[i] = *reinterpret_cast<const float4*>(x + r * DP + lane * 4);
+      }
+    }
+    const float to = fmaxf(top, fmaxf(fmaxf(ref[0], ref[1]), fmaxf(ref[2], ref[3])));
+    const float f0 = scale_of(top, to);
+    z *= f0;
+    acc.x *= f0, acc.y *= f0, acc.z *= f0, acc.w *= f0;
+    top = to;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float f = scale_of(ref[i], to);
+      z += f * sum[i];
+      acc.x += f * v[i].x, acc.y += f * v[i].y, acc.z += f * v[i].z, acc.w += f * v[i].w;
+    }
   }
   outs[warp][lane] = acc;
   if (lane == 0) refs[warp] = top, sums[warp] = z;
   __syncthreads();
   if (warp != 0) return;
-  top = fmaxf(fmaxf(refs[0], refs[1]), fmaxf(refs[2], refs[3]));
+  top = refs[0];
+  for (int w = 1; w < kJoinWarps; ++w) top = fmaxf(top, refs[w]);
   acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   z = 0.0f;
-  for (int w = 0; w < kWarps; ++w) {
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
     const float f = scale_of(refs[w], top);
     const float4 v = outs[w][lane];
     z += f * sums[w];
@@ -467,17 +531,31 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const __grid_cons
 
 size_t before_bytes(int seqs) { return (static_cast<size_t>(seqs) + 1 + 1) / 2 * 16; }
 
+// The kernel's shared memory, asked for once on each device.
+template <class K>
+cudaError_t with_smem(K kernel, int bytes, unsigned long long& devices) {
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (device & 63);
+  if (device < 64 && (__atomic_load_n(&devices, __ATOMIC_ACQUIRE) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && device < 64) __atomic_fetch_or(&devices, bit, __ATOMIC_RELEASE);
+  return e;
+}
+
 template <bool BF16, int DP>
 cudaError_t launch_of(const DecodeParams& p, const Plan& plan, cudaStream_t stream) {
+  static unsigned long long devices = 0;
   auto kernel = decode_kernel<BF16, DP>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<DP>::kSmem);
+  cudaError_t e = with_smem(kernel, Cfg<DP>::kSmem, devices);
   if (e != cudaSuccess) return e;
-  kernel<<<plan.grid, kThreads, Cfg<DP>::kSmem, stream>>>(p, plan);
+  kernel<<<plan.grid + plan.extra, kThreads, Cfg<DP>::kSmem, stream>>>(p, plan);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.seqs) * static_cast<unsigned>(p.heads));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -491,7 +569,7 @@ cudaError_t launch_of(const DecodeParams& p, const Plan& plan, cudaStream_t stre
 
 size_t decode_workspace(int seqs, int, int, int dim, int num_sms) {
   const size_t part = static_cast<size_t>(dim > 64 ? Cfg<128>::kPart : Cfg<64>::kPart) * 4;
-  return before_bytes(seqs) + static_cast<size_t>(num_sms) * kCtasPerSm * 2 * part;
+  return before_bytes(seqs) + static_cast<size_t>(num_sms) * kCtasPerSm * 3 * 2 * part;
 }
 
 cudaError_t launch_decode(const DecodeParams& p, void* workspace, int num_sms, cudaStream_t stream) {
@@ -500,6 +578,10 @@ cudaError_t launch_decode(const DecodeParams& p, void* workspace, int num_sms, c
   plan.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + before_bytes(p.seqs));
   plan.grid = num_sms * kCtasPerSm;
   plan.tiles = (p.heads / p.kv_heads + kRows - 1) / kRows;
+  // the most blocks that the lengths can come to
+  const double tokens = static_cast<double>(p.table_pages) * p.page_size;
+  const double most = (p.window > 0 && p.window < tokens ? p.window : tokens) / kBlock * p.seqs * p.kv_heads * plan.tiles;
+  plan.extra = most >= static_cast<double>(kFew) * plan.grid ? 2 * plan.grid : 0;
   if (p.dim > 64)
     return p.is_bf16 ? launch_of<true, 128>(p, plan, stream) : launch_of<false, 128>(p, plan, stream);
   return p.is_bf16 ? launch_of<true, 64>(p, plan, stream) : launch_of<false, 64>(p, plan, stream);
