@@ -18,15 +18,17 @@
 // tokens of its own through its own ring of asynchronous copies and keeps its own
 // sums; the warps of a CTA meet once at the end of a sequence's part.
 //
-// The work of all sequences and key heads, in blocks of 64 tokens laid end to
-// end, is cut into shares, one a CTA, on the device: lengths are not known to the
-// host. With equal shares the SMs ended at very different times (on average 85 %
-// through the kernel), so three quarters are cut equally among the CTAs that the
-// device holds and the rest into smaller shares for those that end first. A sequence whose blocks lie in more than one share is joined from
-// its parts, in their order, by a second kernel, launched so that it is there when
-// the first ends. Sums do not depend on timing.
+// The work of all sequences, in blocks of 64 tokens laid end to end, is cut into
+// equal shares on the device: lengths are not known to the host. A share is taken by
+// a CTA for each key head, neighbours in the grid, so that the keys and values that
+// lie side by side are read at about the same time (ragged batch of 64 sequences, 8
+// key heads of 128: 213 us; with the heads of a sequence one after the other in the
+// shares 239). A sequence whose blocks lie in more than one share is joined from its
+// parts, in their order, by a second kernel, launched so that it is there when the
+// first ends. Sums do not depend on timing.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "fgemm_attn.cuh"
@@ -43,8 +45,6 @@ constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kTokens = 16;                 // of a warp's block
 constexpr int kBlock = kWarps * kTokens;    // tokens of a share's block
 constexpr int kRows = 16;                   // query heads of a CTA
-constexpr int kCtasPerSm = 2;
-constexpr int kFew = 16;                    // blocks of a share that is not cut further
 constexpr int kMostScanned = 4096;          // sequences whose blocks the join adds up itself
 constexpr long long kMostTokens = (1LL << 31) - 4096;  // of a sequence: its blocks stay inside 32 bits
 constexpr float kSlack = 8.0f;              // log2 of how far the maximum may be above the reference
@@ -52,7 +52,8 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int DP>  // values of a head, padded
 struct Cfg {
-  static constexpr int kStages = DP == 128 ? 3 : 6;
+  static constexpr int kCtasPerSm = DP == 128 ? 2 : 3;
+  static constexpr int kStages = DP == 128 ? 3 : 4;
   static constexpr int kTile = kTokens * DP * 2;                  // keys (or values) of a block
   static constexpr int kRing = kStages * 2 * kTile;               // of a warp
   static constexpr int kPart = kRows * DP + 2 * kRows;            // floats of a part: outputs, references, sums
@@ -64,9 +65,9 @@ struct Cfg {
 struct Plan {
   long long* before;  // seqs + 1: blocks of the sequences before
   float* parts;       // two a CTA
-  // CTAs that the device holds at once and, where there is enough for them, as many
-  // again that start when one of those ends; groups of kRows query heads of a key head
-  int grid, extra, tiles;
+  int tiles;   // groups of kRows query heads of a key head
+  int units;   // of a sequence: key heads by tiles
+  int shares;  // of the blocks of all sequences, each taken by `units` CTAs
 };
 
 struct Span {
@@ -84,23 +85,8 @@ __device__ __forceinline__ int blocks_of(const DecodeParams& p, int s) {
   return (span_of(p, s).count + kBlock - 1) / kBlock;
 }
 
-// The shares: block ranges of CTAs, in the CTAs' order.
-struct Shares {
-  long long total, large, small;  // blocks: all; of one of the first `grid` CTAs; of one of the others
-  int grid;
-  __device__ __forceinline__ Shares(long long all, const Plan& plan) : total(all), grid(plan.grid) {
-    const long long even = max((total + grid - 1) / grid, 1LL);
-    large = plan.extra && even >= kFew ? even * 3 / 4 : even;
-    small = max((total - large * grid + plan.extra - 1) / max(plan.extra, 1), 4LL);
-  }
-  __device__ __forceinline__ long long begin(int cta) const {
-    return cta < grid ? cta * large : grid * large + (cta - grid) * small;
-  }
-  __device__ __forceinline__ int owner(long long block) const {
-    const long long first = grid * large;
-    return static_cast<int>(block < first ? block / large : grid + (block - first) / small);
-  }
-};
+// Blocks of a share; share i begins at block i times that.
+__device__ __forceinline__ long long share_of(long long total, int shares) { return max((total + shares - 1) / shares, 1LL); }
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -148,7 +134,7 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
 }
 
 template <bool BF16, int DP>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __grid_constant__ DecodeParams p,
+__global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtasPerSm) decode_kernel(const __grid_constant__ DecodeParams p,
                                                                       const __grid_constant__ Plan plan) {
   using C = Cfg<DP>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -158,12 +144,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- shares: a prefix sum over the sequences, `each` of them a thread
-  const int per_seq = p.kv_heads * plan.tiles;  // units of a sequence, each of all its blocks
+  const int share = blockIdx.x / plan.units, unit = blockIdx.x % plan.units;
   const int each = (p.seqs + kThreads - 1) / kThreads;
   {
     const int s0 = min(p.seqs, static_cast<int>(threadIdx.x) * each), s1 = min(p.seqs, s0 + each);
     long long n = 0;
-    for (int s = s0; s < s1; ++s) n += static_cast<long long>(blocks_of(p, s)) * per_seq;
+    for (int s = s0; s < s1; ++s) n += blocks_of(p, s);
     long long scan = n;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -182,14 +168,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
       long long at = sums[threadIdx.x];
       for (int s = s0; s < s1; ++s) {
         plan.before[s] = at;
-        at += static_cast<long long>(blocks_of(p, s)) * per_seq;
+        at += blocks_of(p, s);
       }
       if (threadIdx.x == 0) plan.before[p.seqs] = sums[kThreads];
     }
   }
   const long long total = sums[kThreads];
-  const Shares shares(total, plan);
-  const long long b0 = shares.begin(blockIdx.x), b1 = min(shares.begin(blockIdx.x + 1), total);
+  const long long size = share_of(total, plan.shares), b0 = share * size, b1 = min(b0 + size, total);
   if (b0 >= b1) return;
   // the sequence of block b0
   int seq;
@@ -201,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
     seq = t * each;
     at = sums[t];
     while (true) {
-      const long long n = static_cast<long long>(blocks_of(p, seq)) * per_seq;
+      const int n = blocks_of(p, seq);
       if (at + n > b0) break;
       at += n;
       ++seq;
@@ -214,14 +199,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
   const bool alike = p.k_page == p.v_page && p.k_token == p.v_token && p.k_head == p.v_head;
 
   for (long long b = b0; b < b1;) {
-    // ---- a part: blocks [b, end) of one unit
+    // ---- a part: blocks [b, end) of one sequence
     const int blocks = blocks_of(p, seq);
     if (blocks == 0) {
       ++seq;
       continue;
     }
-    const int unit = static_cast<int>((b - at) / blocks);
-    const long long unit0 = at + static_cast<long long>(unit) * blocks, unit1 = unit0 + blocks;
+    const long long unit0 = at, unit1 = at + blocks;
     const long long end = min(b1, unit1);
     const Span span = span_of(p, seq);
     const int t0 = static_cast<int>(b - unit0) * kBlock;
@@ -418,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const __gr
     }
     __syncthreads();  // the rings are free again
     b = end;
-    if (b == at + static_cast<long long>(blocks) * per_seq) {
+    if (b == unit1) {
       at = b;
       ++seq;
     }
@@ -438,7 +422,6 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
   __shared__ long long blocks_sum[2][kJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int seq = blockIdx.x / p.heads, head = blockIdx.x % p.heads, group = p.heads / p.kv_heads;
-  const int per_seq = p.kv_heads * plan.tiles;
   long long before, total;
   const long long blocks = blocks_of(p, seq);
   if (p.seqs <= kMostScanned) {
@@ -457,8 +440,6 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
     __syncthreads();
     total = before = 0;
     for (int w = 0; w < kJoinWarps; ++w) total += blocks_sum[0][w], before += blocks_sum[1][w];
-    total *= per_seq;
-    before *= per_seq;
     asm volatile("griddepcontrol.wait;" ::: "memory");
   } else {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -472,13 +453,14 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
     return;
   }
   const int unit = head / group * plan.tiles + head % group / kRows, r = head % group % kRows;
-  const long long u0 = before + unit * blocks, u1 = u0 + blocks;
-  const Shares shares(total, plan);
-  const int c0 = shares.owner(u0), c1 = shares.owner(u1 - 1);
+  const long long size = share_of(total, plan.shares);
+  const int c0 = static_cast<int>(before / size), c1 = static_cast<int>((before + blocks - 1) / size);
   if (c0 == c1) return;
   float top = -INFINITY, z = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  auto part = [&](int c) { return plan.parts + (2LL * c + (c == c0 ? 1 : 0)) * C::kPart; };
+  auto part = [&](int c) {
+    return plan.parts + (2LL * (c * plan.units + unit) + (c == c0 ? 1 : 0)) * C::kPart;
+  };
 #pragma unroll 1
   for (int c = c0 + warp; c <= c1; c += 4 * kJoinWarps) {
     // four parts at once
@@ -550,7 +532,7 @@ cudaError_t launch_of(const DecodeParams& p, const Plan& plan, cudaStream_t stre
   auto kernel = decode_kernel<BF16, DP>;
   cudaError_t e = with_smem(kernel, Cfg<DP>::kSmem, devices);
   if (e != cudaSuccess) return e;
-  kernel<<<plan.grid + plan.extra, kThreads, Cfg<DP>::kSmem, stream>>>(p, plan);
+  kernel<<<plan.shares * plan.units, kThreads, Cfg<DP>::kSmem, stream>>>(p, plan);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -567,21 +549,26 @@ cudaError_t launch_of(const DecodeParams& p, const Plan& plan, cudaStream_t stre
 
 }  // namespace
 
-size_t decode_workspace(int seqs, int, int, int dim, int num_sms) {
+namespace {
+int tiles_of(int heads, int kv_heads) { return (heads / kv_heads + kRows - 1) / kRows; }
+int shares_held(int units, int dim, int num_sms) {
+  return std::max(num_sms * (dim > 64 ? Cfg<128>::kCtasPerSm : Cfg<64>::kCtasPerSm) / units, 1);
+}
+}  // namespace
+
+size_t decode_workspace(int seqs, int heads, int kv_heads, int dim, int num_sms) {
   const size_t part = static_cast<size_t>(dim > 64 ? Cfg<128>::kPart : Cfg<64>::kPart) * 4;
-  return before_bytes(seqs) + static_cast<size_t>(num_sms) * kCtasPerSm * 3 * 2 * part;
+  const int units = kv_heads * tiles_of(heads, kv_heads);
+  return before_bytes(seqs) + static_cast<size_t>(shares_held(units, dim, num_sms)) * units * 2 * part;
 }
 
 cudaError_t launch_decode(const DecodeParams& p, void* workspace, int num_sms, cudaStream_t stream) {
   Plan plan;
   plan.before = static_cast<long long*>(workspace);
   plan.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + before_bytes(p.seqs));
-  plan.grid = num_sms * kCtasPerSm;
-  plan.tiles = (p.heads / p.kv_heads + kRows - 1) / kRows;
-  // the most blocks that the lengths can come to
-  const double tokens = static_cast<double>(p.table_pages) * p.page_size;
-  const double most = (p.window > 0 && p.window < tokens ? p.window : tokens) / kBlock * p.seqs * p.kv_heads * plan.tiles;
-  plan.extra = most >= static_cast<double>(kFew) * plan.grid ? 2 * plan.grid : 0;
+  plan.tiles = tiles_of(p.heads, p.kv_heads);
+  plan.units = p.kv_heads * plan.tiles;
+  plan.shares = shares_held(plan.units, p.dim, num_sms);
   if (p.dim > 64)
     return p.is_bf16 ? launch_of<true, 128>(p, plan, stream) : launch_of<false, 128>(p, plan, stream);
   return p.is_bf16 ? launch_of<true, 64>(p, plan, stream) : launch_of<false, 64>(p, plan, stream);
