@@ -48,44 +48,66 @@ __device__ __forceinline__ void rotate(uint32_t a, uint32_t b, const float2 t0, 
   to_b = pack2<BF16>(b0 * t0.x + a0 * t0.y, b1 * t1.x + a1 * t1.y);
 }
 
-// One head of a token: part `part` of its parts (parts_of).
-// MODE 0: pairs (i, i + rot / 2) with rot a multiple of 16, 16-byte accesses;
-// MODE 1: pairs (2 i, 2 i + 1), 16-byte accesses; MODE 2: pairs (i, i + rot / 2)
-// one at a time.
+// A head is passed over in parts (parts_of). MODE 0: pairs (i, i + rot / 2) with rot a
+// multiple of 16, 16-byte accesses; MODE 1: pairs (2 i, 2 i + 1), 16-byte accesses;
+// MODE 2: pairs (i, i + rot / 2) one at a time.
+template <int MODE>
+__host__ __device__ inline int parts_of(int dim, int rot) {
+  return MODE == 2 ? dim - rot / 2 : MODE == 1 ? dim / 8 : dim / 8 - rot / 16;
+}
+
+// What a part reads: up to two vectors of 16 bytes, or two values.
+struct Loaded {
+  uint4 a, b;
+};
+
+template <int MODE>
+__device__ __forceinline__ Loaded load_part(const uint16_t* from, int part, int rot) {
+  Loaded v;
+  if (MODE == 2) {
+    const int half = rot / 2;
+    v.a.x = part < half ? from[part] : 0u;
+    v.b.x = from[part + half];
+  } else {
+    const uint4* const in = reinterpret_cast<const uint4*>(from);
+    const int pairs = rot / 16;
+    v.a = in[MODE == 1 || part < pairs ? part : part + pairs];
+    if (MODE == 0 && part < pairs) v.b = in[part + pairs];
+  }
+  return v;
+}
+
 template <bool BF16, int MODE>
-__device__ __forceinline__ void head_part(const uint16_t* from, uint16_t* to, int part, int rot, const float2* turns) {
+__device__ __forceinline__ void store_part(uint16_t* to, const Loaded& v, int part, int rot, const float2* turns) {
   if (MODE == 2) {
     const int half = rot / 2;
     if (part < half) {
-      const float a = to_f32<BF16>(from[part]), b = to_f32<BF16>(from[part + half]);
+      const float a = to_f32<BF16>(v.a.x), b = to_f32<BF16>(v.b.x);
       const float2 t = turns[part];
       to[part] = to_16<BF16>(a * t.x - b * t.y);
       to[part + half] = to_16<BF16>(b * t.x + a * t.y);
     } else {
-      to[part + half] = from[part + half];
+      to[part + half] = static_cast<uint16_t>(v.b.x);
     }
     return;
   }
-  const uint4* const in = reinterpret_cast<const uint4*>(from);
   uint4* const out = reinterpret_cast<uint4*>(to);
   if (MODE == 0) {
     const int pairs = rot / 16;
     if (part >= pairs) {
-      out[part + pairs] = in[part + pairs];
+      out[part + pairs] = v.a;
       return;
     }
-    const uint4 a = in[part], b = in[part + pairs];
     const float2* const t = turns + part * 8;
     uint4 x, y;
-    rotate<BF16>(a.x, b.x, t[0], t[1], x.x, y.x);
-    rotate<BF16>(a.y, b.y, t[2], t[3], x.y, y.y);
-    rotate<BF16>(a.z, b.z, t[4], t[5], x.z, y.z);
-    rotate<BF16>(a.w, b.w, t[6], t[7], x.w, y.w);
+    rotate<BF16>(v.a.x, v.b.x, t[0], t[1], x.x, y.x);
+    rotate<BF16>(v.a.y, v.b.y, t[2], t[3], x.y, y.y);
+    rotate<BF16>(v.a.z, v.b.z, t[4], t[5], x.z, y.z);
+    rotate<BF16>(v.a.w, v.b.w, t[6], t[7], x.w, y.w);
     out[part] = x;
     out[part + pairs] = y;
   } else {
-    uint4 v = in[part];
-    uint32_t* const w = reinterpret_cast<uint32_t*>(&v);
+    uint32_t w[4] = {v.a.x, v.a.y, v.a.z, v.a.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int pair = part * 4 + i;
@@ -95,70 +117,91 @@ __device__ __forceinline__ void head_part(const uint16_t* from, uint16_t* to, in
         w[i] = pack2<BF16>(a * t.x - b * t.y, b * t.x + a * t.y);
       }
     }
-    out[part] = v;
+    out[part] = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
-template <int MODE>
-__host__ __device__ inline int parts_of(int dim, int rot) {
-  return MODE == 2 ? dim - rot / 2 : MODE == 1 ? dim / 8 : dim / 8 - rot / 16;
-}
-
-// blockIdx.x: `each` tokens.
-template <bool BF16, int MODE>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryParams p, int each) {
+// blockIdx.x: EACH tokens. A thread takes the same part of each, all loads first.
+template <bool BF16, int MODE, int EACH>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
   extern __shared__ float2 turns[];  // [token][rot / 2]
+  __shared__ long long k_at[EACH], v_at[EACH];  // of the tokens' places in the cache, -1: none
   const int half = p.rot / 2;
-  const long long t0 = static_cast<long long>(blockIdx.x) * each;
-  const int count = static_cast<int>(min(static_cast<long long>(each), p.tokens - t0));
-  for (int i = threadIdx.x; i < count * half; i += kThreads)
-    turns[i] = turn(p.positions[t0 + i / half], p.inv_freq[i % half]);
-  __syncthreads();
-  const int parts = parts_of<MODE>(p.dim, p.rot), chunks = p.dim / 8;
-  const int queries = p.heads * parts, keys = p.kv_heads * parts, tasks = queries + keys + p.kv_heads * chunks;
-  for (int i = 0; i < count; ++i) {
-    const long long t = t0 + i;
-    const int slot = p.slots[t];
+  const long long t0 = static_cast<long long>(blockIdx.x) * EACH;
+  const int count = static_cast<int>(min(static_cast<long long>(EACH), p.tokens - t0));
+  if (threadIdx.x < count) {
+    const int slot = p.slots[t0 + threadIdx.x];
     const bool kept = slot >= 0 && slot < p.cache_slots;
     const long long page = kept ? slot / p.page_size : 0, in_page = kept ? slot % p.page_size : 0;
-    for (int task = threadIdx.x; task < tasks; task += kThreads) {
-      if (task < queries) {
-        const int head = task / parts, part = task - head * parts;
-        head_part<BF16, MODE>(p.q.p + t * p.q.ld + head * p.q.hs, p.out.p + t * p.out.ld + head * p.out.hs, part, p.rot,
-                              turns + i * half);
-      } else if (kept && task < queries + keys) {
-        const int head = (task - queries) / parts, part = task - queries - head * parts;
-        head_part<BF16, MODE>(p.k.p + t * p.k.ld + head * p.k.hs,
-                              p.k_cache + page * p.k_page + in_page * p.k_token + head * p.k_head, part, p.rot,
-                              turns + i * half);
-      } else if (kept) {
-        const int head = (task - queries - keys) / chunks, c = task - queries - keys - head * chunks;
-        reinterpret_cast<uint4*>(p.v_cache + page * p.v_page + in_page * p.v_token + head * p.v_head)[c] =
-            reinterpret_cast<const uint4*>(p.v.p + t * p.v.ld + head * p.v.hs)[c];
-      }
-    }
+    k_at[threadIdx.x] = kept ? page * p.k_page + in_page * p.k_token : -1;
+    v_at[threadIdx.x] = kept ? page * p.v_page + in_page * p.v_token : -1;
   }
+  for (int i = threadIdx.x; i < count * half; i += kThreads)
+    turns[i] = turn(p.positions[t0 + i / half], p.inv_freq[i % half]);
+  const int parts = parts_of<MODE>(p.dim, p.rot), chunks = p.dim / 8;
+  const int queries = p.heads * parts, keys = p.kv_heads * parts, tasks = queries + keys + p.kv_heads * chunks;
+  bool formed = false;
+  for (int task = threadIdx.x; task < tasks || !formed; task += kThreads) {
+    // queries, keys, then values (copied as they are)
+    const int kind = task < queries ? 0 : task < queries + keys ? 1 : 2;
+    const int at = kind == 0 ? task : kind == 1 ? task - queries : task - queries - keys;
+    const int head = at / (kind == 2 ? chunks : parts), part = at - head * (kind == 2 ? chunks : parts);
+    Loaded v[EACH];
+    if (task < tasks) {
+      const Heads& from = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
+#pragma unroll
+      for (int i = 0; i < EACH; ++i)
+        if (i < count) {
+          const uint16_t* const x = from.p + (t0 + i) * from.ld + head * from.hs;
+          if (kind == 2)
+            v[i].a = reinterpret_cast<const uint4*>(x)[part];
+          else
+            v[i] = load_part<MODE>(x, part, p.rot);
+        }
+    }
+    if (!formed) __syncthreads();  // the turns (the first loads are on their way)
+    formed = true;
+    if (task >= tasks) continue;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i)
+      if (i < count) {
+        if (kind == 0) {
+          store_part<BF16, MODE>(p.out.p + (t0 + i) * p.out.ld + head * p.out.hs, v[i], part, p.rot, turns + i * half);
+        } else if (kind == 1) {
+          if (k_at[i] >= 0)
+            store_part<BF16, MODE>(p.k_cache + k_at[i] + head * p.k_head, v[i], part, p.rot, turns + i * half);
+        } else if (v_at[i] >= 0) {
+          reinterpret_cast<uint4*>(p.v_cache + v_at[i] + head * p.v_head)[part] = v[i].a;
+        }
+      }
+  }
+}
+
+template <bool BF16, int MODE>
+cudaError_t launch_mode(const RotaryParams& p, int num_sms, cudaStream_t stream) {
+  // several tokens a CTA once there are enough for every SM
+  constexpr int kEach = 4;
+  const int each = p.tokens >= static_cast<long long>(num_sms) * kEach * 4 ? kEach : 1;
+  const unsigned grid = static_cast<unsigned>((p.tokens + each - 1) / each);
+  const size_t smem = static_cast<size_t>(each) * (p.rot / 2) * sizeof(float2);
+  if (each == 1)
+    rotary_kernel<BF16, MODE, 1><<<grid, kThreads, smem, stream>>>(p);
+  else
+    rotary_kernel<BF16, MODE, kEach><<<grid, kThreads, smem, stream>>>(p);
+  return cudaGetLastError();
 }
 
 template <bool BF16>
-cudaError_t launch_of(const RotaryParams& p, cudaStream_t stream) {
-  const int each = p.tokens >= 4096 ? 4 : 1;
-  const unsigned grid = static_cast<unsigned>((p.tokens + each - 1) / each);
-  const size_t smem = static_cast<size_t>(each) * (p.rot / 2) * sizeof(float2);
-  if (p.interleaved)
-    rotary_kernel<BF16, 1><<<grid, kThreads, smem, stream>>>(p, each);
-  else if (p.rot % 16 == 0)
-    rotary_kernel<BF16, 0><<<grid, kThreads, smem, stream>>>(p, each);
-  else
-    rotary_kernel<BF16, 2><<<grid, kThreads, smem, stream>>>(p, each);
-  return cudaGetLastError();
+cudaError_t launch_of(const RotaryParams& p, int num_sms, cudaStream_t stream) {
+  if (p.interleaved) return launch_mode<BF16, 1>(p, num_sms, stream);
+  if (p.rot % 16 == 0) return launch_mode<BF16, 0>(p, num_sms, stream);
+  return launch_mode<BF16, 2>(p, num_sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_rotary(const RotaryParams& p, int num_sms, cudaStream_t stream) {
-  (void)num_sms;
-  return p.is_bf16 ? launch_of<true>(p, stream) : launch_of<false>(p, stream);
+  return p.is_bf16 ? launch_of<true>(p, num_sms, stream) : launch_of<false>(p, num_sms, stream);
 }
 
 }  // namespace fgemm
