@@ -214,7 +214,7 @@ fgemm_status_t fgemm_attention(fgemm_handle_t h, int64_t seqs, int64_t T, int64_
   if ((s = check_softmax(h, scale, window, lse)) != FGEMM_OK) return s;
   if (window > 0 && !causal) return bad_arg(h, "a window needs causal");
   if (fgemm::prompt_ctas(T, static_cast<int>(seqs), heads) > kMaxDim)
-    return bad(h, FGEMM_ERR_UNSUPPORTED, "(T / 256 + seqs) * heads must be below 2^31 - 1024");
+    return bad(h, FGEMM_ERR_UNSUPPORTED, "(T / 128 + seqs) * heads must be below 2^31");
   if (T == 0 || seqs == 0) return nothing(h);
   if (!starts) return bad_arg(h, "starts must not be NULL");
   if (off(starts, 4) || off(k_starts, 4))

@@ -540,7 +540,7 @@ fgemm_status_t fgemm_attention_paged(fgemm_handle_t h, int64_t seqs, int32_t hea
  *   starts    seqs + 1 ascending entries in 0 .. T.  k_starts  the same in
  *             0 .. T_k, or NULL: starts.
  *   lse       NULL or T x heads fp32 entries.
- * (T / 256 + seqs) * heads of 2^31 or more -> FGEMM_ERR_UNSUPPORTED.
+ * (T / 128 + seqs) * heads near or above 2^31 -> FGEMM_ERR_UNSUPPORTED.
  * Rows of out and lse that belong to no sequence are left as they were. A value
  * that is not finite reaches only the queries that see its key.
  */
