@@ -14,13 +14,17 @@
 //
 // The most probable tokens: the n-th largest of the threads' maxima is a value that
 // at least n logits reach, so the first n are among the logits from there on. A
-// search on the maxima finds such a value that at most 2 n threads reach, these
-// threads read their logits again and leave the ones from there on in a list, and
-// the list is ranked by counting. A list that does not fit (ties) is not used: the
+// search on the maxima finds such a value that at most 2 n threads reach (ties
+// apart), these threads' logits are read again, the ones from there on go to a list,
+// and the list is ranked by counting. A list that does not fit (ties) is not used: the
 // tokens are then found one by one, a pass each.
 //
-// A row is shared by a cluster of up to 8 CTAs where there are few rows.
-// Memory-bound with many rows, bound by the meetings with few.
+// A row is shared by a cluster of up to 8 CTAs where there are few rows; the others
+// write to its first one.
+// Measured: 4096 x 50257 fp16 78 us (5.25 TB/s; with sums by thread, whose lanes took
+// different branches, 140); 64 x 131072 fp32 9.3 us without alternatives, 15.2 with 20
+// (the search, the second read and two rankings come one after the other); one row of
+// 32000 bf16 4.5 us, with 5 alternatives 7.2.
 #include <cuda_runtime.h>
 
 #include <cstdint>
