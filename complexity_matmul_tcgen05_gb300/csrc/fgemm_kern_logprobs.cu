@@ -21,7 +21,7 @@
 //
 // A row is shared by a cluster of up to 8 CTAs where there are few rows; the others
 // write to its first one.
-// Measured: 4096 x 50257 fp16 78 us (5.25 TB/s; with sums by thread, whose lanes took
+// Measured: 4096 x 50257 fp16 71 us (5.8 TB/s; with sums by thread, whose lanes took
 // different branches, 140); 64 x 131072 fp32 9.3 us without alternatives, 15.2 with 20
 // (the search, the second read and two rankings come one after the other); one row of
 // 32000 bf16 4.5 us, with 5 alternatives 7.2.
@@ -39,12 +39,11 @@ namespace {
 
 using namespace attn;
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kDeep = 4;         // vectors of 16 bytes a thread has on their way
 constexpr int kList = 1024;      // logits that may be ranked
 constexpr int kMostTop = 32;
 constexpr int kMostSplit = 8;
-constexpr int kCtasPerSm = 4;
+constexpr int kThreadsPerSm = 1024;  // that the registers allow
 constexpr float kLog2e = 1.4426950408889634f;
 
 using Key = unsigned long long;
@@ -278,6 +277,7 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 
 // The first `top` of `count` different keys, in order, by all threads of a CTA; four
 // threads a key.
+template <int kThreads>
 __device__ __forceinline__ void rank_list(const Key* list, int count, Key* sorted, int top) {
   for (int i = threadIdx.x / 4; i < (count + 7) / 8 * 8; i += kThreads / 4) {  // (whole warps)
     const Key key = i < count ? list[i] : 0;
@@ -330,10 +330,11 @@ __device__ __forceinline__ uint32_t search(const uint32_t* values, int top) {
 }
 
 // A CTA of a cluster of `split` takes a part of row blockIdx.x / split.
-template <int TYPE>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __grid_constant__ LogprobParams p,
-                                                                        int split) {
+template <int TYPE, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreadsPerSm / kThreads)
+    logprobs_kernel(const __grid_constant__ LogprobParams p, int split) {
   using R = Row<TYPE>;
+  constexpr int kWarps = kThreads / 32;
   __shared__ __align__(16) Key list[kList];
   __shared__ __align__(16) Key theirs[kMostSplit * kMostTop];  // first CTA: every CTA's first tokens
   __shared__ Key sorted[kMostTop];
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
     __syncthreads();
     const int count = listed;
     if (count <= kList) {
-      rank_list(list, count, sorted, top);
+      rank_list<kThreads>(list, count, sorted, top);
     } else {
       Key last = ~0ull;
       for (int n = 0; n < top; ++n) {
@@ -492,13 +493,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
       const int k = (top + split - 1) / split - 1;
       Key least = ~0ull;
       for (int c = 0; c < split; ++c) least = min(least, theirs[c * top + k]);
-      const Key key = threadIdx.x < split * top ? theirs[threadIdx.x] : 0;
       if (threadIdx.x == 0) listed = 0;
       if (threadIdx.x < kMostTop) sorted[threadIdx.x] = 0;
       __syncthreads();
-      if (key != 0 && key >= least) list[atomicAdd(&listed, 1)] = key;
+      for (int i = threadIdx.x; i < split * top; i += kThreads) {
+        const Key key = theirs[i];
+        if (key != 0 && key >= least) list[atomicAdd(&listed, 1)] = key;
+      }
       __syncthreads();
-      rank_list(list, listed, sorted, top);
+      rank_list<kThreads>(list, listed, sorted, top);
     }
     __syncthreads();
   }
@@ -515,15 +518,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
   }
 }
 
-template <int TYPE>
-cudaError_t launch_of(const LogprobParams& p, int num_sms, cudaStream_t stream) {
-  // CTAs of a row: as many as the device holds beside the other rows', each with
-  // a vector a thread at least.
-  const long long vectors = (p.vocab + Row<TYPE>::kVec - 1) / Row<TYPE>::kVec;
-  int split = kMostSplit;
-  while (split > 1 && (static_cast<long long>(p.rows) * split > static_cast<long long>(num_sms) * kCtasPerSm ||
-                       vectors < static_cast<long long>(split) * kThreads))
-    split /= 2;
+template <int TYPE, int kThreads>
+cudaError_t launch_split(const LogprobParams& p, int split, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.rows) * static_cast<unsigned>(split));
   cfg.blockDim = dim3(kThreads);
@@ -535,7 +531,23 @@ cudaError_t launch_of(const LogprobParams& p, int num_sms, cudaStream_t stream) 
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = split > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, logprobs_kernel<TYPE>, p, split);
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<TYPE, kThreads>, p, split);
+}
+
+template <int TYPE>
+cudaError_t launch_of(const LogprobParams& p, int num_sms, cudaStream_t stream) {
+  // CTAs of a row: as many as the device holds beside the other rows', each with
+  // a vector a thread at least.
+  constexpr int kMany = 256, kFew = 128;
+  const long long vectors = (p.vocab + Row<TYPE>::kVec - 1) / Row<TYPE>::kVec;
+  int split = kMostSplit;
+  while (split > 1 && (static_cast<long long>(p.rows) * split > static_cast<long long>(num_sms) * (kThreadsPerSm / kMany) ||
+                       vectors < static_cast<long long>(split) * kMany))
+    split /= 2;
+  // Twice the rows on their way on an SM hide each other's ends better (4096 x 50257
+  // fp16 71 us against 78), but the n-th largest of fewer threads' maxima leaves more
+  // logits to read again (256 x 50257 with 20 alternatives 21 us against 18).
+  return split == 1 && p.top <= 8 ? launch_split<TYPE, kFew>(p, split, stream) : launch_split<TYPE, kMany>(p, split, stream);
 }
 
 }  // namespace
