@@ -4,6 +4,7 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cuda_runtime.h>
 
 #include <cstdint>
 
@@ -41,6 +42,20 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   }
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// A kernel's shared memory, asked for once on each device; `devices` is a word of the
+// kernel's own.
+template <class K>
+cudaError_t with_smem(K kernel, int bytes, unsigned long long& devices) {
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (device & 63);
+  if (device < 64 && (__atomic_load_n(&devices, __ATOMIC_ACQUIRE) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && device < 64) __atomic_fetch_or(&devices, bit, __ATOMIC_RELEASE);
+  return e;
 }
 
 }  // namespace attn

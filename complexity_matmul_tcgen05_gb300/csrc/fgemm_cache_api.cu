@@ -7,7 +7,6 @@
 // into a graph.
 #include <cuda_runtime.h>
 
-#include <cmath>
 #include <cstdint>
 
 #include "fgemm.h"
@@ -18,6 +17,7 @@ namespace {
 constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1024;
 constexpr int64_t kMaxStride = int64_t{1} << 36;  // elements; a tensor map takes strides below 2^40 bytes
 constexpr int32_t kMaxHeads = 1024;
+constexpr float kMaxScale = 18446744073709551616.0f;  // with log2 e it stays finite
 constexpr int64_t kMaxSeqs = int64_t{1} << 20;
 
 fgemm_status_t bad(fgemm_handle_t h, fgemm_status_t s, const char* text) {
@@ -96,7 +96,7 @@ void set_cache(P& p, const fgemm_kv_cache_t& c) {
 }
 
 fgemm_status_t check_softmax(fgemm_handle_t h, float scale, int32_t window, const float* lse) {
-  if (!(scale > 0.0f) || std::isinf(scale)) return bad_arg(h, "scale must be positive and finite");
+  if (!(scale > 0.0f) || scale > kMaxScale) return bad_arg(h, "scale must be positive and at most 2^64");
   if (window < 0) return bad_arg(h, "window must not be negative");
   if (off(lse, 4)) return bad(h, FGEMM_ERR_ALIGNMENT, "lse must be 4-byte aligned");
   return FGEMM_OK;

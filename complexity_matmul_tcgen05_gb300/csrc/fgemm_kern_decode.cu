@@ -518,19 +518,6 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
 
 size_t before_bytes(int seqs) { return (static_cast<size_t>(seqs) + 1 + 1) / 2 * 16; }
 
-// The kernel's shared memory, asked for once on each device.
-template <class K>
-cudaError_t with_smem(K kernel, int bytes, unsigned long long& devices) {
-  int device = 0;
-  cudaError_t e = cudaGetDevice(&device);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = 1ull << (device & 63);
-  if (device < 64 && (__atomic_load_n(&devices, __ATOMIC_ACQUIRE) & bit)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && device < 64) __atomic_fetch_or(&devices, bit, __ATOMIC_RELEASE);
-  return e;
-}
-
 template <bool BF16, int DP>
 cudaError_t launch_of(const DecodeParams& p, const Plan& plan, cudaStream_t stream) {
   static unsigned long long devices = 0;

@@ -928,8 +928,9 @@ bool encode(CUtensorMap* map, const Heads& t, long long tokens, int heads, int d
 
 template <bool BF16, int DP>
 cudaError_t launch_of(const Args& a, unsigned grid, cudaStream_t stream) {
+  static unsigned long long devices = 0;
   auto kernel = prompt_kernel<BF16, DP>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<DP>::kSmem);
+  cudaError_t e = with_smem(kernel, Cfg<DP>::kSmem, devices);
   if (e != cudaSuccess) return e;
   kernel<<<grid, kThreads, Cfg<DP>::kSmem, stream>>>(a);
   return cudaGetLastError();

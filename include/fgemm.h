@@ -513,7 +513,7 @@ fgemm_status_t fgemm_rotary_cache(fgemm_handle_t h, int64_t T, int32_t heads, in
  *               Pages outside the cache count as not there: their tokens are not
  *               seen. Lengths beyond the table are held to it, below 0 to 0.
  *   lengths     seqs entries.
- *   scale       positive and finite.  window  not negative.
+ *   scale       positive, at most 2^64.  window  not negative.
  *   lse         NULL or seqs x heads fp32 entries (natural logarithm).
  *   workspace   at least fgemm_attention_paged_workspace(h, seqs, heads,
  *               kv_heads, dim) bytes of device memory, 16-byte aligned, left with

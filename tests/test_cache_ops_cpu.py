@@ -101,6 +101,7 @@ SOFTMAX_REFUSALS = [
     (dict(scale=-1.0), BAD, "scale"),
     (dict(scale=math.nan), BAD, "scale"),
     (dict(scale=math.inf), BAD, "scale"),
+    (dict(scale=2.0 ** 65), BAD, "scale"),
     (dict(window=-1), BAD, "window"),
     (dict(lse=18), ALIGN, "lse"),
     (dict(heads=3), BAD, "multiple"),

@@ -445,6 +445,37 @@ def test_prompt_bad_starts_stay_inside():
     assert fgemm.default_handle().get_error() == fgemm.OK
 
 
+@pytest.mark.parametrize("causal,window", MASKS)
+@pytest.mark.parametrize("dtype,dim", [("bf16", 128), ("f16", 72), ("bf16", 64), ("f16", 128)])
+def test_prompt_pairs_of_heads(dtype, dim, causal, window):
+    """Enough rows and heads that share their keys for two of them at a time: prefixes,
+    rows that see nothing, no keys, no queries, a value that is not finite."""
+    lengths, k_lengths = [5, 130, 300, 1, 0, 40, 129, 300], [300, 131, 77, 1000, 50, 0, 129, 333]
+    heads, kv = 64, 16
+    q, k, v, starts, k_starts = prompt_inputs(gen(23), lengths, k_lengths, heads, kv, dim, TYPES[dtype])
+    out, lse = fgemm.attention(q, k, v, ints(starts), k_starts=ints(k_starts), causal=causal, window=window)
+    assert fgemm.default_handle().get_error() == fgemm.OK
+    looked = [0, 3, 29, 62, 63]
+    for h in looked:
+        check_prompt(q[:, h:h + 1], k[:, h // 4:h // 4 + 1], v[:, h // 4:h // 4 + 1], starts, k_starts, causal, window,
+                     out[:, h:h + 1], lse[:, h:h + 1], what="prompt pairs")
+    at = k_starts[-2] + 200  # a key of the last sequence; its queries stand at 33 .. 332 of 333
+    v2 = v.clone()
+    v2[at, 7, 5] = INF
+    wild, wild_lse = fgemm.attention(q, k, v2, ints(starts), k_starts=ints(k_starts), causal=causal, window=window)
+    rows = torch.arange(q.shape[0], device=DEV)
+    place = rows - starts[-2] + 33
+    sees = (rows >= starts[-2]) & ((place >= 200) | (not causal)) & ((place < 200 + window) | (window == 0))
+    for h in (28, 31):
+        assert not bool(torch.isfinite(wild[sees][:, h, 5]).any())
+        rest = wild[:, h:h + 1].clone()
+        rest[sees, :, 5] = out[sees, h:h + 1, 5]
+        check_prompt(q[:, h:h + 1], k[:, 7:8], v[:, 7:8], starts, k_starts, causal, window, rest, wild_lse[:, h:h + 1],
+                     what="prompt pairs beside an infinite value")
+    others = [h for h in range(heads) if h // 4 != 7]
+    assert torch.equal(wild[:, others], out[:, others]) and torch.equal(wild_lse, lse)
+
+
 @pytest.mark.parametrize("dim", [64, 128])
 def test_prompt_many_jobs_a_cta(dim):
     """More rows than the SMs hold at once, of sequences of very different
