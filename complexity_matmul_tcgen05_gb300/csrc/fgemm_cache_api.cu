@@ -57,7 +57,8 @@ fgemm_status_t check_heads(fgemm_handle_t h, fgemm::Heads& t, const void* p, int
   if (tokens <= 1) ld = dim;
   if (ld < dim || hs < dim || ld > kMaxStride || hs > kMaxStride)
     return bad_arg(h, "a token or head stride is below dim or above 2^36");
-  if (written && tokens > 1 && heads > 1 && ld < (heads - 1) * hs + dim && hs < (tokens - 1) * ld + dim)
+  // (hs - dim < (tokens - 1) * ld, without that product: it may pass 64 bits)
+  if (written && tokens > 1 && heads > 1 && ld < (heads - 1) * hs + dim && (hs - dim) / ld < tokens - 1)
     return bad_arg(h, "rows of out must not overlap");
   if (off(p, 16) || ld % 8 != 0 || hs % 8 != 0)
     return bad(h, FGEMM_ERR_ALIGNMENT, "tensors of heads must be 16-byte aligned, their strides multiples of 8");

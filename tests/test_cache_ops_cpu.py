@@ -82,6 +82,7 @@ CACHE_REFUSALS = [
     (dict(ldo=(1 << 36) + 8), BAD, "stride"),
     (dict(ldo=64), BAD, "overlap"),
     (dict(hso=64, ldo=192), BAD, "overlap"),
+    (dict(T=(1 << 31) - 1024, heads=1024, kv_heads=1024, hso=1 << 30, ldo=1 << 36), BAD, "overlap"),  # (2^67 values)
     (dict(hsq=68), ALIGN, "16-byte"),
     (dict(q=24), ALIGN, "16-byte"),
     (dict(out=40), ALIGN, "16-byte"),
