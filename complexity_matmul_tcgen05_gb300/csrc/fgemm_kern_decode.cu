@@ -5,10 +5,10 @@
 //
 // One pass over the keys and values with a running reference r of the maximum
 // and sums relative to it: w_j = 2^(x_j log2 e - r). The reference follows the
-// maximum only when that is more than 8 above it (the weights stay below 2^8
-// and sums below 2^40, far inside fp32), so that the outputs in registers are
-// seldom scaled. Weights are rounded to 16 bits for the product with the values,
-// their sum is of the 32-bit ones.
+// maximum only when that is more than 8 above it (the weights stay below 2^8, or
+// below 2^14 in fp16, where small ones would lose bits, and sums below 2^46, far
+// inside fp32), so that the outputs in registers are seldom scaled. Weights are
+// rounded to 16 bits for the product with the values, their sum is of the 32-bit ones.
 //
 // Memory-bound: a key and a value are read once for the up to 16 query heads
 // that share them. The query heads of a key head are the 16 rows of a matrix
@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtasPerSm) decode_kernel(c
   const uint32_t ring = ptx::smem_u32(smem) + warp * C::kRing;
   const int group = p.heads / p.kv_heads;
   const float to_log2 = p.scale * kLog2e;
+  constexpr float kLift = BF16 ? 0.0f : 6.0f;  // log2 of the weights' factor
   const bool alike = p.k_page == p.v_page && p.k_token == p.v_token && p.k_head == p.v_head;
 
   for (long long b = b0; b < b1;) {
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtasPerSm) decode_kernel(c
       }
       float base[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) base[h] = ref[h] == -INFINITY ? 0.0f : ref[h];
+      for (int h = 0; h < 2; ++h) base[h] = ref[h] == -INFINITY ? 0.0f : ref[h] - kLift;
       uint32_t w[4];
 #pragma unroll
       for (int n = 0; n < 2; ++n)
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtasPerSm) decode_kernel(c
       if ((lane & 3) == 0) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          part[kRows * DP + lane / 4 + h * 8] = ref[h];
+          part[kRows * DP + lane / 4 + h * 8] = ref[h] - kLift;
           part[kRows * DP + kRows + lane / 4 + h * 8] = sum[h];
         }
       }

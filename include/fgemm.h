@@ -490,6 +490,7 @@ typedef struct {
  *   positions  T entries.
  *   slots      T entries: page * page_size + token in the page, each slot once
  *              at most. Tokens with a slot outside the cache are not written.
+ *              Nothing that is written overlaps what is read (but for out over q).
  *   inv_freq   rot / 2 entries, radians a position (may be NULL for rot 0).
  *   rot        even, 0 .. dim.
  */

@@ -253,6 +253,30 @@ def test_paged_long_context_and_repeatable():
         assert torch.equal(out, o2) and torch.equal(lse, l2)
 
 
+def small_weights(n, tops):
+    """n keys with scores of 0 at `tops` and -13.8 elsewhere, which many make count: a
+    weight is 16.44 * 2^-24, between two of fp16's steps there.  Values are 0 and 1.  Also the
+    output and its bound: two roundings to fp16, and half of one for the sums of up to
+    n / 4 in 32 bits (2^-24 each step) and the scores (20 * 2^-24)."""
+    scores = torch.full((n,), -13.8359375, dtype=torch.float16, device=DEV)
+    values = torch.ones(n, dtype=torch.float16, device=DEV)
+    scores[tops], values[tops] = 0.0, 0.0
+    w = torch.exp(scores.double().cpu())
+    want = (w * values.double().cpu()).sum() / w.sum()
+    return scores, values, want, want * 2.5 * 2.0 ** -11
+
+
+def test_paged_small_weights_in_f16():
+    n, heads = 16384, 320  # more heads than the device holds shares of: a warp sees a quarter of the keys
+    scores, values, want, bound = small_weights(n, [0, 16, 32, 48])
+    q = torch.ones(1, heads, 8, dtype=torch.float16, device=DEV)
+    k = torch.zeros(n // 64, 64, heads, 8, dtype=torch.float16, device=DEV)
+    v = torch.zeros_like(k)
+    k[..., 0], v[...] = scores.view(-1, 64, 1), values.view(-1, 64, 1, 1)
+    out, _ = fgemm.attention_paged(q, k, v, torch.arange(n // 64, device=DEV, dtype=torch.int32)[None], ints([n]), scale=1.0)
+    within("paged small weights", out, want.expand(out.shape), bound.expand(out.shape))
+
+
 def test_paged_many_sequences():
     g = gen(7)
     lengths = torch.randint(0, 90, (1500,), generator=torch.Generator().manual_seed(1)).tolist()
@@ -429,6 +453,16 @@ def test_prompt_far_scores():
     for causal in (True, False):
         out, lse = fgemm.attention(q, k, v, ints(starts), causal=causal, scale=1.0)
         check_prompt(q, k, v, starts, starts, causal, 0, out, lse, 1.0, "prompt far scores")
+
+
+def test_prompt_small_weights_in_f16():
+    n = 16384
+    scores, values, want, bound = small_weights(n, [0])
+    q = torch.ones(3, 2, 8, dtype=torch.float16, device=DEV)
+    k, v = torch.zeros(n, 2, 8, dtype=torch.float16, device=DEV), torch.zeros(n, 2, 8, dtype=torch.float16, device=DEV)
+    k[..., 0], v[...] = scores[:, None], values[:, None, None]
+    out, _ = fgemm.attention(q, k, v, ints([0, 3]), k_starts=ints([0, n]), causal=False, scale=1.0)
+    within("prompt small weights", out, want.expand(out.shape), bound.expand(out.shape))
 
 
 def test_prompt_bad_starts_stay_inside():
