@@ -11,15 +11,17 @@
 // rounded to 16 bits for the product with the values, their sum is of the 32-bit ones.
 //
 // Memory-bound: a key and a value are read once for the up to 16 query heads
-// that share them. The query heads of a key head are the 16 rows of a matrix
-// instruction (mma.sync: with 4 flop a byte for each query head, its rate is not
-// what counts), 16 tokens its columns, so scores stay in the registers that the
-// product with the values takes them from. Every warp streams blocks of 16
-// tokens of its own through its own ring of asynchronous copies and keeps its own
-// sums; the warps of a CTA meet once at the end of a sequence's part.
+// that share them. 16 tokens are the rows of a matrix instruction (mma.sync) and 8
+// query heads its columns, one or two of them; a sequence's few heads are the short
+// side, where padding costs least (as the 16 rows, 4 heads of 128 took twice the
+// instructions: one sequence of 512 tokens 8.3 us against 6.9, a ragged batch 211
+// against 205). Scores stay in the registers, transposed eight by eight, for the
+// product with the values. Every warp streams blocks of 16 tokens of its own through
+// its own ring of asynchronous copies and keeps its own sums; the warps of a CTA meet
+// once at the end of a sequence's part.
 //
 // Measured, bf16, 32 heads of 128 over 8 key heads: 64 sequences of up to 16384 tokens
-// 210 us (6.26 TB/s); one of 4097 tokens 10.9 us, of which the memory's part is 2.5: two
+// 205 us (6.41 TB/s); one of 4097 tokens 9.4 us, of which the memory's part is 2.5: two
 // launches, the lengths, the page table, the keys and the parts come one after the
 // other. fp16, 28 heads of 64 over 4, 3 sequences of 131071 tokens 68 us (5.9 TB/s).
 //
@@ -49,19 +51,20 @@ using namespace attn;
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kTokens = 16;                 // of a warp's block
 constexpr int kBlock = kWarps * kTokens;    // tokens of a share's block
-constexpr int kRows = 16;                   // query heads of a CTA
 constexpr int kMostScanned = 512;           // sequences whose blocks the join adds up itself
 constexpr long long kMostTokens = (1LL << 31) - 4096;  // of a sequence: its blocks stay inside 32 bits
 constexpr float kSlack = 8.0f;              // log2 of how far the maximum may be above the reference
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-template <int DP>  // values of a head, padded
+template <int DP, int NT>  // values of a head, padded; eights of query heads
 struct Cfg {
+  static constexpr int kRows = 8 * NT;  // query heads of a CTA
   static constexpr int kCtasPerSm = DP == 128 ? 2 : 3;
   static constexpr int kStages = DP == 128 ? 3 : 4;
   static constexpr int kTile = kTokens * DP * 2;                  // keys (or values) of a block
   static constexpr int kRing = kStages * 2 * kTile;               // of a warp
-  static constexpr int kPart = kRows * DP + 2 * kRows;            // floats of a part: outputs, references, sums
+  static constexpr int kLine = DP + 4;                            // floats of a head's outputs in a part
+  static constexpr int kPart = kRows * kLine + 2 * kRows;         // of a part: outputs, references, sums
   static constexpr int kSmem = kWarps * kRing;
   static_assert(kWarps * kPart * 4 <= kSmem, "the parts of the warps reuse the rings");
   static_assert((kSmem + 4096) * kCtasPerSm <= 227 * 1024, "shared memory");
@@ -70,7 +73,7 @@ struct Cfg {
 struct Plan {
   long long* before;  // seqs + 1: blocks of the sequences before
   float* parts;       // two a CTA
-  int tiles;   // groups of kRows query heads of a key head
+  int tiles;   // groups of 8 NT query heads of a key head
   int units;   // of a sequence: key heads by tiles
   int shares;  // of the blocks of all sequences, each taken by `units` CTAs
 };
@@ -124,6 +127,12 @@ __device__ __forceinline__ void ldmatrix4_t(uint32_t at, uint32_t (&r)[4]) {
                : "r"(at)
                : "memory");
 }
+// Eight rows of eight 16-bit values, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
 template <bool BF16>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if (BF16)
@@ -138,10 +147,11 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <bool BF16, int DP>
-__global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtasPerSm) decode_kernel(const __grid_constant__ DecodeParams p,
+template <bool BF16, int DP, int NT>
+__global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtasPerSm) decode_kernel(const __grid_constant__ DecodeParams p,
                                                                       const __grid_constant__ Plan plan) {
-  using C = Cfg<DP>;
+  using C = Cfg<DP, NT>;
+  constexpr int kRows = C::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long sums[kThreads + 1];  // blocks before the sequences of a thread
   __shared__ uint32_t there[kWarps][C::kStages];  // tokens of a block that are seen, a bit each
@@ -222,43 +232,54 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtasPerSm) decode_kernel(c
     const uint16_t* const k_base = p.k_cache + kv * p.k_head;
     const uint16_t* const v_base = p.v_cache + kv * p.v_head;
 
-    // queries: rows lane / 4 and + 8
-    uint32_t q[DP / 16][4];
+    // queries: heads 8 h + lane / 4
+    uint32_t q[DP / 16][NT][2];
 #pragma unroll
     for (int k = 0; k < DP / 16; ++k)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = lane / 4 + (i & 1) * 8, c = k * 16 + (lane & 3) * 2 + (i >> 1) * 8;
-        q[k][i] = r < rows && c < p.dim
-                      ? *reinterpret_cast<const uint32_t*>(p.q.p + seq * p.q.ld + (head0 + r) * p.q.hs + c)
-                      : 0u;
-      }
-    float o[DP / 8][4];
+      for (int h = 0; h < NT; ++h)
 #pragma unroll
-    for (int n = 0; n < DP / 8; ++n)
+        for (int i = 0; i < 2; ++i) {
+          const int r = h * 8 + lane / 4, c = k * 16 + (lane & 3) * 2 + i * 8;
+          q[k][h][i] = r < rows && c < p.dim
+                           ? *reinterpret_cast<const uint32_t*>(p.q.p + seq * p.q.ld + (head0 + r) * p.q.hs + c)
+                           : 0u;
+        }
+    // outputs: values lane / 4 (and + 8) of sixteen, heads 8 h + (lane & 3) * 2 (and + 1)
+    float o[DP / 16][NT][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[n][i] = 0.0f;
-    float ref[2] = {-INFINITY, -INFINITY}, sum[2] = {0.0f, 0.0f};
+    for (int n = 0; n < DP / 16; ++n)
+#pragma unroll
+      for (int h = 0; h < NT; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[n][h][i] = 0.0f;
+    float ref[NT][2], sum[NT][2];  // of these heads
+#pragma unroll
+    for (int h = 0; h < NT; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) ref[h][e] = -INFINITY, sum[h][e] = 0.0f;
 
     const int mine = t1 - t0 > warp * kTokens ? (t1 - t0 - warp * kTokens + kBlock - 1) / kBlock : 0;  // blocks of this warp
     auto token = [&](int i) { return t0 + warp * kTokens + i * kBlock + (lane & 15); };  // of the span
-    auto page_of = [&](int i) {  // lanes 0..15 (and again 16..31): the page of a token of block i, -1: not seen
+    // Lanes 0..15 (and again 16..31): the page of a token of block i, as the table has
+    // it (looked up two blocks ahead); -1: not seen.
+    auto page_of = [&](int i) {
       const int t = token(i);
       if (i >= mine || t >= t1) return -1;
-      const int page = table[(span.first + t) / p.page_size];
-      return page >= 0 && page < p.pages ? page : -1;
+      return table[(span.first + t) / p.page_size];
     };
-    int page = page_of(0);
+    int page = page_of(0), page_next = page_of(1);
     auto load = [&](int i) {
       const int stage = i % C::kStages;
       if (i < mine) {
-        const bool seen = page >= 0;
+        const bool seen = page >= 0 && page < p.pages;
         const uint32_t mask = __ballot_sync(0xFFFFFFFFu, seen) & 0xFFFFu;
         if (lane == 0) there[warp][stage] = mask;
         const long long in_page = seen ? (span.first + token(i)) % p.page_size : 0;
         const long long k_off = seen ? page * p.k_page + in_page * p.k_token : 0;
         const long long v_off = alike || !seen ? k_off : page * p.v_page + in_page * p.v_token;
-        page = page_of(i + 1);
+        page = page_next;
+        page_next = page_of(i + 2);
         constexpr int kChunks = DP / 8, kRowsAtOnce = 32 / kChunks;
         const int chunk = lane % kChunks;
         const uint32_t to = ring + stage * 2 * C::kTile;
@@ -284,94 +305,102 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtasPerSm) decode_kernel(c
       __syncwarp();
       const int stage = i % C::kStages;
       const uint32_t keys = ring + stage * 2 * C::kTile, values = keys + C::kTile;
-      // scores of 16 heads by 16 tokens
-      float s[2][4] = {};
+      // scores of 16 tokens by 8 NT heads, in two sums
+      float s[NT][4] = {}, s2[NT][4] = {};
 #pragma unroll
       for (int k = 0; k < DP / 16; ++k) {
-        uint32_t kb[4];
-        const int r = (lane & 7) + (lane >> 4) * 8, c = 2 * k + ((lane >> 3) & 1);
-        ldmatrix4(keys + r * DP * 2 + ((c ^ (r & 7)) << 4), kb);
-        mma<BF16>(s[0], q[k], kb[0], kb[1]);
-        mma<BF16>(s[1], q[k], kb[2], kb[3]);
+        uint32_t ka[4];
+        const int r = lane & 15, c = 2 * k + (lane >> 4);
+        ldmatrix4(keys + r * DP * 2 + ((c ^ (r & 7)) << 4), ka);
+#pragma unroll
+        for (int h = 0; h < NT; ++h) mma<BF16>(NT == 1 && (k & 1) ? s2[h] : s[h], ka, q[k][h][0], q[k][h][1]);
       }
-      const uint32_t mask = there[warp][stage];
-      float most[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bool seen = (mask >> (n * 8 + (lane & 3) * 2 + (e & 1))) & 1u;
-          s[n][e] = seen ? s[n][e] * to_log2 : -INFINITY;
-          most[e >> 1] = fmaxf(most[e >> 1], s[n][e]);
-        }
+      const uint32_t mask = there[warp][stage] >> (lane / 4);  // bits 0 and 8: this lane's tokens
+      float most[NT][2];
       bool far = false;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        most[h] = fmaxf(most[h], __shfl_xor_sync(0xFFFFFFFFu, most[h], 1));
-        most[h] = fmaxf(most[h], __shfl_xor_sync(0xFFFFFFFFu, most[h], 2));
-        far |= most[h] > ref[h] + kSlack;
-      }
+      for (int h = 0; h < NT; ++h)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int i = e; i < 4; i += 2) {
+            const float x = NT == 1 ? s[h][i] + s2[h][i] : s[h][i];
+            s[h][i] = (mask >> (i >> 1) * 8) & 1u ? x * to_log2 : -INFINITY;
+          }
+          most[h][e] = fmaxf(s[h][e], s[h][e + 2]);
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) most[h][e] = fmaxf(most[h][e], __shfl_xor_sync(0xFFFFFFFFu, most[h][e], d));
+          far |= most[h][e] > ref[h][e] + kSlack;
+        }
       if (__any_sync(0xFFFFFFFFu, far)) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float to = fmaxf(ref[h], most[h]);
-          const float f = to == -INFINITY ? 1.0f : exp2_fast(ref[h] - to);
-          ref[h] = to;
-          sum[h] *= f;
+        for (int h = 0; h < NT; ++h)
 #pragma unroll
-          for (int n = 0; n < DP / 8; ++n) {
-            o[n][2 * h] *= f;
-            o[n][2 * h + 1] *= f;
+          for (int e = 0; e < 2; ++e) {
+            const float to = fmaxf(ref[h][e], most[h][e]);
+            const float f = to == -INFINITY ? 1.0f : exp2_fast(ref[h][e] - to);
+            ref[h][e] = to;
+            sum[h][e] *= f;
+#pragma unroll
+            for (int n = 0; n < DP / 16; ++n) {
+              o[n][h][e] *= f;
+              o[n][h][e + 2] *= f;
+            }
+          }
+      }
+      uint32_t w[NT][2];
+#pragma unroll
+      for (int h = 0; h < NT; ++h) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float base = ref[h][e] == -INFINITY ? 0.0f : ref[h][e] - kLift;
+#pragma unroll
+          for (int i = e; i < 4; i += 2) {
+            s[h][i] = exp2_fast(s[h][i] - base);
+            sum[h][e] += s[h][i];
           }
         }
+        w[h][0] = transposed(pack2<BF16>(s[h][0], s[h][1]));
+        w[h][1] = transposed(pack2<BF16>(s[h][2], s[h][3]));
       }
-      float base[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) base[h] = ref[h] == -INFINITY ? 0.0f : ref[h] - kLift;
-      uint32_t w[4];
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float x = exp2_fast(s[n][2 * h] - base[h]), y = exp2_fast(s[n][2 * h + 1] - base[h]);
-          sum[h] += x + y;
-          w[n * 2 + h] = pack2<BF16>(x, y);
-        }
 #pragma unroll
       for (int n = 0; n < DP / 16; ++n) {
-        uint32_t vb[4];
-        const int r = lane & 15, c = 2 * n + (lane >> 4);
-        ldmatrix4_t(values + r * DP * 2 + ((c ^ (r & 7)) << 4), vb);
-        mma<BF16>(o[2 * n], w, vb[0], vb[1]);
-        mma<BF16>(o[2 * n + 1], w, vb[2], vb[3]);
+        uint32_t va[4];
+        const int r = (lane & 7) + (lane >> 4) * 8, c = 2 * n + ((lane >> 3) & 1);
+        ldmatrix4_t(values + r * DP * 2 + ((c ^ (r & 7)) << 4), va);
+#pragma unroll
+        for (int h = 0; h < NT; ++h) mma<BF16>(o[n][h], va, w[h][0], w[h][1]);
       }
       __syncwarp();  // the stage that is loaded next has been read
       load(i + C::kStages - 1);
     }
     copies_wait<0>();
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      sum[h] += __shfl_xor_sync(0xFFFFFFFFu, sum[h], 1);
-      sum[h] += __shfl_xor_sync(0xFFFFFFFFu, sum[h], 2);
-    }
+    for (int h = 0; h < NT; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) sum[h][e] += __shfl_xor_sync(0xFFFFFFFFu, sum[h][e], d);
     // ---- the warps meet over their rings
     __syncthreads();
     float* const parts = reinterpret_cast<float*>(smem);
     {
       float* const part = parts + warp * C::kPart;
 #pragma unroll
-      for (int n = 0; n < DP / 8; ++n)
+      for (int h = 0; h < NT; ++h)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          *reinterpret_cast<float2*>(part + (lane / 4 + h * 8) * DP + n * 8 + (lane & 3) * 2) =
-              make_float2(o[n][2 * h], o[n][2 * h + 1]);
-      if ((lane & 3) == 0) {
+        for (int e = 0; e < 2; ++e) {
+          const int r = h * 8 + (lane & 3) * 2 + e;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          part[kRows * DP + lane / 4 + h * 8] = ref[h] - kLift;
-          part[kRows * DP + kRows + lane / 4 + h * 8] = sum[h];
+          for (int n = 0; n < DP / 16; ++n) {
+            part[r * C::kLine + n * 16 + lane / 4] = o[n][h][e];
+            part[r * C::kLine + n * 16 + lane / 4 + 8] = o[n][h][e + 2];
+          }
+          if (lane < 4) {
+            part[kRows * C::kLine + r] = ref[h][e] - kLift;
+            part[kRows * C::kLine + kRows + r] = sum[h][e];
+          }
         }
-      }
     }
     __syncthreads();
     const bool whole = unit0 >= b0 && unit1 <= b1;
@@ -380,23 +409,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtasPerSm) decode_kernel(c
       const int r = e / (DP / 4), c = e % (DP / 4) * 4;
       float top = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, parts[w * C::kPart + kRows * DP + r]);
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, parts[w * C::kPart + kRows * C::kLine + r]);
       float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       float z = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float* const part = parts + w * C::kPart;
-        const float mr = part[kRows * DP + r];
+        const float mr = part[kRows * C::kLine + r];
         const float f = scale_of(mr, top);
-        const float4 x = *reinterpret_cast<const float4*>(part + r * DP + c);
-        z += f * part[kRows * DP + kRows + r];
+        const float4 x = *reinterpret_cast<const float4*>(part + r * C::kLine + c);
+        z += f * part[kRows * C::kLine + kRows + r];
         acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
       }
       if (!whole) {
-        *reinterpret_cast<float4*>(to + r * DP + c) = acc;
+        *reinterpret_cast<float4*>(to + r * C::kLine + c) = acc;
         if (c == 0) {
-          to[kRows * DP + r] = top;
-          to[kRows * DP + kRows + r] = z;
+          to[kRows * C::kLine + r] = top;
+          to[kRows * C::kLine + kRows + r] = z;
         }
       } else if (c < p.dim) {
         const float inv = z == 0.0f ? 0.0f : 1.0f / z;
@@ -419,10 +448,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtasPerSm) decode_kernel(c
 // kJoinWarps-th behind it, or zeros where there is nothing. What does not come from
 // the first kernel is done while that one runs.
 constexpr int kJoinWarps = 8, kJoinThreads = kJoinWarps * 32;
-template <bool BF16, int DP>
+template <bool BF16, int DP, int NT>
 __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_constant__ DecodeParams p,
                                                                    const __grid_constant__ Plan plan) {
-  using C = Cfg<DP>;
+  using C = Cfg<DP, NT>;
+  constexpr int kRows = C::kRows;
   __shared__ float4 outs[kJoinWarps][32];
   __shared__ float refs[kJoinWarps], sums[kJoinWarps];
   __shared__ long long blocks_sum[2][kJoinWarps];
@@ -478,9 +508,9 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
       ref[i] = -INFINITY, sum[i] = 0.0f, v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (at <= c1) {
         const float* const x = part(at);
-        ref[i] = x[kRows * DP + r];
-        sum[i] = x[kRows * DP + kRows + r];
-        if (lane * 4 < DP) v[i] = *reinterpret_cast<const float4*>(x + r * DP + lane * 4);
+        ref[i] = x[kRows * C::kLine + r];
+        sum[i] = x[kRows * C::kLine + kRows + r];
+        if (lane * 4 < DP) v[i] = *reinterpret_cast<const float4*>(x + r * C::kLine + lane * 4);
       }
     }
     const float to = fmaxf(top, fmaxf(fmaxf(ref[0], ref[1]), fmaxf(ref[2], ref[3])));
@@ -517,15 +547,18 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
   if (p.lse && lane == 0) p.lse[blockIdx.x] = z == 0.0f ? -INFINITY : (top + log2f(z)) * kLn2;
 }
 
+// Query heads of a CTA in eights: matrix instructions of 16 tokens by 8 heads.
+int eights_of(int heads, int kv_heads) { return heads / kv_heads <= 8 ? 1 : 2; }
+
 size_t before_bytes(int seqs) { return (static_cast<size_t>(seqs) + 1 + 1) / 2 * 16; }
 
-template <bool BF16, int DP>
+template <bool BF16, int DP, int NT>
 cudaError_t launch_of(const DecodeParams& p, const Plan& plan, cudaStream_t stream) {
   static unsigned long long devices = 0;
-  auto kernel = decode_kernel<BF16, DP>;
-  cudaError_t e = with_smem(kernel, Cfg<DP>::kSmem, devices);
+  auto kernel = decode_kernel<BF16, DP, NT>;
+  cudaError_t e = with_smem(kernel, Cfg<DP, NT>::kSmem, devices);
   if (e != cudaSuccess) return e;
-  kernel<<<plan.shares * plan.units, kThreads, Cfg<DP>::kSmem, stream>>>(p, plan);
+  kernel<<<plan.shares * plan.units, kThreads, Cfg<DP, NT>::kSmem, stream>>>(p, plan);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -537,20 +570,31 @@ cudaError_t launch_of(const DecodeParams& p, const Plan& plan, cudaStream_t stre
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_join_kernel<BF16, DP>, p, plan);
+  return cudaLaunchKernelEx(&cfg, decode_join_kernel<BF16, DP, NT>, p, plan);
 }
 
-}  // namespace
+template <bool BF16, int DP>
+cudaError_t launch_rows(const DecodeParams& p, const Plan& plan, cudaStream_t stream) {
+  return eights_of(p.heads, p.kv_heads) == 1 ? launch_of<BF16, DP, 1>(p, plan, stream)
+                                             : launch_of<BF16, DP, 2>(p, plan, stream);
+}
 
-namespace {
-int tiles_of(int heads, int kv_heads) { return (heads / kv_heads + kRows - 1) / kRows; }
+int tiles_of(int heads, int kv_heads) {
+  const int rows = 8 * eights_of(heads, kv_heads);
+  return (heads / kv_heads + rows - 1) / rows;
+}
 int shares_held(int units, int dim, int num_sms) {
-  return std::max(num_sms * (dim > 64 ? Cfg<128>::kCtasPerSm : Cfg<64>::kCtasPerSm) / units, 1);
+  return std::max(num_sms * (dim > 64 ? Cfg<128, 1>::kCtasPerSm : Cfg<64, 1>::kCtasPerSm) / units, 1);
 }
+template <int DP>
+size_t part_bytes(int heads, int kv_heads) {
+  return (eights_of(heads, kv_heads) == 1 ? Cfg<DP, 1>::kPart : Cfg<DP, 2>::kPart) * sizeof(float);
+}
+
 }  // namespace
 
 size_t decode_workspace(int seqs, int heads, int kv_heads, int dim, int num_sms) {
-  const size_t part = static_cast<size_t>(dim > 64 ? Cfg<128>::kPart : Cfg<64>::kPart) * 4;
+  const size_t part = dim > 64 ? part_bytes<128>(heads, kv_heads) : part_bytes<64>(heads, kv_heads);
   const int units = kv_heads * tiles_of(heads, kv_heads);
   return before_bytes(seqs) + static_cast<size_t>(shares_held(units, dim, num_sms)) * units * 2 * part;
 }
@@ -563,8 +607,8 @@ cudaError_t launch_decode(const DecodeParams& p, void* workspace, int num_sms, c
   plan.units = p.kv_heads * plan.tiles;
   plan.shares = shares_held(plan.units, p.dim, num_sms);
   if (p.dim > 64)
-    return p.is_bf16 ? launch_of<true, 128>(p, plan, stream) : launch_of<false, 128>(p, plan, stream);
-  return p.is_bf16 ? launch_of<true, 64>(p, plan, stream) : launch_of<false, 64>(p, plan, stream);
+    return p.is_bf16 ? launch_rows<true, 128>(p, plan, stream) : launch_rows<false, 128>(p, plan, stream);
+  return p.is_bf16 ? launch_rows<true, 64>(p, plan, stream) : launch_rows<false, 64>(p, plan, stream);
 }
 
 }  // namespace fgemm

@@ -175,6 +175,15 @@ def test_paged_groups(dtype, heads, kv_heads):
     check_paged(q, keys, values, 0, 0.2, out, lse)
 
 
+@pytest.mark.parametrize("heads,kv_heads", [(8, 1), (9, 1), (15, 1), (32, 1), (33, 1), (18, 2)])
+@pytest.mark.parametrize("dim", [40, 104])
+def test_paged_groups_at_the_edges_of_tiles(heads, kv_heads, dim):
+    lengths = [65, 0, 500, 17]
+    q, k, v, table, n, keys, values = paged_inputs(gen(27), lengths, heads, kv_heads, dim, 11, torch.float16)
+    out, lse = fgemm.attention_paged(q, k, v, table, n, window=300)
+    check_paged(q, keys, values, 300, None, out, lse, "paged edges of tiles")
+
+
 @pytest.mark.parametrize("layout", LAYOUTS)
 def test_paged_layouts_and_in_place(layout):
     lengths = [37, 0, 400, 129]
