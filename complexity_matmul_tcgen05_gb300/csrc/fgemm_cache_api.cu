@@ -152,7 +152,7 @@ size_t fgemm_attention_paged_workspace(fgemm_handle_t h, int64_t seqs, int32_t h
   if (!h || seqs <= 0 || seqs > kMaxSeqs || heads < 1 || heads > kMaxHeads || kv_heads < 1 || heads % kv_heads != 0 ||
       dim < 8 || dim > FGEMM_MAX_HEAD_DIM || dim % 8 != 0)
     return 0;
-  return fgemm::decode_workspace(static_cast<int>(seqs), heads, kv_heads, dim, fgemm::handle_sms(h));
+  return fgemm::decode_workspace(heads, kv_heads, dim, fgemm::handle_sms(h));
 }
 
 fgemm_status_t fgemm_attention_paged(fgemm_handle_t h, int64_t seqs, int32_t heads, int32_t kv_heads, int32_t dim,
@@ -180,7 +180,7 @@ fgemm_status_t fgemm_attention_paged(fgemm_handle_t h, int64_t seqs, int32_t hea
     return bad_arg(h, "out over q needs q's strides");
   if (!h) return no_handle();
   const int sms = fgemm::handle_sms(h);
-  const size_t need = fgemm::decode_workspace(static_cast<int>(seqs), heads, kv_heads, dim, sms);
+  const size_t need = fgemm::decode_workspace(heads, kv_heads, dim, sms);
   if (need > 0 && (!workspace || workspace_bytes < need))
     return bad_arg(h, "the workspace is smaller than fgemm_attention_paged_workspace says");
   if (need > 0 && off(workspace, 16)) return bad(h, FGEMM_ERR_ALIGNMENT, "workspace must be 16-byte aligned");

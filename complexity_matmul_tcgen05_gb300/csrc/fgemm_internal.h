@@ -485,7 +485,7 @@ struct DecodeParams {
   int seqs, heads, kv_heads, dim, page_size, table_pages, window, is_bf16;
   float scale;
 };
-size_t decode_workspace(int seqs, int heads, int kv_heads, int dim, int num_sms);
+size_t decode_workspace(int heads, int kv_heads, int dim, int num_sms);
 cudaError_t launch_decode(const DecodeParams& p, void* workspace, int num_sms, cudaStream_t stream);
 
 // Attention over packed prompts (fgemm_kern_prompt.cu).

@@ -15,15 +15,16 @@
 // query heads its columns, one or two of them; a sequence's few heads are the short
 // side, where padding costs least (as the 16 rows, 4 heads of 128 took twice the
 // instructions: one sequence of 512 tokens 8.3 us against 6.9, a ragged batch 211
-// against 205). Scores stay in the registers, transposed eight by eight, for the
+// against 205 then). Scores stay in the registers, transposed eight by eight, for the
 // product with the values. Every warp streams blocks of 16 tokens of its own through
 // its own ring of asynchronous copies and keeps its own sums; the warps of a CTA meet
 // once at the end of a sequence's part.
 //
 // Measured, bf16, 32 heads of 128 over 8 key heads: 64 sequences of up to 16384 tokens
-// 205 us (6.41 TB/s); one of 4097 tokens 9.4 us, of which the memory's part is 2.5: two
-// launches, the lengths, the page table, the keys and the parts come one after the
-// other. fp16, 28 heads of 64 over 4, 3 sequences of 131071 tokens 68 us (5.9 TB/s).
+// 203 us (6.48 TB/s), 256 of 300 tokens 68 us (4.6 TB/s); one of 4097 tokens 9.5 us, of
+// which the memory's part is 2.5: two launches, the lengths, the page table, the keys and
+// the parts come one after the other. fp16, 28 heads of 64 over 4, 3 sequences of 131071
+// tokens 67 us (6.0 TB/s).
 //
 // The work of all sequences, in blocks of 64 tokens laid end to end, is cut into
 // equal shares on the device: lengths are not known to the host. A share is taken by
@@ -51,7 +52,6 @@ using namespace attn;
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kTokens = 16;                 // of a warp's block
 constexpr int kBlock = kWarps * kTokens;    // tokens of a share's block
-constexpr int kMostScanned = 512;           // sequences whose blocks the join adds up itself
 constexpr long long kMostTokens = (1LL << 31) - 4096;  // of a sequence: its blocks stay inside 32 bits
 constexpr float kSlack = 8.0f;              // log2 of how far the maximum may be above the reference
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -70,9 +70,14 @@ struct Cfg {
   static_assert((kSmem + 4096) * kCtasPerSm <= 227 * 1024, "shared memory");
 };
 
+// The sequence that begins in a share and ends in a later one, `last`; seq -1: none.
+struct Straddle {
+  int seq, last;
+};
+
 struct Plan {
-  long long* before;  // seqs + 1: blocks of the sequences before
-  float* parts;       // two a CTA
+  Straddle* straddles;  // by share
+  float* parts;         // two a CTA
   int tiles;   // groups of 8 NT query heads of a key head
   int units;   // of a sequence: key heads by tiles
   int shares;  // of the blocks of all sequences, each taken by `units` CTAs
@@ -179,18 +184,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtasPerSm) decode_kern
     sums[threadIdx.x] = start + scan - n;
     if (threadIdx.x == kThreads - 1) sums[kThreads] = start + scan;
     __syncthreads();
-    if (blockIdx.x == 0) {  // for the join
-      long long at = sums[threadIdx.x];
-      for (int s = s0; s < s1; ++s) {
-        plan.before[s] = at;
-        at += blocks_of(p, s);
-      }
-      if (threadIdx.x == 0) plan.before[p.seqs] = sums[kThreads];
-    }
   }
+  // Sequences of which nothing is seen: rows of zeros.
+  for (int s = share + static_cast<int>(threadIdx.x) * plan.shares; s < p.seqs; s += kThreads * plan.shares)
+    if (blocks_of(p, s) == 0) {
+      const int group = p.heads / p.kv_heads, kv = unit / plan.tiles, row0 = unit % plan.tiles * kRows;
+      for (int head = kv * group + row0; head < kv * group + min(group, row0 + kRows); ++head) {
+        uint4* const out = reinterpret_cast<uint4*>(p.out.p + s * p.out.ld + head * p.out.hs);
+        for (int c = 0; c < p.dim / 8; ++c) out[c] = make_uint4(0, 0, 0, 0);
+        if (p.lse) p.lse[static_cast<long long>(s) * p.heads + head] = -INFINITY;
+      }
+    }
   const long long total = sums[kThreads];
   const long long size = share_of(total, plan.shares), b0 = share * size, b1 = min(b0 + size, total);
-  if (b0 >= b1) return;
+  Straddle straddle{-1, 0};
+  if (b0 >= b1) {
+    if (unit == 0 && threadIdx.x == 0) plan.straddles[share] = straddle;
+    return;
+  }
   // the sequence of block b0
   int seq;
   long long at;  // blocks before it
@@ -404,6 +415,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtasPerSm) decode_kern
     }
     __syncthreads();
     const bool whole = unit0 >= b0 && unit1 <= b1;
+    if (unit0 >= b0 && unit1 > b1) straddle = {seq, static_cast<int>((unit1 - 1) / size)};
     float* const to = plan.parts + (2LL * blockIdx.x + (unit0 >= b0 ? 1 : 0)) * C::kPart;
     for (int e = threadIdx.x; e < rows * (DP / 4); e += kThreads) {
       const int r = e / (DP / 4), c = e % (DP / 4) * 4;
@@ -442,11 +454,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtasPerSm) decode_kern
       ++seq;
     }
   }
+  if (unit == 0 && threadIdx.x == 0) plan.straddles[share] = straddle;
 }
 
-// One CTA a query head: the parts of its unit, warp w taking part w and every
-// kJoinWarps-th behind it, or zeros where there is nothing. What does not come from
-// the first kernel is done while that one runs.
+// Joins the parts of a query head's unit, warp w taking part w and every kJoinWarps-th
+// behind it. A CTA a sequence and head, which finds the sequence's shares while the first
+// kernel runs; or, where the sequences are more than the shares, a CTA a share and head:
+// of many short sequences few lie in two shares (256 of 300 tokens, 32 heads of 128
+// over 8: 68 us; with 8192 CTAs, most of them without parts, 86).
 constexpr int kJoinWarps = 8, kJoinThreads = kJoinWarps * 32;
 template <bool BF16, int DP, int NT>
 __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_constant__ DecodeParams p,
@@ -457,10 +472,11 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
   __shared__ float refs[kJoinWarps], sums[kJoinWarps];
   __shared__ long long blocks_sum[2][kJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int seq = blockIdx.x / p.heads, head = blockIdx.x % p.heads, group = p.heads / p.kv_heads;
-  long long before, total;
-  const long long blocks = blocks_of(p, seq);
-  if (p.seqs <= kMostScanned) {
+  int seq = blockIdx.x / p.heads;
+  const int head = blockIdx.x % p.heads, group = p.heads / p.kv_heads;
+  int c0, c1;  // the sequence's shares
+  if (p.seqs <= plan.shares) {
+    const long long blocks = blocks_of(p, seq);
     long long all = 0, ahead = 0;
     for (int s = threadIdx.x; s < p.seqs; s += kJoinThreads) {
       const int n = blocks_of(p, s);
@@ -474,24 +490,22 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
     }
     if (lane == 0) blocks_sum[0][warp] = all, blocks_sum[1][warp] = ahead;
     __syncthreads();
-    total = before = 0;
+    long long total = 0, before = 0;
     for (int w = 0; w < kJoinWarps; ++w) total += blocks_sum[0][w], before += blocks_sum[1][w];
+    const long long size = share_of(total, plan.shares);
+    c0 = static_cast<int>(before / size);
+    c1 = blocks > 0 ? static_cast<int>((before + blocks - 1) / size) : c0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
   } else {
+    c0 = seq;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    before = plan.before[seq];
-    total = plan.before[p.seqs];
+    const Straddle x = plan.straddles[c0];
+    seq = x.seq;
+    c1 = seq >= 0 ? x.last : c0;
   }
-  uint16_t* const out = p.out.p + seq * p.out.ld + head * p.out.hs;
-  if (blocks == 0) {
-    if (threadIdx.x < p.dim / 8) reinterpret_cast<uint4*>(out)[threadIdx.x] = make_uint4(0, 0, 0, 0);
-    if (p.lse && threadIdx.x == 0) p.lse[blockIdx.x] = -INFINITY;
-    return;
-  }
-  const int unit = head / group * plan.tiles + head % group / kRows, r = head % group % kRows;
-  const long long size = share_of(total, plan.shares);
-  const int c0 = static_cast<int>(before / size), c1 = static_cast<int>((before + blocks - 1) / size);
   if (c0 == c1) return;
+  uint16_t* const out = p.out.p + seq * p.out.ld + head * p.out.hs;
+  const int unit = head / group * plan.tiles + head % group / kRows, r = head % group % kRows;
   float top = -INFINITY, z = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   auto part = [&](int c) {
@@ -544,13 +558,13 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
   if (lane * 4 < p.dim)
     *reinterpret_cast<uint2*>(out + lane * 4) =
         make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
-  if (p.lse && lane == 0) p.lse[blockIdx.x] = z == 0.0f ? -INFINITY : (top + log2f(z)) * kLn2;
+  if (p.lse && lane == 0) p.lse[static_cast<long long>(seq) * p.heads + head] = z == 0.0f ? -INFINITY : (top + log2f(z)) * kLn2;
 }
 
 // Query heads of a CTA in eights: matrix instructions of 16 tokens by 8 heads.
 int eights_of(int heads, int kv_heads) { return heads / kv_heads <= 8 ? 1 : 2; }
 
-size_t before_bytes(int seqs) { return (static_cast<size_t>(seqs) + 1 + 1) / 2 * 16; }
+size_t straddle_bytes(int shares) { return (static_cast<size_t>(shares) + 1) / 2 * 16; }
 
 template <bool BF16, int DP, int NT>
 cudaError_t launch_of(const DecodeParams& p, const Plan& plan, cudaStream_t stream) {
@@ -562,7 +576,7 @@ cudaError_t launch_of(const DecodeParams& p, const Plan& plan, cudaStream_t stre
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.seqs) * static_cast<unsigned>(p.heads));
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min(p.seqs, plan.shares)) * static_cast<unsigned>(p.heads));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
@@ -593,19 +607,19 @@ size_t part_bytes(int heads, int kv_heads) {
 
 }  // namespace
 
-size_t decode_workspace(int seqs, int heads, int kv_heads, int dim, int num_sms) {
+size_t decode_workspace(int heads, int kv_heads, int dim, int num_sms) {
   const size_t part = dim > 64 ? part_bytes<128>(heads, kv_heads) : part_bytes<64>(heads, kv_heads);
-  const int units = kv_heads * tiles_of(heads, kv_heads);
-  return before_bytes(seqs) + static_cast<size_t>(shares_held(units, dim, num_sms)) * units * 2 * part;
+  const int units = kv_heads * tiles_of(heads, kv_heads), shares = shares_held(units, dim, num_sms);
+  return straddle_bytes(shares) + static_cast<size_t>(shares) * units * 2 * part;
 }
 
 cudaError_t launch_decode(const DecodeParams& p, void* workspace, int num_sms, cudaStream_t stream) {
   Plan plan;
-  plan.before = static_cast<long long*>(workspace);
-  plan.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + before_bytes(p.seqs));
   plan.tiles = tiles_of(p.heads, p.kv_heads);
   plan.units = p.kv_heads * plan.tiles;
   plan.shares = shares_held(plan.units, p.dim, num_sms);
+  plan.straddles = static_cast<Straddle*>(workspace);
+  plan.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + straddle_bytes(plan.shares));
   if (p.dim > 64)
     return p.is_bf16 ? launch_rows<true, 128>(p, plan, stream) : launch_rows<false, 128>(p, plan, stream);
   return p.is_bf16 ? launch_rows<true, 64>(p, plan, stream) : launch_rows<false, 64>(p, plan, stream);

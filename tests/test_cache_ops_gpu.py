@@ -262,6 +262,18 @@ def test_paged_long_context_and_repeatable():
         assert torch.equal(out, o2) and torch.equal(lse, l2)
 
 
+def test_paged_long_short_and_empty_sequences():
+    """More sequences than shares, some of them in many shares."""
+    lengths = [0] * 30 + [5000] + [3] * 20 + [0, 700, 0] + [64] * 40 + [9000, 0]
+    q, k, v, table, n, keys, values = paged_inputs(gen(28), lengths, 16, 8, 72, 16, torch.bfloat16)
+    for _ in range(2):
+        out, lse = fgemm.attention_paged(q, k, v, table, n)
+        check_paged(q, keys, values, 0, None, out, lse, "paged mixed lengths")
+    plain = out.clone()
+    out, lse2 = fgemm.attention_paged(q, k, v, table, n, out=q)
+    assert out is q and torch.equal(out, plain) and torch.equal(lse, lse2)
+
+
 def small_weights(n, tops):
     """n keys with scores of 0 at `tops` and -13.8 elsewhere, which many make count: a
     weight is 16.44 * 2^-24, between two of fp16's steps there.  Values are 0 and 1.  Also the
