@@ -481,7 +481,7 @@ typedef struct {
 /*
  * Rotary positions of queries and keys, and the write of keys and values into
  * a paged cache. For token t and i < rot / 2, with
- * angle = positions[t] * inv_freq[i] (formed in 64 bits), a pair (a, b) becomes
+ * angle = positions[t] * inv_freq[i] (less its whole turns, to 2^-32 turns), a pair (a, b) becomes
  *   (a cos - b sin, b cos + a sin)       in fp32, rounded once;
  * pairs are values i and i + rot / 2 of a head, or 2 i and 2 i + 1 where
  * interleaved is not 0; values from rot on stay as they are.

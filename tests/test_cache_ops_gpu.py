@@ -2,6 +2,7 @@
 (cache_reference.py), at the sizes, strides, masks and special values where
 they can go wrong."""
 import math
+from fractions import Fraction
 
 import pytest
 import torch
@@ -110,6 +111,31 @@ def test_rotary_layouts_padding_slots_and_in_place(layout, interleaved):
     check_rotary(*a, interleaved, out)
     same = fgemm.rotary_cache(*a, interleaved=interleaved, out=q)
     assert same is q and torch.equal(q, out) and not torch.equal(q, before)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rotary_any_frequency_and_position(interleaved):
+    """Against angles reduced exactly: of every size of frequency, at the last positions."""
+    freq = torch.tensor([1.0, -0.37, 1e-40, 3.1e-9, 1.9999999, 2.0, -1234.5678, 7.7e22], device=DEV)
+    positions = ints([0, 1, -1, 12345, 999999937, 2 ** 31 - 1, -2 ** 31])
+    turn = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899"
+                        "8628034825342117067982148086513282306647093844609550582231725359408128481117450")
+    angle = torch.tensor([[float((Fraction(f) * n) % turn) for f in freq.tolist()] for n in positions.tolist()],
+                         dtype=torch.float64)
+    n, half = angle.shape
+    q, k, v = (rand(gen(29), n, 1, 2 * half).bfloat16() for _ in range(3))
+    cache = [torch.zeros(1, n, 1, 2 * half, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    out = fgemm.rotary_cache(q, k, v, positions, ints(range(n)), freq, *cache, interleaved=interleaved)
+    # (the reference forms position * frequency: positions of 1 leave the angles as they are)
+    for row in range(n):
+        want, b = ref.rotate(ref.f64(q[row:row + 1]), torch.ones(1), angle[row], interleaved)
+        within("rotary any frequency", out[row:row + 1], want, b + ref.store(want, torch.bfloat16))
+    freq[2], freq[5] = NAN, INF
+    out = fgemm.rotary_cache(q, k, v, positions, ints(range(n)), freq, *cache, interleaved=interleaved)
+    at = torch.tensor([4, 5, 10, 11] if interleaved else [2, 5, half + 2, half + 5])
+    lost = torch.zeros(2 * half, dtype=torch.bool)
+    lost[at] = True
+    assert bool(torch.isnan(out[..., lost.to(DEV)]).all()) and bool(torch.isfinite(out[..., ~lost.to(DEV)]).all())
 
 
 def test_rotary_many_tokens_far_and_negative_positions():
