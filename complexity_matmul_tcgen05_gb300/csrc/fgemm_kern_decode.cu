@@ -99,7 +99,9 @@ __device__ __forceinline__ int blocks_of(const DecodeParams& p, int s) {
 }
 
 // Blocks of a share; share i begins at block i times that.
-__device__ __forceinline__ long long share_of(long long total, int shares) { return max((total + shares - 1) / shares, 1LL); }
+__device__ __forceinline__ long long share_of(long long total, int shares) {
+  return max((total + shares - 1) / shares, 1LL);
+}
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -270,7 +272,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtasPerSm) decode_kern
 #pragma unroll
       for (int e = 0; e < 2; ++e) ref[h][e] = -INFINITY, sum[h][e] = 0.0f;
 
-    const int mine = t1 - t0 > warp * kTokens ? (t1 - t0 - warp * kTokens + kBlock - 1) / kBlock : 0;  // blocks of this warp
+    // blocks of this warp
+    const int mine = t1 - t0 > warp * kTokens ? (t1 - t0 - warp * kTokens + kBlock - 1) / kBlock : 0;
     auto token = [&](int i) { return t0 + warp * kTokens + i * kBlock + (lane & 15); };  // of the span
     // Lanes 0..15 (and again 16..31): the page of a token of block i, as the table has
     // it (looked up two blocks ahead); -1: not seen.
@@ -558,7 +561,8 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
   if (lane * 4 < p.dim)
     *reinterpret_cast<uint2*>(out + lane * 4) =
         make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
-  if (p.lse && lane == 0) p.lse[static_cast<long long>(seq) * p.heads + head] = z == 0.0f ? -INFINITY : (top + log2f(z)) * kLn2;
+  if (p.lse && lane == 0)
+    p.lse[static_cast<long long>(seq) * p.heads + head] = z == 0.0f ? -INFINITY : (top + log2f(z)) * kLn2;
 }
 
 // Query heads of a CTA in eights: matrix instructions of 16 tokens by 8 heads.
