@@ -309,8 +309,10 @@ struct Tile {
 __device__ __forceinline__ int key_end(const PromptParams& p, int at, int keys) {
   return p.causal ? max(0, min(at + 1, keys)) : keys;
 }
+// (a query in front of the first key has a position below 0, and a window may be the
+// largest number there is: the difference is formed only where it stays inside 32 bits)
 __device__ __forceinline__ int key_begin(const PromptParams& p, int at) {
-  return p.window > 0 ? max(0, at + 1 - p.window) : 0;
+  return p.window > 0 && at >= p.window ? at + 1 - p.window : 0;
 }
 __device__ __forceinline__ Tile tile_of(const PromptParams& p, int row0, int queries, int keys) {
   Tile t;
