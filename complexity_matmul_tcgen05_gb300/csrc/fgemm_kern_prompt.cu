@@ -57,6 +57,7 @@ constexpr int kEarly = 96;            // keys of a step whose weights are handed
 constexpr int kThreads = 384;
 constexpr int kIssue = 0, kLoad = 2, kLook = 3, kWeights = 4;  // warps (two that issue)
 constexpr float kSlack = 8.0f;        // log2 of how far the maximum may be above the reference
+constexpr float kFar = 65536.0f;      // size of a reference from which on it is held as a score
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int DP>  // values of a head, padded: 64 or 128
@@ -205,9 +206,9 @@ __device__ __forceinline__ bool elect_one() {
 // A value that is the same in all lanes, known as such to the compiler.
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 
-template <bool V>
+template <int V>
 struct Constant {
-  static constexpr bool value = V;
+  static constexpr int value = V;
 };
 
 // A ring position: stage and phase parity.
@@ -769,11 +770,22 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         ahead -= tiles.from;
         tile_from = tiles[t].from, tile_to = tiles[t].to, all_from = tiles[t].all_from, all_to = tiles[t].all_to;
       }
+      // Rounded to fp32 the reference is off by up to half of its last place: nothing to
+      // the weights of a row, which are all off alike, but at 2^27 it is 8, beyond what
+      // a weight of 16 bits holds. From kFar on the reference is a score itself, and the
+      // other scores' differences from it (exact near it) meet scale log2 e.
       float ref = -INFINITY, sum = 0.0f;
-      // One step; MASKED: not every row sees every key. (Two copies of the code: the
-      // one that runs again and again stays short enough for the instruction cache.)
-      auto step = [&](auto masked, int j) {
-        constexpr bool MASKED = decltype(masked)::value;
+      bool far = false;    // of some row of the warp
+      float shift = 0.0f;  // log2 of what sums gain when ref becomes a score
+      // One step. Three copies of the code, so that the one that runs again and again
+      // stays short enough for the instruction cache: for steps in which every row sees
+      // every key, for the others, and, in a loop of its own, for both behind a far
+      // reference. The step that finds one is left as it was and taken again there.
+      // (As a branch of the first two copies this cost packed prompts 3.5 %; so 0.4 %,
+      // heads of 64 3 %.)
+      constexpr int kAll = 0, kSome = 1, kFarRows = 2;
+      auto step = [&](auto kind, int j) {
+        constexpr bool MASKED = decltype(kind)::value != kAll, FAR = decltype(kind)::value == kFarRows;
         if (!(ok = wait_warp(s_full(t), turn, p, 2))) return;
         turn ^= 1u;
         ptx::tc_fence_after();
@@ -799,10 +811,20 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         for (int c = 0; c < 32; c += 2)
 #pragma unroll
           for (int i = 0; i < 4; ++i) m[i] = max3(m[i], __uint_as_float(s[i][c]), __uint_as_float(s[i][c + 1]));
-        const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * to_log2;
-        if (__any_sync(0xFFFFFFFFu, most > ref + kSlack)) {
-          const float next = most > ref + kSlack ? most : ref;
-          const float f = next == -INFINITY ? 1.0f : exp2_fast(ref - next);
+        const float unit = FAR ? to_log2 : 1.0f;  // of the reference and the maximum
+        const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * (FAR ? 1.0f : to_log2);
+        const bool above = most * unit > fmaf(ref, unit, kSlack);
+        if (__any_sync(0xFFFFFFFFu, above || (FAR && shift != 0.0f))) {
+          if (!FAR) {
+            far = __any_sync(0xFFFFFFFFu, above && fabsf(most) > kFar);
+            if (far) {
+              turn ^= 1u;
+              return;
+            }
+          }
+          const float next = above ? most : ref;
+          const float f = next == -INFINITY ? 1.0f : exp2_fast((ref - next) * unit + (FAR ? shift : 0.0f));
+          if (FAR) shift = 0.0f;
           ref = next;
           sum *= f;
           if (j != tile_from) {
@@ -817,8 +839,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             }
           }
         }
+        if (FAR) {
+          const float base = ref == -INFINITY ? 0.0f : ref;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < 32; ++c) s[i][c] = __float_as_uint(__uint_as_float(s[i][c]) - base);
+        }
         const uint64_t to_log2_2 = pair(to_log2, to_log2);
-        const float less = ref == -INFINITY ? 0.0f : kLift - ref;
+        const float less = ref == -INFINITY ? 0.0f : FAR ? kLift : kLift - ref;
         const uint64_t less2 = pair(less, less);
         uint64_t sum2[2] = {pair(sum, 0.0f), pair(0.0f, 0.0f)};
 #pragma unroll
@@ -853,7 +882,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           const int n = ahead + j, st = n % C::kValues;
           const uint32_t ph = (n / C::kValues) & 1u;
           if (!(ok = wait_warp(v_full(st), ph, p, 2) && wait_warp(v_ok(st), ph, p, 2))) return;
-          if (wild[st] != 0) {
+          if ((!FAR || j < all_from || j >= all_to) && wild[st] != 0) {
             product_by_rows<BF16, DP>(s_at, o_at, v_at(st), lo, hi, j == tile_from);
             ptx::fence_proxy_async_smem();
           }
@@ -862,11 +891,20 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(w_full(t));
       };
-      for (int j = tile_from; ok && j < tile_to; ++j) {
+      int j = tile_from;
+      for (; ok && j < tile_to; ++j) {
         if (j >= all_from && j < all_to)
-          step(Constant<false>{}, j);
+          step(Constant<kAll>{}, j);
         else
-          step(Constant<true>{}, j);
+          step(Constant<kSome>{}, j);
+        if (far) break;
+      }
+      if (far) {
+        const float score = __fdividef(ref, to_log2);
+        if (ref > -INFINITY) shift = fmaf(-score, to_log2, ref - kLift) + kLift;  // (ref - kLift: as rounded for the weights)
+        ref = score;
+        for (; ok && j < tile_to; ++j) step(Constant<kFarRows>{}, j);
+        ref *= to_log2;
       }
       // outputs: a row a thread
       if (!ok) break;

@@ -3,8 +3,9 @@ windows, scores, values and angles that the ordinary tests do not reach."""
 import pytest
 import torch
 
+import cache_reference as ref
 from complexity_matmul_tcgen05_gb300 import fgemm
-from test_cache_ops_gpu import check_prompt, gen, ints, prompt_inputs
+from test_cache_ops_gpu import DEV, TYPES, check_prompt, gen, ints, prompt_inputs, rand, within
 
 pytestmark = pytest.mark.gpu
 
@@ -22,3 +23,96 @@ def test_prompt_window_without_limit(window, heads, kv_heads):
     for h in (0, heads - 1):
         check_prompt(q[:, h:h + 1], k[:, h // group:h // group + 1], v[:, h // group:h // group + 1], starts, k_starts, True,
                      window, out[:, h:h + 1], lse[:, h:h + 1], what="prompt, window without limit")
+
+
+def far_inputs(dtype, n, dim):
+    """Keys of one head whose scores with every query are exact in fp32, far from 0 and,
+    times a scale of 64, more than 2^13 apart: a query's output is the value of the
+    largest one it sees.  Half of the keys have a score of 0; one query in four has the
+    others below it."""
+    g = gen(61)
+    side = torch.arange(n, device=DEV)
+    q, k = torch.zeros(n, 1, dim, device=DEV), torch.zeros(n, 1, dim, device=DEV)
+    q[:, 0, 0] = torch.where(side % 4 == 3, -2047.0, 2047.0)  # products of 11 and 9 bits
+    order = torch.randperm(n, generator=g, device=DEV)
+    k[:, 0, 0] = (256.0 - order % 256) * (16.0 if dtype == torch.float16 else 2.0 ** 20)
+    k[order >= 256, 0, 0] = 0.0
+    v = rand(g, n, 1, dim).to(dtype)
+    if dtype == torch.bfloat16:
+        q[:, 0, 0] = q[:, 0, 0].sign() * 255.0
+    return q.to(dtype), k.to(dtype), v
+
+
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 100)])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_scores_far_from_zero(dtype, dim, causal, window):
+    """Scores of 10^9 and beyond, whose product with log2 e rounds by more than a 16-bit
+    weight's exponent holds.  A weight of the largest score rounds by half a step of
+    16 bits at most, the output by another, its reciprocal sum by 2^-23."""
+    n, scale = 500, 64.0
+    q, k, v = far_inputs(TYPES[dtype], n, dim)
+    scores = (ref.f64(q)[:, 0] @ ref.f64(k)[:, 0].t()) * scale
+    scores = torch.where(ref.seen_by(n, n, causal, window), scores, -torch.inf)
+    most = scores.amax(1, keepdim=True)
+    # (keys with a score of 0 share the weight where nothing is above them)
+    first = torch.softmax(scores, 1)
+    values = ref.f64(v)[:, 0]
+    want = (first @ values)[:, None]
+    half = torch.finfo(TYPES[dtype]).eps / 2
+    bound = (first @ values.abs())[:, None] * (2 * half + (n / 16 + 16) * 4 * ref.U32) + ref.store(want, TYPES[dtype])
+    want_lse = torch.logsumexp(scores, 1)[:, None]
+    # log2 e and ln 2 as fp32 numbers, their two products with the score, the sums of weights
+    bound_lse = most.abs() * 6 * ref.U32 + 2.0 ** -12
+    out, lse = fgemm.attention(q, k, v, ints([0, n]), causal=causal, window=window, scale=scale)
+    within("far scores, prompt", out, want, bound)
+    within("far scores, prompt lse", lse, want_lse, bound_lse)
+    if causal:
+        # the same keys in pages, the last queries one at a time
+        pages = -(-n // 16)
+        k_cache, v_cache = (torch.zeros(pages, 16, 1, dim, dtype=q.dtype, device=DEV) for _ in range(2))
+        k_cache.view(-1, 1, dim)[:n], v_cache.view(-1, 1, dim)[:n] = k, v
+        rows = torch.arange(n - 200, n, device=DEV)
+        table = torch.arange(pages, device=DEV, dtype=torch.int32).expand(len(rows), pages)
+        out, lse = fgemm.attention_paged(q[rows], k_cache, v_cache, table.contiguous(), (rows + 1).to(torch.int32),
+                                         window=window, scale=scale)
+        within("far scores, paged", out, want[rows.cpu()], bound[rows.cpu()])
+        within("far scores, paged lse", lse, want_lse[rows.cpu()], bound_lse[rows.cpu()])
+
+
+def test_scores_far_from_zero_beside_a_value_that_is_not_finite():
+    """Only the queries that see it have it."""
+    n, scale, at = 500, 64.0, 301
+    q, k, v = far_inputs(torch.float16, n, 64)
+    v[at, 0, 5] = torch.inf
+    out, lse = fgemm.attention(q, k, v, ints([0, n]), scale=scale)
+    plain, plain_lse = fgemm.attention(q, k, torch.where(torch.isinf(v), 0.0, v), ints([0, n]), scale=scale)
+    assert torch.equal(lse, plain_lse) and torch.equal(out[:at], plain[:at])
+    assert not bool(torch.isfinite(out[at:, 0, 5]).any())
+    rest = torch.arange(64, device=DEV) != 5
+    assert bool(torch.isfinite(out[:, :, rest]).all())
+
+
+def test_scores_beside_a_row_far_from_zero():
+    """Rows whose scores are in the ten thousands, with two keys of the same score in two
+    steps, beside one that becomes far in the second: both keys weigh the same.  A
+    weight rounds to fp16 by up to 2^-11 of itself (in the first step it is no power of 2: it
+    carries what the reference was rounded by), which moves a value's share of one half by
+    up to 2^-12; the sum and the quotient round a few times in fp32."""
+    n, dim = 300, 64
+    for scale in (1.0, 0.9137, 1.0371):
+        q, k = torch.zeros(64, 1, dim, device=DEV), torch.zeros(n, 1, dim, device=DEV)
+        q[:, 0, 0] = 1.0 - torch.arange(64, device=DEV) / 128
+        q[17, 0, 0], q[17, 0, 1] = 0.0, 2047.0
+        k[3, 0, 0] = k[200, 0, 0] = 40000.0
+        k[200, 0, 1] = 60000.0
+        v = rand(gen(64), n, 1, dim).half()
+        out, lse = fgemm.attention(q.half(), k.half(), v, ints([0, 64]), k_starts=ints([0, n]), causal=False, scale=scale)
+        a, b = ref.f64(v[3, 0]), ref.f64(v[200, 0])
+        want = ((a + b) / 2).expand(64, 1, dim).clone()
+        want[17] = b
+        within("beside a far row", out, want, ref.store(want, torch.float16) + (a.abs() + b.abs()) * (2.0 ** -12 + 2.0 ** -20))
+        most = (q.half().double() @ k.half().double()[:, 0].t()).amax(2).cpu() * scale
+        two = torch.full_like(most, 2.0).log()
+        two[17] = 0.0
+        within("beside a far row, lse", lse, most + two, most * 6 * ref.U32 + 2.0 ** -20)
