@@ -5,10 +5,12 @@
 //
 // One pass over the keys and values with a running reference r of the maximum
 // and sums relative to it: w_j = 2^(x_j log2 e - r). The reference follows the
-// maximum only when that is more than 8 above it (the weights stay below 2^8, or
-// below 2^14 in fp16, where small ones would lose bits, and sums below 2^46, far
-// inside fp32), so that the outputs in registers are seldom scaled. Weights are
-// rounded to 16 bits for the product with the values, their sum is of the 32-bit ones.
+// maximum only when that is more than 8 above it, so that the outputs in registers are
+// seldom scaled. In bf16 the weights are lowered by 2^8 and stay at most 1: no sum is
+// larger than it were relative to the maximum, and values may be near the end of fp32. In
+// fp16, where small ones would lose bits, they are lifted by 2^6 and stay below 2^14, sums
+// below 2^61. Weights are rounded to 16 bits for the product with the values, their sum is
+// of the 32-bit ones.
 //
 // Memory-bound: a key and a value are read once for the up to 16 query heads
 // that share them. 16 tokens are the rows of a matrix instruction (mma.sync) and 8
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtasPerSm) decode_kern
   const uint32_t ring = ptx::smem_u32(smem) + warp * C::kRing;
   const int group = p.heads / p.kv_heads;
   const float to_log2 = p.scale * kLog2e;
-  constexpr float kLift = BF16 ? 0.0f : 6.0f;  // log2 of the weights' factor
+  constexpr float kLift = BF16 ? -kSlack : 6.0f;  // log2 of the weights' factor
   const bool alike = p.k_page == p.v_page && p.k_token == p.v_token && p.k_head == p.v_head;
 
   for (long long b = b0; b < b1;) {

@@ -8,8 +8,10 @@
 // so a row's maximum and sum need no other thread, and writes the weights, rounded to
 // 16 bits, over S in tensor memory, from where they are an operand of the product
 // with the values. The reference r follows the row's maximum only when that is more
-// than 8 above it: the weights stay below 2^8 (fp16: below 2^14, so that small ones
-// keep their bits) and O is seldom scaled.
+// than 8 above it, so that O is seldom scaled; in bf16 the weights are lowered by 2^8 and
+// stay at most 1, so that O is never larger than the sum of w |V| with the maximum as
+// reference (values may be near the end of fp32), in fp16 they are lifted by 2^6 and stay
+// below 2^14, so that small ones keep their bits.
 //
 // A CTA has two tiles of queries at a time: while the tensor core works on one tile's
 // products the threads of the other tile form its weights. A tile's round is about
@@ -753,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + t * kTile, o_at = tmem + lanes + C::kOAt + t * 128;
     const float to_log2 = p.scale * kLog2e;
-    constexpr float kLift = BF16 ? 0.0f : 6.0f;
+    constexpr float kLift = BF16 ? -kSlack : 6.0f;  // log2 of the weights' factor
     uint32_t turn = 0, o_turn = 0;
     bool ok = true;
     // (What a step seldom needs of its job is read again there: registers are short.)

@@ -520,7 +520,9 @@ fgemm_status_t fgemm_rotary_cache(fgemm_handle_t h, int64_t T, int32_t heads, in
  *               kv_heads, dim) bytes of device memory, 16-byte aligned, left with
  *               nothing of use. Calls that may run at the same time need one each.
  * Sums are fp32 and their order depends on the sizes, the lengths and the SM
- * count only; weights are rounded to dtype before they meet the values.
+ * count only; weights are rounded to dtype before they meet the values. Before the
+ * division an output is a sum of e^(x_j - m) v_j, m the largest x_j, which has to
+ * stay inside fp32 (values of bf16 may be as large).
  */
 size_t fgemm_attention_paged_workspace(fgemm_handle_t h, int64_t seqs, int32_t heads, int32_t kv_heads, int32_t dim);
 fgemm_status_t fgemm_attention_paged(fgemm_handle_t h, int64_t seqs, int32_t heads, int32_t kv_heads, int32_t dim,

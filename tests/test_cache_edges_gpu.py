@@ -5,7 +5,7 @@ import torch
 
 import cache_reference as ref
 from complexity_matmul_tcgen05_gb300 import fgemm
-from test_cache_ops_gpu import DEV, TYPES, check_prompt, gen, ints, prompt_inputs, rand, within
+from test_cache_ops_gpu import DEV, TYPES, check_paged, check_prompt, gen, ints, prompt_inputs, rand, within
 
 pytestmark = pytest.mark.gpu
 
@@ -116,3 +116,27 @@ def test_scores_beside_a_row_far_from_zero():
         two = torch.full_like(most, 2.0).log()
         two[17] = 0.0
         within("beside a far row, lse", lse, most + two, most * 6 * ref.U32 + 2.0 ** -20)
+
+
+def test_large_values_behind_rising_scores():
+    """Values near the end of bf16, the second of them behind a score that rises by
+    less than 2^8: nothing on the way is larger than the values' sum."""
+    n, dim, heads = 300, 8, 320  # (as many heads as leave a share of the cache several blocks)
+    scores = torch.full((n,), -60.0, device=DEV)
+    scores[3], scores[131] = 0.0, 5.0
+    q = torch.ones(1, heads, dim, dtype=torch.bfloat16, device=DEV)
+    k, v = (torch.zeros(n, heads, dim, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    k[..., 0] = scores[:, None]
+    v[...] = rand(gen(62), n, heads, dim)
+    v[3], v[131] = 1e38, 2e38
+    pages = -(-n // 16)
+    k_cache, v_cache = (torch.zeros(pages, 16, heads, dim, dtype=q.dtype, device=DEV) for _ in range(2))
+    k_cache.view(-1, heads, dim)[:n], v_cache.view(-1, heads, dim)[:n] = k, v
+    table = torch.arange(pages, device=DEV, dtype=torch.int32)[None]
+    few = [0, 7, heads - 1]
+    out, lse = fgemm.attention_paged(q, k_cache, v_cache, table, ints([n]), scale=1.0)
+    check_paged(q[:, few], [k[:, few]], [v[:, few]], 0, 1.0, out[:, few], lse[:, few], "large values, paged")
+    for h in few:
+        got = fgemm.attention(q[:, h:h + 1].contiguous(), k[:, h:h + 1].contiguous(), v[:, h:h + 1].contiguous(),
+                              ints([0, 1]), k_starts=ints([0, n]), scale=1.0)
+        check_prompt(q[:, h:h + 1], k[:, h:h + 1], v[:, h:h + 1], [0, 1], [0, n], True, 0, *got, 1.0, "large values, prompt")
