@@ -481,8 +481,10 @@ typedef struct {
 /*
  * Rotary positions of queries and keys, and the write of keys and values into
  * a paged cache. For token t and i < rot / 2, with
- * angle = positions[t] * inv_freq[i] (less its whole turns, to 2^-32 turns), a pair (a, b) becomes
+ * angle = positions[t] * inv_freq[i], a pair (a, b) becomes
  *   (a cos - b sin, b cos + a sin)       in fp32, rounded once;
+ * the angle less its whole turns (at most half a turn to either side) is off by 2^-24 of
+ * itself and |positions[t]| * 2^-63 turns;
  * pairs are values i and i + rot / 2 of a head, or 2 i and 2 i + 1 where
  * interleaved is not 0; values from rot on stay as they are.
  *   q, out     T x heads x dim; out may be q itself.

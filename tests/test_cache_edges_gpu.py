@@ -140,3 +140,29 @@ def test_large_values_behind_rising_scores():
         got = fgemm.attention(q[:, h:h + 1].contiguous(), k[:, h:h + 1].contiguous(), v[:, h:h + 1].contiguous(),
                               ints([0, 1]), k_starts=ints([0, n]), scale=1.0)
         check_prompt(q[:, h:h + 1], k[:, h:h + 1], v[:, h:h + 1], [0, 1], [0, n], True, 0, *got, 1.0, "large values, prompt")
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rotary_small_angles(interleaved):
+    """The sine of a small angle has its bits: pairs (a, 0) and (0, b).  An angle rounds by
+    2^-24 of itself and position * 2^-63 turns, the sine by two roundings more."""
+    freq = torch.tensor([1e-8, -1e-8, 3e-9, -7e-10, 1e-6, 2e-3, 2.0 ** -30, 1.0], device=DEV)
+    positions = [1, -1, 2, 3, -7, 100, 0]
+    n, half = len(positions), len(freq)
+    q = torch.zeros(n, 2, 2 * half, dtype=torch.bfloat16, device=DEV)
+    first = slice(0, 2 * half, 2) if interleaved else slice(0, half)
+    second = slice(1, 2 * half, 2) if interleaved else slice(half, 2 * half)
+    q[:, 0, first], q[:, 1, second] = 1.0, 1.0
+    cache = [torch.zeros(1, n, 1, 2 * half, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    kv = torch.zeros(n, 1, 2 * half, dtype=torch.bfloat16, device=DEV)
+    out = fgemm.rotary_cache(q, kv, kv, ints(positions), ints(range(n)), freq, *cache, interleaved=interleaved)
+    at = torch.tensor(positions, dtype=torch.float64)[:, None]
+    angle = at * ref.f64(freq)
+    sine = torch.sin(angle)
+    bound = 4 * ref.U32 * angle.abs() + at.abs() * 2.0 ** -60 + ref.store(sine, torch.bfloat16)
+    within("small angles, a sin", out[:, 0, second], sine, bound)
+    within("small angles, -b sin", out[:, 1, first], -sine, bound)
+    cosine = torch.cos(angle)
+    off = 4 * ref.U32 + ref.store(cosine, torch.bfloat16)
+    within("small angles, a cos", out[:, 0, first], cosine, off)
+    within("small angles, b cos", out[:, 1, second], cosine, off)
