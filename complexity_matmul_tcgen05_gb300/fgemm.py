@@ -817,11 +817,24 @@ def sample(logits: torch.Tensor, u: torch.Tensor, *, temperature: float | torch.
 # ---------------------------------- operators around a key-value cache
 
 
+# The C calls take heads, page sizes and windows in 32 bits, and ctypes drops what is
+# above them.
+_INT32_MAX = 2 ** 31 - 1
+
+
+def _softmax(scale: float | None, window: int, dim: int) -> tuple[float, int]:
+    """scale (None: 1 / sqrt(dim)) and window for a C call; a window beyond 32 bits is
+    the largest there is."""
+    return (max(dim, 1) ** -0.5 if scale is None else scale), max(-1, min(window, _INT32_MAX))
+
+
 def _heads(t: torch.Tensor, name: str, shape, dtype, dev: int) -> tuple[int, int, int]:
     """(address, token stride, head stride) of a tokens x heads x dim operand on
     device dev, checked."""
     if t.shape != shape or t.dtype != dtype or t.get_device() != dev:
         raise FgemmError(ERR_INVALID_ARG, f"{name} must be a {tuple(shape)} {dtype} tensor on cuda:{dev}")
+    if shape[1] > _INT32_MAX or shape[2] > _INT32_MAX:
+        raise FgemmError(ERR_INVALID_ARG, f"{name} has more heads, or values of a head, than 32 bits count")
     ld, hs, unit = t.stride()
     if unit != 1 and shape[2] > 1:
         raise FgemmError(ERR_INVALID_ARG, f"the values of a head of {name} must be adjacent")
@@ -835,6 +848,8 @@ def _cache(k: torch.Tensor, v: torch.Tensor, kv_heads: int | None, dim: int, dty
             k.dtype != dtype or v.dtype != dtype or k.get_device() != dev or v.get_device() != dev:
         raise FgemmError(ERR_INVALID_ARG, f"k_cache and v_cache must be pages x page size x key heads x {dim} {dtype} "
                                           f"tensors of one shape on cuda:{dev}")
+    if shape[1] > _INT32_MAX or shape[2] > _INT32_MAX:
+        raise FgemmError(ERR_INVALID_ARG, "a page of the cache has more tokens, or heads, than 32 bits count")
     k_page, k_token, k_head, k_unit = k.stride()
     v_page, v_token, v_head, v_unit = v.stride()
     if (k_unit != 1 or v_unit != 1) and dim > 1:
@@ -866,6 +881,8 @@ def rotary_cache(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: t
     pp = _vector(positions, "positions", n, torch.int32, dev)
     sp = _vector(slots, "slots", n, torch.int32, dev)
     half = inv_freq.shape[0] if inv_freq.dim() == 1 else 0
+    if 2 * half > dim:
+        raise FgemmError(ERR_INVALID_ARG, "inv_freq has more entries than a head has pairs")
     fp = _vector(inv_freq, "inv_freq", half, torch.float32, dev)
     cache = _cache(k_cache, v_cache, kv[1], dim, t, dev)
     if out is None:
@@ -904,11 +921,11 @@ def attention_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         out = torch.empty_like(q)
     oa = _heads(out, "out", q.shape, t, dev)
     lse = torch.empty((n, heads), dtype=torch.float32, device=q.device)
+    scale, window = _softmax(scale, window, dim)
     size = L.fgemm_attention_paged_workspace(h, n, heads, kv_heads, dim)
     work = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
     s = L.fgemm_attention_paged(h, n, heads, kv_heads, dim, *qa, ctypes.byref(cache), tp, ldt, pages, lp,
-                                dim ** -0.5 if scale is None else scale, window, dt, *oa, lse.data_ptr(),
-                                None if work is None else work.data_ptr(), size)
+                                scale, window, dt, *oa, lse.data_ptr(), None if work is None else work.data_ptr(), size)
     if s != OK:
         _check(s, h)
     return out, lse
@@ -948,8 +965,9 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, starts: torch.T
         lse = torch.empty((n, heads), dtype=torch.float32, device=q.device)
     elif lse.shape != (n, heads) or lse.dtype != torch.float32 or lse.get_device() != dev or not lse.is_contiguous():
         raise FgemmError(ERR_INVALID_ARG, f"lse must be a contiguous {(n, heads)} float32 tensor on cuda:{dev}")
+    scale, window = _softmax(scale, window, dim)
     s = L.fgemm_attention(h, seqs, n, kv[0], heads, kv[1], dim, *qa, *ka, *va, sp, kp, 1 if causal else 0, window,
-                          dim ** -0.5 if scale is None else scale, dt, *oa, lse.data_ptr())
+                          scale, dt, *oa, lse.data_ptr())
     if s != OK:
         _check(s, h)
     return out, lse

@@ -166,3 +166,26 @@ def test_rotary_small_angles(interleaved):
     off = 4 * ref.U32 + ref.store(cosine, torch.bfloat16)
     within("small angles, a cos", out[:, 0, first], cosine, off)
     within("small angles, b cos", out[:, 1, second], cosine, off)
+
+
+def test_sizes_beyond_32_bits():
+    """What a C argument of 32 bits cannot hold is held to its largest, or refused; never
+    taken less its upper bits."""
+    q, k, v, starts, _ = prompt_inputs(gen(63), [90], [90], 2, 1, 64, torch.bfloat16)
+    at = ints(starts)
+    plain = fgemm.attention(q, k, v, at)
+    cache = [x.view(6, 15, 1, 64) for x in (k, v)]
+    table, n = ints([range(6)]), ints([90])
+    step = fgemm.attention_paged(q[:1], *cache, table, n)
+    for window in (2 ** 31, 2 ** 32 + 5, 2 ** 40 + 1):
+        got = fgemm.attention(q, k, v, at, window=window)
+        assert torch.equal(got[0], plain[0]) and torch.equal(got[1], plain[1])
+        got = fgemm.attention_paged(q[:1], *cache, table, n, window=window)
+        assert torch.equal(got[0], step[0]) and torch.equal(got[1], step[1])
+    for call in (
+            lambda: fgemm.attention(q, k, v, at, window=-2 ** 32),
+            lambda: fgemm.attention_paged(q[:1], *cache, table, n, window=-2 ** 32),
+            lambda: fgemm.attention(q[..., :0], k[..., :0], v[..., :0], at),
+            lambda: fgemm.attention_paged(q[:1, :, :0], *(x[..., :0] for x in cache), table, n)):
+        with pytest.raises(fgemm.FgemmError):
+            call()
