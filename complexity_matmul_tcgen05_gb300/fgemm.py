@@ -269,9 +269,16 @@ def validate(M, N, K, A_ptr, lda, B_ptr, ldb, C_ptr, ldc, dtype: int, epilogue: 
 
 
 class Handle:
-    """An fgemm handle on the current CUDA device."""
+    """An fgemm handle on the current CUDA device.
+
+    The C library wants a handle used by one host thread at a time: the functions of this
+    module hold `lock` from setting their thread's current stream to the end of the C
+    call, so threads may share one (the default handle).  A product's workspace is the
+    handle's, though: products on two streams need a handle each, as do threads that
+    call the methods."""
 
     def __init__(self):
+        self.lock = threading.Lock()
         h = ctypes.c_void_p()
         _check(lib().fgemm_create(ctypes.byref(h)))
         self._h = h
@@ -369,14 +376,18 @@ class Handle:
 
 
 _handles: dict[int, Handle] = {}
+_handles_lock = threading.Lock()
 
 
 def default_handle() -> Handle:
     dev = torch.cuda.current_device()
     h = _handles.get(dev)
     if h is None:
-        h = Handle()
-        _handles[dev] = h
+        with _handles_lock:  # one for all threads
+            h = _handles.get(dev)
+            if h is None:
+                h = Handle()
+                _handles[dev] = h
     return h
 
 
@@ -438,15 +449,13 @@ def matmul(A: torch.Tensor, B: torch.Tensor, *, out: torch.Tensor | None = None,
         bias = bias.contiguous()
         bias_ptr = bias.data_ptr()
     h = handle if handle is not None else default_handle()
-    h.set_stream(torch.cuda.current_stream(A.device).cuda_stream)
+    stream = torch.cuda.current_stream(A.device).cuda_stream
     epi = make_epilogue(epilogue, alpha, bias_ptr)
     lda = A.stride(0) if M > 1 else max(K, 1)
     ldb = B.stride(0) if K > 1 else max(N, 1)
     ldc = out.stride(0) if M > 1 else max(n_out, 1)
-    if sumsq_out is None and sumsq_in is None:
-        s = h.matmul_raw(M, N, K, A.data_ptr(), lda, B.data_ptr(), ldb, out.data_ptr(), ldc, dt,
-                         epi, algo, tile_n, tile_m)
-    else:
+    rms = None
+    if sumsq_out is not None or sumsq_in is not None:
         parts = 0
         for t, name in ((sumsq_out, "sumsq_out"), (sumsq_in, "sumsq_in")):
             if t is not None and (t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous()):
@@ -460,9 +469,10 @@ def matmul(A: torch.Tensor, B: torch.Tensor, *, out: torch.Tensor | None = None,
         rms = Rms(None if sumsq_out is None else sumsq_out.data_ptr(),
                   None if sumsq_in is None else sumsq_in.data_ptr(), parts, int(norm_width),
                   float(rms_eps))
-        s = h.matmul_rms_raw(M, N, K, A.data_ptr(), lda, B.data_ptr(), ldb, out.data_ptr(), ldc, dt,
-                             epi, algo, tile_n, tile_m, rms)
-    _check(s, h.ptr)
+    args = (M, N, K, A.data_ptr(), lda, B.data_ptr(), ldb, out.data_ptr(), ldc, dt, epi, algo, tile_n, tile_m)
+    with h.lock:
+        h.set_stream(stream)
+        _check(h.matmul_raw(*args) if rms is None else h.matmul_rms_raw(*args, rms), h.ptr)
     return out
 
 
@@ -498,16 +508,20 @@ def _matmul_host(A, B, out, epilogue, alpha, bias, algo, tile_n, tile_m, handle,
         bias = bias.contiguous()
         bias_ptr = bias.data_ptr()
     h = handle if handle is not None else default_handle()
-    h.set_stream(torch.cuda.current_stream().cuda_stream)
+    stream = torch.cuda.current_stream().cuda_stream
     epi = make_epilogue(epilogue, alpha, bias_ptr)
-    s = lib().fgemm_matmul_host_ex(h.ptr, M, N, K, A.data_ptr(), A.stride(0) if M > 1 else max(K, 1),
-                                   B.data_ptr(), B.stride(0) if K > 1 else max(N, 1), out.data_ptr(),
-                                   out.stride(0) if M > 1 else max(n_out, 1), dt, ctypes.byref(epi),
-                                   ALGOS[algo], tile_m, tile_n, 0 if blocking else HOST_OVERLAP)
-    _check(s, h.ptr)
+    with h.lock:
+        h.set_stream(stream)
+        s = lib().fgemm_matmul_host_ex(h.ptr, M, N, K, A.data_ptr(), A.stride(0) if M > 1 else max(K, 1),
+                                       B.data_ptr(), B.stride(0) if K > 1 else max(N, 1), out.data_ptr(),
+                                       out.stride(0) if M > 1 else max(n_out, 1), dt, ctypes.byref(epi),
+                                       ALGOS[algo], tile_m, tile_n, 0 if blocking else HOST_OVERLAP)
+        _check(s, h.ptr)
     if blocking:
         torch.cuda.current_stream().synchronize()
-        _check(h.get_error(), h.ptr)
+        with h.lock:
+            h.set_stream(stream)
+            _check(h.get_error(), h.ptr)
     return out
 
 
@@ -542,16 +556,18 @@ def matmul_mx(A: torch.Tensor, scale_a: torch.Tensor, B: torch.Tensor, scale_b: 
         bias = bias.contiguous()
         bias_ptr = bias.data_ptr()
     h = handle if handle is not None else default_handle()
-    h.set_stream(torch.cuda.current_stream(A.device).cuda_stream)
+    stream = torch.cuda.current_stream(A.device).cuda_stream
     epi = make_epilogue(epilogue, alpha, bias_ptr)
-    s = lib().fgemm_matmul_mx(h.ptr, M, N, K, A.data_ptr(), A.stride(0) if M > 1 else max(K, 1),
-                              scale_a.data_ptr(), scale_a.stride(0) if M > 1 else max(kb, 1),
-                              FP8_FORMATS[a_format], B.data_ptr(), B.stride(0) if K > 1 else max(N, 1),
-                              scale_b.data_ptr(), scale_b.stride(0) if kb > 1 else max(N, 1),
-                              FP8_FORMATS[b_format], out.data_ptr(),
-                              out.stride(0) if M > 1 else max(n_out, 1), ctypes.byref(epi),
-                              ALGOS[algo], tile_m, tile_n)
-    _check(s, h.ptr)
+    with h.lock:
+        h.set_stream(stream)
+        s = lib().fgemm_matmul_mx(h.ptr, M, N, K, A.data_ptr(), A.stride(0) if M > 1 else max(K, 1),
+                                  scale_a.data_ptr(), scale_a.stride(0) if M > 1 else max(kb, 1),
+                                  FP8_FORMATS[a_format], B.data_ptr(), B.stride(0) if K > 1 else max(N, 1),
+                                  scale_b.data_ptr(), scale_b.stride(0) if kb > 1 else max(N, 1),
+                                  FP8_FORMATS[b_format], out.data_ptr(),
+                                  out.stride(0) if M > 1 else max(n_out, 1), ctypes.byref(epi),
+                                  ALGOS[algo], tile_m, tile_n)
+        _check(s, h.ptr)
     return out
 
 
@@ -567,12 +583,14 @@ def mx_to_bf16(X: torch.Tensor, S: torch.Tensor, fmt: str = "e4m3", along: str =
         raise ValueError("out must be a bf16 tensor of X's shape and device with unit column stride")
     Y = out if out is not None else torch.empty((rows, cols), dtype=torch.bfloat16, device=X.device)
     h = handle if handle is not None else default_handle()
-    h.set_stream(torch.cuda.current_stream(X.device).cuda_stream)
-    s = lib().fgemm_mx_to_bf16(h.ptr, rows, cols, X.data_ptr(), X.stride(0) if rows > 1 else max(cols, 1),
-                               S.data_ptr(), S.stride(0) if S.shape[0] > 1 else max(S.shape[1], 1),
-                               FP8_FORMATS[fmt], 0 if along == "row" else 1, Y.data_ptr(),
-                               Y.stride(0) if rows > 1 else max(cols, 1))
-    _check(s, h.ptr)
+    stream = torch.cuda.current_stream(X.device).cuda_stream
+    with h.lock:
+        h.set_stream(stream)
+        s = lib().fgemm_mx_to_bf16(h.ptr, rows, cols, X.data_ptr(), X.stride(0) if rows > 1 else max(cols, 1),
+                                   S.data_ptr(), S.stride(0) if S.shape[0] > 1 else max(S.shape[1], 1),
+                                   FP8_FORMATS[fmt], 0 if along == "row" else 1, Y.data_ptr(),
+                                   Y.stride(0) if rows > 1 else max(cols, 1))
+        _check(s, h.ptr)
     return Y
 
 
@@ -614,8 +632,7 @@ def _vector(t: torch.Tensor | None, name: str, n: int, dtype, dev: int) -> int |
 
 
 def _on(t: torch.Tensor, name: str, handle: Handle | None, dims: int = 2):
-    """(library, handle pointer, device index) of a call whose main operand is
-    t; the handle is set to the current stream of t's device."""
+    """(library, handle, device index) of a call whose main operand is t."""
     dev = t.get_device()
     if dev < 0:
         raise FgemmError(ERR_INVALID_ARG, f"{name} must be a CUDA tensor")
@@ -624,9 +641,18 @@ def _on(t: torch.Tensor, name: str, handle: Handle | None, dims: int = 2):
     h = handle if handle is not None else _handles.get(_current_device()) or default_handle()
     if dev != h.device:
         raise FgemmError(ERR_INVALID_ARG, f"{name} is on cuda:{dev}, the handle on cuda:{h.device}")
-    L = _lib or lib()
-    L.fgemm_set_stream(h._h, _raw_stream(dev))
-    return L, h._h, dev
+    return _lib or lib(), h, dev
+
+
+def _run(h: Handle, dev: int, f, *args):
+    """The C call f on h and args, on the current stream of device dev.  (ctypes lets other
+    threads run during each call: without the lock another's stream could be set
+    between the two.)"""
+    with h.lock:
+        _lib.fgemm_set_stream(h._h, _raw_stream(dev))
+        s = f(h._h, *args)
+        if s != OK:
+            _check(s, h._h)
 
 
 def _like(x: torch.Tensor) -> torch.Tensor:
@@ -659,7 +685,7 @@ def _norm_operands(x, gain, residual, total, inv_rms, eps, handle, out=None):
         ip = inv_rms.data_ptr()
     else:
         ip = _vector(inv_rms, "inv_rms", m, torch.float32, dev)
-    return L, h, dev, (h, m, n, xp, ldx, rp, ldr, gp, eps, dt, tp, ldt), total, inv_rms, ip
+    return L, h, dev, (m, n, xp, ldx, rp, ldr, gp, eps, dt, tp, ldt), total, inv_rms, ip
 
 
 def rms_norm(x: torch.Tensor, gain: torch.Tensor, *, residual: torch.Tensor | None = None, eps: float = 1e-6,
@@ -677,9 +703,7 @@ def rms_norm(x: torch.Tensor, gain: torch.Tensor, *, residual: torch.Tensor | No
     if out is None:
         out = torch.empty_like(x)
     yp, ldy = _rows(out, "out", x.shape, x.dtype, dev)
-    s = L.fgemm_rms_norm(*args, yp, ldy, ip)
-    if s != OK:
-        _check(s, h)
+    _run(h, dev, L.fgemm_rms_norm, *args, yp, ldy, ip)
     return out, total, inv_rms
 
 
@@ -696,9 +720,8 @@ def rms_norm_mx(x: torch.Tensor, gain: torch.Tensor, *, residual: torch.Tensor |
     blocks = (n + 31) // 32
     q = torch.empty((m, n), dtype=torch.uint8, device=x.device)
     scales = torch.empty((m, blocks), dtype=torch.uint8, device=x.device)
-    s = L.fgemm_rms_norm_mx(*args, FP8_FORMATS[fmt], q.data_ptr(), max(n, 1), scales.data_ptr(), max(blocks, 1), ip)
-    if s != OK:
-        _check(s, h)
+    _run(h, dev, L.fgemm_rms_norm_mx, *args, FP8_FORMATS[fmt], q.data_ptr(), max(n, 1), scales.data_ptr(),
+         max(blocks, 1), ip)
     return q, scales, total, inv_rms
 
 
@@ -725,12 +748,10 @@ def rms_norm_backward(dy: torch.Tensor, total: torch.Tensor, gain: torch.Tensor,
     if dgain is None:
         dgain = torch.empty(n, dtype=torch.float32, device=dy.device)
     dgp = _vector(dgain, "dgain", n, torch.float32, dev)
-    size = L.fgemm_rms_norm_backward_workspace(h, m, n)
+    size = L.fgemm_rms_norm_backward_workspace(h._h, m, n)
     work = torch.empty(size, dtype=torch.uint8, device=dy.device)
-    s = L.fgemm_rms_norm_backward(h, m, n, dyp, lddy, tp, ldt, gp, ip, dtp, lddt, dt, op, ldo, dgp, work.data_ptr(),
-                                  size)
-    if s != OK:
-        _check(s, h)
+    _run(h, dev, L.fgemm_rms_norm_backward, m, n, dyp, lddy, tp, ldt, gp, ip, dtp, lddt, dt, op, ldo, dgp,
+         work.data_ptr(), size)
     return out, dgain
 
 
@@ -766,11 +787,8 @@ def matmul_w4(A: torch.Tensor, W: torch.Tensor, scales: torch.Tensor, *, zeros: 
     cp, ldc = _rows(out, "out", (m, n_out), t, dev)
     size = L.fgemm_matmul_w4_workspace(m, k, group)
     work = torch.empty(size, dtype=torch.uint8, device=A.device) if size else None
-    s = L.fgemm_matmul_w4(h, m, n, k, ap, lda, wp, ldw, sp, lds, zp, ldz, group, cp, ldc, dt,
-                          ctypes.byref(Epilogue(EPILOGUES[epilogue], alpha, bp)),
-                          None if work is None else work.data_ptr(), size)
-    if s != OK:
-        _check(s, h)
+    _run(h, dev, L.fgemm_matmul_w4, m, n, k, ap, lda, wp, ldw, sp, lds, zp, ldz, group, cp, ldc, dt,
+         ctypes.byref(Epilogue(EPILOGUES[epilogue], alpha, bp)), None if work is None else work.data_ptr(), size)
     return out
 
 
@@ -807,10 +825,8 @@ def sample(logits: torch.Tensor, u: torch.Tensor, *, temperature: float | torch.
     up = _vector(u, "u", rows, torch.float32, dev)
     token = torch.empty(rows, dtype=torch.int32, device=logits.device)
     prob = torch.empty(rows, dtype=torch.float32, device=logits.device)
-    s = L.fgemm_sample(h, rows, vocab, lp, ld, code, up, ctypes.byref(Sampling(*one, *each)), token.data_ptr(),
-                       prob.data_ptr())
-    if s != OK:
-        _check(s, h)
+    _run(h, dev, L.fgemm_sample, rows, vocab, lp, ld, code, up, ctypes.byref(Sampling(*one, *each)), token.data_ptr(),
+         prob.data_ptr())
     return token, prob
 
 
@@ -888,10 +904,8 @@ def rotary_cache(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: t
     if out is None:
         out = torch.empty_like(q)
     oa = _heads(out, "out", q.shape, t, dev)
-    s = L.fgemm_rotary_cache(h, n, heads, kv[1], dim, *qa, *ka, *va, pp, sp, fp, 2 * half, 1 if interleaved else 0, dt,
-                             *oa, ctypes.byref(cache))
-    if s != OK:
-        _check(s, h)
+    _run(h, dev, L.fgemm_rotary_cache, n, heads, kv[1], dim, *qa, *ka, *va, pp, sp, fp, 2 * half,
+         1 if interleaved else 0, dt, *oa, ctypes.byref(cache))
     return out
 
 
@@ -922,12 +936,10 @@ def attention_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     oa = _heads(out, "out", q.shape, t, dev)
     lse = torch.empty((n, heads), dtype=torch.float32, device=q.device)
     scale, window = _softmax(scale, window, dim)
-    size = L.fgemm_attention_paged_workspace(h, n, heads, kv_heads, dim)
+    size = L.fgemm_attention_paged_workspace(h._h, n, heads, kv_heads, dim)
     work = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
-    s = L.fgemm_attention_paged(h, n, heads, kv_heads, dim, *qa, ctypes.byref(cache), tp, ldt, pages, lp,
-                                scale, window, dt, *oa, lse.data_ptr(), None if work is None else work.data_ptr(), size)
-    if s != OK:
-        _check(s, h)
+    _run(h, dev, L.fgemm_attention_paged, n, heads, kv_heads, dim, *qa, ctypes.byref(cache), tp, ldt, pages, lp,
+         scale, window, dt, *oa, lse.data_ptr(), None if work is None else work.data_ptr(), size)
     return out, lse
 
 
@@ -966,10 +978,8 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, starts: torch.T
     elif lse.shape != (n, heads) or lse.dtype != torch.float32 or lse.get_device() != dev or not lse.is_contiguous():
         raise FgemmError(ERR_INVALID_ARG, f"lse must be a contiguous {(n, heads)} float32 tensor on cuda:{dev}")
     scale, window = _softmax(scale, window, dim)
-    s = L.fgemm_attention(h, seqs, n, kv[0], heads, kv[1], dim, *qa, *ka, *va, sp, kp, 1 if causal else 0, window,
-                          scale, dt, *oa, lse.data_ptr())
-    if s != OK:
-        _check(s, h)
+    _run(h, dev, L.fgemm_attention, seqs, n, kv[0], heads, kv[1], dim, *qa, *ka, *va, sp, kp, 1 if causal else 0,
+         window, scale, dt, *oa, lse.data_ptr())
     return out, lse
 
 
@@ -995,8 +1005,6 @@ def logprobs(logits: torch.Tensor, tokens: torch.Tensor, *, top: int = 0, handle
     entropy = torch.empty(rows, dtype=torch.float32, device=logits.device)
     top_tokens = torch.empty((rows, top), dtype=torch.int32, device=logits.device)
     top_logprobs = torch.empty((rows, top), dtype=torch.float32, device=logits.device)
-    s = L.fgemm_logprobs(h, rows, vocab, lp, ld, code, tp, top, logprob.data_ptr(), entropy.data_ptr(),
-                         top_tokens.data_ptr() if top else None, top_logprobs.data_ptr() if top else None)
-    if s != OK:
-        _check(s, h)
+    _run(h, dev, L.fgemm_logprobs, rows, vocab, lp, ld, code, tp, top, logprob.data_ptr(), entropy.data_ptr(),
+         top_tokens.data_ptr() if top else None, top_logprobs.data_ptr() if top else None)
     return logprob, entropy, top_tokens, top_logprobs

@@ -1,5 +1,8 @@
 """What the calls around a key-value cache do with arguments that their C forms cannot
 hold, or may not take: no device needed."""
+import threading
+import time
+
 import pytest
 import torch
 
@@ -31,3 +34,70 @@ def test_windows_beyond_32_bits():
                          (-1, -1), (-2 ** 32, -1)):
         assert fgemm._softmax(0.5, window, 64) == (0.5, held)
     assert fgemm._softmax(None, 0, 64) == (0.125, 0) and fgemm._softmax(None, 0, 0) == (1.0, 0)
+
+
+# ------------------------------------------------------------------------ threads
+
+
+class OnDevice(torch.Tensor):
+    """A CPU tensor that the binding takes for one on cuda:0."""
+
+    def get_device(self):
+        return 0
+
+
+class Library:
+    """Stands for the C library: a call notes the stream that the handle has then.  The
+    first thread that sets a stream waits a while for the second to set its own."""
+
+    def __init__(self):
+        self.stream, self.seen, self.both, self.sets = None, {}, threading.Event(), 0
+
+    def fgemm_set_stream(self, handle, stream):
+        self.stream = stream
+        self.sets += 1
+        if self.sets == 1:
+            self.both.wait(0.5)
+        else:
+            self.both.set()
+        return fgemm.OK
+
+    def called(self, *args):
+        self.seen[threading.get_ident()] = self.stream
+        return fgemm.OK
+
+    fgemm_logprobs = fgemm_rms_norm = called
+
+
+def in_two_threads(call):
+    threads = [threading.Thread(target=call) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+
+
+def test_threads_share_a_handle(monkeypatch):
+    """Each call runs on its own thread's stream."""
+    for call in (lambda x, n, h: fgemm.logprobs(x, n, handle=h), lambda x, n, h: fgemm.rms_norm(x, x[0], handle=h)):
+        library = Library()
+        monkeypatch.setattr(fgemm, "_lib", library)
+        monkeypatch.setattr(fgemm, "_raw_stream", lambda dev: threading.get_ident())
+        handle = fgemm.Handle.__new__(fgemm.Handle)
+        handle._h, handle.device, handle.lock = None, 0, threading.Lock()
+        x, n = torch.zeros(2, 8).half().as_subclass(OnDevice), torch.zeros(2, dtype=torch.int32).as_subclass(OnDevice)
+        in_two_threads(lambda: call(x, n, handle))
+        assert len(library.seen) == 2 and all(thread == stream for thread, stream in library.seen.items())
+
+
+def test_threads_get_one_default_handle(monkeypatch):
+    class Slow:
+        def __init__(self):
+            time.sleep(0.2)
+
+    monkeypatch.setattr(fgemm, "Handle", Slow)
+    monkeypatch.setattr(fgemm, "_handles", {})
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    got = []
+    in_two_threads(lambda: got.append(fgemm.default_handle()))
+    assert len(got) == 2 and got[0] is got[1]

@@ -1,5 +1,7 @@
 """The operators around a key-value cache at the ends of their arguments and types:
 windows, scores, values and angles that the ordinary tests do not reach."""
+import threading
+
 import pytest
 import torch
 
@@ -21,8 +23,9 @@ def test_prompt_window_without_limit(window, heads, kv_heads):
     assert torch.equal(out, plain) and torch.equal(lse, plain_lse)
     group = heads // kv_heads
     for h in (0, heads - 1):
-        check_prompt(q[:, h:h + 1], k[:, h // group:h // group + 1], v[:, h // group:h // group + 1], starts, k_starts, True,
-                     window, out[:, h:h + 1], lse[:, h:h + 1], what="prompt, window without limit")
+        at = slice(h // group, h // group + 1)
+        check_prompt(q[:, h:h + 1], k[:, at], v[:, at], starts, k_starts, True, window, out[:, h:h + 1],
+                     lse[:, h:h + 1], what="prompt, window without limit")
 
 
 def far_inputs(dtype, n, dim):
@@ -107,11 +110,13 @@ def test_scores_beside_a_row_far_from_zero():
         k[3, 0, 0] = k[200, 0, 0] = 40000.0
         k[200, 0, 1] = 60000.0
         v = rand(gen(64), n, 1, dim).half()
-        out, lse = fgemm.attention(q.half(), k.half(), v, ints([0, 64]), k_starts=ints([0, n]), causal=False, scale=scale)
+        out, lse = fgemm.attention(q.half(), k.half(), v, ints([0, 64]), k_starts=ints([0, n]), causal=False,
+                                   scale=scale)
         a, b = ref.f64(v[3, 0]), ref.f64(v[200, 0])
         want = ((a + b) / 2).expand(64, 1, dim).clone()
         want[17] = b
-        within("beside a far row", out, want, ref.store(want, torch.float16) + (a.abs() + b.abs()) * (2.0 ** -12 + 2.0 ** -20))
+        bound = ref.store(want, torch.float16) + (a.abs() + b.abs()) * (2.0 ** -12 + 2.0 ** -20)
+        within("beside a far row", out, want, bound)
         most = (q.half().double() @ k.half().double()[:, 0].t()).amax(2).cpu() * scale
         two = torch.full_like(most, 2.0).log()
         two[17] = 0.0
@@ -139,7 +144,8 @@ def test_large_values_behind_rising_scores():
     for h in few:
         got = fgemm.attention(q[:, h:h + 1].contiguous(), k[:, h:h + 1].contiguous(), v[:, h:h + 1].contiguous(),
                               ints([0, 1]), k_starts=ints([0, n]), scale=1.0)
-        check_prompt(q[:, h:h + 1], k[:, h:h + 1], v[:, h:h + 1], [0, 1], [0, n], True, 0, *got, 1.0, "large values, prompt")
+        check_prompt(q[:, h:h + 1], k[:, h:h + 1], v[:, h:h + 1], [0, 1], [0, n], True, 0, *got, 1.0,
+                     "large values, prompt")
 
 
 @pytest.mark.parametrize("interleaved", [False, True])
@@ -189,3 +195,47 @@ def test_sizes_beyond_32_bits():
             lambda: fgemm.attention_paged(q[:1, :, :0], *(x[..., :0] for x in cache), table, n)):
         with pytest.raises(fgemm.FgemmError):
             call()
+
+
+def test_threads_on_streams_of_their_own():
+    """Two threads that share the default handle: each call runs on its thread's stream, so
+    it reads what the thread wrote before and its results are there for what comes after."""
+    g = gen(65)
+    lengths = [700, 31, 1500]
+    sets = []
+    for i in range(2):
+        q, k, v, starts, _ = prompt_inputs(gen(66 + i), lengths, lengths, 8, 2, 64, torch.bfloat16)
+        table = torch.arange(140, device=DEV, dtype=torch.int32).view(1, -1)[:, :sum(lengths) // 16]
+        logits = 3 * rand(g, 64, 5000)
+        sets.append((q, k, v, ints(starts), table, ints([table.shape[1] * 16]), logits,
+                     torch.arange(64, device=DEV, dtype=torch.int32)))
+
+    def calls(q, k, v, starts, table, n, logits, tokens):
+        """Inputs are written anew on this thread's stream, behind work that takes a while."""
+        big = torch.empty(1 << 26, device=DEV).fill_(1.0)
+        q, k, v, logits = (x * 1 for x in (q, k, v, logits + big[:1] - 1))
+        out, lse = fgemm.attention(q, k, v, starts)
+        pages = (k.shape[0] // 16, 16, *k.shape[1:])
+        rows = pages[0] * 16
+        step = fgemm.attention_paged(out[-1:], k[:rows].view(pages), v[:rows].view(pages), table, n)
+        got = fgemm.logprobs(logits, tokens, top=3)
+        return [x.clone() for x in (out, lse, *step, *got)]
+
+    want = [calls(*x) for x in sets]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(40):
+                got = calls(*sets[i])
+                if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                    wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not wrong and fgemm.default_handle().get_error() == fgemm.OK
