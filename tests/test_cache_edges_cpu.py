@@ -36,6 +36,41 @@ def test_windows_beyond_32_bits():
     assert fgemm._softmax(None, 0, 64) == (0.125, 0) and fgemm._softmax(None, 0, 0) == (1.0, 0)
 
 
+# ------------------------------------------------- refusals of the C entry points
+
+
+@pytest.fixture(scope="module")
+def L():
+    from complexity_matmul_tcgen05_gb300 import build
+    build.build()
+    return fgemm.lib()
+
+
+def refused(L, status, got, text):
+    said = L.fgemm_last_message(None).decode()
+    assert got == status and text in said, (got, said)
+
+
+@pytest.mark.parametrize("kw,status,text", [
+    (dict(seqs=(1 << 20) + 1), fgemm.ERR_INVALID_ARG, "seqs must be"),
+    (dict(seqs=1 << 20), fgemm.ERR_INVALID_ARG, "handle is NULL"),
+    (dict(T=(1 << 31) - 1024, heads=128), fgemm.ERR_UNSUPPORTED, "below 2^31"),
+    (dict(T=128, seqs=1 << 20, heads=1024, ldq=1024 * 64, ldo=1024 * 64), fgemm.ERR_INVALID_ARG, "handle is NULL"),
+    (dict(T=(1 << 31) - 1024, heads=126, ldq=126 * 64, ldo=126 * 64), fgemm.ERR_INVALID_ARG, "handle is NULL"),
+    (dict(lse=None), fgemm.ERR_INVALID_ARG, "handle is NULL"),
+])
+def test_prompt_sizes_that_a_launch_cannot_have(L, kw, status, text):
+    a = {**dict(seqs=2, T=8, T_k=8, heads=4, kv_heads=2, dim=64, q=16, ldq=256, hsq=64, k=64, ldk=128, hsk=64, v=80,
+                ldv=128, hsv=64, starts=16, k_starts=16, causal=1, window=0, scale=0.125, dtype=fgemm.F16, out=32,
+                ldo=256, hso=64, lse=16), **kw}
+    refused(L, status, L.fgemm_attention(None, *a.values()), text)
+
+
+@pytest.mark.parametrize("rows,text", [((1 << 27) + 1, "rows must be"), (1 << 27, "handle is NULL")])
+def test_logprobs_of_too_many_rows(L, rows, text):
+    refused(L, fgemm.ERR_INVALID_ARG, L.fgemm_logprobs(None, rows, 100, 16, 100, 2, 16, 5, 16, 16, 16, 16), text)
+
+
 # ------------------------------------------------------------------------ threads
 
 

@@ -1,5 +1,6 @@
 """The operators around a key-value cache at the ends of their arguments and types:
 windows, scores, values and angles that the ordinary tests do not reach."""
+import ctypes
 import threading
 
 import pytest
@@ -7,7 +8,8 @@ import torch
 
 import cache_reference as ref
 from complexity_matmul_tcgen05_gb300 import fgemm
-from test_cache_ops_gpu import DEV, TYPES, check_paged, check_prompt, gen, ints, prompt_inputs, rand, within
+from test_cache_ops_gpu import (DEV, TYPES, check_paged, check_prompt, gen, ints, paged_inputs, prompt_inputs, rand,
+                                within)
 
 pytestmark = pytest.mark.gpu
 
@@ -239,3 +241,41 @@ def test_threads_on_streams_of_their_own():
         t.join()
     torch.cuda.synchronize()
     assert not wrong and fgemm.default_handle().get_error() == fgemm.OK
+
+
+@pytest.mark.parametrize("heads,kv_heads", [(8, 2), (16, 1), (40, 2), (64, 1), (320, 320)])
+@pytest.mark.parametrize("dim", [8, 64, 72, 128])
+def test_paged_workspace(dim, heads, kv_heads):
+    """Nothing is written around the workspace that a call asks for, and less, or one not on 16
+    bytes, is refused: query heads of one and two eights and of several tiles, more key heads
+    than the device holds shares."""
+    few = kv_heads > 100
+    lengths = [300, 0, 5000 if not few else 500, 64, 65]
+    q, k, v, table, n, keys, values = paged_inputs(gen(heads + dim), lengths, heads, kv_heads, dim, 16, torch.bfloat16)
+    L, h = fgemm.lib(), fgemm.default_handle()
+    torch.cuda.synchronize()  # (the call below runs on whatever stream the handle has)
+    h.set_stream(torch.cuda.current_stream().cuda_stream)
+    size = L.fgemm_attention_paged_workspace(h.ptr, len(lengths), heads, kv_heads, dim)
+    assert size > 0
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device=DEV)
+    cache = fgemm._cache(k, v, kv_heads, dim, q.dtype, 0)
+
+    def call(workspace, count):
+        return L.fgemm_attention_paged(h.ptr, len(lengths), heads, kv_heads, dim, q.data_ptr(), q.stride(0),
+                                       q.stride(1), ctypes.byref(cache), table.data_ptr(), table.stride(0), table.shape[1],
+                                       n.data_ptr(), dim ** -0.5, 0, fgemm.BF16, out.data_ptr(), out.stride(0),
+                                       out.stride(1), lse.data_ptr(), workspace, count)
+
+    guard = 1 << 16
+    space = torch.full((size + 2 * guard,), 0xA5, dtype=torch.uint8, device=DEV)
+    at = space.data_ptr() + guard
+    for workspace, count, status in ((at, size - 1, fgemm.ERR_INVALID_ARG), (None, size, fgemm.ERR_INVALID_ARG),
+                                     (at + 8, size + 8, fgemm.ERR_ALIGNMENT), (at, 0, fgemm.ERR_INVALID_ARG)):
+        assert call(workspace, count) == status and "workspace" in h.last_message()
+    assert call(at, size) == fgemm.OK
+    torch.cuda.synchronize()
+    assert bool((space[:guard] == 0xA5).all()) and bool((space[guard + size:] == 0xA5).all())
+    for i in (0, heads - 1):
+        one, of = slice(i, i + 1), slice(i // (heads // kv_heads), i // (heads // kv_heads) + 1)
+        check_paged(q[:, one], [x[:, of] for x in keys], [x[:, of] for x in values], 0, None, out[:, one], lse[:, one],
+                    "paged, workspace with guards")
