@@ -44,6 +44,27 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// As pack2, but what would be infinity in fp16 is its largest number.
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack_sat(float lo, float hi) {
+  if (BF16) return pack2<true>(lo, hi);
+  uint32_t w;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  return w;
+}
+
+// Two outputs of attention in one word: sums of weighted values a and b times the
+// reciprocal of the weights' sum. An output is a mean of values, but weights of 16 bits
+// and their 32-bit sum differ by up to 2^-11: at 65504 that would be infinity, so in fp16 a
+// finite sum stays finite. (In bf16 the types end alike: such a sum is no number of fp32.)
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack_means(float a, float b, float inv) {
+  const float x = a * inv, y = b * inv;
+  if (BF16) return pack2<true>(x, y);
+  return pack2<false>(fabsf(a) < INFINITY ? fminf(fmaxf(x, -65504.0f), 65504.0f) : x,
+                      fabsf(b) < INFINITY ? fminf(fmaxf(y, -65504.0f), 65504.0f) : y);
+}
+
 // A kernel's shared memory, asked for once on each device; `devices` is a word of the
 // kernel's own.
 template <class K>

@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, NT>::kCtasPerSm) decode_kern
       } else if (c < p.dim) {
         const float inv = z == 0.0f ? 0.0f : 1.0f / z;
         *reinterpret_cast<uint2*>(p.out.p + seq * p.out.ld + (head0 + r) * p.out.hs + c) =
-            make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
+            make_uint2(pack_means<BF16>(acc.x, acc.y, inv), pack_means<BF16>(acc.z, acc.w, inv));
         if (p.lse && c == 0)
           p.lse[static_cast<long long>(seq) * p.heads + head0 + r] = z == 0.0f ? -INFINITY : (top + log2f(z)) * kLn2;
       }
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
   const float inv = z == 0.0f ? 0.0f : 1.0f / z;
   if (lane * 4 < p.dim)
     *reinterpret_cast<uint2*>(out + lane * 4) =
-        make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
+        make_uint2(pack_means<BF16>(acc.x, acc.y, inv), pack_means<BF16>(acc.z, acc.w, inv));
   if (p.lse && lane == 0)
     p.lse[static_cast<long long>(seq) * p.heads + head] = z == 0.0f ? -INFINITY : (top + log2f(z)) * kLn2;
 }

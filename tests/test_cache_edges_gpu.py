@@ -279,3 +279,38 @@ def test_paged_workspace(dim, heads, kv_heads):
         one, of = slice(i, i + 1), slice(i // (heads // kv_heads), i // (heads // kv_heads) + 1)
         check_paged(q[:, one], [x[:, of] for x in keys], [x[:, of] for x in values], 0, None, out[:, one], lse[:, one],
                     "paged, workspace with guards")
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_outputs_at_the_end_of_f16(dim):
+    """Values at +-65504, where many a pipeline saturates: an output is a mean of values and
+    no larger, though 16-bit weights and their 32-bit sum differ by up to 2^-11.  Infinite
+    values stay what they are."""
+    lengths, heads, kv = [40, 300, 1, 700], 6, 2
+    q, k, v, starts, _ = prompt_inputs(gen(68), lengths, lengths, heads, kv, dim, torch.float16)
+    q *= 2
+    k[50] = 0.0  # (the second sequence's eleventh key)
+    v = (torch.finfo(torch.float16).max * rand(gen(69), 1, kv, dim).sign()).expand_as(v).half().contiguous()
+    out, lse = fgemm.attention(q, k, v, ints(starts))
+    check_prompt(q, k, v, starts, starts, True, 0, out, lse, what="largest values, prompt")
+    pages = -(-max(lengths) // 16)
+    table = torch.arange(len(lengths) * pages, device=DEV, dtype=torch.int32).view(-1, pages)
+    caches = [torch.zeros(table.numel(), 16, kv, dim, dtype=q.dtype, device=DEV) for _ in range(2)]
+    for s, n in enumerate(lengths):
+        for c, x in zip(caches, (k, v)):
+            c.view(len(lengths), -1, kv, dim)[s, :n] = x[starts[s]:starts[s + 1]]
+    last = torch.tensor(starts[1:], device=DEV) - 1
+    step = fgemm.attention_paged(q[last], *caches, table, ints(lengths))
+    of = lambda x: [x[a:b] for a, b in zip(starts, starts[1:])]  # noqa: E731
+    check_paged(q[last], of(k), of(v), 0, None, *step, "largest values, paged")
+    v[50, 0, 3], v[50, 1, 5] = torch.inf, -torch.inf
+    caches[1].view(len(lengths), -1, kv, dim)[1, 10] = v[50]
+    wild, _ = fgemm.attention(q, k, v, ints(starts))
+    assert bool((wild[50:340, :3, 3] == torch.inf).all()) and bool((wild[50:340, 3:, 5] == -torch.inf).all())
+    rest = wild.clone()
+    rest[50:340, :3, 3], rest[50:340, 3:, 5] = out[50:340, :3, 3], out[50:340, 3:, 5]
+    v[50] = v[51]
+    check_prompt(q, k, v, starts, starts, True, 0, rest, lse, what="largest values beside infinite ones, prompt")
+    got, _ = fgemm.attention_paged(q[last], *caches, table, ints(lengths))
+    assert bool((got[1, :3, 3] == torch.inf).all()) and bool((got[1, 3:, 5] == -torch.inf).all())
+    assert int(torch.isinf(got).sum()) == heads
