@@ -603,6 +603,9 @@ int tiles_of(int heads, int kv_heads) {
   const int rows = 8 * eights_of(heads, kv_heads);
   return (heads / kv_heads + rows - 1) / rows;
 }
+// A share is taken by `units` CTAs, so places are left over where units do not divide
+// them: 16 sequences of the same bytes take 160 us with 8, 32, 38 or 76 key heads of 128
+// (304, 288, 304 and 304 of 304 places), 162 with 40 (280), 163 with 48 or 64 (288, 256).
 int shares_held(int units, int dim, int num_sms) {
   return std::max(num_sms * (dim > 64 ? Cfg<128, 1>::kCtasPerSm : Cfg<64, 1>::kCtasPerSm) / units, 1);
 }

@@ -544,10 +544,12 @@ cudaError_t launch_of(const LogprobParams& p, int num_sms, cudaStream_t stream) 
   while (split > 1 && (static_cast<long long>(p.rows) * split > static_cast<long long>(num_sms) * (kThreadsPerSm / kMany) ||
                        vectors < static_cast<long long>(split) * kMany))
     split /= 2;
-  // Twice the rows on their way on an SM hide each other's ends better (4096 x 50257
-  // fp16 71 us against 78), but the n-th largest of fewer threads' maxima leaves more
-  // logits to read again (256 x 50257 with 20 alternatives 21 us against 18).
-  return split == 1 && p.top <= 8 ? launch_split<TYPE, kFew>(p, split, stream) : launch_split<TYPE, kMany>(p, split, stream);
+  // Twice the rows on their way on an SM hide each other's ends better, but the n-th
+  // largest of fewer threads' maxima leaves more logits to read again. 128 threads against
+  // 256, 4096 x 50257 fp16 with 0, 1, 2, 3, 5, 8, 20 alternatives: 70 / 77 us, 78 / 87, 83 / 88,
+  // 92 / 90, 102 / 95, 115 / 100, 145 / 134; 700 x 131072 fp32: 58 / 66, 69 / 74, 77 / 75, 83 / 75,
+  // 93 / 81, 107 / 87, 134 / 105.
+  return split == 1 && p.top <= 1 ? launch_split<TYPE, kFew>(p, split, stream) : launch_split<TYPE, kMany>(p, split, stream);
 }
 
 }  // namespace
