@@ -125,6 +125,52 @@ def test_scores_beside_a_row_far_from_zero():
         within("beside a far row, lse", lse, most + two, most * 6 * ref.U32 + 2.0 ** -20)
 
 
+@pytest.mark.parametrize("heads,kv_heads", [(4, 2), (64, 16)])  # two tiles of a head, two heads
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_exact_scores_of_any_size(dtype, dim, heads, kv_heads):
+    """Scores that fp32 holds exactly, each query's and key's of a size of its own from 1 to
+    2^40, times a scale of a power of 2: what is left to differ is a weight's exponent, off by
+    2^-23 of it (log2 e, the product; below -40 a weight does not count), its exponential,
+    its rounding to 16 bits, the sums and the store."""
+    t, half = TYPES[dtype], torch.finfo(TYPES[dtype]).eps / 2
+    g = gen(70)
+    lengths, k_lengths = [300, 130, 5, 700], [300, 260, 400, 600]
+    q, k, v, starts, k_starts = prompt_inputs(g, lengths, k_lengths, heads, kv_heads, dim, t)
+
+    def sizes(n, most):
+        return 2.0 ** torch.randint(0, most, (n, 1, 1), generator=g, device=DEV).float()
+
+    # three products of 4 and 4 bits for each score
+    q, k = (torch.zeros_like(x).index_copy_(2, ints([0, 1, dim - 1]).long(), torch.randint(
+        -15, 16, (*x.shape[:2], 3), generator=g, device=DEV).to(t)) for x in (q, k))
+    q *= sizes(len(q), 11 if t == torch.float16 else 20).to(t)
+    k *= sizes(len(k), 12 if t == torch.float16 else 13).to(t)
+    few = [0, 1, heads - 1]
+    for scale in (0.125, 2.0 ** -10, 16.0):
+        for causal, window in ((True, 0), (False, 0), (True, 150)):
+            out, lse = fgemm.attention(q, k, v, ints(starts), k_starts=ints(k_starts), causal=causal, window=window,
+                                       scale=scale)
+            for s in range(len(lengths)):
+                a, b, c, d = starts[s], starts[s + 1], k_starts[s], k_starts[s + 1]
+                seen = ref.seen_by(b - a, d - c, causal, window)
+                any_seen = seen.any(1)
+                for h in few:
+                    x = ref.f64(q[a:b, h]) @ ref.f64(k[c:d, h * kv_heads // heads]).t() * scale
+                    x = torch.where(seen, x, -torch.inf)
+                    z = torch.logsumexp(x, 1)
+                    p = torch.where(seen, torch.exp(x - torch.where(any_seen, z, 0.0)[:, None]), 0.0)
+                    values = ref.f64(v[c:d, h * kv_heads // heads])
+                    want = p @ values
+                    off = 2 * half + 2.0 ** -23 * 40 + (8 + 4 * ((d - c) / 16 + 16)) * ref.U32
+                    bound = (p @ values.abs()) * off + ref.store(want, t)
+                    if t == torch.float16:  # (weights below 2^-14, lifted by 2^6)
+                        bound = bound + 2.0 ** -25 * (seen.double() @ values.abs())
+                    within("exact scores", out[a:b, h], want, bound)
+                    most = torch.where(any_seen, x.amax(1).abs(), 0.0)
+                    within("exact scores, lse", lse[a:b, h], z, most * 6 * ref.U32 + off)
+
+
 def test_large_values_behind_rising_scores():
     """Values near the end of bf16, the second of them behind a score that rises by
     less than 2^8: nothing on the way is larger than the values' sum."""
