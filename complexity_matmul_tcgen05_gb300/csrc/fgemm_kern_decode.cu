@@ -23,10 +23,10 @@
 // once at the end of a sequence's part.
 //
 // Measured, bf16, 32 heads of 128 over 8 key heads: 64 sequences of up to 16384 tokens
-// 203 us (6.48 TB/s), 256 of 300 tokens 68 us (4.6 TB/s); one of 4097 tokens 9.5 us, of
-// which the memory's part is 2.5: two launches, the lengths, the page table, the keys and
+// 197 to 203 us (6.5 to 6.7 TB/s), 256 of 300 tokens 65 us (4.8 TB/s); one of 4097 tokens
+// 9.2 us, of which the memory's part is 2.5: two launches, the lengths, the page table, the keys and
 // the parts come one after the other. fp16, 28 heads of 64 over 4, 3 sequences of 131071
-// tokens 67 us (6.0 TB/s).
+// tokens 64 to 67 us (6.0 to 6.2 TB/s).
 //
 // The work of all sequences, in blocks of 64 tokens laid end to end, is cut into
 // equal shares on the device: lengths are not known to the host. A share is taken by

@@ -21,10 +21,10 @@
 //
 // A row is shared by a cluster of up to 8 CTAs where there are few rows; the others
 // write to its first one.
-// Measured: 4096 x 50257 fp16 71 us (5.8 TB/s; with sums by thread, whose lanes took
-// different branches, 140); 64 x 131072 fp32 9.3 us without alternatives, 15.2 with 20
+// Measured: 4096 x 50257 fp16 70 us (5.9 TB/s; with sums by thread, whose lanes took
+// different branches, 140); 64 x 131072 fp32 9.3 us without alternatives, 14.4 with 20
 // (the search, the second read and two rankings come one after the other); one row of
-// 32000 bf16 4.5 us, with 5 alternatives 7.2.
+// 32000 bf16 4.5 us, with 5 alternatives 6.9.
 #include <cuda_runtime.h>
 
 #include <cstdint>

@@ -29,11 +29,11 @@
 // the step's product is taken row by row over the keys that each row sees
 // (product_by_rows), without the tensor core.
 //
-// Measured, bf16 with 32 heads of 128 over 8 key heads: 16384 tokens, causal, 1.25 ms
-// (1.76 PFLOP/s; a card at its power limit 1.3); 8192 tokens 332 us causal, 618 us not
-// (1.78 PFLOP/s); 13 packed prompts of 177 to 1819 tokens 143 us, bound by the fill and
-// the end of every job, in which the two tiles have nothing to run under; 37 tokens
-// 7.2 us. Heads of 64 are bound by the weights: 1.0 PFLOP/s.
+// Measured, bf16 with 32 heads of 128 over 8 key heads: 16384 tokens, causal, 1.22 to 1.36
+// ms (1.8 to 1.6 PFLOP/s: a card comes to its power limit); 8192 tokens 328 to 350 us
+// causal, 620 to 660 us not (1.77 to 1.67 PFLOP/s); 13 packed prompts of 177 to 1819 tokens
+// 141 us, bound by the fill and the end of every job, in which the two tiles have nothing
+// to run under; 37 tokens 7.1 us. Heads of 64 are bound by the weights: 1.0 PFLOP/s.
 //
 // Every wait is bounded; a wait that runs out latches the error word and all roles
 // leave.
@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 
   // Registers of warps 0-3 go to the others, of 168 for each of 384 threads at launch:
   // without, a few dozen words of the rows' loop live in local memory and 16384 tokens
-  // take 1.33 ms against 1.23. (No function of this kernel is called: with calls the
+  // took 8 % longer. (No function of this kernel is called: with calls the
   // compiler cannot give the rows' warps more than at launch.)
   if (warp < kWeights) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
 

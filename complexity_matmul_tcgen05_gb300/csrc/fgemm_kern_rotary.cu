@@ -12,8 +12,8 @@
 // rotation's own roundings are.
 //
 // Memory-bound: each value is read and written once. Measured, 8191 tokens, 32 heads of
-// 128 over 8 key heads: pairs (i, i + rot / 2) bf16 34 us (5.9 TB/s), with 64 heads 53 us
-// (6.3 TB/s); pairs (2 i, 2 i + 1) 37 us (5.4 TB/s); one token 2.8 us, a launch. Before,
+// 128 over 8 key heads: pairs (i, i + rot / 2) bf16 32 us (6.2 TB/s), with 64 heads 53 us
+// (6.3 TB/s); pairs (2 i, 2 i + 1) 36 us (5.6 TB/s); one token 2.6 us, a launch. Before,
 // with angles in 64-bit floating point and the turns of a part side by side, where a warp
 // met the same banks, the first took 65 us, 1024 tokens 10.5 us (now 7.3).
 #include <cuda_runtime.h>

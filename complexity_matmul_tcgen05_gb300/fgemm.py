@@ -885,7 +885,7 @@ def rotary_cache(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: t
     pairs (i, i + rot / 2), or (2 i, 2 i + 1) if interleaved.  k_cache and v_cache are
     pages x page size x key heads x dim; slot = page * page size + token in the
     page, tokens with a slot outside the cache (-1) are not written.  out, if
-    given, is written (it may be q)."""
+    given, is written (it may be q).  The outputs carry no gradients."""
     L, h, dev = _on(q, "q", handle, 3)
     t = q.dtype
     dt = _dtype_code(t)
@@ -920,7 +920,7 @@ def attention_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     scale None: 1 / sqrt(dim); window 0: every token, else the last `window`.
     lse is the natural logarithm of each row's sum (sequences x heads, fp32); a
     sequence of length 0 gives zeros and -inf.  out, if given, is written (it
-    may be q)."""
+    may be q).  The outputs carry no gradients."""
     L, h, dev = _on(q, "q", handle, 3)
     t = q.dtype
     dt = _dtype_code(t)
@@ -956,7 +956,7 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, starts: torch.T
     window > 0.  scale None: 1 / sqrt(dim).  lse is the natural logarithm of each
     row's sum (T x heads, fp32).  A query that sees no key gives zeros and -inf;
     rows of no sequence are left as they are.  out and lse, if given, are
-    written."""
+    written.  The outputs carry no gradients."""
     L, h, dev = _on(q, "q", handle, 3)
     t = q.dtype
     dt = _dtype_code(t)
@@ -991,7 +991,7 @@ def logprobs(logits: torch.Tensor, tokens: torch.Tensor, *, top: int = 0, handle
     index) with their log probabilities (fp32).
 
     A token outside the vocabulary has -inf; where fewer than `top` logits are
-    above -inf the rest is token -1 with -inf."""
+    above -inf the rest is token -1 with -inf.  The outputs carry no gradients."""
     L, h, dev = _on(logits, "logits", handle)
     rows, vocab = logits.shape
     code = LOGIT_TYPES.get(logits.dtype)
