@@ -524,7 +524,7 @@ fgemm_status_t fgemm_rotary_cache(fgemm_handle_t h, int64_t T, int32_t heads, in
  * Sums are fp32 and their order depends on the sizes, the lengths and the SM
  * count only; weights are rounded to dtype before they meet the values. Before the
  * division an output is a sum of e^(x_j - m) v_j, m the largest x_j, which has to
- * stay inside fp32 (values of bf16 may be as large).
+ * stay inside fp32 (values of bf16 may be as large), as have q . k_j and x_j log2 e.
  */
 size_t fgemm_attention_paged_workspace(fgemm_handle_t h, int64_t seqs, int32_t heads, int32_t kv_heads, int32_t dim);
 fgemm_status_t fgemm_attention_paged(fgemm_handle_t h, int64_t seqs, int32_t heads, int32_t kv_heads, int32_t dim,
